@@ -9,6 +9,9 @@ works but every call raises ``RuntimeError`` -- there is no fallback path.
     o      = decode_step(q, k, v, beta, S)        # S updated in place
     o      = decode_tokens(q, k, v, beta, S)      # m tokens per sequence, S in place
 
+The gated delta rule (a decay per token and head, shared key heads) and the norms around a gated
+mixer are the ``gated_*`` and ``norm_gate*`` calls of ``gated.py``.
+
 Semantics (per head): lambda = ||k||^2, alpha = (1 - e^{-beta*lambda})/lambda,
 S <- (I - alpha k k^T) S + alpha k v^T, o = S^T q with the updated S.
 ["Exact Flow Linear Attention" (gist.science), Metodologia 3;
@@ -26,7 +29,9 @@ import torch
 __all__ = ["EflaError", "lib_path", "load", "fwd_chunked", "fwd_chunked_scan", "fwd_chunked_scan_static",
            "scan_workspace", "fwd_recurrent", "decode_step", "decode_tokens", "bwd_recurrent", "bwd_chunked",
            "fwd_chunked_train",
-           "bwd_workspace", "prep", "device_status", "error_string", "set_wait_limit_ns", "set_debug_stall", "abi_version", "STATUS", "UPDATES"]
+           "bwd_workspace", "prep", "device_status", "error_string", "set_wait_limit_ns", "set_debug_stall", "abi_version", "STATUS", "UPDATES",
+           "gated_fwd_chunked", "gated_fwd_chunked_train", "gated_bwd_chunked", "gated_bwd_workspace",
+           "gated_decode_step", "gated_decode_tokens", "gated_prep", "gated_prep_bwd", "norm_gate", "norm_gate_bwd"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_PKG, "libefla.so")
@@ -474,3 +479,7 @@ def set_debug_stall(on) -> None:
     True (or 1) names the chunk kernel; an int is the header's set of kernel bits (1 chunk
     kernel, 2 backward state pass, 4 backward gradient kernel)."""
     load().efla_debug_set_stall(int(on) & 7)
+
+
+from .gated import (gated_bwd_chunked, gated_bwd_workspace, gated_decode_step, gated_decode_tokens,  # noqa: E402
+                    gated_fwd_chunked, gated_fwd_chunked_train, gated_prep, gated_prep_bwd, norm_gate, norm_gate_bwd)

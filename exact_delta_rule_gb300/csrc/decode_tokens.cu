@@ -22,7 +22,14 @@
 // in shared memory ([d][t], read as broadcasts), the Gram terms k_t.k_i and q_t.k_i are
 // formed once per block, and the partial sums of X and Y of every row group are added in a
 // shared-memory pass (no atomics).
-#include "internal.cuh"
+//
+// The gated form (S_t = e^{g_t} (I - alpha_t k_t k_t^T) S_{t-1} + alpha_t k_t v_t^T) is the same with
+// X_t, Y_t times e^{G_t}, the Gram terms times Gamma_ti = e^{G_t - G_i} and
+// S = e^{G_last} S_0 + sum_i e^{G_last - G_i} k_i u_i^T, G the running sum of g over the block; its
+// value heads share key heads (value head h reads key head h / (H / Hk)).
+#include <type_traits>
+
+#include "gated.cuh"
 
 namespace efla {
 namespace {
@@ -34,11 +41,11 @@ constexpr int NT = 256;
 constexpr int CW = 2;   // columns of S per thread
 constexpr size_t PART_BYTES = 2 * (size_t)NT * CW * MB * sizeof(float);  // [2][NRG][MB][DV] (64 KB)
 
-template <int DK, int DV, typename TIn, typename TOut>
+template <int DK, int DV, typename TIn, typename TOut, bool GATED>
 __global__ void __launch_bounds__(256, 2) decode_tokens_kernel(const TIn *__restrict__ q, const TIn *__restrict__ k,
-                                                            const TIn *__restrict__ v, const float *__restrict__ beta,
-                                                            float *__restrict__ S, TOut *__restrict__ o, int m, int H,
-                                                            int euler) {
+                                                            const TIn *__restrict__ v, const float *__restrict__ g,
+                                                            const float *__restrict__ beta, float *__restrict__ S,
+                                                            TOut *__restrict__ o, int m, int H, int Hk, int euler) {
     constexpr int NCL = DV / CW;   // column lanes per row group
     constexpr int NRG = NT / NCL;  // row groups
     constexpr int RW = DK / NRG;   // rows of S per thread
@@ -49,6 +56,7 @@ __global__ void __launch_bounds__(256, 2) decode_tokens_kernel(const TIn *__rest
     __shared__ __align__(16) float vs[MB][DV];  // v of the block, then u in place (same thread, same (t, j))
     __shared__ float gkk[MB][MB + 1], gqk[MB][MB + 1];
     __shared__ float al[MB], bs[MB];
+    __shared__ float gh[MB], gl[MB], eg[MB], ec[MB];  // (gated form: block_decay16)
     extern __shared__ __align__(16) float part[];  // [X, Y][row group][t][j]; group 0 then holds the sums
 
     const int unit = blockIdx.x;  // b * H + h
@@ -74,7 +82,7 @@ __global__ void __launch_bounds__(256, 2) decode_tokens_kernel(const TIn *__rest
 #pragma unroll
         for (int x = 0; x < NKQ; ++x) {
             const int e = tid + x * NT, t = e / DK, d = e % DK;
-            const size_t row = ((size_t)b * m + t0 + t) * H + h;
+            const size_t row = GATED ? ((size_t)b * m + t0 + t) * Hk + h / (H / Hk) : ((size_t)b * m + t0 + t) * H + h;
             kr[x] = t < mb ? to_f32(k[row * DK + d]) : 0.f;
             qr[x] = t < mb ? to_f32(q[row * DK + d]) : 0.f;
         }
@@ -84,6 +92,9 @@ __global__ void __launch_bounds__(256, 2) decode_tokens_kernel(const TIn *__rest
             vr[x] = t < mb ? to_f32(v[(((size_t)b * m + t0 + t) * H + h) * DV + c]) : 0.f;
         }
         const float br = tid < mb ? beta[((size_t)b * m + t0 + tid) * H + h] : 0.f;
+        if constexpr (GATED) {
+            if (tid < 32) block_decay16(tid < mb ? g[((size_t)b * m + t0 + tid) * H + h] : 0.f, tid, gh, gl, eg, ec);
+        }
 #pragma unroll
         for (int x = 0; x < NKQ; ++x) {
             const int e = tid + x * NT, t = e / DK, d = e % DK;
@@ -127,8 +138,10 @@ __global__ void __launch_bounds__(256, 2) decode_tokens_kernel(const TIn *__rest
             if (dq == 0) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    gkk[t][4 * i4 + e] = a[e];
-                    gqk[t][4 * i4 + e] = c[e];
+                    float d = 1.f;  // (entries above the diagonal are not read)
+                    if constexpr (GATED) d = 4 * i4 + e <= t ? pair_decay(gh[t], gl[t], gh[4 * i4 + e], gl[4 * i4 + e]) : 0.f;
+                    gkk[t][4 * i4 + e] = GATED ? d * a[e] : a[e];
+                    gqk[t][4 * i4 + e] = GATED ? d * c[e] : c[e];
                 }
                 if ((t >> 2) == i4) {
                     const int e = t & 3;
@@ -180,14 +193,14 @@ __global__ void __launch_bounds__(256, 2) decode_tokens_kernel(const TIn *__rest
             float u[MB];
 #pragma unroll
             for (int t = 0; t < MB; ++t) {
-                float acc = vs[t][j] - X[t * DV + j];
+                float acc = GATED ? fmaf(-eg[t], X[t * DV + j], vs[t][j]) : vs[t][j] - X[t * DV + j];
 #pragma unroll
                 for (int i = 0; i < t; ++i) acc = fmaf(-gkk[t][i], u[i], acc);
                 u[t] = al[t] * acc;
-                float ov = Y[t * DV + j];
+                float ov = GATED ? eg[t] * Y[t * DV + j] : Y[t * DV + j];
 #pragma unroll
                 for (int i = 0; i <= t; ++i) ov = fmaf(gqk[t][i], u[i], ov);
-                vs[t][j] = u[t];
+                vs[t][j] = GATED ? ec[t] * u[t] : u[t];  // (what the state update takes)
                 if (t < mb) o[(((size_t)b * m + t0 + t) * H + h) * DV + j] = from_f32<TOut>(ov);
             }
         }
@@ -204,6 +217,10 @@ __global__ void __launch_bounds__(256, 2) decode_tokens_kernel(const TIn *__rest
         for (int r = 0; r < RW; ++r) {
             const float4 *row = reinterpret_cast<const float4 *>(kT[r0 + r]);
             float a0 = s[r][0], a1 = s[r][1];
+            if constexpr (GATED) {
+                a0 *= eg[MB - 1];
+                a1 *= eg[MB - 1];
+            }
 #pragma unroll
             for (int t4 = 0; t4 < MB / 4; ++t4) {
                 const float4 a = row[t4];
@@ -223,26 +240,33 @@ __global__ void __launch_bounds__(256, 2) decode_tokens_kernel(const TIn *__rest
         *reinterpret_cast<float2 *>(Su + (size_t)(r0 + r) * DV + c0) = make_float2(s[r][0], s[r][1]);
 }
 
-template <int DK, int DV, typename TIn, typename TOut>
-cudaError_t tokens_launch(const DecodeArgs &a) {
+template <int DK, int DV, typename TIn, typename TOut, typename A>
+cudaError_t tokens_launch(const A &a) {
+    constexpr bool GATED = std::is_same_v<A, GatedDecodeArgs>;
+    const float *g = nullptr;
+    int Hk = a.H;
+    if constexpr (GATED) {
+        g = a.g;
+        Hk = a.Hk;
+    }
     static bool attr[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !attr[dev]) {
-        e = cudaFuncSetAttribute(decode_tokens_kernel<DK, DV, TIn, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)PART_BYTES);
+        e = cudaFuncSetAttribute(decode_tokens_kernel<DK, DV, TIn, TOut, GATED>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PART_BYTES);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr[dev] = true;
     }
-    decode_tokens_kernel<DK, DV, TIn, TOut><<<a.B * a.H, NT, PART_BYTES, a.stream>>>(
-        static_cast<const TIn *>(a.q), static_cast<const TIn *>(a.k), static_cast<const TIn *>(a.v), a.beta, a.S,
-        static_cast<TOut *>(a.o), a.m, a.H, a.euler);
+    decode_tokens_kernel<DK, DV, TIn, TOut, GATED><<<a.B * a.H, NT, PART_BYTES, a.stream>>>(
+        static_cast<const TIn *>(a.q), static_cast<const TIn *>(a.k), static_cast<const TIn *>(a.v), g, a.beta, a.S,
+        static_cast<TOut *>(a.o), a.m, a.H, Hk, a.euler);
     return cudaGetLastError();
 }
 
-template <int DK, int DV>
-cudaError_t tokens_types(const DecodeArgs &a) {
+template <int DK, int DV, typename A>
+cudaError_t tokens_types(const A &a) {
     const bool ib = a.in_dtype == EFLA_BF16, ob = a.o_dtype == EFLA_BF16;
     if (ib && ob) return tokens_launch<DK, DV, __nv_bfloat16, __nv_bfloat16>(a);
     if (ib) return tokens_launch<DK, DV, __nv_bfloat16, float>(a);
@@ -250,8 +274,8 @@ cudaError_t tokens_types(const DecodeArgs &a) {
     return tokens_launch<DK, DV, float, float>(a);
 }
 
-template <int DK>
-cudaError_t tokens_dv(const DecodeArgs &a) {
+template <int DK, typename A>
+cudaError_t tokens_dv(const A &a) {
     switch (a.dv) {
         case 32: return tokens_types<DK, 32>(a);
         case 64: return tokens_types<DK, 64>(a);
@@ -259,9 +283,8 @@ cudaError_t tokens_dv(const DecodeArgs &a) {
     }
 }
 
-}  // namespace
-
-cudaError_t launch_decode_tokens(const DecodeArgs &a) {
+template <typename A>
+cudaError_t tokens_dk(const A &a) {
     if (a.B == 0 || a.m == 0) return cudaSuccess;
     switch (a.dk) {
         case 32: return tokens_dv<32>(a);
@@ -269,5 +292,10 @@ cudaError_t launch_decode_tokens(const DecodeArgs &a) {
         default: return tokens_dv<128>(a);
     }
 }
+
+}  // namespace
+
+cudaError_t launch_decode_tokens(const DecodeArgs &a) { return tokens_dk(a); }
+cudaError_t launch_gated_decode_tokens(const GatedDecodeArgs &a) { return tokens_dk(a); }
 
 }  // namespace efla

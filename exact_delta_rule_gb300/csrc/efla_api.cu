@@ -25,13 +25,18 @@ static __device__ __align__(256) unsigned char g_scan_scratch[SCAN_SCRATCH_BYTES
 
 thread_local std::string g_last_error;
 
-efla_status fail(efla_status s, const char *fmt, ...) {
+efla_status vfail(efla_status s, const char *fmt, va_list ap) {
     char buf[512];
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    g_last_error = buf;
+    return s;
+}
+
+efla_status fail(efla_status s, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
+    s = vfail(s, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
     return s;
 }
 
@@ -124,6 +129,19 @@ efla_status run_fwd(FwdArgs a, bool chunked) {
 }
 
 }  // namespace
+
+efla_status api_fail(efla_status s, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    s = vfail(s, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+efla_status api_ok() {
+    g_last_error.clear();
+    return EFLA_OK;
+}
 
 int *device_status_ptr() {
     // One status word per device: the symbol's device address differs per device, so it is

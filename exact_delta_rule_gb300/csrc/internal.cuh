@@ -22,6 +22,11 @@ unsigned long long wait_limit_ns();
 enum { STALL_CHUNK = 1, STALL_BWD_STATE = 2, STALL_BWD_GRAD = 4 };
 int debug_stall();
 
+// Records the reason of a failing call for efla_last_error (efla_api.cu) and returns its status;
+// api_ok clears it.
+efla_status api_fail(efla_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+efla_status api_ok();
+
 struct FwdArgs {
     const void *q, *k, *v;
     const float *beta;

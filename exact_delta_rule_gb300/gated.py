@@ -1,0 +1,372 @@
+"""Gated delta rule and the norms around it: the binding of the ``efla_gated_*`` and
+``efla_norm_gate*`` calls of ``include/efla.h`` (argument marshalling only).
+
+    S_t = e^{g_t} (I - alpha_t k_t k_t^T) S_{t-1} + alpha_t k_t v_t^T,   o_t = S_t^T q_t
+
+H value heads read H_k query/key heads (value head h reads key head ``h // (H // H_k)``);
+``update="euler"`` (alpha = beta) is the gated delta rule, ``update="exact"`` the exact gate with the
+same decay.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import UPDATES, EflaError, _check, load
+
+_DT = {torch.bfloat16: 0, torch.float32: 1}
+_vp, _ip, _sz, _ll, _fl = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float
+_SIGNATURES = {
+    "efla_gated_fwd_chunked": [_vp] * 9 + [_ip] * 10 + [_vp],
+    "efla_gated_fwd_chunked_train": [_vp] * 8 + [_ip] * 8 + [_vp, _sz, _vp],
+    "efla_gated_bwd_workspace": [_ip] * 7 + [ctypes.POINTER(_sz)],
+    "efla_gated_bwd_chunked": [_vp] * 14 + [_ip] * 9 + [_vp, _sz, _vp],
+    "efla_gated_decode_step": [_vp] * 7 + [_ip] * 8 + [_vp],
+    "efla_gated_decode_tokens": [_vp] * 7 + [_ip] * 9 + [_vp],
+    "efla_gated_prep": [_vp] * 10 + [_ll] + [_ip] * 4 + [_fl, _fl, _vp],
+    "efla_gated_prep_bwd": [_vp] * 16 + [_ll] + [_ip] * 4 + [_fl, _fl, _vp, _sz, _vp],
+    "efla_gated_prep_bwd_workspace": [_ll, _ip, ctypes.POINTER(_sz)],
+    "efla_norm_gate": [_vp] * 4 + [_ll, _ip, _ip, _fl, _vp],
+    "efla_norm_gate_bwd": [_vp] * 7 + [_ll, _ip, _ip, _fl, _vp, _sz, _vp],
+    "efla_norm_gate_bwd_workspace": [_ip, ctypes.POINTER(_sz)],
+}
+_bound = None
+
+
+def _lib():
+    global _bound
+    if _bound is None:
+        L = load()
+        for name, types in _SIGNATURES.items():
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = _ip, types
+        _bound = L
+    return _bound
+
+
+def _bad(msg: str):
+    raise EflaError(1, msg)
+
+
+def _need(name: str, t: torch.Tensor, shape, dtype, like: torch.Tensor):
+    """`t` is a contiguous tensor of this shape and dtype on `like`'s device."""
+    if t.dtype is not dtype or t.shape != shape:
+        _bad(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.device != like.device:
+        _bad(f"{name} is on {t.device}, the first argument on {like.device}")
+    if not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _first(name: str, t: torch.Tensor, dims: int) -> int:
+    """Checks of the argument the others are held to; its dtype's code.  The device is checked last,
+    so that every other fault is reported on a machine without a GPU too."""
+    if t.dim() != dims or (code := _DT.get(t.dtype)) is None:
+        _bad(f"{name} must be a {dims}-D bfloat16 or float32 tensor, got {t.dtype} {list(t.shape)}")
+    return code
+
+
+def _on_device(t: torch.Tensor):
+    if not t.is_cuda:
+        _bad("the tensors must be CUDA tensors")
+    if t.device.index != torch.cuda.current_device():
+        _bad(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An allocation the call's kernels use on `stream` (the allocator must not hand it out again
+    before they are done, where that is not the current stream)."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _update(update: str) -> int:
+    code = UPDATES.get(update)
+    if code is None:
+        _bad(f"unknown update rule {update!r}")
+    return code
+
+
+def _heads(q, k, v, g, beta, lead: int):
+    """Shapes of the mixer's inputs with `lead` leading dimensions; (lead shape, Hk, H, dk, dv, dtype code)."""
+    code = _first("q", q, lead + 2)
+    if v.dim() != lead + 2:
+        _bad(f"v must be {lead + 2}-D, got {list(v.shape)}")
+    at = tuple(q.shape[:lead])
+    Hk, dk = q.shape[lead:]
+    H, dv = v.shape[lead:]
+    if Hk < 1 or H % Hk:
+        _bad(f"v's {H} heads must be a multiple of q's and k's {Hk}")
+    _need("q", q, q.shape, q.dtype, q)
+    _need("k", k, q.shape, q.dtype, q)
+    _need("v", v, (*at, H, dv), q.dtype, q)
+    _need("g", g, (*at, H), torch.float32, q)
+    _need("beta", beta, (*at, H), torch.float32, q)
+    return at, Hk, H, dk, dv, code
+
+
+def _given(name: str, t: Optional[torch.Tensor], shape, dtype, like, stream) -> torch.Tensor:
+    """An output: the caller's, checked, or a new one."""
+    if t is None:
+        return _empty(shape, dtype, like, stream)
+    _need(name, t, shape, dtype, like)
+    return t
+
+
+def _o_dtype(o, o_dtype, q) -> torch.dtype:
+    dtype = o.dtype if o is not None else q.dtype if o_dtype is None else o_dtype
+    if dtype not in _DT:
+        _bad(f"o must be bfloat16 or float32, not {dtype}")
+    return dtype
+
+
+def gated_fwd_chunked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                      S0: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, *,
+                      o: Optional[torch.Tensor] = None, S_T: Optional[torch.Tensor] = None,
+                      o_dtype: Optional[torch.dtype] = None, stream=None, return_state: bool = True,
+                      update: str = "euler") -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The gated delta rule over whole sequences (``efla_gated_fwd_chunked``).
+
+    q, k [B,T,H_k,dk], v [B,T,H,dv] (bf16 or fp32); g (log decay, <= 0), beta [B,T,H] fp32;
+    S0 [N,H,dk,dv] fp32; cu_seqlens [N+1] int32 (then B == 1).  Returns (o [B,T,H,dv], S_T
+    [N,H,dk,dv] fp32 or None when ``return_state`` is False).
+    """
+    (B, T), Hk, H, dk, dv, code = _heads(q, k, v, g, beta, 2)
+    rule = _update(update)
+    N = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            _bad("cu_seqlens must be a 1-D int32 tensor of at least one bound")
+        _need("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, q)
+        if B != 1:
+            _bad(f"cu_seqlens given with B={B} (must be 1)")
+        N = cu_seqlens.shape[0] - 1
+    if S0 is not None:
+        _need("S0", S0, (N, H, dk, dv), torch.float32, q)
+    od = _o_dtype(o, o_dtype, q)
+    _on_device(q)
+    L = _lib()
+    o = _given("o", o, (B, T, H, dv), od, q, stream)
+    if S_T is not None or return_state:
+        S_T = _given("S_T", S_T, (N, H, dk, dv), torch.float32, q, stream)
+    _check(L.efla_gated_fwd_chunked(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
+                                    _ptr(cu_seqlens), o.data_ptr(), _ptr(S_T), B, T, Hk, H, dk, dv, N, code, _DT[od],
+                                    rule, _stream(stream)))
+    return o, S_T
+
+
+def gated_bwd_workspace(B: int, T: int, Hk: int, H: int, dk: int, dv: int, dtype: torch.dtype) -> int:
+    """Workspace bytes of ``gated_fwd_chunked_train`` and ``gated_bwd_chunked``."""
+    if dtype not in _DT:
+        _bad(f"unsupported dtype {dtype}")
+    n = _sz(0)
+    _check(_lib().efla_gated_bwd_workspace(B, T, Hk, H, dk, dv, _DT[dtype], ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, like: torch.Tensor, stream) -> torch.Tensor:
+    if ws is None:
+        return _empty((max(need, 16),), torch.uint8, like, stream)
+    if ws.device != like.device or not ws.is_contiguous():
+        _bad(f"workspace must be a contiguous tensor on {like.device}")
+    if ws.numel() * ws.element_size() < need:
+        _bad(f"workspace of {need} bytes needed, got {ws.numel() * ws.element_size()}")
+    return ws
+
+
+def gated_fwd_chunked_train(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                            S0: Optional[torch.Tensor] = None, *, workspace: Optional[torch.Tensor] = None,
+                            o: Optional[torch.Tensor] = None, S_T: Optional[torch.Tensor] = None, stream=None,
+                            update: str = "euler") -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """``gated_fwd_chunked`` over rows of [B, T] (o in q's dtype) that also fills ``workspace`` for one
+    ``gated_bwd_chunked(..., workspace=..., saved=True)`` of the same inputs.  Returns (o, S_T, workspace)."""
+    (B, T), Hk, H, dk, dv, code = _heads(q, k, v, g, beta, 2)
+    rule = _update(update)
+    if S0 is not None:
+        _need("S0", S0, (B, H, dk, dv), torch.float32, q)
+    _on_device(q)
+    L = _lib()
+    o = _given("o", o, (B, T, H, dv), q.dtype, q, stream)
+    S_T = _given("S_T", S_T, (B, H, dk, dv), torch.float32, q, stream)
+    need = gated_bwd_workspace(B, T, Hk, H, dk, dv, q.dtype)
+    ws = _workspace(workspace, need, q, stream)
+    _check(L.efla_gated_fwd_chunked_train(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                          _ptr(S0), o.data_ptr(), S_T.data_ptr(), B, T, Hk, H, dk, dv, code, rule,
+                                          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+    return o, S_T, ws
+
+
+def gated_bwd_chunked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                      S0: Optional[torch.Tensor], dO: torch.Tensor, dS_T: Optional[torch.Tensor] = None, *,
+                      need_dS0: bool = True, workspace: Optional[torch.Tensor] = None, saved: bool = False,
+                      stream=None, update: str = "euler") -> dict:
+    """Gradients of ``gated_fwd_chunked`` (no cu_seqlens) from dO [B,T,H,dv] in q's dtype and dS_T
+    [B,H,dk,dv] fp32 (or None): dq, dk, dv in q's dtype, dg, dbeta and dS0 fp32
+    (``efla_gated_bwd_chunked``).  ``saved=True`` takes the workspace ``gated_fwd_chunked_train``
+    filled for these inputs and does not run the forward again; it serves one backward."""
+    (B, T), Hk, H, dk, dv, code = _heads(q, k, v, g, beta, 2)
+    rule = _update(update)
+    if saved and workspace is None:
+        _bad("saved=True needs the workspace that gated_fwd_chunked_train filled")
+    _need("dO", dO, v.shape, q.dtype, q)
+    for name, t in (("S0", S0), ("dS_T", dS_T)):
+        if t is not None:
+            _need(name, t, (B, H, dk, dv), torch.float32, q)
+    _on_device(q)
+    L = _lib()
+    need = gated_bwd_workspace(B, T, Hk, H, dk, dv, q.dtype)
+    ws = _workspace(workspace, need, q, stream)
+    out = {"dq": _empty(q.shape, q.dtype, q, stream), "dk": _empty(q.shape, q.dtype, q, stream),
+           "dv": _empty(v.shape, q.dtype, q, stream), "dg": _empty(g.shape, torch.float32, q, stream),
+           "dbeta": _empty(g.shape, torch.float32, q, stream),
+           "dS0": _empty((B, H, dk, dv), torch.float32, q, stream) if need_dS0 else None}
+    _check(L.efla_gated_bwd_chunked(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
+                                    dO.data_ptr(), _ptr(dS_T), *(_ptr(t) for t in out.values()), B, T, Hk, H, dk, dv,
+                                    code, rule, int(saved), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                    _stream(stream)))
+    return out
+
+
+def _decode(fn, lead, q, k, v, g, beta, S, o, o_dtype, stream, update):
+    at, Hk, H, dk, dv, code = _heads(q, k, v, g, beta, lead)
+    rule = _update(update)
+    _need("S", S, (at[0], H, dk, dv), torch.float32, q)
+    od = _o_dtype(o, o_dtype, q)
+    _on_device(q)
+    o = _given("o", o, v.shape, od, q, stream)
+    _check(getattr(_lib(), fn)(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), S.data_ptr(),
+                               o.data_ptr(), *at, Hk, H, dk, dv, code, _DT[od], rule, _stream(stream)))
+    return o
+
+
+def gated_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                      S: torch.Tensor, *, o: Optional[torch.Tensor] = None, o_dtype: Optional[torch.dtype] = None,
+                      stream=None, update: str = "euler") -> torch.Tensor:
+    """One token per sequence; S [B,H,dk,dv] fp32 is updated in place (``efla_gated_decode_step``).
+    q, k [B,H_k,dk], v [B,H,dv], g, beta [B,H] fp32.  Returns o [B,H,dv]."""
+    return _decode("efla_gated_decode_step", 1, q, k, v, g, beta, S, o, o_dtype, stream, update)
+
+
+def gated_decode_tokens(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                        S: torch.Tensor, *, o: Optional[torch.Tensor] = None, o_dtype: Optional[torch.dtype] = None,
+                        stream=None, update: str = "euler") -> torch.Tensor:
+    """m tokens per sequence appended to the state, S [B,H,dk,dv] fp32 updated in place
+    (``efla_gated_decode_tokens``).  q, k [B,m,H_k,dk], v [B,m,H,dv], g, beta [B,m,H] fp32.
+    Returns o [B,m,H,dv].  Equal to m ``gated_decode_step`` calls."""
+    return _decode("efla_gated_decode_tokens", 2, q, k, v, g, beta, S, o, o_dtype, stream, update)
+
+
+def _prep_args(q, k, a, b, A_log, dt_bias):
+    code = _first("q", q, q.dim())
+    if q.dim() < 3 or a.dim() != q.dim() - 1:
+        _bad(f"q must be [..., H_k, dk] and a [..., H], got {list(q.shape)} and {list(a.shape)}")
+    lead, H = tuple(q.shape[:-2]), a.shape[-1]
+    _need("q", q, q.shape, q.dtype, q)
+    _need("k", k, q.shape, q.dtype, q)
+    _need("a", a, (*lead, H), q.dtype, q)
+    _need("b", b, (*lead, H), q.dtype, q)
+    _need("A_log", A_log, (H,), torch.float32, q)
+    _need("dt_bias", dt_bias, (H,), torch.float32, q)
+    tokens = 1
+    for n in lead:
+        tokens *= n
+    return code, tokens, H
+
+
+def gated_prep(q: torch.Tensor, k: torch.Tensor, a: torch.Tensor, b: torch.Tensor, A_log: torch.Tensor,
+               dt_bias: torch.Tensor, *, scale: float = 1.0, eps: float = 1e-6, stream=None) -> dict:
+    """The norms and gates before the mixer (``efla_gated_prep``): q^ = scale q / sqrt(|q|^2 + eps), k^
+    likewise without the scale, g = -exp(A_log) softplus(a + dt_bias), beta = sigmoid(b).
+
+    q, k [..., H_k, dk] and a, b [..., H] (bf16 or fp32), A_log, dt_bias [H] fp32.  Returns a dict
+    with q and k in q's dtype and g, beta [..., H] fp32."""
+    code, tokens, H = _prep_args(q, k, a, b, A_log, dt_bias)
+    _on_device(q)
+    out = {"q": _empty(q.shape, q.dtype, q, stream), "k": _empty(q.shape, q.dtype, q, stream),
+           "g": _empty(a.shape, torch.float32, q, stream), "beta": _empty(a.shape, torch.float32, q, stream)}
+    _check(_lib().efla_gated_prep(q.data_ptr(), k.data_ptr(), a.data_ptr(), b.data_ptr(), A_log.data_ptr(),
+                                  dt_bias.data_ptr(), *(t.data_ptr() for t in out.values()), tokens, q.shape[-2], H,
+                                  q.shape[-1], code, scale, eps, _stream(stream)))
+    return out
+
+
+def gated_prep_bwd(q: torch.Tensor, k: torch.Tensor, a: torch.Tensor, b: torch.Tensor, A_log: torch.Tensor,
+                   dt_bias: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dg: torch.Tensor, dbeta: torch.Tensor, *,
+                   scale: float = 1.0, eps: float = 1e-6, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of ``gated_prep`` from those of its outputs (``efla_gated_prep_bwd``): a dict with dq,
+    dk, da, db in q's dtype and dA_log, ddt_bias [H] fp32."""
+    code, tokens, H = _prep_args(q, k, a, b, A_log, dt_bias)
+    _need("dq", dq, q.shape, q.dtype, q)
+    _need("dk", dk, q.shape, q.dtype, q)
+    _need("dg", dg, a.shape, torch.float32, q)
+    _need("dbeta", dbeta, a.shape, torch.float32, q)
+    _on_device(q)
+    L = _lib()
+    need = _sz(0)
+    _check(L.efla_gated_prep_bwd_workspace(tokens, H, ctypes.byref(need)))
+    ws = _workspace(workspace, need.value, q, stream)
+    out = {"dq": _empty(q.shape, q.dtype, q, stream), "dk": _empty(q.shape, q.dtype, q, stream),
+           "da": _empty(a.shape, q.dtype, q, stream), "db": _empty(a.shape, q.dtype, q, stream),
+           "dA_log": _empty((H,), torch.float32, q, stream), "ddt_bias": _empty((H,), torch.float32, q, stream)}
+    _check(L.efla_gated_prep_bwd(q.data_ptr(), k.data_ptr(), a.data_ptr(), b.data_ptr(), A_log.data_ptr(),
+                                 dt_bias.data_ptr(), dq.data_ptr(), dk.data_ptr(), dg.data_ptr(), dbeta.data_ptr(),
+                                 *(t.data_ptr() for t in out.values()), tokens, q.shape[-2], H, q.shape[-1], code,
+                                 scale, eps, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+    return out
+
+
+def _norm_args(o, z, w):
+    if o.dim() < 1:
+        _bad("o must have at least one dimension")
+    code = _first("o", o, o.dim())
+    d = o.shape[-1]
+    _need("o", o, o.shape, o.dtype, o)
+    _need("z", z, o.shape, o.dtype, o)
+    _need("w", w, (d,), torch.float32, o)
+    rows = 1
+    for n in o.shape[:-1]:
+        rows *= n
+    return code, rows, d
+
+
+def norm_gate(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, *, eps: float = 1e-6,
+              y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The norm after the mixer fused with its output gate (``efla_norm_gate``):
+    y = o / sqrt(mean(o^2) + eps) * w * silu(z) over the last dimension.  o, z [..., d] (bf16 or
+    fp32), w [d] fp32; ``y`` may be o or z."""
+    code, rows, d = _norm_args(o, z, w)
+    _on_device(o)
+    y = _given("y", y, o.shape, o.dtype, o, stream)
+    _check(_lib().efla_norm_gate(o.data_ptr(), z.data_ptr(), w.data_ptr(), y.data_ptr(), rows, d, code, eps,
+                                 _stream(stream)))
+    return y
+
+
+def norm_gate_bwd(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, *, eps: float = 1e-6,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of ``norm_gate`` (``efla_norm_gate_bwd``): a dict with do, dz in o's dtype and dw [d] fp32."""
+    code, rows, d = _norm_args(o, z, w)
+    _need("dy", dy, o.shape, o.dtype, o)
+    _on_device(o)
+    L = _lib()
+    need = _sz(0)
+    _check(L.efla_norm_gate_bwd_workspace(d, ctypes.byref(need)))
+    ws = _workspace(workspace, need.value, o, stream)
+    out = {"do": _empty(o.shape, o.dtype, o, stream), "dz": _empty(o.shape, o.dtype, o, stream),
+           "dw": _empty((d,), torch.float32, o, stream)}
+    _check(L.efla_norm_gate_bwd(o.data_ptr(), z.data_ptr(), w.data_ptr(), dy.data_ptr(),
+                                *(t.data_ptr() for t in out.values()), rows, d, code, eps, ws.data_ptr(),
+                                ws.numel() * ws.element_size(), _stream(stream)))
+    return out

@@ -45,7 +45,7 @@
 extern "C" {
 #endif
 
-#define EFLA_ABI_VERSION 10
+#define EFLA_ABI_VERSION 11
 
 typedef enum {
     EFLA_OK = 0,
@@ -349,6 +349,114 @@ efla_status efla_decode_step_ex(const void *q, const void *k, const void *v, con
 efla_status efla_prep(const void *k, const void *v, const float *beta, float *lam, float *alpha,
                       void *ak, void *av, long long n, int d_k, int d_v, efla_dtype dtype,
                       efla_update update, efla_stream_t stream);
+
+/*
+ * Gated delta rule.
+ *
+ *   S_t = e^{g_t} (I - alpha_t k_t k_t^T) S_{t-1} + alpha_t k_t v_t^T,   o_t = S_t^T q_t
+ *
+ * the update rule above with a decay e^{g_t} of the whole state per token and head.  With
+ * EFLA_UPDATE_EULER (alpha = beta) this is the gated delta rule; EFLA_UPDATE_EXACT gives the exact
+ * gate the same decay.  H value heads read H_k query/key heads, H a multiple of H_k: value head h
+ * reads key head h / (H / H_k).  As everywhere here, q is not scaled and q, k are not normalised
+ * (efla_gated_prep does both).
+ *
+ *   q, k  [B, T, H_k, d_k]  in_dtype      v [B, T, H, d_v] in_dtype
+ *   g, beta [B, T, H] fp32.  g is the log of the decay, g <= 0 (a gate below -700, or -inf, is a
+ *         decay of 0: the state restarts).  Positive gates are evaluated by the same formulas as long
+ *         as their sum over 64 tokens keeps e^sum finite.
+ *   S0, S_T [N, H, d_k, d_v] fp32;  o [B, T, H, d_v] o_dtype;  cu_seqlens as for efla_fwd_chunked
+ * Supported: d_k, d_v in {32, 64, 128}, bf16 or fp32.  bf16 inputs with d_k = d_v = 128 run on the
+ * tensor cores, every other combination on CUDA cores in fp32.  State and sums are fp32 everywhere.
+ */
+
+/* The forward over whole sequences, in chunks of 64 tokens.  S0 and S_T may be NULL (zeros / not
+ * written), and S0 == S_T is allowed. */
+efla_status efla_gated_fwd_chunked(const void *q, const void *k, const void *v, const float *g,
+                                   const float *beta, const float *S0, const int32_t *cu_seqlens,
+                                   void *o, float *S_T, int B, int T, int H_k, int H, int d_k, int d_v,
+                                   int N, efla_dtype in_dtype, efla_dtype o_dtype, efla_update update,
+                                   efla_stream_t stream);
+
+/* The training forward (rows of [B, T], o in in_dtype): also keeps in `workspace` what
+ * efla_gated_bwd_chunked(saved = 1) needs.  workspace: 16-byte aligned, at least
+ * efla_gated_bwd_workspace bytes, overlapping no argument. */
+efla_status efla_gated_fwd_chunked_train(const void *q, const void *k, const void *v, const float *g,
+                                         const float *beta, const float *S0, void *o, float *S_T, int B,
+                                         int T, int H_k, int H, int d_k, int d_v, efla_dtype in_dtype,
+                                         efla_update update, void *workspace, size_t workspace_bytes,
+                                         efla_stream_t stream);
+
+efla_status efla_gated_bwd_workspace(int B, int T, int H_k, int H, int d_k, int d_v,
+                                     efla_dtype in_dtype, size_t *bytes);
+
+/* Gradients of the forward over rows of [B, T].  dO [B, T, H, d_v] in_dtype; dS_T [B, H, d_k, d_v]
+ * fp32 or NULL (zero).  dq, dk [B, T, H_k, d_k] (summed over the value heads of each key head) and
+ * dv [B, T, H, d_v] in in_dtype; dg, dbeta [B, T, H] fp32; dS0 fp32 or NULL (not written).
+ * saved != 0: `workspace` was filled by efla_gated_fwd_chunked_train for the same inputs (the
+ * caller's contract) and the forward is not run again; such a workspace serves one backward.
+ * Results do not depend on the order in which CTAs finish. */
+efla_status efla_gated_bwd_chunked(const void *q, const void *k, const void *v, const float *g,
+                                   const float *beta, const float *S0, const void *dO, const float *dS_T,
+                                   void *dq, void *dk, void *dv, float *dg, float *dbeta, float *dS0,
+                                   int B, int T, int H_k, int H, int d_k, int d_v, efla_dtype in_dtype,
+                                   efla_update update, int saved, void *workspace,
+                                   size_t workspace_bytes, efla_stream_t stream);
+
+/* One token per sequence, S [B, H, d_k, d_v] updated in place: q, k [B, H_k, d_k], v [B, H, d_v],
+ * g, beta [B, H], o [B, H, d_v]. */
+efla_status efla_gated_decode_step(const void *q, const void *k, const void *v, const float *g,
+                                   const float *beta, float *S, void *o, int B, int H_k, int H, int d_k,
+                                   int d_v, efla_dtype in_dtype, efla_dtype o_dtype, efla_update update,
+                                   efla_stream_t stream);
+
+/* m tokens per sequence, S updated in place, read and written once: q, k [B, m, H_k, d_k],
+ * v [B, m, H, d_v], g, beta [B, m, H], o [B, m, H, d_v].  Equal to m steps. */
+efla_status efla_gated_decode_tokens(const void *q, const void *k, const void *v, const float *g,
+                                     const float *beta, float *S, void *o, int B, int m, int H_k, int H,
+                                     int d_k, int d_v, efla_dtype in_dtype, efla_dtype o_dtype,
+                                     efla_update update, efla_stream_t stream);
+
+/*
+ * efla_gated_prep -- the norms and gates before a gated mixer, for `tokens` tokens.
+ *
+ *   q_out = scale q / sqrt(||q||^2 + eps),  k_out = k / sqrt(||k||^2 + eps)   (per head)
+ *   g = -e^{A_log} softplus(a + dt_bias),  beta = sigmoid(b)
+ *
+ *   q, k, q_out, k_out [tokens, H_k, d_k] dtype;  a, b [tokens, H] dtype
+ *   A_log, dt_bias [H] fp32;  g, beta [tokens, H] fp32
+ * An output may be its own input (q_out == q, k_out == k).  H and H_k are independent here.
+ */
+efla_status efla_gated_prep(const void *q, const void *k, const void *a, const void *b,
+                            const float *A_log, const float *dt_bias, void *q_out, void *k_out, float *g,
+                            float *beta, long long tokens, int H_k, int H, int d_k, efla_dtype dtype,
+                            float scale, float eps, efla_stream_t stream);
+
+/* Its gradients: from those of its outputs (dq_out, dk_out dtype; dg, dbeta fp32) to dq, dk, da, db
+ * in dtype and dA_log, ddt_bias [H] fp32 (sums over the tokens).  workspace: at least
+ * efla_gated_prep_bwd_workspace bytes, overlapping no argument. */
+efla_status efla_gated_prep_bwd(const void *q, const void *k, const void *a, const void *b,
+                                const float *A_log, const float *dt_bias, const void *dq_out,
+                                const void *dk_out, const float *dg, const float *dbeta, void *dq, void *dk,
+                                void *da, void *db, float *dA_log, float *ddt_bias, long long tokens,
+                                int H_k, int H, int d_k, efla_dtype dtype, float scale, float eps,
+                                void *workspace, size_t workspace_bytes, efla_stream_t stream);
+efla_status efla_gated_prep_bwd_workspace(long long tokens, int H, size_t *bytes);
+
+/*
+ * efla_norm_gate -- the norm after a mixer fused with its output gate, for `rows` rows of d:
+ *   y = o / sqrt(mean(o^2) + eps) * w * silu(z)
+ *   o, z, y [rows, d] dtype;  w [d] fp32;  d in {32, 64, 128}.  y == o or y == z is allowed.
+ */
+efla_status efla_norm_gate(const void *o, const void *z, const float *w, void *y, long long rows, int d,
+                           efla_dtype dtype, float eps, efla_stream_t stream);
+
+/* Its gradients: d_o, d_z [rows, d] dtype and d_w [d] fp32 (the sum over the rows).  workspace: at
+ * least efla_norm_gate_bwd_workspace bytes, overlapping no argument. */
+efla_status efla_norm_gate_bwd(const void *o, const void *z, const float *w, const void *dy, void *d_o,
+                               void *d_z, float *d_w, long long rows, int d, efla_dtype dtype, float eps,
+                               void *workspace, size_t workspace_bytes, efla_stream_t stream);
+efla_status efla_norm_gate_bwd_workspace(int d, size_t *bytes);
 
 /* Reads the calling thread's current device's status word on `stream`
  * (synchronising that stream), resets it to EFLA_OK and returns what it held:

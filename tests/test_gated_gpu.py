@@ -1,0 +1,473 @@
+"""Gated delta rule and the norms around it on the GPU against the 64-bit oracle (oracle/gated.py).
+
+Tolerances, relative to the 2-norm and to the largest value of an output:
+  fp32 on CUDA cores   an output is a chain of sums of d_k, 64, d_k and 64 products (K S, T'' R, Q S,
+                       P U), each rounding by at most 2^-24 a term; a gradient is twice as long.  What
+                       comes from earlier chunks is contracted by the decay and by I - alpha k k^T.
+  tensor cores         operands that are not exact bf16 are two rounded bf16 parts: 2^-18 off at most,
+                       and the product of two low parts, left out, is 2^-18 at most; 8 such in the
+                       chain of an output, 16 in a gradient's.
+  bf16 outputs         half a step more: 2^-8 of the value.
+"""
+import math
+
+import pytest
+import torch
+
+import exact_delta_rule_gb300 as efla
+from oracle import gated
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def tol(dtype, dk, dv, grad=False):
+    links = 2 if grad else 1
+    t = links * 2 * (dk + 64) * 2.0 ** -24
+    if dtype == BF16 and dk == dv == 128:
+        t += links * 8 * 2.0 ** -18
+    return t
+
+
+def close(got, ref, t, what=""):
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    step = 2.0 ** -8 if got.dtype == BF16 else 0.0
+    got, ref = got.double(), ref.double().to(got.device)
+    assert bool(torch.isfinite(got).all()), f"{what}: non-finite values"
+    if not ref.numel():
+        return
+    d = (got - ref).abs()
+    worst = float((d - step * ref.abs() - t * ref.abs().max()).max())
+    assert worst <= 0, f"{what}: {float(d.max()):.3e} off, largest value {float(ref.abs().max()):.3e}, tolerance {t:.1e}"
+    norm = float(ref.norm())
+    assert float(d.norm()) <= (t + step) * norm, f"{what}: rel {float(d.norm()) / max(norm, 1e-300):.3e}, tolerance {t + step:.1e}"
+
+
+def make(B=2, T=70, Hk=2, H=4, dk=64, dv=64, dtype=F32, S0=True, N=None, seed=0, norm=1.0, rate=None):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    rate = torch.exp(r(H) - 1) if rate is None else rate
+    return {"q": (unit(r(B, T, Hk, dk))).to(dtype), "k": (norm * unit(r(B, T, Hk, dk))).to(dtype), "v": r(B, T, H, dv).to(dtype),
+            "g": -rate * torch.nn.functional.softplus(r(B, T, H)), "beta": torch.sigmoid(r(B, T, H)),
+            "S0": 0.3 * r(B if N is None else N, H, dk, dv) if S0 else None}
+
+
+def check_fwd(x, update="euler", **kw):
+    o, S = efla.gated_fwd_chunked(**x, update=update, **kw)
+    ref_o, ref_S = gated.fwd(**x, update=update)
+    t = tol(x["q"].dtype, x["q"].shape[-1], x["v"].shape[-1])
+    close(o, ref_o, t, "o")
+    close(S, ref_S, t, "S_T")
+    assert efla.device_status() == 0
+    return o, S
+
+
+SHAPES = [(F32, 32, 32), (F32, 64, 128), (F32, 128, 128), (BF16, 64, 64), (BF16, 128, 64), (BF16, 128, 128)]
+
+
+@pytest.mark.parametrize("T", [0, 1, 2, 15, 63, 64, 65, 127, 128, 130, 321])
+@pytest.mark.parametrize("dtype, dk, dv", SHAPES)
+def test_forward_lengths(dtype, dk, dv, T):
+    check_fwd(make(T=T, dk=dk, dv=dv, dtype=dtype, seed=T))
+
+
+@pytest.mark.parametrize("Hk, H", [(1, 1), (1, 5), (3, 3), (2, 6)])
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 32, 64), (BF16, 128, 128)])
+@pytest.mark.parametrize("update", ["euler", "exact"])
+def test_forward_heads_and_rules(dtype, dk, dv, Hk, H, update):
+    check_fwd(make(B=3, T=200, Hk=Hk, H=H, dk=dk, dv=dv, dtype=dtype, S0=False, norm=1.3 if update == "exact" else 1.0), update)
+
+
+@pytest.mark.parametrize("dtype, d", [(F32, 64), (BF16, 128)])
+def test_forward_options(dtype, d):
+    x = make(T=150, dk=d, dv=d, dtype=dtype)
+    o, S = check_fwd(x)
+    for od in (BF16, F32):
+        o2, _ = efla.gated_fwd_chunked(**x, o_dtype=od)
+        close(o2, gated.fwd(**x)[0], tol(dtype, d, d), f"o as {od}")
+    o2, none = efla.gated_fwd_chunked(**x, return_state=False)
+    assert none is None and torch.equal(o, o2)
+    inplace = {**x, "S0": x["S0"].clone()}  # S0 and S_T the same memory
+    o2, S2 = efla.gated_fwd_chunked(**inplace, S_T=inplace["S0"])
+    assert torch.equal(o2, o) and torch.equal(S2, S) and S2.data_ptr() == inplace["S0"].data_ptr()
+    o3, S3, _ = efla.gated_fwd_chunked_train(**x)  # the training forward gives the same bits
+    assert torch.equal(o3, o) and torch.equal(S3, S)
+
+
+@pytest.mark.parametrize("dtype, d", [(F32, 64), (BF16, 128)])
+def test_forward_is_causal_and_splits(dtype, d):
+    """A prefix does not see what follows it, and a state handed over continues the sequence."""
+    x = make(T=200, dk=d, dv=d, dtype=dtype)
+    o, S = efla.gated_fwd_chunked(**x)
+    for cut in (1, 64, 101):
+        head = {n: t if n == "S0" else t[:, :cut].contiguous() for n, t in x.items()}
+        o1, S1 = efla.gated_fwd_chunked(**head)
+        tail = {n: S1 if n == "S0" else t[:, cut:].contiguous() for n, t in x.items()}
+        o2, S2 = efla.gated_fwd_chunked(**tail)
+        t = 2 * tol(dtype, d, d)
+        close(torch.cat([o1, o2], 1).float(), o.double(), t + (2 ** -7 if dtype == BF16 else 0), "o")
+        close(S2, S.double(), t, "S_T")
+
+
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 32, 64), (BF16, 128, 128)])
+def test_forward_packed(dtype, dk, dv):
+    lens = [5, 0, 64, 1, 130, 0, 63, 200, 65]
+    x = make(B=1, T=sum(lens), N=len(lens), dk=dk, dv=dv, dtype=dtype)
+    cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+    o, S = efla.gated_fwd_chunked(**x, cu_seqlens=cu)
+    t = tol(dtype, dk, dv)
+    for i, n in enumerate(lens):
+        a = int(cu[i])
+        part = {m: y[i:i + 1] if m == "S0" else y[:, a:a + n] for m, y in x.items()}
+        ro, rS = gated.fwd(**part)
+        close(o[:, a:a + n], ro, t, f"o of sequence {i}")
+        close(S[i:i + 1], rS, t, f"S_T of sequence {i}")
+    assert efla.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype, d", [(F32, 32), (BF16, 128)])
+def test_forward_packed_bad_bounds_are_flagged(dtype, d):
+    """A sequence with bounds outside the tokens is not touched; the others are computed."""
+    x = make(B=1, T=100, N=3, dk=d, dv=d, dtype=dtype)
+    for bounds in ([0, 40, 200, 100], [0, 60, 30, 100], [-5, 10, 40, 100]):
+        cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+        S_T = torch.full((3, 4, d, d), 7.0, device="cuda")
+        o = torch.full((1, 100, 4, d), 7.0, device="cuda", dtype=dtype)
+        efla.gated_fwd_chunked(**x, cu_seqlens=cu, o=o, S_T=S_T)
+        assert efla.device_status() == 1
+        for n in range(3):
+            a, b = bounds[n], bounds[n + 1]
+            if a < 0 or b < a or b > 100:
+                assert bool((S_T[n] == 7).all())
+        assert efla.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 64, 64), (F32, 32, 128), (BF16, 128, 128)])
+@pytest.mark.parametrize("what", ["none", "resets", "strong", "weak", "zero keys", "zero beta", "one beta", "same key"])
+def test_forward_extremes(dtype, dk, dv, what):
+    x = make(B=1, T=190, dk=dk, dv=dv, dtype=dtype, seed=3)
+    g, beta, k = x["g"], x["beta"], x["k"]
+    if what == "none":
+        g.zero_()
+    elif what == "resets":  # documents that begin inside the sequence, one at a chunk's first token, a run of them
+        g[:, [0, 10, 64, 65, 66, 150]] = -math.inf
+        g[:, 100] = -1e30
+    elif what == "strong":
+        g.mul_(0).sub_(20.0)
+    elif what == "weak":
+        g.mul_(1e-4)
+    elif what == "zero keys":
+        k[:, ::3] = 0
+    elif what == "zero beta":
+        beta[:, ::2] = 0
+    elif what == "one beta":
+        beta.fill_(1.0)
+    else:
+        k[:] = k[:, :1]
+    check_fwd(x)
+    check_fwd(x, "exact")
+
+
+def test_forward_reset_equals_a_new_sequence():
+    x = make(B=1, T=150, dk=128, dv=128, dtype=BF16, S0=False)
+    x["g"][:, 70] = -math.inf
+    o, S = efla.gated_fwd_chunked(**x)
+    tail = {n: None if t is None else t[:, 70:].contiguous() for n, t in x.items()}
+    o2, S2 = efla.gated_fwd_chunked(**tail)
+    close(S, S2.double(), 2 * tol(BF16, 128, 128), "S_T")
+    close(o[:, 70:].float(), o2.double(), 2 * tol(BF16, 128, 128) + 2 ** -7, "o")
+
+
+@pytest.mark.parametrize("dtype, d", [(F32, 64), (BF16, 128)])
+def test_calls_write_only_their_outputs(dtype, d):
+    """Outputs inside larger buffers: nothing before or behind them changes, and a repeat gives the same bits."""
+    x = make(B=2, T=90, dk=d, dv=d, dtype=dtype)
+    n_o, n_s = 2 * 90 * 4 * d, 2 * 4 * d * d
+    bo, bs = torch.full((n_o + 512,), 3.0, dtype=dtype, device="cuda"), torch.full((n_s + 512,), 3.0, device="cuda")
+    o, S = efla.gated_fwd_chunked(**x, o=bo[256:256 + n_o].view(2, 90, 4, d), S_T=bs[256:256 + n_s].view(2, 4, d, d))
+    for b, n in ((bo, n_o), (bs, n_s)):
+        assert bool((b[:256] == 3).all()) and bool((b[256 + n:] == 3).all())
+    o2, S2 = efla.gated_fwd_chunked(**x)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
+# ------------------------------------------------------------------------------ backward
+def check_bwd(x, update="euler", dS=True, saved=True, seed=5):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dO = torch.randn(x["v"].shape, generator=gen, device="cuda").to(x["q"].dtype)
+    B, _, H, dv = x["v"].shape
+    dk = x["q"].shape[-1]
+    dS_T = torch.randn((B, H, dk, dv), generator=gen, device="cuda") if dS else None
+    ws = efla.gated_fwd_chunked_train(**x, update=update)[2] if saved else None
+    got = efla.gated_bwd_chunked(*x.values(), dO, dS_T, workspace=ws, saved=saved, update=update)
+    ref = gated.bwd(*x.values(), dO, dS_T, update)
+    assert efla.device_status() == 0
+    for n, r in ref.items():
+        close(got[n], r, tol(x["q"].dtype, dk, dv, True), n)
+    return got
+
+
+@pytest.mark.parametrize("T", [0, 1, 2, 63, 64, 65, 129, 200])
+@pytest.mark.parametrize("dtype, dk, dv", SHAPES)
+def test_backward_lengths(dtype, dk, dv, T):
+    check_bwd(make(T=T, dk=dk, dv=dv, dtype=dtype, seed=T))
+
+
+@pytest.mark.parametrize("Hk, H", [(1, 1), (1, 5), (3, 3), (2, 6)])
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 32, 64), (BF16, 128, 128)])
+@pytest.mark.parametrize("update", ["euler", "exact"])
+def test_backward_heads_and_rules(dtype, dk, dv, Hk, H, update):
+    x = make(B=2, T=140, Hk=Hk, H=H, dk=dk, dv=dv, dtype=dtype, S0=False, norm=1.3 if update == "exact" else 1.0)
+    check_bwd(x, update, dS=False, saved=False)
+
+
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 64, 64), (BF16, 128, 128)])
+@pytest.mark.parametrize("what", ["none", "strong", "weak", "zero keys", "zero beta", "one beta", "resets"])
+def test_backward_extremes(dtype, dk, dv, what):
+    x = make(B=1, T=190, dk=dk, dv=dv, dtype=dtype, seed=3)
+    if what == "none":
+        x["g"].zero_()
+    elif what == "strong":
+        x["g"].mul_(0).sub_(20.0)
+    elif what == "weak":
+        x["g"].mul_(1e-4)
+    elif what == "zero keys":
+        x["k"][:, ::3] = 0
+    elif what == "zero beta":
+        x["beta"][:, ::2] = 0
+    elif what == "one beta":
+        x["beta"].fill_(1.0)
+    else:
+        x["g"][:, [0, 10, 64, 150]] = -1000.0
+    check_bwd(x)
+    if what in ("none", "zero keys"):
+        check_bwd(x, "exact")
+
+
+@pytest.mark.parametrize("dtype, d", [(F32, 64), (BF16, 128)])
+def test_backward_repeats_bit_for_bit(dtype, d):
+    x = make(T=150, dk=d, dv=d, dtype=dtype)
+    a, b, c = check_bwd(x), check_bwd(x), check_bwd(x, saved=False)
+    for n in a:
+        assert torch.equal(a[n], b[n]) and torch.equal(a[n], c[n]), n
+
+
+def test_backward_without_dS0():
+    x = make(T=70)
+    dO = torch.ones_like(x["v"])
+    got = efla.gated_bwd_chunked(*x.values(), dO, need_dS0=False)
+    want = efla.gated_bwd_chunked(*x.values(), dO)
+    assert got["dS0"] is None and all(torch.equal(got[n], want[n]) for n in got if n != "dS0")
+
+
+# ------------------------------------------------------------------------------ decode
+@pytest.mark.parametrize("B", [1, 3, 40])
+@pytest.mark.parametrize("m", [0, 1, 2, 15, 16, 17, 40])
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 32, 64), (F32, 128, 128), (BF16, 64, 32), (BF16, 128, 128)])
+def test_decode_tokens(dtype, dk, dv, m, B):
+    x = make(B=B, T=m, dk=dk, dv=dv, dtype=dtype, seed=m)
+    S = x.pop("S0")
+    ref_o, ref_S = gated.fwd(**x, S0=S)
+    S1 = S.clone()
+    o = efla.gated_decode_tokens(**x, S=S1)
+    close(o, ref_o, tol(dtype, dk, dv), "o")
+    close(S1, ref_S, tol(dtype, dk, dv), "S")
+    if 0 < m <= 17:  # the same by single steps
+        S2, outs = S.clone(), []
+        for t in range(m):
+            outs.append(efla.gated_decode_step(**{n: y[:, t].contiguous() for n, y in x.items()}, S=S2))
+        close(torch.stack(outs, 1), ref_o, tol(dtype, dk, dv), "o by steps")
+        close(S2, ref_S, tol(dtype, dk, dv), "S by steps")
+    assert efla.device_status() == 0
+
+
+@pytest.mark.parametrize("B, Hk, H", [(1, 1, 1), (400, 1, 1), (160, 1, 2), (2, 3, 9)])
+@pytest.mark.parametrize("dk", [32, 64, 128])
+@pytest.mark.parametrize("dv", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_decode_step_shapes(dtype, dk, dv, B, Hk, H):
+    x = make(B=B, T=1, Hk=Hk, H=H, dk=dk, dv=dv, dtype=dtype)
+    S = x.pop("S0")
+    for update in ("euler", "exact"):
+        ref_o, ref_S = gated.fwd(**x, S0=S, update=update)
+        S1 = S.clone()
+        o = efla.gated_decode_step(**{n: y[:, 0].contiguous() for n, y in x.items()}, S=S1, update=update, o_dtype=F32)
+        close(o, ref_o[:, 0], tol(F32, dk, dv), "o")
+        close(S1, ref_S, tol(F32, dk, dv), "S")
+
+
+@pytest.mark.parametrize("dtype, d", [(F32, 64), (BF16, 128)])
+def test_decode_resets(dtype, d):
+    x = make(B=2, T=20, dk=d, dv=d, dtype=dtype)
+    x["g"][:, [0, 7]] = -math.inf
+    S = x.pop("S0")
+    ref_o, ref_S = gated.fwd(**x, S0=S)
+    o = efla.gated_decode_tokens(**x, S=S)
+    close(o, ref_o, tol(dtype, d, d), "o")
+    close(S, ref_S, tol(dtype, d, d), "S")
+
+
+# ------------------------------------------------------------------------------ norms
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lead, Hk, H, dk", [((1, 1), 1, 1, 32), ((2, 3), 2, 4, 64), ((1, 517), 3, 7, 128), ((4,), 16, 33, 128),
+                                             ((0,), 2, 2, 64), ((3, 300), 1, 70, 32)])
+def test_prep(dtype, lead, Hk, H, dk):
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    q, k = r(*lead, Hk, dk).to(dtype), (3 * r(*lead, Hk, dk)).to(dtype)
+    a, b = (4 * r(*lead, H)).to(dtype), (4 * r(*lead, H)).to(dtype)
+    if q.numel():
+        q[..., 0, :] = 0  # a zero row: 0 / sqrt(eps)
+        a.view(-1)[0], b.view(-1)[0] = 60.0, -60.0  # saturated gates
+    A, d = r(H), r(H)
+    # sums of dk squares, then a handful of roundings; exp, log and the square root are within 2 steps
+    t = (dk + 16) * 2.0 ** -24
+    got, ref = efla.gated_prep(q, k, a, b, A, d, scale=0.25), gated.prep(q, k, a, b, A, d, 0.25)
+    for n in ref:
+        close(got[n], ref[n], t, n)
+    dys = [r(*x.shape).to(x.dtype) for x in got.values()]
+    got, ref = efla.gated_prep_bwd(q, k, a, b, A, d, *dys, scale=0.25), gated.prep_bwd(q, k, a, b, A, d, *dys, 0.25)
+    tokens = math.prod(lead)
+    for n in ref:  # a token's sum is rounded once a term: 2^-24 of the terms' sizes, whose sum may be small
+        close(got[n], ref[n], (2 * t + max(tokens, 1) ** 0.5 * 2.0 ** -22) if n in ("dA_log", "ddt_bias") else 2 * t, n)
+    again = efla.gated_prep_bwd(q, k, a, b, A, d, *dys, scale=0.25)
+    assert all(torch.equal(got[n], again[n]) for n in got)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(1, 32), (3, 64), (7, 5, 128), (2, 1111, 3, 64), (0, 128), (130, 32), (40000, 128)])
+def test_norm_gate(dtype, shape):
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    o, z, w = (2 * r(*shape)).to(dtype), (3 * r(*shape)).to(dtype), r(shape[-1])
+    if o.numel():
+        o.view(-1, shape[-1])[0] = 0
+        z.view(-1)[0], z.view(-1)[-1] = 80.0, -80.0
+    t = (shape[-1] + 16) * 2.0 ** -24
+    y = efla.norm_gate(o, z, w)
+    close(y, gated.norm_gate(o, z, w), t, "y")
+    for alias in (o, z):  # in place
+        c = alias.clone()
+        args = (c, z, w) if alias is o else (o, c, w)
+        assert torch.equal(efla.norm_gate(*args, y=c), y)
+    dy = r(*shape).to(dtype)
+    got, ref = efla.norm_gate_bwd(o, z, w, dy), gated.norm_gate_bwd(o, z, w, dy)
+    rows = max(1, math.prod(shape[:-1]))
+    if rows > 0 and o.numel():  # a zero row has a gradient of size 1 / sqrt(eps): compared by itself
+        close(got["do"].view(-1, shape[-1])[:1], ref["do"].view(-1, shape[-1])[:1], 2 * t, "do of the zero row")
+        close(got["do"].view(-1, shape[-1])[1:], ref["do"].view(-1, shape[-1])[1:], 2 * t, "do")
+    close(got["dz"], ref["dz"], 2 * t, "dz")
+    close(got["dw"], ref["dw"], 2 * t + rows ** 0.5 * 2.0 ** -22, "dw")
+    again = efla.norm_gate_bwd(o, z, w, dy)
+    assert all(torch.equal(got[n], again[n]) for n in got)
+
+
+# ------------------------------------------------------------------------------ together
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 64, 32), (BF16, 128, 128)])
+def test_a_mixer_trains_and_decodes(dtype, dk, dv):
+    """Norms and gates, the rule, the gated output norm: gradients of the run against the oracle's
+    (from the same rounded values between the operators), and the same tokens one by one."""
+    B, T, Hk, H = 2, 100, 2, 4
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    q, k, v, z = (r(B, T, n, d).to(dtype) for n, d in ((Hk, dk), (Hk, dk), (H, dv), (H, dv)))
+    a, b, A, bias, w = r(B, T, H).to(dtype), r(B, T, H).to(dtype), r(H), r(H) - 2, 1 + 0.1 * r(dv)
+    p = efla.gated_prep(q, k, a, b, A, bias, scale=dk ** -0.5)
+    o, S, ws = efla.gated_fwd_chunked_train(p["q"], p["k"], v, p["g"], p["beta"])
+    y = efla.norm_gate(o, z, w)
+    dy = r(B, T, H, dv).to(dtype)
+    dn = efla.norm_gate_bwd(o, z, w, dy)
+    dm = efla.gated_bwd_chunked(p["q"], p["k"], v, p["g"], p["beta"], None, dn["do"], workspace=ws, saved=True)
+    dp = efla.gated_prep_bwd(q, k, a, b, A, bias, dm["dq"], dm["dk"], dm["dg"], dm["dbeta"], scale=dk ** -0.5)
+    t = tol(dtype, dk, dv, True) + (dk + 16) * 2.0 ** -23
+    ro, rS = gated.fwd(p["q"], p["k"], v, p["g"], p["beta"])
+    close(S, rS, t, "S")
+    close(y, gated.norm_gate(o, z, w), t, "y")
+    rn = gated.norm_gate_bwd(o, z, w, dy)
+    rm = gated.bwd(p["q"], p["k"], v, p["g"], p["beta"], None, dn["do"])
+    rp = gated.prep_bwd(q, k, a, b, A, bias, dm["dq"], dm["dk"], dm["dg"], dm["dbeta"], dk ** -0.5)
+    for got, ref in ((dn, rn), (dm, rm), (dp, rp)):
+        for n in ref:
+            close(got[n], ref[n], t + (T * B) ** 0.5 * 2.0 ** -22, n)
+    S1 = torch.zeros_like(S)
+    for i in range(T):
+        x = efla.gated_prep(q[:, i].contiguous(), k[:, i].contiguous(), a[:, i].contiguous(), b[:, i].contiguous(), A, bias,
+                            scale=dk ** -0.5)
+        assert torch.equal(x["q"], p["q"][:, i]) and torch.equal(x["g"], p["g"][:, i])
+        o1 = efla.gated_decode_step(x["q"], x["k"], v[:, i].contiguous(), x["g"], x["beta"], S1)
+        close(o1, ro[:, i], t, f"o of token {i}")
+    close(S1, rS, t, "S by steps")
+
+
+def test_captured_calls_replay():
+    """Every call captured into one graph and replayed on new inputs gives the eager results."""
+    def run(x, S, dO):
+        p = efla.gated_prep(x["q"], x["k"], x["a"], x["b"], x["A"], x["bias"], scale=0.5)
+        o, S_T, ws = efla.gated_fwd_chunked_train(p["q"], p["k"], x["v"], p["g"], p["beta"])
+        d = efla.gated_bwd_chunked(p["q"], p["k"], x["v"], p["g"], p["beta"], None, dO, workspace=ws, saved=True)
+        e = efla.gated_prep_bwd(x["q"], x["k"], x["a"], x["b"], x["A"], x["bias"], d["dq"], d["dk"], d["dg"], d["dbeta"])
+        y = efla.norm_gate(o, dO, x["w"])
+        n = efla.norm_gate_bwd(o, dO, x["w"], y)
+        t = efla.gated_decode_tokens(p["q"], p["k"], x["v"], p["g"], p["beta"], S)
+        return [o, S_T, y, t, *d.values(), *e.values(), *n.values()]
+
+    def fresh(seed):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+        x = {"q": r(2, 80, 2, 128).bfloat16(), "k": r(2, 80, 2, 128).bfloat16(), "v": r(2, 80, 4, 128).bfloat16(),
+             "a": r(2, 80, 4).bfloat16(), "b": r(2, 80, 4).bfloat16(), "A": r(4), "bias": r(4), "w": r(128)}
+        return x, r(2, 4, 128, 128), r(2, 80, 4, 128).bfloat16()
+
+    x, S, dO = fresh(0)
+    S_graph = S.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(x, S.clone(), dO)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(x, S_graph, dO)
+    for seed in (1, 2):
+        x2, S2, dO2 = fresh(seed)
+        for n in x:
+            x[n].copy_(x2[n])
+        S_graph.copy_(S2)
+        dO.copy_(dO2)
+        graph.replay()
+        for got, want in zip(out + [S_graph], run(x2, S2, dO2) + [S2]):
+            assert torch.equal(got, want)
+
+
+def test_streams():
+    """A call on another stream than the current one, its outputs and workspace allocated here."""
+    x = make(T=300, dk=128, dv=128, dtype=BF16)
+    dO = torch.ones_like(x["v"])
+    want_o, want_S = efla.gated_fwd_chunked(**x)
+    want = efla.gated_bwd_chunked(*x.values(), dO)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    o, S = efla.gated_fwd_chunked(**x, stream=side)
+    got = efla.gated_bwd_chunked(*x.values(), dO, stream=side)
+    junk = [torch.full((1 << 20,), 9.0, device="cuda") for _ in range(8)]  # reuses whatever was freed too early
+    side.synchronize()
+    assert torch.equal(o, want_o) and torch.equal(S, want_S)
+    assert all(torch.equal(got[n], want[n]) for n in got), len(junk)
+
+
+@pytest.mark.parametrize("dtype, d", [(F32, 64), (BF16, 128)])
+def test_long_sequence(dtype, d):
+    """4096 tokens, weak and strong decays side by side: errors do not pile up."""
+    rate = torch.tensor([1e-3, 2.0], device="cuda")
+    x = make(B=1, T=4096, Hk=1, H=2, dk=d, dv=d, dtype=dtype, rate=rate)
+    check_fwd(x)
+    check_bwd(x)
+
+
+def test_many_heads():
+    """More (sequence, head) units than one wave of CTAs."""
+    x = make(B=40, T=66, Hk=4, H=8, dk=128, dv=128, dtype=BF16)
+    check_fwd(x)
+    check_bwd(x)
