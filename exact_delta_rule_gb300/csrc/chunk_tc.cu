@@ -50,11 +50,21 @@
 //     T'' and P for the NEXT chunk while the state warpgroup works on the current one.
 // Every wait is bounded; on expiry the CTA records EFLA_ERR_DEVICE_TIMEOUT and
 // leaves.
+//
+// Gated instantiation (the gated delta rule; formulas in gated.cuh).  The decays enter as row and
+// column factors of the same products:
+//   A~ and P take Gamma_ts = e^{G_t - G_s} in the prep; X takes e^{G_t} where it is split;
+//   O1 = Q S, in TMEM, is multiplied by e^{G_t} and S by e^{G_C} while the tensor core forms X and u
+//   (the state warpgroup waits there anyway); u is split twice, c_t u_t for S += K^T diag(c) u (first:
+//   the chain) and u_t for O += P u (while the state is updated).
+// Operands are split with rounding to nearest, so that S_T is good to about 2^-18 (its truncated
+// split leaves 2^-15); key heads are shared by H / Hk value heads.
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
-#include "internal.cuh"
+#include "gated.cuh"
 #include "ptx.cuh"
 #include "tc_common.cuh"
 #include "tri_inverse.cuh"
@@ -81,12 +91,20 @@ constexpr uint32_t OFF_AT = OFF_TPP + 2 * TPP_BYTES;  // fp32 [64][68]: A~, then
 constexpr uint32_t AT_LD = 68;
 constexpr uint32_t OFF_ROW = OFF_AT + 64 * AT_LD * 4;  // fp32: invn[64], gn[64]
 constexpr uint32_t ROW_BYTES = 2 * 64 * 4;
-constexpr uint32_t OFF_BAR = OFF_ROW + ROW_BYTES;       // mbarriers (struct Bars)
-constexpr uint32_t OFF_MISC = OFF_BAR + 224;            // tmem base (u32), abort flag (i32), sequence slot (i32)
-constexpr uint32_t SMEM_USED = OFF_MISC + 16;
-constexpr uint32_t SMEM_ALLOC = SMEM_USED + 1024;       // + alignment slack for the 1024-byte base
+constexpr uint32_t OFF_BAR_N = OFF_ROW + ROW_BYTES;       // mbarriers (struct Bars)
+constexpr uint32_t OFF_MISC_N = OFF_BAR_N + 224;            // tmem base (u32), abort flag (i32), sequence slot (i32)
+constexpr uint32_t SMEM_USED = OFF_MISC_N + 16;
+constexpr uint32_t SMEM_ALLOC_N = SMEM_USED + 1024;       // + alignment slack for the 1024-byte base
 static_assert(OFF_TPP % 1024 == 0 && OFF_AT % 1024 == 0, "operand buffers must be 1024-byte aligned");
-static_assert(SMEM_ALLOC <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
+static_assert(SMEM_ALLOC_N <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
+// Gated: the hi and lo of G_t lie in the padding of At's rows (columns 64 and 65), e^{G_t} and c_t of
+// both chunk parities behind the barriers.  This leaves no room for alignment slack: the array itself
+// is declared 1024-byte aligned, and the kernel refuses to run on another base.
+constexpr uint32_t OFF_BAR_G = OFF_ROW + ROW_BYTES;
+constexpr uint32_t OFF_MISC_G = OFF_BAR_G + 256;
+constexpr uint32_t OFF_DEC_G = OFF_MISC_G + 16;             // fp32 [2 parities]{e^{G_t} [64], c_t [64]}
+constexpr uint32_t SMEM_ALLOC_G = OFF_DEC_G + 2 * 2 * 64 * 4;
+static_assert(SMEM_ALLOC_G <= 232448 && OFF_DEC_G % 16 == 0, "gated shared memory");
 
 // TMEM columns (32-bit; lane = row of the MMA result)
 // A tcgen05.mma of M = 128 occupies the tensor pipe for about the same time at
@@ -134,6 +152,8 @@ struct TcParams {
     uint8_t *tpp;                // with states: every chunk's T'' tile as formed below (16 KB a chunk) or nullptr
     unsigned long long wait_ns;  // bound on every wait between roles (2 s unless a test lowers it)
     int debug_stall;             // test hook: the MMA thread first waits on a barrier nothing completes
+    const float *g;              // gated: [B, T, H] log decays
+    int rep;                     // gated: value heads a key head
 };
 
 struct Bars {
@@ -157,6 +177,12 @@ struct Bars {
     uint64_t never;           // never completed (the debug_stall test hook waits on it)
 };
 static_assert(sizeof(Bars) <= 224, "mbarrier block exceeds its slot");
+struct GatedBars : Bars {
+    uint64_t gate_ready[2];   // a chunk's decays written
+    uint64_t o1_done;         // O1^T = S^T Q^T of a chunk
+    uint64_t uo_ready;        // state warpgroup wrote u^T hi/lo for the outputs (128 arrivals)
+};
+static_assert(sizeof(GatedBars) <= 256, "mbarrier block exceeds its slot");
 
 // G = [K; Q] K^T of chunk c (M = 128, N = C, K = d_k) into TM_G, completion on g_done.
 __device__ __forceinline__ void issue_gram(uint32_t tmem, uint32_t s_sm, int c, Bars *bars) {
@@ -183,14 +209,24 @@ __device__ __noinline__ void dump_state_rows(uint8_t *tile, uint32_t ts, int g0,
     }
 }
 
-template <bool OUT_BF16>
+template <bool OUT_BF16, bool GATED>
 __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant__ TcParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = GATED ? smem_raw
+                        : reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    using BarsT = std::conditional_t<GATED, GatedBars, Bars>;
+    constexpr uint32_t OFF_BAR = GATED ? OFF_BAR_G : OFF_BAR_N, OFF_MISC = GATED ? OFF_MISC_G : OFF_MISC_N;
+    if constexpr (GATED) {
+        if (smem_u32(sm) & 1023u) {  // (the operand layout needs the base aligned)
+            if (threadIdx.x == 0) atomicExch(p.status, (int)EFLA_ERR_CUDA);
+            return;
+        }
+    }
+    float *dec = reinterpret_cast<float *>(sm + OFF_DEC_G);  // gated only
     float *row_invn = reinterpret_cast<float *>(sm + OFF_ROW);  // [64] 1/n_t
     float *row_gn = row_invn + 64;                              // [64] gamma_t/n_t
     float *At = reinterpret_cast<float *>(sm + OFF_AT);
-    Bars *bars = reinterpret_cast<Bars *>(sm + OFF_BAR);
+    BarsT *bars = reinterpret_cast<BarsT *>(sm + OFF_BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + OFF_MISC + 4);
 
@@ -290,6 +326,12 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
         mbar_init(&bars->r_ready, 128);
         mbar_init(&bars->u_ready, 128);
         mbar_init(&bars->never, 1);
+        if constexpr (GATED) {
+            mbar_init(&bars->gate_ready[0], 1);
+            mbar_init(&bars->gate_ready[1], 1);
+            mbar_init(&bars->o1_done, 1);
+            mbar_init(&bars->uo_ready, 128);
+        }
         fence_mbar_init();
         *abort_flag = 0;
     }
@@ -324,6 +366,16 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                        ? p.beta[((size_t)b * p.T + (size_t)(t0n + row)) * p.H + h] : 0.f;
         };
         float beta_next = load_beta(0);
+        // gated: warp 7 forms the decays; lane l loads the gates of tokens 2 l, 2 l + 1, a chunk ahead
+        auto load_g = [&](int cc, int odd) {
+            const long t = bos + (long)cc * C + 2 * (tid & 31) + odd;
+            return (warp == 7 && cc < nchunks && t < eos) ? p.g[((size_t)b * p.T + (size_t)t) * p.H + h] : 0.f;
+        };
+        float g0_next = 0.f, g1_next = 0.f;
+        if constexpr (GATED) {
+            g0_next = load_g(0, 0);
+            g1_next = load_g(0, 1);
+        }
         for (int c = 0; c < nchunks; ++c) {
             const int st = c % NSTAGE, buf = c & 1;
             const long tok0 = bos + (long)c * C;
@@ -332,6 +384,11 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
 
             const float beta_t = beta_next;
             beta_next = load_beta(c + 1);
+            const float g0_c = g0_next, g1_c = g1_next;
+            if constexpr (GATED) {
+                g0_next = load_g(c + 1, 0);
+                g1_next = load_g(c + 1, 1);
+            }
             bool ok = true;
             // Gram products G = [K;Q] K^T: the MMA thread issues a full chunk's once its stage
             // has landed (the prep reads nothing else of the stage); a partial chunk's tail is
@@ -381,6 +438,9 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                     row_invn[t] = invn;
                     row_gn[t] = gam * invn;
                 }
+                if constexpr (GATED) {
+                    if (warp == 7) chunk_decay(g0_c, g1_c, tid & 31, At + 64, At + 65, AT_LD, dec + buf * 128, dec + buf * 128 + 64);
+                }
                 // [gate: terms computed]
                 if (named_bar_any(BAR_PREP, 256, !ok || *abort_flag)) {  // also spreads an abort
                     *abort_flag = 1;
@@ -388,6 +448,16 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 }
                 // [gate: barrier passed]
                 if (leader) mbar_arrive(&bars->g_free);  // every row of G has been read
+                if constexpr (GATED) {
+                    if (leader) mbar_arrive(&bars->gate_ready[buf]);
+                    // G[t][s] times Gamma_ts (t: this row's token; entries above the diagonal are masked below)
+                    const float2 gt = *reinterpret_cast<const float2 *>(At + (row & (C - 1)) * AT_LD + 64);
+#pragma unroll
+                    for (int s = 0; s < 32; ++s) {
+                        const float2 gs = *reinterpret_cast<const float2 *>(At + (col0 + s) * AT_LD + 64);
+                        g[s] *= pair_decay(gt.x, gt.y, gs.x, gs.y);
+                    }
+                }
                 if (row < C) {  // A~[t][col0 .. col0+31]
                     const int t = row;
                     const float rs = row_gn[t];  // gamma_t / n_t
@@ -422,7 +492,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
 #pragma unroll
                     for (int c8 = 0; c8 < 32; c8 += 8) {
                         uint32_t hh[4], ll[4];
-                        split_pack<4>(g + c8, hh, ll);
+                        split_as<GATED, 4>(g + c8, hh, ll);
                         const uint32_t off = swz_offset(t, col0 + c8, 8192);
                         *reinterpret_cast<uint4 *>(phi + off) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
                         *reinterpret_cast<uint4 *>(plo + off) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
@@ -454,7 +524,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                         x[e + 1] = s0 + c8 + e + 1 <= t ? y.y : 0.f;
                     }
                     uint32_t hh[4], ll[4];
-                    split_pack<4>(x, hh, ll);
+                    split_as<GATED, 4>(x, hh, ll);
                     const uint32_t off = swz_offset(t, s0 + c8, 8192);
                     *reinterpret_cast<uint4 *>(hi + off) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
                     *reinterpret_cast<uint4 *>(lo + off) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
@@ -601,7 +671,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 uint32_t hi[16], lo[16];
                 tmem_ld32(lane_base + TM_S + g * 32, sv);
                 tmem_ld_wait();
-                split_pack<16>(sv, hi, lo);
+                split_as<GATED, 16>(sv, hi, lo);
                 tmem_st16u(lane_base + TM_SA + g * 16, hi);
                 tmem_st16u(lane_base + TM_SA + 64 + g * 16, lo);
             }
@@ -610,7 +680,14 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             mbar_arrive(&bars->sa_ready);
             // with `states`, rows 0-63 of the start state go out while the tensor core forms X and
             // rows 64-127 while it forms u (TM_S changes only at this chunk's state update)
-            if (st_c) dump_state_rows(st_c, lane_base + TM_S, 0, j);
+            const float *eg = dec + (c & 1) * 128, *ec = eg + 64;  // gated: e^{G_t}, c_t
+            if constexpr (GATED) {
+                ok = wait_bar_warp(&bars->gate_ready[c & 1], (c >> 1) & 1, abort_flag, wait_ns);
+                if (!ok) break;
+                decay_state_rows(st_c, lane_base + TM_S, 0, 2, j, eg[C - 1]);
+            } else {
+                if (st_c) dump_state_rows(st_c, lane_base + TM_S, 0, j);
+            }
             if (c >= 2) release_staging(c - 2);  // its stores were issued during chunk c - 1
             const long tok0 = bos + (long)c * C;
             const int valid = (int)min((long)C, eos - tok0);
@@ -625,24 +702,95 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 tmem_ld32(lane_base + TM_X + 32, x1);
                 tmem_ld_wait();
                 uint32_t hi[16], lo[16];
+                if constexpr (GATED) {
+                    float f[32];
+                    load32(eg, f);
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) x0[t] *= f[t];
+                }
 #pragma unroll
                 for (int t = 0; t < 32; ++t) x0[t] = t < valid ? -x0[t] : 0.f;
-                split_pack<16>(x0, hi, lo);
+                split_as<GATED, 16>(x0, hi, lo);
                 tmem_st16u(lane_base + TM_X, hi);
                 tmem_st16u(lane_base + TM_X + 32, lo);
+                if constexpr (GATED) {
+                    float f[32];
+                    load32(eg + 32, f);
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) x1[t] *= f[t];
+                }
 #pragma unroll
                 for (int t = 0; t < 32; ++t) x1[t] = 32 + t < valid ? -x1[t] : 0.f;
-                split_pack<16>(x1, hi, lo);
+                split_as<GATED, 16>(x1, hi, lo);
                 tmem_st16u(lane_base + TM_X + 16, hi);
                 tmem_st16u(lane_base + TM_X + 48, lo);
             }
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&bars->r_ready);
-            if (st_c) dump_state_rows(st_c, lane_base + TM_S, 2, j);
+            if constexpr (GATED) {
+                decay_state_rows(st_c, lane_base + TM_S, 2, 4, j, eg[C - 1]);
+                if (write_o) {  // O1^T times e^{G_t}
+                    ok = wait_bar_warp(&bars->o1_done, c & 1, abort_flag, wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t ob = lane_base + TM_O + (uint32_t)(c & 1) * 64;
+#pragma unroll 1
+                    for (int hf = 0; hf < 2; hf = opaque(hf + 1)) {
+                        float x[32], f[32];
+                        tmem_ld32(ob + hf * 32, x);
+                        load32(eg + hf * 32, f);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int t = 0; t < 32; ++t) x[t] *= f[t];
+                        tmem_st32(ob + hf * 32, x);
+                    }
+                    tmem_st_wait();
+                }
+            } else {
+                if (st_c) dump_state_rows(st_c, lane_base + TM_S, 2, j);
+            }
             ok = wait_bar_warp(&bars->u_done, c & 1, abort_flag, wait_ns);
             if (!ok) break;
             tc_fence_after();
+            if constexpr (GATED) {
+                // c_t u_t -> hi in columns 0-31, lo in columns 64-95 of TM_SA: over the two partial sums, which
+                // this thread has read by then; free again once the state update that reads them is complete.
+                // Then u_t -> TM_X, which the next chunk's X overwrites behind the outputs in the pipe.
+                float u[64];
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float(&ua)[32] = *reinterpret_cast<float(*)[32]>(u + 32 * hf);
+                    float ub[32], f[32];
+                    tmem_ld32(lane_base + TM_SA + hf * 32, ua);
+                    tmem_ld32(lane_base + TM_SA + 64 + hf * 32, ub);
+                    tmem_ld_wait();
+                    load32(ec + hf * 32, f);
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) {
+                        ua[t] += ub[t];
+                        f[t] *= ua[t];
+                    }
+                    split_pack_rn<16>(f, hi, lo);
+                    tmem_st16u(lane_base + TM_SA + hf * 16, hi);
+                    tmem_st16u(lane_base + TM_SA + 64 + hf * 16, lo);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bars->u_ready);
+                if (write_o) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        split_pack_rn<16>(u + 32 * hf, hi, lo);
+                        tmem_st16u(lane_base + TM_X + hf * 16, hi);
+                        tmem_st16u(lane_base + TM_X + 32 + hf * 16, lo);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&bars->uo_ready);
+                }
+            } else {
             // u^T = U1 + U2 -> bf16 hi/lo operand in TMEM
 #pragma unroll 1
             for (int hf = 0; hf < 2; hf = opaque(hf + 1)) {
@@ -660,6 +808,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&bars->u_ready);
+            }
             // the outputs of the previous chunk leave while the tensor core updates the state
             if (c >= 1) {
                 ok = wait_bar_warp(&bars->o_done[(c - 1) & 1], ((c - 1) >> 1) & 1, abort_flag, wait_ns);
@@ -703,8 +852,9 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             const int tok = (int)(bos + (long)c * C);
             mbar_arrive_expect_tx(&bars->tma_full[st], STAGE_BYTES);
             for (int cb = 0; cb < 2; ++cb) {
-                tma_load_4d(dst + cb * 16384, &p.map_k, &bars->tma_full[st], cb * 64, h, tok, (int)b);
-                tma_load_4d(dst + cb * 16384 + 8192, &p.map_q, &bars->tma_full[st], cb * 64, h, tok, (int)b);
+                const int hk = GATED ? h / p.rep : h;
+                tma_load_4d(dst + cb * 16384, &p.map_k, &bars->tma_full[st], cb * 64, hk, tok, (int)b);
+                tma_load_4d(dst + cb * 16384 + 8192, &p.map_q, &bars->tma_full[st], cb * 64, hk, tok, (int)b);
                 tma_load_4d(dst + OFF_V + cb * 8192, &p.map_v, &bars->tma_full[st], cb * 64, h, tok, (int)b);
             }
             issued = c + 1;
@@ -795,6 +945,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                         mma_bf16_ts_e(tmem + ob, tmem + TM_SA + part * 64 + ks * 8, smem_desc(kq_s + off, 16, 1024),
                                       idesc64, (part | ks) != 0);
                     }
+                if constexpr (GATED) mma_commit_e(&bars->o1_done);
             }
             // the rest of the chunk needs its prep (T'', P)
             if (!(ok = wait_bar_warp(&bars->prep_ready[buf], (c >> 1) & 1, abort_flag, wait_ns))) break;
@@ -837,10 +988,16 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16_ts_e(tmem + TM_S, tmem + TM_X + part * 32 + ks * 8,
+                        mma_bf16_ts_e(tmem + TM_S, tmem + (GATED ? TM_SA + part * 64 : TM_X + part * 32) + ks * 8,
                                       smem_desc(kq_s + ks * 2048, 16384, 1024), idesc_s, 1);
                 mma_commit_e(&bars->s_done);
                 mma_commit_e(&bars->s_free[c % NSTAGE]);
+                if constexpr (GATED) {
+                    if (write_o) {
+                        if (!(ok = wait_bar_warp(&bars->uo_ready, c & 1, abort_flag, wait_ns))) break;
+                        tc_fence_after();
+                    }
+                }
                 // O^T += u_hi^T P_hi^T + u_hi^T P_lo^T + u_lo^T P_hi^T (N = 64 each)
                 if (write_o) {
 #pragma unroll
@@ -903,19 +1060,20 @@ bool make_map(CUtensorMap *m, const void *ptr, int B, int T, int H, bool f32, in
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool OUT_BF16>
+template <bool OUT_BF16, bool GATED>
 cudaError_t launch_typed(const TcParams &p, unsigned grid, cudaStream_t stream) {
+    constexpr uint32_t SMEM_ALLOC = GATED ? SMEM_ALLOC_G : SMEM_ALLOC_N;
     static bool attr_done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !attr_done[dev]) {
-        e = cudaFuncSetAttribute(chunk_tc_kernel<OUT_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(chunk_tc_kernel<OUT_BF16, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)SMEM_ALLOC);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_done[dev] = true;
     }
-    chunk_tc_kernel<OUT_BF16><<<grid, 448, SMEM_ALLOC, stream>>>(p);
+    chunk_tc_kernel<OUT_BF16, GATED><<<grid, 448, SMEM_ALLOC, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -957,7 +1115,46 @@ cudaError_t launch_chunk_tc(const FwdArgs &a, const char **why) {
     *why = "tcgen05 chunk kernel launch";
     const long units = a.seg_len > 0 ? (a.maps ? 2L * a.B * (a.G - 1) * a.H : (long)a.B * a.G * a.H) : (long)a.N * a.H;
     const unsigned grid = (unsigned)units;
-    return o_bf16 ? launch_typed<true>(p, grid, a.stream) : launch_typed<false>(p, grid, a.stream);
+    return o_bf16 ? launch_typed<true, false>(p, grid, a.stream) : launch_typed<false, false>(p, grid, a.stream);
+}
+
+cudaError_t launch_gated_chunk_tc(const GatedFwdArgs &a, const char **why) {
+    if (a.N == 0) return cudaSuccess;
+    TcParams p;
+    memset(&p, 0, sizeof p);
+    const bool o_bf16 = a.o_dtype == EFLA_BF16;
+    if ((long long)a.B * a.T > 0) {
+        if (!make_map(&p.map_q, a.q, a.B, a.T, a.Hk, false, 64, true) ||
+            !make_map(&p.map_k, a.k, a.B, a.T, a.Hk, false, 64, true) ||
+            !make_map(&p.map_v, a.v, a.B, a.T, a.H, false, 64, true) ||
+            (a.o && !make_map(&p.map_o, a.o, a.B, a.T, a.H, !o_bf16, 32, false, o_bf16 ? 64 : 32))) {
+            *why = "cuTensorMapEncodeTiled failed";
+            return cudaErrorInvalidValue;
+        }
+    }
+    p.beta = a.beta;
+    p.S0 = a.S0;
+    p.cu_seqlens = a.cu_seqlens;
+    p.o = a.o;
+    p.S_T = a.S_T;
+    p.status = a.status;
+    p.B = a.B;
+    p.T = a.T;
+    p.H = a.H;
+    p.N = a.N;
+    p.euler = a.euler;
+    p.g = a.g;
+    p.rep = a.H / a.Hk;
+    if (a.ws) {
+        const GatedWs w = gated_ws(a.B, a.T, a.Hk, a.H, a.dk, a.dv, a.in_dtype);
+        p.states = reinterpret_cast<float *>(static_cast<char *>(a.ws) + w.states);
+        p.tpp = static_cast<uint8_t *>(a.ws) + w.w;
+    }
+    p.wait_ns = wait_limit_ns();
+    p.debug_stall = (debug_stall() & STALL_CHUNK) ? 1 : 0;
+    *why = "tcgen05 gated chunk kernel launch";
+    const unsigned grid = (unsigned)((long)a.N * a.H);
+    return o_bf16 ? launch_typed<true, true>(p, grid, a.stream) : launch_typed<false, true>(p, grid, a.stream);
 }
 
 }  // namespace efla

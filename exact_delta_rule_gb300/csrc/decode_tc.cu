@@ -36,12 +36,18 @@
 //   state mover (warp 7): per unit, a bulk copy of the new S (64 KB) from the staging buffer to
 //     HBM, then the bulk load of the S two units ahead into the same buffer.
 // Every wait is bounded; on expiry the CTA records EFLA_ERR_DEVICE_TIMEOUT and leaves.
+//
+// Gated instantiation (gated.cuh): A~ and P take Gamma_ts in the prep warp, X takes e^{G_t} and S the
+// block's decay where the state warpgroup waits for u, the state update takes c_t u_t (a second split
+// operand), and O = e^{G_t} O1 + u^T P^T is joined where it is read out.  Operands are rounded to
+// nearest in both parts.
 #include <cudaTypedefs.h>
 
 #include <mutex>
 
-#include "internal.cuh"
+#include "gated.cuh"
 #include "ptx.cuh"
+#include "tc_common.cuh"
 
 namespace efla {
 namespace {
@@ -63,7 +69,8 @@ constexpr uint32_t OFF_OT = OFF_PP + 4096;        // o tiles: 2 buffers x 8 KB (
 constexpr uint32_t OFF_G = OFF_OT + 2 * 8192;     // fp32 A~ [16][17], T~ [16][17]
 constexpr uint32_t G_LD = 17;
 constexpr uint32_t OFF_ROW = OFF_G + 2 * 16 * G_LD * 4;  // fp32 invn[16], gn[16]
-constexpr uint32_t OFF_BAR = OFF_ROW + 128;
+constexpr uint32_t OFF_DEC = OFF_ROW + 128;  // gated, fp32: G_t hi [16], lo [16], then per block parity e^{G_t} [16], c_t [16]
+constexpr uint32_t OFF_BAR = OFF_DEC + (2 + 4) * 64;
 constexpr uint32_t OFF_MISC = OFF_BAR + 256;  // tmem base, abort flag
 constexpr uint32_t SMEM_USED = OFF_MISC + 16;
 constexpr uint32_t SMEM_ALLOC = SMEM_USED + 1024;
@@ -81,6 +88,8 @@ constexpr uint32_t TM_X = 256;   // X^T fp32 (16); then (-X)^T hi (8) | lo (8); 
 constexpr uint32_t TM_O = 272;   // O^T fp32 (16), adjacent to TM_X: [X | O1] is one N = 32 product
 constexpr uint32_t TM_U = 288;   // u^T fp32 (16)
 constexpr uint32_t TM_G = 304;   // Gram rows: lane t < 16 k_t . k_s, lane 16 + t q_t . k_s (16)
+constexpr uint32_t TM_UC = 320;  // gated: diag(c) u hi (8) | lo (8)
+constexpr uint32_t TM_O2 = 336;  // gated: u^T P^T fp32 (16)
 constexpr uint32_t TM_COLS = 512;
 
 constexpr int THREADS = 256;
@@ -99,6 +108,8 @@ struct DtParams {
     int B, m, H;
     int euler;
     unsigned long long wait_ns;
+    const float *g;  // gated: [B, m, H] log decays
+    int rep;         // gated: value heads a key head
 };
 
 struct Bars {
@@ -130,24 +141,11 @@ __device__ __forceinline__ bool dt_wait_warp(uint64_t *bar, uint32_t parity, vol
     return __all_sync(0xffffffffu, dt_wait(bar, parity, abort_flag, limit));
 }
 
-// x = hi + lo as packed bf16 pairs (hi: x truncated to bf16; lo: the remainder truncated).
-template <int NP>
-__device__ __forceinline__ void split_pairs(const float *x, uint32_t *hi, uint32_t *lo) {
-#pragma unroll
-    for (int c = 0; c < NP; ++c) {
-        const uint32_t b0 = __float_as_uint(x[2 * c]), b1 = __float_as_uint(x[2 * c + 1]);
-        hi[c] = __byte_perm(b0, b1, 0x7632);
-        // the two remainders x - hi (exact) in one packed fp32x2 fma: hi * (-1) + x
-        const float2 r = __ffma2_rn(make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)),
-                                    make_float2(-1.f, -1.f), make_float2(x[2 * c], x[2 * c + 1]));
-        lo[c] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632);
-    }
-}
-
 // 16 fp32 values of row `row` of a 16-row operand tile (128B swizzle) as bf16 hi at `tile`, lo at tile + 2048.
+template <bool RN>
 __device__ __forceinline__ void put_row16(uint8_t *tile, int row, const float (&x)[16]) {
     uint32_t hh[8], ll[8];
-    split_pairs<8>(x, hh, ll);
+    tc::split_as<RN, 8>(x, hh, ll);
 #pragma unroll
     for (int h8 = 0; h8 < 2; ++h8) {
         const uint32_t off = swz_offset(row, 8 * h8, 2048);
@@ -157,7 +155,7 @@ __device__ __forceinline__ void put_row16(uint8_t *tile, int row, const float (&
     }
 }
 
-template <bool OUT_BF16>
+template <bool OUT_BF16, bool GATED>
 __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_constant__ DtParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -168,6 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
     const uint64_t wait_ns = p.wait_ns;
     const int units = p.B * p.H;
     const int nblk = (p.m + MB - 1) / MB;
+    float *dec_gh = reinterpret_cast<float *>(sm + OFF_DEC), *dec_gl = dec_gh + 16, *dec = dec_gl + 16;
     if ((int)blockIdx.x >= units) return;
 
     if (tid == 0) {
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
 #pragma unroll
                             for (int i = 0; i < 32; ++i) sv[i] = stg[(g * 32 + i) * D + j];
                             tmem_st32(lane_base + TM_S + g * 32, sv);
-                            split_pairs<16>(sv, hi, lo);
+                            tc::split_as<GATED, 16>(sv, hi, lo);
                             tmem_st16u(lane_base + TM_SA + g * 16, hi);
                             tmem_st16u(lane_base + TM_SA + 64 + g * 16, lo);
                         }
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                             uint32_t hi[16], lo[16];
                             tmem_ld32(lane_base + TM_S + g * 32, sv);
                             tmem_ld_wait();
-                            split_pairs<16>(sv, hi, lo);
+                            tc::split_as<GATED, 16>(sv, hi, lo);
                             tmem_st16u(lane_base + TM_SA + g * 16, hi);
                             tmem_st16u(lane_base + TM_SA + 64 + g * 16, lo);
                         }
@@ -253,6 +252,8 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                 tc_fence_before();
                 mbar_arrive(&bars->sa_ready);
                 ok = ok && dt_wait_warp(&bars->x_done, gb & 1, abort_flag, wait_ns);
+                const float *eg = dec + (gb & 1) * 32, *ec = eg + 16;  // gated: e^{G_t}, c_t of the block
+                if constexpr (GATED) ok = ok && dt_wait_warp(&bars->prep_ready, gb & 1, abort_flag, wait_ns);
                 if (ok) {  // (-X)^T -> bf16 hi | lo (tokens past the block end are zero)
                     tc_fence_after();
                     float x[16];
@@ -260,13 +261,26 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                     tmem_ld16(lane_base + TM_X, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int t = 0; t < 16; ++t) x[t] = t < mb ? -x[t] : 0.f;
-                    split_pairs<8>(x, hi, lo);
+                    for (int t = 0; t < 16; ++t) x[t] = t < mb ? (GATED ? -eg[t] * x[t] : -x[t]) : 0.f;
+                    tc::split_as<GATED, 8>(x, hi, lo);
                     tmem_st8u(lane_base + TM_X, hi);
                     tmem_st8u(lane_base + TM_X + 8, lo);
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(&bars->r_ready);
+                    if constexpr (GATED) {  // S times the block's decay while the tensor core forms u
+                        const float el = eg[MB - 1];
+#pragma unroll 1
+                        for (int g = 0; g < 4; ++g) {
+                            float sv[32];
+                            tmem_ld32(lane_base + TM_S + g * 32, sv);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sv[i] *= el;
+                            tmem_st32(lane_base + TM_S + g * 32, sv);
+                        }
+                        tmem_st_wait();
+                    }
                 }
                 ok = ok && dt_wait_warp(&bars->u_done, gb & 1, abort_flag, wait_ns);
                 if (ok) {  // u^T -> bf16 hi | lo
@@ -275,9 +289,16 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                     uint32_t hi[8], lo[8];
                     tmem_ld16(lane_base + TM_U, x);
                     tmem_ld_wait();
-                    split_pairs<8>(x, hi, lo);
+                    tc::split_as<GATED, 8>(x, hi, lo);
                     tmem_st8u(lane_base + TM_X, hi);
                     tmem_st8u(lane_base + TM_X + 8, lo);
+                    if constexpr (GATED) {
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) x[t] *= ec[t];
+                        tc::split_pack_rn<8>(x, hi, lo);
+                        tmem_st8u(lane_base + TM_UC, hi);
+                        tmem_st8u(lane_base + TM_UC + 8, lo);
+                    }
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(&bars->u_ready);
@@ -288,6 +309,13 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                     tc_fence_after();
                     float ov[16];
                     tmem_ld16(lane_base + TM_O, ov);
+                    if constexpr (GATED) {
+                        float o2[16];
+                        tmem_ld16(lane_base + TM_O2, o2);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) ov[t] = fmaf(eg[t], ov[t], o2[t]);
+                    }
                     tmem_ld_wait();
 #pragma unroll
                     for (int t = 0; t < 16; ++t) {
@@ -343,8 +371,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                 const int t0 = blk * MB, mb = min(MB, p.m - t0);
                 // beta of token `lane` (issued before the waits so that its latency overlaps them)
                 const float bt = lane < mb ? p.beta[((size_t)b * p.m + t0 + lane) * p.H + h] : 0.f;
+                float gt = 0.f;
+                if constexpr (GATED) gt = lane < mb ? p.g[((size_t)b * p.m + t0 + lane) * p.H + h] : 0.f;
                 if (!(ok = dt_wait_warp(&bars->g_done, gb & 1, abort_flag, wait_ns))) break;
                 tc_fence_after();
+                if constexpr (GATED) block_decay16(gt, lane, dec_gh, dec_gl, dec + (gb & 1) * 32, dec + (gb & 1) * 32 + 16);
                 float row[16];  // lane t < 16: k_t . k_s; lane 16 + t: q_t . k_s
                 tmem_ld16(tmem + TM_G, row);
                 tmem_ld_wait();
@@ -364,6 +395,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                     }
                 }
                 __syncwarp();
+                if constexpr (GATED) {  // Gram terms times Gamma_ts (entries above the diagonal are not used)
+                    const float ht = dec_gh[lane & 15], lt = dec_gl[lane & 15];
+#pragma unroll
+                    for (int s = 0; s < 16; ++s) row[s] *= pair_decay(ht, lt, dec_gh[s], dec_gl[s]);
+                }
                 if (lane < 16) {  // A~ row t = lane: gamma_t/n_t (k_t . k_s) / n_s, s < t
                     const float g_t = gn[lane];
 #pragma unroll
@@ -399,7 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
 #pragma unroll
                         for (int s = 0; s < 16; ++s) x[s] = s <= t ? row[s] : 0.f;
                     }
-                    put_row16(sm + (lane < 16 ? OFF_TP : OFF_PP), t, x);
+                    put_row16<GATED>(sm + (lane < 16 ? OFF_TP : OFF_PP), t, x);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -456,14 +492,16 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                 if (!(ok = dt_wait_warp(&bars->u_ready, gb & 1, abort_flag, wait_ns))) break;
                 tc_fence_after();
                 // S^T += u_hi^T K + u_lo^T K  (K as an MN-major operand: its 16 rows are the K dimension)
-                mma_bf16_ts_e(tmem + TM_S, tmem + TM_X, smem_desc(kq_s, 4096, 1024), id128k, 1);
-                mma_bf16_ts_e(tmem + TM_S, tmem + TM_X + 8, smem_desc(kq_s, 4096, 1024), id128k, 1);
+                constexpr uint32_t US = GATED ? TM_UC : TM_X;
+                mma_bf16_ts_e(tmem + TM_S, tmem + US, smem_desc(kq_s, 4096, 1024), id128k, 1);
+                mma_bf16_ts_e(tmem + TM_S, tmem + US + 8, smem_desc(kq_s, 4096, 1024), id128k, 1);
                 mma_commit_e(&bars->s_done);
                 mma_commit_e(&bars->kqv_empty[st]);
                 // O^T += u_hi^T P_hi^T + u_hi^T P_lo^T + u_lo^T P_hi^T
-                mma_bf16_ts_e(tmem + TM_O, tmem + TM_X, smem_desc(pp, 16, 1024), id16, 1);
-                mma_bf16_ts_e(tmem + TM_O, tmem + TM_X, smem_desc(pp + 2048, 16, 1024), id16, 1);
-                mma_bf16_ts_e(tmem + TM_O, tmem + TM_X + 8, smem_desc(pp, 16, 1024), id16, 1);
+                constexpr uint32_t OD = GATED ? TM_O2 : TM_O;
+                mma_bf16_ts_e(tmem + OD, tmem + TM_X, smem_desc(pp, 16, 1024), id16, GATED ? 0 : 1);
+                mma_bf16_ts_e(tmem + OD, tmem + TM_X, smem_desc(pp + 2048, 16, 1024), id16, 1);
+                mma_bf16_ts_e(tmem + OD, tmem + TM_X + 8, smem_desc(pp, 16, 1024), id16, 1);
                 mma_commit_e(&bars->o_done);
                 mma_commit_e(&bars->tp_free);
             }
@@ -487,11 +525,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                 const int st = gb & 1;
                 if (gb >= 2 && !(ok = dt_wait(&bars->kqv_empty[st], ((gb - 2) >> 1) & 1, abort_flag, wait_ns))) break;
                 mbar_arrive_expect_tx(&bars->kqv_full[st], KQ_BYTES + V_BYTES);
-                const int t0 = blk * MB;
+                const int t0 = blk * MB, hk = GATED ? h / p.rep : h;
                 uint8_t *kq = sm + OFF_KQ + st * KQ_BYTES, *vv = sm + OFF_V + st * V_BYTES;
                 for (int cb = 0; cb < 2; ++cb) {
-                    tma_load_4d(kq + cb * 4096, &p.map_k, &bars->kqv_full[st], cb * 64, h, t0, b);
-                    tma_load_4d(kq + cb * 4096 + 2048, &p.map_q, &bars->kqv_full[st], cb * 64, h, t0, b);
+                    tma_load_4d(kq + cb * 4096, &p.map_k, &bars->kqv_full[st], cb * 64, hk, t0, b);
+                    tma_load_4d(kq + cb * 4096 + 2048, &p.map_q, &bars->kqv_full[st], cb * 64, hk, t0, b);
                     tma_load_4d(vv + cb * 2048, &p.map_v, &bars->kqv_full[st], cb * 64, h, t0, b);
                 }
                 kqv_issued = gb + 1;
@@ -577,30 +615,29 @@ bool dt_map(CUtensorMap *mp, const void *ptr, int B, int m, int H, bool f32, boo
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool OUT_BF16>
+template <bool OUT_BF16, bool GATED>
 cudaError_t dt_launch(const DtParams &p, unsigned grid, cudaStream_t stream) {
     static bool attr_done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !attr_done[dev]) {
-        e = cudaFuncSetAttribute(decode_tc_kernel<OUT_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(decode_tc_kernel<OUT_BF16, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)SMEM_ALLOC);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_done[dev] = true;
     }
-    decode_tc_kernel<OUT_BF16><<<grid, THREADS, SMEM_ALLOC, stream>>>(p);
+    decode_tc_kernel<OUT_BF16, GATED><<<grid, THREADS, SMEM_ALLOC, stream>>>(p);
     return cudaGetLastError();
 }
 
-}  // namespace
-
-// Multi-token decode on the tensor cores: bf16 q, k, v with d_k = d_v = 128.
-cudaError_t launch_decode_tokens_tc(const DecodeArgs &a, const char **why) {
+// q, k with Hk heads; g is nullptr for the ungated update.
+template <bool GATED, typename A>
+cudaError_t tokens_tc(const A &a, int Hk, const float *g, const char **why) {
     if (a.B == 0 || a.m == 0) return cudaSuccess;
     DtParams p;
     memset(&p, 0, sizeof p);
-    if (!dt_map(&p.map_q, a.q, a.B, a.m, a.H, false, true) || !dt_map(&p.map_k, a.k, a.B, a.m, a.H, false, true) ||
+    if (!dt_map(&p.map_q, a.q, a.B, a.m, Hk, false, true) || !dt_map(&p.map_k, a.k, a.B, a.m, Hk, false, true) ||
         !dt_map(&p.map_v, a.v, a.B, a.m, a.H, false, true) ||
         !dt_map(&p.map_o, a.o, a.B, a.m, a.H, a.o_dtype != EFLA_BF16, false)) {
         *why = "cuTensorMapEncodeTiled failed";
@@ -615,6 +652,8 @@ cudaError_t launch_decode_tokens_tc(const DecodeArgs &a, const char **why) {
     p.H = a.H;
     p.euler = a.euler;
     p.wait_ns = wait_limit_ns();
+    p.g = g;
+    p.rep = a.H / Hk;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -625,7 +664,13 @@ cudaError_t launch_decode_tokens_tc(const DecodeArgs &a, const char **why) {
     const long units = (long)a.B * a.H;
     const unsigned grid = (unsigned)std::min<long>(units, sms);
     *why = "tcgen05 decode kernel launch";
-    return a.o_dtype == EFLA_BF16 ? dt_launch<true>(p, grid, a.stream) : dt_launch<false>(p, grid, a.stream);
+    return a.o_dtype == EFLA_BF16 ? dt_launch<true, GATED>(p, grid, a.stream) : dt_launch<false, GATED>(p, grid, a.stream);
 }
+
+}  // namespace
+
+// Multi-token decode on the tensor cores: bf16 q, k, v with d_k = d_v = 128.
+cudaError_t launch_decode_tokens_tc(const DecodeArgs &a, const char **why) { return tokens_tc<false>(a, a.H, nullptr, why); }
+cudaError_t launch_gated_decode_tokens_tc(const GatedDecodeArgs &a, const char **why) { return tokens_tc<true>(a, a.Hk, a.g, why); }
 
 }  // namespace efla

@@ -63,9 +63,9 @@ struct GatedDecodeArgs {
 //     its end, d_k x d_v x 4 bytes each;
 //   w [B H][nc]: T'' = (I + diag(alpha) L)^{-1} diag(alpha) of every chunk, 64 x 64 x 4 bytes;
 //   p [B H][nc]: P likewise (CUDA-core path only);
-//   sdot [B H][nc][4]: partial sums of <S, dS'> of every chunk;
+//   sdot [B H][nc][4]: partial sums of <S, dS'> of every chunk (CUDA-core path only);
 //   part [2][B T H][d_k] fp32: dq and dk of every value head (where key heads are shared);
-//   tok: per-token scratch of the tensor-core path: G [B T H][128] fp32, then -dR as bf16 hi and lo.
+//   tok: per-token scratch of the tensor-core path: G [B T H][128] fp32, then the low part of dR in bf16.
 struct GatedWs {
     size_t states, dse, w, p, sdot, part, tok, bytes;
 };
@@ -84,10 +84,10 @@ inline GatedWs gated_ws(int B, int T, int Hk, int H, int dk, int dv, efla_dtype 
     w.states = take(units * nc * mat);
     w.dse = take(units * nc * mat);
     w.w = take(units * nc * 64 * 64 * 4);
-    w.p = take(units * nc * 64 * 64 * 4);
-    w.sdot = take(units * nc * 4 * sizeof(float));
+    w.p = take(tc ? 0 : units * nc * 64 * 64 * 4);
+    w.sdot = take(tc ? 0 : units * nc * 4 * sizeof(float));
     w.part = take(Hk != H ? 2 * tok * dk * sizeof(float) : 0);
-    w.tok = take(tc ? tok * 128 * (4 + 2 + 2) : 0);
+    w.tok = take(tc ? tok * 128 * (4 + 2) : 0);
     w.bytes = T > 0 && units > 0 ? at : 0;
     return w;
 }
@@ -95,6 +95,10 @@ inline GatedWs gated_ws(int B, int T, int Hk, int H, int dk, int dv, efla_dtype 
 // CUDA cores, every supported shape (gated_simt.cu).
 cudaError_t launch_gated_chunk_simt(const GatedFwdArgs &a);
 cudaError_t launch_gated_bwd_simt(const GatedBwdArgs &a);
+// Tensor cores: bf16, d_k = d_v = 128, gated_tc() (chunk_tc.cu).
+cudaError_t launch_gated_chunk_tc(const GatedFwdArgs &a, const char **why);
+cudaError_t launch_gated_bwd_tc(const GatedBwdArgs &a, const char **why);  // T > 0 (gated_bwd_tc.cu)
+cudaError_t launch_gated_decode_tokens_tc(const GatedDecodeArgs &a, const char **why);  // (decode_tc.cu)
 // dq, dk [B T Hk][d] = the sums over each key head's value heads of part [2][B T H][d] (fp32), in
 // the input type, one fixed order of addition.
 cudaError_t launch_gated_reduce_heads(const GatedBwdArgs &a, const float *part);
@@ -111,11 +115,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 // G_t of a chunk's 64 tokens in units of log2, as the unevaluated sum hi + lo of two floats, and
 // the two factors every token needs, by one warp (64 values of g, 0 past the chunk's end; lane l
-// holds tokens 2 l and 2 l + 1).  The running sum is taken in 64 bits: a difference G_t - G_s of
+// holds tokens 2 l and 2 l + 1; token t's two floats go to gh[t stride] and gl[t stride]).  The running sum is taken in 64 bits: a difference G_t - G_s of
 // two far sums is then exact to about 2^-46 of the sums, where a 32-bit sum of 64 gates of size 2
 // would already be off by 2^-17 in the exponent, more than every other rounding of the chunk.
 // A gate of -inf (or below -700) is taken as -700: e^-700 is 0 in fp32, and sums stay finite.
-__device__ __forceinline__ void chunk_decay(float g0, float g1, int lane, float *gh, float *gl, float *eg, float *ec) {
+__device__ __forceinline__ void chunk_decay(float g0, float g1, int lane, float *gh, float *gl, int stride,
+                                            float *eg, float *ec) {
     constexpr double LOG2E = 1.4426950408889634;
     const double a = (double)(g0 < -700.f ? -700.f : g0) * LOG2E, b = (double)(g1 < -700.f ? -700.f : g1) * LOG2E;
     double s = a + b;
@@ -126,10 +131,10 @@ __device__ __forceinline__ void chunk_decay(float g0, float g1, int lane, float 
     }
     const double last = __shfl_sync(0xffffffffu, s, 31), G1 = s, G0 = s - b;
     const float h0 = (float)G0, h1 = (float)G1;
-    gh[2 * lane] = h0;
-    gh[2 * lane + 1] = h1;
-    gl[2 * lane] = (float)(G0 - (double)h0);
-    gl[2 * lane + 1] = (float)(G1 - (double)h1);
+    gh[2 * lane * stride] = h0;
+    gh[(2 * lane + 1) * stride] = h1;
+    gl[2 * lane * stride] = (float)(G0 - (double)h0);
+    gl[(2 * lane + 1) * stride] = (float)(G1 - (double)h1);
     eg[2 * lane] = ex2(h0);  // (rounding the exponent x costs 2^-25 |x| of a factor 2^x)
     eg[2 * lane + 1] = ex2(h1);
     ec[2 * lane] = ex2((float)(last - G0));

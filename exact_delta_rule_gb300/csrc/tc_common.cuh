@@ -62,19 +62,49 @@ __device__ __forceinline__ void split_pack(const float *x, uint32_t *hi, uint32_
     }
 }
 
+// The same with both parts rounded to nearest: |e| <= 2^-18 |x| and no bias, where the truncated split
+// is 2^-14 off in one direction (the state it feeds is an fp32 output of the gated kernels).
+template <int NP>
+__device__ __forceinline__ void split_pack_rn(const float *x, uint32_t *hi, uint32_t *lo) {
+#pragma unroll
+    for (int c = 0; c < NP; ++c) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * c], x[2 * c + 1]);
+        hi[c] = *reinterpret_cast<const uint32_t *>(&h);
+        const float2 r = __ffma2_rn(make_float2(__uint_as_float(hi[c] << 16), __uint_as_float(hi[c] & 0xffff0000u)),
+                                    make_float2(-1.f, -1.f), make_float2(x[2 * c], x[2 * c + 1]));
+        const __nv_bfloat162 l = __floats2bfloat162_rn(r.x, r.y);
+        lo[c] = *reinterpret_cast<const uint32_t *>(&l);
+    }
+}
+template <bool RN, int NP>
+__device__ __forceinline__ void split_as(const float *x, uint32_t *hi, uint32_t *lo) {
+    if constexpr (RN)
+        split_pack_rn<NP>(x, hi, lo);
+    else
+        split_pack<NP>(x, hi, lo);
+}
+// One value: hi and lo rounded to nearest, as bf16 bits.
+__device__ __forceinline__ void split1_rn(float x, uint32_t &h16, uint32_t &l16) {
+    const uint32_t r = __float_as_uint(x) + 0x8000u;
+    h16 = r >> 16;
+    l16 = (__float_as_uint(x - __uint_as_float(r & 0xffff0000u)) + 0x8000u) >> 16;
+}
+
 // Rows row0 .. row0 + 31 of column j (this lane) of a 128 x 128 fp32 matrix, x[i] = M[row0 + i][j],
 // into the operand-tile layout the backward kernels load whole: bf16 hi (truncated) in the first
 // 32 KB and lo (the remainder, truncated) in the next, each as 2 column blocks of [128 rows][64]
 // with the 128-byte swizzle.  Lanes j and j ^ 1 of a warp (consecutive columns) pair up: each
 // shuffle hands one half to the partner, the even lane stores the hi word, the odd lane the lo
 // word.  All 32 lanes take part.
+template <bool RN = false>  // RN: both parts rounded to nearest
 __device__ __forceinline__ void put_col_split_tile(uint8_t *tile, int row0, int j, const float (&x)[32]) {
     const bool odd = (j & 1) != 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const uint32_t b = __float_as_uint(x[i]);
-        const uint32_t h16 = b >> 16;
-        const uint32_t l16 = __float_as_uint(x[i] - __uint_as_float(b & 0xffff0000u)) >> 16;
+        uint32_t h16 = b >> 16;
+        uint32_t l16 = __float_as_uint(x[i] - __uint_as_float(b & 0xffff0000u)) >> 16;
+        if constexpr (RN) split1_rn(x[i], h16, l16);
         const uint32_t recv = __shfl_xor_sync(0xffffffffu, odd ? h16 : l16, 1);
         const uint32_t word = odd ? (recv | (l16 << 16)) : (h16 | (recv << 16));
         *reinterpret_cast<uint32_t *>(tile + swz_offset(row0 + i, j & ~1, 16384) + (odd ? 32768u : 0u)) = word;
@@ -98,6 +128,35 @@ __device__ __forceinline__ void put_col_split_rows(__nv_bfloat16 *hi, __nv_bfloa
         const uint32_t l16 = __float_as_uint(v - __uint_as_float(b & 0xffff0000u)) >> 16;
         const uint32_t recv = __shfl_xor_sync(0xffffffffu, odd ? h16 : l16, 1);
         if (t0 + i < valid) dst[(size_t)(t0 + i) * stride / 2] = odd ? (recv | (l16 << 16)) : (h16 | (recv << 16));
+    }
+}
+
+// Gated kernels: rows 32 g0 .. 32 g1 - 1 of the state (column j = this thread's TMEM lane, TMEM address
+// ts of its transpose) times the chunk's decay el; with `tile` their values before it go into an
+// operand tile first.  Out of line for the instruction cache.
+__device__ __noinline__ void decay_state_rows(uint8_t *tile, uint32_t ts, int g0, int g1, int j, float el) {
+#pragma unroll 1
+    for (int g = g0; g < g1; ++g) {
+        float sv[32];
+        tmem_ld32(ts + g * 32, sv);
+        tmem_ld_wait();
+        if (tile) put_col_split_tile<true>(tile, g * 32, j, sv);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sv[i] *= el;
+        tmem_st32(ts + g * 32, sv);
+    }
+    tmem_st_wait();
+}
+
+// 32 values of shared memory (16-byte aligned) into registers, the same in every lane.
+__device__ __forceinline__ void load32(const float *src, float (&x)[32]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 f = reinterpret_cast<const float4 *>(src)[i];
+        x[4 * i] = f.x;
+        x[4 * i + 1] = f.y;
+        x[4 * i + 2] = f.z;
+        x[4 * i + 3] = f.w;
     }
 }
 
