@@ -147,6 +147,7 @@ struct TcParams {
     int seg_len, G;
     const float *s_in;
     float *maps;
+    // (gated: the tiles hold S^T and T, see gated_bwd_tc.cu)
     float *states;               // chunk-start states [N, H, nchunks] x 64 KB (rows of [B, T]) or nullptr: S as
                                  // bf16 hi/lo operand tiles (put_col_split_tile) for the tensor-core backward
     uint8_t *tpp;                // with states: every chunk's T'' tile as formed below (16 KB a chunk) or nullptr
@@ -437,6 +438,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                     const float gam = !live ? 0.f : p.euler ? beta_t * lam : -expm1f(-beta_t * lam);
                     row_invn[t] = invn;
                     row_gn[t] = gam * invn;
+                    if constexpr (GATED) At[t * AT_LD + 66] = lam * invn;  // n_t
                 }
                 if constexpr (GATED) {
                     if (warp == 7) chunk_decay(g0_c, g1_c, tid & 31, At + 64, At + 65, AT_LD, dec + buf * 128, dec + buf * 128 + 64);
@@ -528,6 +530,16 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                     const uint32_t off = swz_offset(t, s0 + c8, 8192);
                     *reinterpret_cast<uint4 *>(hi + off) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
                     *reinterpret_cast<uint4 *>(lo + off) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
+                    if constexpr (GATED) {
+                        if (ghi) {  // T = diag(1/n) T~ diag(n) for the backward: 1 on the diagonal, zero keys included
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int s = s0 + c8 + e;
+                                x[e] = s < t ? rsc * tt8[e] * At[s * AT_LD + 66] : s == t ? 1.f : 0.f;
+                            }
+                            split_pack_rn<4>(x, hh, ll);
+                        }
+                    }
                     if (ghi) {
                         *reinterpret_cast<uint4 *>(ghi + off) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
                         *reinterpret_cast<uint4 *>(ghi + 8192 + off) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
@@ -674,6 +686,9 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 split_as<GATED, 16>(sv, hi, lo);
                 tmem_st16u(lane_base + TM_SA + g * 16, hi);
                 tmem_st16u(lane_base + TM_SA + 64 + g * 16, lo);
+                if constexpr (GATED) {
+                    if (st_c) put_state_row(st_c, g, j, hi, lo);
+                }
             }
             tmem_st_wait();
             tc_fence_before();
@@ -684,7 +699,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             if constexpr (GATED) {
                 ok = wait_bar_warp(&bars->gate_ready[c & 1], (c >> 1) & 1, abort_flag, wait_ns);
                 if (!ok) break;
-                decay_state_rows(st_c, lane_base + TM_S, 0, 2, j, eg[C - 1]);
+                decay_state_rows(lane_base + TM_S, 0, 2, eg[C - 1]);
             } else {
                 if (st_c) dump_state_rows(st_c, lane_base + TM_S, 0, j);
             }
@@ -729,7 +744,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             tc_fence_before();
             mbar_arrive(&bars->r_ready);
             if constexpr (GATED) {
-                decay_state_rows(st_c, lane_base + TM_S, 2, 4, j, eg[C - 1]);
+                decay_state_rows(lane_base + TM_S, 2, 4, eg[C - 1]);
                 if (write_o) {  // O1^T times e^{G_t}
                     ok = wait_bar_warp(&bars->o1_done, c & 1, abort_flag, wait_ns);
                     if (!ok) break;

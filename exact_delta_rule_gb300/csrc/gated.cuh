@@ -61,11 +61,12 @@ struct GatedDecodeArgs {
 // Workspace of the backward (bytes from its base, every region 256-byte aligned).  nc = ceil(T / 64).
 //   states and dse [B H][nc]: the state at the start of every chunk and the gradient of the state at
 //     its end, d_k x d_v x 4 bytes each;
-//   w [B H][nc]: T'' = (I + diag(alpha) L)^{-1} diag(alpha) of every chunk, 64 x 64 x 4 bytes;
+//   w [B H][nc]: T'' = (I + diag(alpha) L)^{-1} diag(alpha) of every chunk (the tensor-core path: the
+//     inverse without diag(alpha)), 64 x 64 x 4 bytes;
 //   p [B H][nc]: P likewise (CUDA-core path only);
-//   sdot [B H][nc][4]: partial sums of <S, dS'> of every chunk (CUDA-core path only);
+//   sdot [B H][nc][4]: partial sums of <S, dS'> of every chunk;
 //   part [2][B T H][d_k] fp32: dq and dk of every value head (where key heads are shared);
-//   tok: per-token scratch of the tensor-core path: G [B T H][128] fp32, then the low part of dR in bf16.
+//   tok: per-token scratch of the tensor-core path: dY [B T H][128] as bf16 hi, then lo (gated_bwd_tc.cu).
 struct GatedWs {
     size_t states, dse, w, p, sdot, part, tok, bytes;
 };
@@ -85,9 +86,9 @@ inline GatedWs gated_ws(int B, int T, int Hk, int H, int dk, int dv, efla_dtype 
     w.dse = take(units * nc * mat);
     w.w = take(units * nc * 64 * 64 * 4);
     w.p = take(tc ? 0 : units * nc * 64 * 64 * 4);
-    w.sdot = take(tc ? 0 : units * nc * 4 * sizeof(float));
+    w.sdot = take(units * nc * 4 * sizeof(float));
     w.part = take(Hk != H ? 2 * tok * dk * sizeof(float) : 0);
-    w.tok = take(tc ? tok * 128 * (4 + 2) : 0);
+    w.tok = take(tc ? tok * 128 * (2 + 2) : 0);
     w.bytes = T > 0 && units > 0 ? at : 0;
     return w;
 }

@@ -154,6 +154,12 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes
     return d;
 }
 
+// The same without a swizzle: 8 x 16-byte core matrices of 128 contiguous bytes.  K-major operands: `lbo`
+// between core matrices along K, `sbo` along M or N; MN-major ones: `lbo` along K, `sbo` along M or N.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    return smem_desc(saddr, lbo_bytes, sbo_bytes) & ~(static_cast<uint64_t>(7) << 61);
+}
+
 // Instruction descriptor for kind::f16 with bf16 A and B and an fp32
 // accumulator.  a_mn / b_mn select MN-major (1) or K-major (0) operands.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {

@@ -83,12 +83,6 @@ __device__ __forceinline__ void split_as(const float *x, uint32_t *hi, uint32_t 
     else
         split_pack<NP>(x, hi, lo);
 }
-// One value: hi and lo rounded to nearest, as bf16 bits.
-__device__ __forceinline__ void split1_rn(float x, uint32_t &h16, uint32_t &l16) {
-    const uint32_t r = __float_as_uint(x) + 0x8000u;
-    h16 = r >> 16;
-    l16 = (__float_as_uint(x - __uint_as_float(r & 0xffff0000u)) + 0x8000u) >> 16;
-}
 
 // Rows row0 .. row0 + 31 of column j (this lane) of a 128 x 128 fp32 matrix, x[i] = M[row0 + i][j],
 // into the operand-tile layout the backward kernels load whole: bf16 hi (truncated) in the first
@@ -96,15 +90,13 @@ __device__ __forceinline__ void split1_rn(float x, uint32_t &h16, uint32_t &l16)
 // with the 128-byte swizzle.  Lanes j and j ^ 1 of a warp (consecutive columns) pair up: each
 // shuffle hands one half to the partner, the even lane stores the hi word, the odd lane the lo
 // word.  All 32 lanes take part.
-template <bool RN = false>  // RN: both parts rounded to nearest
 __device__ __forceinline__ void put_col_split_tile(uint8_t *tile, int row0, int j, const float (&x)[32]) {
     const bool odd = (j & 1) != 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const uint32_t b = __float_as_uint(x[i]);
-        uint32_t h16 = b >> 16;
-        uint32_t l16 = __float_as_uint(x[i] - __uint_as_float(b & 0xffff0000u)) >> 16;
-        if constexpr (RN) split1_rn(x[i], h16, l16);
+        const uint32_t h16 = b >> 16;
+        const uint32_t l16 = __float_as_uint(x[i] - __uint_as_float(b & 0xffff0000u)) >> 16;
         const uint32_t recv = __shfl_xor_sync(0xffffffffu, odd ? h16 : l16, 1);
         const uint32_t word = odd ? (recv | (l16 << 16)) : (h16 | (recv << 16));
         *reinterpret_cast<uint32_t *>(tile + swz_offset(row0 + i, j & ~1, 16384) + (odd ? 32768u : 0u)) = word;
@@ -132,20 +124,33 @@ __device__ __forceinline__ void put_col_split_rows(__nv_bfloat16 *hi, __nv_bfloa
 }
 
 // Gated kernels: rows 32 g0 .. 32 g1 - 1 of the state (column j = this thread's TMEM lane, TMEM address
-// ts of its transpose) times the chunk's decay el; with `tile` their values before it go into an
-// operand tile first.  Out of line for the instruction cache.
-__device__ __noinline__ void decay_state_rows(uint8_t *tile, uint32_t ts, int g0, int g1, int j, float el) {
+// ts of its transpose) times the chunk's decay el.  Out of line for the instruction cache.
+__device__ __noinline__ void decay_state_rows(uint32_t ts, int g0, int g1, float el) {
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
         float sv[32];
         tmem_ld32(ts + g * 32, sv);
         tmem_ld_wait();
-        if (tile) put_col_split_tile<true>(tile, g * 32, j, sv);
 #pragma unroll
         for (int i = 0; i < 32; ++i) sv[i] *= el;
         tmem_st32(ts + g * 32, sv);
     }
     tmem_st_wait();
+}
+
+// The gated backward's state tile: the transpose (rows j = d_v) of a 128 x 128 state as bf16 hi (32 KB),
+// then lo, in core matrices without a swizzle: the 16 bytes of row j, columns 8 c .. 8 c + 7, lie at c *
+// 2048 + j * 16.  A thread that owns a row then stores, and a bulk copy loads, whole lines.  As a K-major
+// operand (rows j = M) its core matrices are 128 bytes apart along M and 2048 along K; as an MN-major one
+// (rows j = K, columns = M) 2048 along M and 128 along K.
+// Columns 32 g .. 32 g + 31 of row j, as split_pack gives them:
+__device__ __forceinline__ void put_state_row(uint8_t *tile, int g, int j, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
+    uint8_t *row = tile + g * 8192 + j * 16;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        *reinterpret_cast<uint4 *>(row + q * 2048) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+        *reinterpret_cast<uint4 *>(row + 32768 + q * 2048) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+    }
 }
 
 // 32 values of shared memory (16-byte aligned) into registers, the same in every lane.
