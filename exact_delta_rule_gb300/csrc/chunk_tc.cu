@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             const int valid = (int)min((long)C, eos - tok0);
             uint8_t *KQ = sm + OFF_STAGE + st * STAGE_BYTES;
 
-            const float beta_t = beta_next;
+            const float beta_t = GATED ? live_beta(beta_next) : beta_next;
             beta_next = load_beta(c + 1);
             const float g0_c = g0_next, g1_c = g1_next;
             if constexpr (GATED) {
@@ -441,7 +441,11 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                     if constexpr (GATED) At[t * AT_LD + 66] = lam * invn;  // n_t
                 }
                 if constexpr (GATED) {
-                    if (warp == 7) chunk_decay(g0_c, g1_c, tid & 31, At + 64, At + 65, AT_LD, dec + buf * 128, dec + buf * 128 + 64);
+                    if (warp == 7) {
+                        const bool fast = chunk_decay(g0_c, g1_c, tid & 31, At + 64, At + 65, At + 67, AT_LD, dec + buf * 128,
+                                                      dec + buf * 128 + 64);
+                        if ((tid & 31) == 0) *reinterpret_cast<volatile int *>(sm + OFF_MISC + 12) = fast;
+                    }
                 }
                 // [gate: terms computed]
                 if (named_bar_any(BAR_PREP, 256, !ok || *abort_flag)) {  // also spreads an abort
@@ -452,12 +456,26 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 if (leader) mbar_arrive(&bars->g_free);  // every row of G has been read
                 if constexpr (GATED) {
                     if (leader) mbar_arrive(&bars->gate_ready[buf]);
-                    // G[t][s] times Gamma_ts (t: this row's token; entries above the diagonal are masked below)
-                    const float2 gt = *reinterpret_cast<const float2 *>(At + (row & (C - 1)) * AT_LD + 64);
+                    // G[t][s] times Gamma_ts (t: this row's token; entries above the diagonal are masked below, whole
+                    // warps of them not even scaled)
+                    const int t = row & (C - 1);
+                    const float2 gt = *reinterpret_cast<const float2 *>(At + t * AT_LD + 64);
+                    if ((t | 31) < col0) {
+                    } else if (*reinterpret_cast<volatile int *>(sm + OFF_MISC + 12)) {
+                        float up[2];
 #pragma unroll
-                    for (int s = 0; s < 32; ++s) {
-                        const float2 gs = *reinterpret_cast<const float2 *>(At + (col0 + s) * AT_LD + 64);
-                        g[s] *= pair_decay(gt.x, gt.y, gs.x, gs.y);
+                        for (int q = 0; q < 2; ++q) {
+                            const float2 gq = *reinterpret_cast<const float2 *>(At + (col0 + 16 * q) * AT_LD + 64);
+                            up[q] = pair_decay(gt.x, gt.y, gq.x, gq.y);
+                        }
+#pragma unroll
+                        for (int s = 0; s < 32; ++s) g[s] *= up[s >> 4] * At[(col0 + s) * AT_LD + 67];
+                    } else {
+#pragma unroll
+                        for (int s = 0; s < 32; ++s) {
+                            const float2 gs = *reinterpret_cast<const float2 *>(At + (col0 + s) * AT_LD + 64);
+                            g[s] *= pair_decay(gt.x, gt.y, gs.x, gs.y);
+                        }
                     }
                 }
                 if (row < C) {  // A~[t][col0 .. col0+31]
@@ -711,32 +729,31 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             tc_fence_after();
             // (-X)^T = -(K S)^T -> bf16 hi/lo operand in TMEM (rows past the sequence end are zero),
             // written over X once all of X is in registers
-            {
+            if constexpr (GATED) {  // ... times e^{G_t}, split in place
+#pragma unroll 1
+                for (int hf = 0; hf < 2; hf = opaque(hf + 1)) {
+                    float x[32], f[32];
+                    tmem_ld32(lane_base + TM_X + 32 * hf, x);
+                    load32(eg + 32 * hf, f);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) x[t] = 32 * hf + t < valid ? -f[t] * x[t] : 0.f;
+                    split_half(lane_base + TM_X, hf, x);
+                }
+            } else {
                 float x0[32], x1[32];
                 tmem_ld32(lane_base + TM_X, x0);
                 tmem_ld32(lane_base + TM_X + 32, x1);
                 tmem_ld_wait();
                 uint32_t hi[16], lo[16];
-                if constexpr (GATED) {
-                    float f[32];
-                    load32(eg, f);
-#pragma unroll
-                    for (int t = 0; t < 32; ++t) x0[t] *= f[t];
-                }
 #pragma unroll
                 for (int t = 0; t < 32; ++t) x0[t] = t < valid ? -x0[t] : 0.f;
-                split_as<GATED, 16>(x0, hi, lo);
+                split_pack<16>(x0, hi, lo);
                 tmem_st16u(lane_base + TM_X, hi);
                 tmem_st16u(lane_base + TM_X + 32, lo);
-                if constexpr (GATED) {
-                    float f[32];
-                    load32(eg + 32, f);
-#pragma unroll
-                    for (int t = 0; t < 32; ++t) x1[t] *= f[t];
-                }
 #pragma unroll
                 for (int t = 0; t < 32; ++t) x1[t] = 32 + t < valid ? -x1[t] : 0.f;
-                split_as<GATED, 16>(x1, hi, lo);
+                split_pack<16>(x1, hi, lo);
                 tmem_st16u(lane_base + TM_X + 16, hi);
                 tmem_st16u(lane_base + TM_X + 48, lo);
             }
@@ -771,23 +788,22 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             if constexpr (GATED) {
                 // c_t u_t -> hi in columns 0-31, lo in columns 64-95 of TM_SA: over the two partial sums, which
                 // this thread has read by then; free again once the state update that reads them is complete.
-                // Then u_t -> TM_X, which the next chunk's X overwrites behind the outputs in the pipe.
-                float u[64];
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float(&ua)[32] = *reinterpret_cast<float(*)[32]>(u + 32 * hf);
-                    float ub[32], f[32];
-                    tmem_ld32(lane_base + TM_SA + hf * 32, ua);
-                    tmem_ld32(lane_base + TM_SA + 64 + hf * 32, ub);
+                // u_t itself -> TM_X, split in place after that; the next chunk's X overwrites it behind the
+                // outputs in the pipe.
+#pragma unroll 1
+                for (int hf = 0; hf < 2; hf = opaque(hf + 1)) {
+                    float u[32], u2[32];
+                    uint32_t hi[16], lo[16];
+                    tmem_ld32(lane_base + TM_SA + hf * 32, u);
+                    tmem_ld32(lane_base + TM_SA + 64 + hf * 32, u2);
                     tmem_ld_wait();
-                    load32(ec + hf * 32, f);
 #pragma unroll
-                    for (int t = 0; t < 32; ++t) {
-                        ua[t] += ub[t];
-                        f[t] *= ua[t];
-                    }
-                    split_pack_rn<16>(f, hi, lo);
+                    for (int t = 0; t < 32; ++t) u[t] += u2[t];
+                    if (write_o) tmem_st32(lane_base + TM_X + hf * 32, u);
+                    load32(ec + hf * 32, u2);
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) u[t] *= u2[t];
+                    split_pack_rn<16>(u, hi, lo);
                     tmem_st16u(lane_base + TM_SA + hf * 16, hi);
                     tmem_st16u(lane_base + TM_SA + 64 + hf * 16, lo);
                 }
@@ -795,11 +811,12 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 tc_fence_before();
                 mbar_arrive(&bars->u_ready);
                 if (write_o) {
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        split_pack_rn<16>(u + 32 * hf, hi, lo);
-                        tmem_st16u(lane_base + TM_X + hf * 16, hi);
-                        tmem_st16u(lane_base + TM_X + 32 + hf * 16, lo);
+#pragma unroll 1
+                    for (int hf = 0; hf < 2; hf = opaque(hf + 1)) {
+                        float u[32];
+                        tmem_ld32(lane_base + TM_X + hf * 32, u);
+                        tmem_ld_wait();
+                        split_half(lane_base + TM_X, hf, u);
                     }
                     tmem_st_wait();
                     tc_fence_before();
@@ -904,7 +921,11 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                         break;
                 }
                 tc_fence_after();
-                {
+                if constexpr (GATED) {
+                    run_gram(tmem + TM_G, smem_desc(s_sm + OFF_STAGE + (g_next % NSTAGE) * STAGE_BYTES, 16, 1024), 16384,
+                             idesc_bf16_f32(128, 64, 0, 0));
+                    mma_commit_e(&bars->g_done);
+                } else {
                     const uint32_t kq = s_sm + OFF_STAGE + (g_next % NSTAGE) * STAGE_BYTES;
                     const uint32_t idesc = idesc_bf16_f32(128, 64, 0, 0);
 #pragma unroll
@@ -933,7 +954,10 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             if (!(ok = wait_bar_warp(&bars->sa_ready, c & 1, abort_flag, wait_ns))) break;
             tc_fence_after();
             const uint32_t idesc64 = idesc_bf16_f32(128, 64, 0, 0);
-            {  // X^T = S^T K^T (the chain): issued as soon as the S^T operand is written
+            if constexpr (GATED) {
+                run_ts_kmajor(tmem + TM_X, tmem + TM_SA, smem_desc(kq_s, 16, 1024), 16384, idesc64, 0);
+                mma_commit_e(&bars->x_done);
+            } else {  // X^T = S^T K^T (the chain): issued as soon as the S^T operand is written
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -952,6 +976,10 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 if (c >= 2 && !(ok = wait_bar_warp(&bars->o_free[c & 1], ((c - 2) >> 1) & 1, abort_flag, wait_ns)))
                     break;
                 tc_fence_after();
+                if constexpr (GATED) {
+                    run_ts_kmajor(tmem + ob, tmem + TM_SA, smem_desc(kq_s + 8192, 16, 1024), 16384, idesc64, 0);
+                    mma_commit_e(&bars->o1_done);
+                } else {
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -960,7 +988,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                         mma_bf16_ts_e(tmem + ob, tmem + TM_SA + part * 64 + ks * 8, smem_desc(kq_s + off, 16, 1024),
                                       idesc64, (part | ks) != 0);
                     }
-                if constexpr (GATED) mma_commit_e(&bars->o1_done);
+                }
             }
             // the rest of the chunk needs its prep (T'', P)
             if (!(ok = wait_bar_warp(&bars->prep_ready[buf], (c >> 1) & 1, abort_flag, wait_ns))) break;
@@ -972,7 +1000,9 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                // earlier, executed in order) have already read.
                 const uint32_t idesc = idesc_bf16_f32(128, 128, 1, 0);
                 const uint32_t v_s = kq_s + OFF_V;
-                if (mode != 1) {  // (the map from S = I takes v = 0)
+                if constexpr (GATED) {
+                    mma4_ss(tmem + TM_SA, smem_desc(v_s, 8192, 1024), 128, smem_desc(tp, 16, 1024), 2, idesc, 0);
+                } else if (mode != 1) {  // (the map from S = I takes v = 0)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_bf16_e(tmem + TM_SA, smem_desc(v_s + ks * 2048, 8192, 1024),
@@ -983,6 +1013,12 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             tc_fence_after();
             {  // u^T = [U1 | U2] + (-X)_hi^T [T''_hi; T''_lo]^T + (-X)_lo^T T''_hi^T  (u = U1 + U2)
                 const uint32_t idesc2 = idesc_bf16_f32(128, 128, 0, 0);
+                if constexpr (GATED) {
+                    // (the low part against both parts of T'': its product with the low one is 2^-18, and costs nothing here)
+#pragma unroll 1
+                    for (int part = 0; part < 2; part = opaque(part + 1))
+                        run_ts_halves(tmem + TM_SA, tmem + TM_X + part * 16, smem_desc(tp, 16, 1024), 2, idesc2, 1);
+                } else {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16_ts_e(tmem + TM_SA, tmem + TM_X + ks * 8, smem_desc(tp + ks * 32, 16, 1024), idesc2,
@@ -991,6 +1027,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16_ts_e(tmem + TM_SA, tmem + TM_X + 32 + ks * 8, smem_desc(tp + ks * 32, 16, 1024), idesc64,
                                   1);
+                }
                 mma_commit_e(&bars->u_done);
             }
             // the Gram products two chunks ahead execute while the state warpgroup forms u
@@ -999,12 +1036,18 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             tc_fence_after();
             {  // S^T += u^T K  (the chain), then O^T += u^T P^T
                 const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 1);
+                if constexpr (GATED) {
+#pragma unroll 1
+                    for (int part = 0; part < 2; part = opaque(part + 1))
+                        run_ts(tmem + TM_S, tmem + TM_SA + part * 64, smem_desc(kq_s, 16384, 1024), 128, idesc_s, 1);
+                } else {
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16_ts_e(tmem + TM_S, tmem + (GATED ? TM_SA + part * 64 : TM_X + part * 32) + ks * 8,
+                        mma_bf16_ts_e(tmem + TM_S, tmem + TM_X + part * 32 + ks * 8,
                                       smem_desc(kq_s + ks * 2048, 16384, 1024), idesc_s, 1);
+                }
                 mma_commit_e(&bars->s_done);
                 mma_commit_e(&bars->s_free[c % NSTAGE]);
                 if constexpr (GATED) {
@@ -1014,7 +1057,14 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                     }
                 }
                 // O^T += u_hi^T P_hi^T + u_hi^T P_lo^T + u_lo^T P_hi^T (N = 64 each)
-                if (write_o) {
+                if constexpr (GATED) {
+                    if (write_o) {
+#pragma unroll 1
+                        for (int pr = 0; pr < 3; pr = opaque(pr + 1))
+                            run_ts_halves(tmem + ob, tmem + TM_X + (pr == 2 ? 16 : 0), smem_desc(pb + (pr == 1 ? 8192 : 0), 16, 1024), 2,
+                                          idesc64, 1);
+                    }
+                } else if (write_o) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_bf16_ts_e(tmem + ob, tmem + TM_X + ks * 8, smem_desc(pb + ks * 32, 16, 1024), idesc64, 1);

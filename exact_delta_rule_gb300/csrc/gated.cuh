@@ -64,9 +64,10 @@ struct GatedDecodeArgs {
 //   w [B H][nc]: T'' = (I + diag(alpha) L)^{-1} diag(alpha) of every chunk (the tensor-core path: the
 //     inverse without diag(alpha)), 64 x 64 x 4 bytes;
 //   p [B H][nc]: P likewise (CUDA-core path only);
-//   sdot [B H][nc][4]: partial sums of <S, dS'> of every chunk;
+//   sdot [B H][nc][4]: partial sums of <S, dS'> of every chunk (CUDA-core path only);
 //   part [2][B T H][d_k] fp32: dq and dk of every value head (where key heads are shared);
-//   tok: per-token scratch of the tensor-core path: dY [B T H][128] as bf16 hi, then lo (gated_bwd_tc.cu).
+//   tok [B H][nc]: dY hi, dO and dY lo of every chunk as operand tiles, 48 KB (tensor-core path,
+//     gated_bwd_tc.cu).
 struct GatedWs {
     size_t states, dse, w, p, sdot, part, tok, bytes;
 };
@@ -86,9 +87,9 @@ inline GatedWs gated_ws(int B, int T, int Hk, int H, int dk, int dv, efla_dtype 
     w.dse = take(units * nc * mat);
     w.w = take(units * nc * 64 * 64 * 4);
     w.p = take(tc ? 0 : units * nc * 64 * 64 * 4);
-    w.sdot = take(units * nc * 4 * sizeof(float));
+    w.sdot = take(tc ? 0 : units * nc * 4 * sizeof(float));
     w.part = take(Hk != H ? 2 * tok * dk * sizeof(float) : 0);
-    w.tok = take(tc ? tok * 128 * (2 + 2) : 0);
+    w.tok = take(tc ? units * nc * 49152 : 0);
     w.bytes = T > 0 && units > 0 ? at : 0;
     return w;
 }
@@ -114,51 +115,88 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// G_t of a chunk's 64 tokens in units of log2, as the unevaluated sum hi + lo of two floats, and
-// the two factors every token needs, by one warp (64 values of g, 0 past the chunk's end; lane l
-// holds tokens 2 l and 2 l + 1; token t's two floats go to gh[t stride] and gl[t stride]).  The running sum is taken in 64 bits: a difference G_t - G_s of
-// two far sums is then exact to about 2^-46 of the sums, where a 32-bit sum of 64 gates of size 2
-// would already be off by 2^-17 in the exponent, more than every other rounding of the chunk.
-// A gate of -inf (or below -700) is taken as -700: e^-700 is 0 in fp32, and sums stay finite.
-__device__ __forceinline__ void chunk_decay(float g0, float g1, int lane, float *gh, float *gl, int stride,
+// An unevaluated sum hi + lo of two floats, and the sum of two of them to about 2^-46 (the error of
+// the floats' own sum, recovered exactly).
+struct Sum2 {
+    float h, l;
+};
+__device__ __forceinline__ Sum2 add2(Sum2 a, Sum2 b) {
+    const float s = a.h + b.h, t = s - a.h, e = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+__device__ __forceinline__ float diff2(Sum2 a, Sum2 b) { return (a.h - b.h) + (a.l - b.l); }
+// A gate in units of log2.  A gate of -inf (or below -700) is taken as -700: e^-700 is 0 in fp32, and
+// sums stay finite.
+__device__ __forceinline__ Sum2 gate2(float g) {
+    constexpr float L_HI = 1.44269504f, L_LO = 1.92596299e-8f;  // log2(e) = L_HI + L_LO
+    g = g < -700.f ? -700.f : g;
+    const float h = g * L_HI;
+    return {h, fmaf(g, L_HI, -h) + g * L_LO};
+}
+__device__ __forceinline__ Sum2 shfl_up2(Sum2 x, int off) {
+    return {__shfl_up_sync(0xffffffffu, x.h, off), __shfl_up_sync(0xffffffffu, x.l, off)};
+}
+__device__ __forceinline__ Sum2 shfl2(Sum2 x, int lane) {
+    return {__shfl_sync(0xffffffffu, x.h, lane), __shfl_sync(0xffffffffu, x.l, lane)};
+}
+
+// The decays of a chunk's 64 tokens from its gates (0 past the chunk's end), by one warp: lane l holds
+// tokens 2 l and 2 l + 1.  Writes, token t at [t stride], the two floats of G_t (log2) to gh and gl, and
+// to dn e^{G_q - G_t} with q the first token of t's quarter of 16; to eg[t] e^{G_t} and to ec[t]
+// e^{G_C - G_t}.  Returns (in every lane) whether every dn is below 2^100: then Gamma_ts = e^{G_t - G_q}
+// dn_s for s in quarter q and t >= s costs a product an entry; otherwise pair_decay takes the
+// difference of the sums, an exponential an entry.
+// The running sum is kept to about 2^-46: a plain 32-bit sum of 64 gates of size 2 is off by 2^-17 in
+// the exponent, more than every other rounding of the chunk.
+__device__ __forceinline__ bool chunk_decay(float g0, float g1, int lane, float *gh, float *gl, float *dn, int stride,
                                             float *eg, float *ec) {
-    constexpr double LOG2E = 1.4426950408889634;
-    const double a = (double)(g0 < -700.f ? -700.f : g0) * LOG2E, b = (double)(g1 < -700.f ? -700.f : g1) * LOG2E;
-    double s = a + b;
+    const Sum2 a = gate2(g0), b = gate2(g1);
+    Sum2 G1 = add2(a, b);
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += x;
+        const Sum2 x = shfl_up2(G1, off), y = add2(G1, x);
+        if (lane >= off) G1 = y;
     }
-    const double last = __shfl_sync(0xffffffffu, s, 31), G1 = s, G0 = s - b;
-    const float h0 = (float)G0, h1 = (float)G1;
-    gh[2 * lane * stride] = h0;
-    gh[(2 * lane + 1) * stride] = h1;
-    gl[2 * lane * stride] = (float)(G0 - (double)h0);
-    gl[(2 * lane + 1) * stride] = (float)(G1 - (double)h1);
-    eg[2 * lane] = ex2(h0);  // (rounding the exponent x costs 2^-25 |x| of a factor 2^x)
-    eg[2 * lane + 1] = ex2(h1);
-    ec[2 * lane] = ex2((float)(last - G0));
-    ec[2 * lane + 1] = ex2((float)(last - G1));
+    Sum2 G0 = shfl_up2(G1, 1);  // G_{2 l - 1}
+    if (lane == 0) G0 = {0.f, 0.f};
+    G0 = add2(G0, a);
+    const Sum2 last = shfl2(G1, 31), q = shfl2(G0, lane & 24);
+    const float d0 = ex2(diff2(q, G0)), d1 = ex2(diff2(q, G1));
+    const int t = 2 * lane;
+    gh[t * stride] = G0.h;
+    gh[(t + 1) * stride] = G1.h;
+    gl[t * stride] = G0.l;
+    gl[(t + 1) * stride] = G1.l;
+    dn[t * stride] = d0;
+    dn[(t + 1) * stride] = d1;
+    eg[t] = ex2(G0.h + G0.l);
+    eg[t + 1] = ex2(G1.h + G1.l);
+    ec[t] = ex2(diff2(last, G0));
+    ec[t + 1] = ex2(diff2(last, G1));
+    return __all_sync(0xffffffffu, d0 < 0x1p100f && d1 < 0x1p100f);
 }
+
 // The same for a block of 16 tokens, one per lane (lanes 16-31 take part with g = 0 and write nothing).
 __device__ __forceinline__ void block_decay16(float g, int lane, float *gh, float *gl, float *eg, float *ec) {
-    const double a = (double)(g < -700.f ? -700.f : g) * 1.4426950408889634;
-    double s = a;
+    Sum2 G = gate2(g);
 #pragma unroll
     for (int off = 1; off < 16; off <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += x;
+        const Sum2 x = shfl_up2(G, off), y = add2(G, x);
+        if (lane >= off) G = y;
     }
-    const double last = __shfl_sync(0xffffffffu, s, 15);
-    const float h = (float)s;
+    const Sum2 last = shfl2(G, 15);
     if (lane < 16) {
-        gh[lane] = h;
-        gl[lane] = (float)(s - (double)h);
-        eg[lane] = ex2(h);
-        ec[lane] = ex2((float)(last - s));
+        gh[lane] = G.h;
+        gl[lane] = G.l;
+        eg[lane] = ex2(G.h + G.l);
+        ec[lane] = ex2(diff2(last, G));
     }
 }
+// beta as the tensor-core path takes it: magnitudes below 2^-90 become 2^-90.  Its backward gets
+// d alpha_t as (dY U^T)_tt / alpha_t; with U_t proportional to alpha_t that is exact for any alpha but 0,
+// and a step of 2^-90 changes no output.
+__device__ __forceinline__ float live_beta(float b) { return fabsf(b) < 0x1p-90f ? copysignf(0x1p-90f, b) : b; }
 // Gamma_ts from the two sums.
 __device__ __forceinline__ float pair_decay(float ht, float lt, float hs, float ls) { return ex2((ht - hs) + (lt - ls)); }
 

@@ -365,6 +365,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
         : "r"(taddr));
 }
 
+// 32 lanes x 16 consecutive columns store from registers.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&r)[16]) {
+    tmem_st16u(taddr, reinterpret_cast<const uint32_t(&)[16]>(r));
+}
+
 // 32 lanes x 8 consecutive columns store of raw 32-bit words.
 __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&u)[8]) {
     asm volatile(

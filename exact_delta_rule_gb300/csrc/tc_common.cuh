@@ -123,6 +123,65 @@ __device__ __forceinline__ void put_col_split_rows(__nv_bfloat16 *hi, __nv_bfloa
     }
 }
 
+// Four K = 16 steps of one product, issued together: one election and one block of code for the four.
+// b and a (descriptors) advance by their steps in 16-byte units; the first step accumulates if `acc`.
+// The kernels' roles run concurrently out of one instruction cache, so loops over these stay rolled; a
+// loop over single steps took 118 cycles an MMA of 50 (election and descriptor arithmetic).
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint64_t b, uint32_t bs,
+                                        uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b32 r;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, t;\n\t}" ::"r"(d),
+        "r"(a0), "r"(a1), "r"(a2), "r"(a3), "l"(b), "l"(b + bs), "l"(b + 2 * bs), "l"(b + 3 * bs), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint32_t as, uint64_t b, uint32_t bs, uint32_t idesc,
+                                        uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b32 r;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, t;\n\t}" ::"r"(d),
+        "l"(a), "l"(a + as), "l"(a + 2 * as), "l"(a + 3 * as), "l"(b), "l"(b + bs), "l"(b + 2 * bs), "l"(b + 3 * bs), "r"(idesc),
+        "r"(acc)
+        : "memory");
+}
+// D (+)= (hi + lo of A in TMEM, 64 columns each from a) B over K = 128; B K-major, column blocks `cb` bytes apart
+__device__ __forceinline__ void run_ts_kmajor(uint32_t d, uint32_t a, uint64_t b, uint32_t cb, uint32_t idesc, uint32_t acc) {
+#pragma unroll 1
+    for (int i = 0; i < 4; i = opaque(i + 1)) {
+        const uint32_t x = a + i * 32;
+        mma4_ts(d, x, x + 8, x + 16, x + 24, b + (i & 1) * (cb >> 4), 2, idesc, acc | (uint32_t)i);
+    }
+}
+// ... over K = 64: four steps of 8 TMEM columns
+__device__ __forceinline__ void run_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t b_step, uint32_t idesc, uint32_t acc) {
+    mma4_ts(d, a, a + 8, a + 16, a + 24, b, b_step, idesc, acc);
+}
+// ... with an operand of 64 tokens that was split in place, half by half: tokens 0-31 as hi in columns
+// 0-15 and lo in 16-31, tokens 32-63 in columns 32-63 likewise (split_half).  a: its hi or lo.
+__device__ __forceinline__ void run_ts_halves(uint32_t d, uint32_t a, uint64_t b, uint32_t b_step, uint32_t idesc, uint32_t acc) {
+    mma4_ts(d, a, a + 8, a + 32, a + 40, b, b_step, idesc, acc);
+}
+// Gram product of a K-major tile with its first rows, K = 128
+__device__ __forceinline__ void run_gram(uint32_t d, uint64_t kq, uint32_t cb, uint32_t idesc) {
+#pragma unroll 1
+    for (int i = 0; i < 2; i = opaque(i + 1)) mma4_ss(d, kq + i * (cb >> 4), 2, kq + i * (cb >> 4), 2, idesc, (uint32_t)i);
+}
+__device__ __forceinline__ void split_half(uint32_t base, int hf, const float (&x)[32]) {
+    uint32_t hi[16], lo[16];
+    split_pack_rn<16>(x, hi, lo);
+    tmem_st16u(base + 32 * hf, hi);
+    tmem_st16u(base + 32 * hf + 16, lo);
+}
 // Gated kernels: rows 32 g0 .. 32 g1 - 1 of the state (column j = this thread's TMEM lane, TMEM address
 // ts of its transpose) times the chunk's decay el.  Out of line for the instruction cache.
 __device__ __noinline__ void decay_state_rows(uint32_t ts, int g0, int g1, float el) {
