@@ -195,6 +195,9 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
             return row < C && t < p.T ? p.beta[((size_t)b * p.T + t) * p.H + h] : 0.f;
         };
         float g0 = load_g(0, 0), g1 = load_g(0, 1), bt = load_beta(0);
+        for (int e = row; e < 2 * 1024; e += 128)  // both P buffers
+            *reinterpret_cast<uint4 *>(sm + OFF_TPP + (e >> 10) * TPP_BYTES + 16384 + (e & 1023) * 16) = make_uint4(0, 0, 0, 0);
+        named_bar(BAR_PREP, 128);
         bool ok = true;
         for (int it = 0; it < nchunks; ++it) {
             const int buf = it & 1, st = it % NSTAGE;
@@ -231,8 +234,9 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
                 const float4 gt = reinterpret_cast<const float4 *>(gsum)[t];
                 const bool fast = gsum[3] != 0.f;
                 uint8_t *phi = sm + OFF_TPP + buf * TPP_BYTES + 16384;
-#pragma unroll 1
-                for (int q = 0; q < 4; q = opaque(q + 1)) {
+                // (16-column blocks above a warp's rows stay the zeros they were set to at the start)
+#pragma unroll 2
+                for (int q = 0; q < (row >= 96 ? 4 : 2); ++q) {
                     float x[16];
                     tmem_ld16(lane_base + TM_G + 16 * q, x);
                     const float *gs = gsum + 64 * q;
@@ -292,11 +296,21 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
                 tc_fence_before();
                 mbar_arrive(&bars->do_ready);
             }
-            // dS' times e^{G_C} in TM_S once the state warps have read it
+            // dS' times e^{G_C} in TM_S, once the state warps have read it
             ok = ok && wait_bar_warp(&bars->sa_ready, it & 1, abort_flag, wait_ns);
             if (ok) {
                 tc_fence_after();
-                decay_state_rows(lane_base + TM_S, 0, 4, eg[C - 1]);
+                const float el = eg[C - 1];
+#pragma unroll 1
+                for (int g = 0; g < 4; g = opaque(g + 1)) {
+                    float sv[32];
+                    tmem_ld32(lane_base + TM_S + g * 32, sv);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sv[i] *= el;
+                    tmem_st32(lane_base + TM_S + g * 32, sv);
+                }
+                tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&bars->sc_ready);
             }
@@ -336,11 +350,15 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
                 ok = false;
                 break;
             }
-#pragma unroll 1
-            for (int q = 0; q < 4; q = opaque(q + 1)) {
-                float x[16];
-                tmem_ld16(lane_base + TM_G2 + 16 * q, x);
-                tmem_ld_wait();
+            float y[64];
+            tmem_ld32(lane_base + TM_G2, *reinterpret_cast<float(*)[32]>(y));
+            tmem_ld32(lane_base + TM_G2 + 32, *reinterpret_cast<float(*)[32]>(y + 32));
+            tmem_ld_wait();
+            tc_fence_before();
+            mbar_arrive(&bars->y_read);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float *x = y + 16 * q;
                 uint32_t hi[8], lo[8];
                 split_pack_rn<8>(x, hi, lo);
 #pragma unroll
@@ -355,8 +373,6 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
                     stage_pair(d, j, t, *reinterpret_cast<const uint32_t *>(&v));
                 }
             }
-            tc_fence_before();
-            mbar_arrive(&bars->y_read);
             fence_proxy_async_smem();
             named_bar(BAR_OUT, 128);
             if (j == 0) {
@@ -535,7 +551,6 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
                 mma4_ss(tmem + TM_G2, ad, 128, bp + (8192 >> 4), 128, idesc, 1);
                 mma_commit_e(&bars->x_done);
             }
-            issue_grams(it + 1, false);
             if (!(ok = wait_bar_warp(&bars->r_ready, it & 1, abort_flag, wait_ns))) break;
             tc_fence_after();
             {  // dY^T = G^T T (T read as an MN-major operand, K = s), over dO^T P, which the state warps have read
@@ -556,6 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
 #pragma unroll 1
             for (int part = 0; part < 2; part = opaque(part + 1))
                 run_ts(tmem + TM_S, tmem + TM_DO + part * 32, smem_desc(kq_s + 8192, 16384, 1024), 128, idesc_s, 1);
+            issue_grams(it + 1, false);  // (the prep has read this chunk's by now)
             if (!(ok = wait_bar_warp(&bars->u_ready, it & 1, abort_flag, wait_ns))) break;
             tc_fence_after();
             {  // dS^T += (-diag(alpha e^G) dY)^T K (the chain)
@@ -914,7 +930,7 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
         // sums by warp: part[0]: a (lanes 0-15, a token each) and w (lanes 16-31); part[1]: M's columns (lanes 0-15)
         float *part = reinterpret_cast<float *>(sm + OFF_PART);
         float *rsum = part + 2 * 16 * 32;  // [4 quarters][128]: row sums of M within a quarter of columns
-        float *tok = rsum + 512;           // [64] each: a, w, the rows' sums over the quarters before quarter 1, 2, 3, dalpha
+        float *tok = rsum + 512;           // [64] each: a, w, the rows' sums over the quarters before quarter 1, 2, 3, dY . U
         // TMEM: this thread reads and writes lane `ln`, the columns of token quarter `qt`
         const int qt = warp >> 2, ln = (warp & 3) * 32 + lane, col0 = 16 * qt;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -963,6 +979,9 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
+        auto copy4 = [&](float *dst, const float *src, bool there) {  // (zero if not there)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+        };
         // gates and step sizes on their way into R.gate and R.beta (threads 0-63 and 64-127, tokens past the end as
         // zeros), an item ahead
         auto copy_gates = [&](const Items &X) {
@@ -970,9 +989,7 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
                 const int t = tid & (C - 1);
                 const bool there = X.c * C + t < p.T;
                 const float *src = (tid < C ? p.gate : p.beta) + X.row0(p.T, p.H) + (there ? (size_t)t * p.H : 0);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(tid < C ? &R.gate[t] : &R.beta[t])), "l"(src),
-                             "r"(there ? 4 : 0)
-                             : "memory");
+                copy4(tid < C ? &R.gate[t] : &R.beta[t], src, there);
             }
         };
         Items I(blockIdx.x, grid, nc, p.H);
@@ -1100,12 +1117,11 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
                     float m[16];
                     tmem_ld16(lane_base + TM_E + col0, m);
                     tmem_ld_wait();
-                    if (gate_thr) {  // dalpha_t = (dY U^T)_tt / alpha_t
-                        float d = 0.f;
+                    // dalpha_t = (dY U^T)_tt / alpha_t: the diagonal by predicated stores (a branch that few threads take
+                    // costs more than its instructions: its code is cold each time)
 #pragma unroll
-                        for (int s = 0; s < 16; ++s) d = (s == (ln & 15)) ? x[s] : d;
-                        tok[5 * C + tr] = ln < valid ? __fdiv_rn(d, R.al[tr]) : 0.f;
-                    }
+                    for (int s = 0; s < 16; ++s)
+                        if (col0 + s == ln) tok[5 * C + ln] = x[s];
                     // dL = -diag(alpha) (dY U^T): M_ts = dP_ts P_ts and dL_ts L_ts (s < t; m is 0 elsewhere); exclusive prefix
                     // sums along the row, from this quarter's first column
                     const float fac = ln < C ? -R.al[tr] : 1.f;
@@ -1154,7 +1170,7 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
             {  // E = dL' + dL'^T + diag(2 dalpha dalpha/dlambda)
                 const int t = tid >> 3, s0 = (tid & 7) * 8;
                 float dg = 0.f;
-                if (!EULER) dg = 2.f * tok[5 * C + t] * R.dadl[t];
+                if (!EULER) dg = 2.f * __fdividef(tok[5 * C + t], R.al[t]) * R.dadl[t];
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -1197,7 +1213,8 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
 #pragma unroll
                 for (int off = 1; off < 8; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
                 if (k == 0 && t < valid) {
-                    p.dbeta[row0 + (size_t)t * p.H] = EULER ? tok[5 * C + t] : tok[5 * C + t] * R.g[t].w;
+                    const float dal = __fdividef(tok[5 * C + t], R.al[t]);
+                    p.dbeta[row0 + (size_t)t * p.H] = EULER ? dal : dal * R.g[t].w;
                     p.dg[row0 + (size_t)t * p.H] = s;
                 }
             }
