@@ -54,7 +54,7 @@ def _need(name: str, t: torch.Tensor, shape, dtype, like: torch.Tensor):
     """`t` is a contiguous tensor of this shape and dtype on `like`'s device."""
     if t.dtype is not dtype or t.shape != shape:
         _bad(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         _bad(f"{name} is on {t.device}, the first argument on {like.device}")
     if not t.is_contiguous():
         _bad(f"{name} must be contiguous")
@@ -75,12 +75,14 @@ def _first(name: str, t: torch.Tensor, dims: int) -> int:
 def _on_device(t: torch.Tensor):
     if not t.is_cuda:
         _bad("the tensors must be CUDA tensors")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         _bad(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
-def _stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _stream(stream, like: torch.Tensor) -> int:
+    """The handle of `stream`, or of the current one (of `like`'s device, which is current) without the
+    Stream object that torch.cuda.current_stream() makes: 0.1 us in place of 2.9."""
+    return torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -104,16 +106,17 @@ def _heads(q, k, v, g, beta, lead: int):
     code = _first("q", q, lead + 2)
     if v.dim() != lead + 2:
         _bad(f"v must be {lead + 2}-D, got {list(v.shape)}")
-    at = tuple(q.shape[:lead])
-    Hk, dk = q.shape[lead:]
+    qs = q.shape
+    *at, Hk, dk = qs
     H, dv = v.shape[lead:]
     if Hk < 1 or H % Hk:
         _bad(f"v's {H} heads must be a multiple of q's and k's {Hk}")
-    _need("q", q, q.shape, q.dtype, q)
-    _need("k", k, q.shape, q.dtype, q)
+    per_head = (*at, H)
+    _need("q", q, qs, q.dtype, q)
+    _need("k", k, qs, q.dtype, q)
     _need("v", v, (*at, H, dv), q.dtype, q)
-    _need("g", g, (*at, H), torch.float32, q)
-    _need("beta", beta, (*at, H), torch.float32, q)
+    _need("g", g, per_head, torch.float32, q)
+    _need("beta", beta, per_head, torch.float32, q)
     return at, Hk, H, dk, dv, code
 
 
@@ -163,7 +166,7 @@ def gated_fwd_chunked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torc
         S_T = _given("S_T", S_T, (N, H, dk, dv), torch.float32, q, stream)
     _check(L.efla_gated_fwd_chunked(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
                                     _ptr(cu_seqlens), o.data_ptr(), _ptr(S_T), B, T, Hk, H, dk, dv, N, code, _DT[od],
-                                    rule, _stream(stream)))
+                                    rule, _stream(stream, q)))
     return o, S_T
 
 
@@ -204,7 +207,7 @@ def gated_fwd_chunked_train(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     ws = _workspace(workspace, need, q, stream)
     _check(L.efla_gated_fwd_chunked_train(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                           _ptr(S0), o.data_ptr(), S_T.data_ptr(), B, T, Hk, H, dk, dv, code, rule,
-                                          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+                                          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream, q)))
     return o, S_T, ws
 
 
@@ -235,7 +238,7 @@ def gated_bwd_chunked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torc
     _check(L.efla_gated_bwd_chunked(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
                                     dO.data_ptr(), _ptr(dS_T), *(_ptr(t) for t in out.values()), B, T, Hk, H, dk, dv,
                                     code, rule, int(saved), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                    _stream(stream)))
+                                    _stream(stream, q)))
     return out
 
 
@@ -247,7 +250,7 @@ def _decode(fn, lead, q, k, v, g, beta, S, o, o_dtype, stream, update):
     _on_device(q)
     o = _given("o", o, v.shape, od, q, stream)
     _check(getattr(_lib(), fn)(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), S.data_ptr(),
-                               o.data_ptr(), *at, Hk, H, dk, dv, code, _DT[od], rule, _stream(stream)))
+                               o.data_ptr(), *at, Hk, H, dk, dv, code, _DT[od], rule, _stream(stream, q)))
     return o
 
 
@@ -298,7 +301,7 @@ def gated_prep(q: torch.Tensor, k: torch.Tensor, a: torch.Tensor, b: torch.Tenso
            "g": _empty(a.shape, torch.float32, q, stream), "beta": _empty(a.shape, torch.float32, q, stream)}
     _check(_lib().efla_gated_prep(q.data_ptr(), k.data_ptr(), a.data_ptr(), b.data_ptr(), A_log.data_ptr(),
                                   dt_bias.data_ptr(), *(t.data_ptr() for t in out.values()), tokens, q.shape[-2], H,
-                                  q.shape[-1], code, scale, eps, _stream(stream)))
+                                  q.shape[-1], code, scale, eps, _stream(stream, q)))
     return out
 
 
@@ -323,7 +326,7 @@ def gated_prep_bwd(q: torch.Tensor, k: torch.Tensor, a: torch.Tensor, b: torch.T
     _check(L.efla_gated_prep_bwd(q.data_ptr(), k.data_ptr(), a.data_ptr(), b.data_ptr(), A_log.data_ptr(),
                                  dt_bias.data_ptr(), dq.data_ptr(), dk.data_ptr(), dg.data_ptr(), dbeta.data_ptr(),
                                  *(t.data_ptr() for t in out.values()), tokens, q.shape[-2], H, q.shape[-1], code,
-                                 scale, eps, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+                                 scale, eps, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream, q)))
     return out
 
 
@@ -350,7 +353,7 @@ def norm_gate(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, *, eps: float =
     _on_device(o)
     y = _given("y", y, o.shape, o.dtype, o, stream)
     _check(_lib().efla_norm_gate(o.data_ptr(), z.data_ptr(), w.data_ptr(), y.data_ptr(), rows, d, code, eps,
-                                 _stream(stream)))
+                                 _stream(stream, o)))
     return y
 
 
@@ -368,5 +371,5 @@ def norm_gate_bwd(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, dy: torch.T
            "dw": _empty((d,), torch.float32, o, stream)}
     _check(L.efla_norm_gate_bwd(o.data_ptr(), z.data_ptr(), w.data_ptr(), dy.data_ptr(),
                                 *(t.data_ptr() for t in out.values()), rows, d, code, eps, ws.data_ptr(),
-                                ws.numel() * ws.element_size(), _stream(stream)))
+                                ws.numel() * ws.element_size(), _stream(stream, o)))
     return out
