@@ -42,7 +42,7 @@ struct NormGateArgs {
     float eps;
     cudaStream_t stream;
 };
-constexpr int NORM_GATE_PARTS = 152 * 4;
+constexpr int NORM_GATE_PARTS = 152 * 2;  // the CTAs that are resident at once (100 registers a thread)
 
 cudaError_t launch_mixer_prep(const MixerPrepArgs &p, bool bwd);
 cudaError_t launch_norm_gate(const NormGateArgs &p, bool bwd);
