@@ -560,11 +560,11 @@ PFN_cuTensorMapEncodeTiled_v12000 bt_encode_fn() {
 
 // [B, T, H, 128] bf16: box of 64 features x 1 head x 64 tokens x 1, 128-byte swizzle (the
 // backward kernels' operand tiles).
-bool bwd_row_map(CUtensorMap *m, const void *ptr, int B, int T, int H) {
+bool bwd_row_map(CUtensorMap *m, const void *ptr, int B, int T, int H, int d) {
     auto fn = bt_encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
-    cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2, (cuuint64_t)T * H * D * 2};
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2, (cuuint64_t)T * H * d * 2};
     cuuint32_t box[4] = {64, 1, (cuuint32_t)C, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, es,

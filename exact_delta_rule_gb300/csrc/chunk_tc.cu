@@ -58,7 +58,8 @@
 //   (the state warpgroup waits there anyway); u is split twice, c_t u_t for S += K^T diag(c) u (first:
 //   the chain) and u_t for O += P u (while the state is updated).
 // Operands are split with rounding to nearest, so that S_T is good to about 2^-18 (its truncated
-// split leaves 2^-15); key heads are shared by H / Hk value heads.
+// split leaves 2^-15); key heads are shared by H / Hk value heads.  Head sizes below 128 run as 128 with
+// zeros, which TMA fills in beyond a tensor's features.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -155,6 +156,7 @@ struct TcParams {
     int debug_stall;             // test hook: the MMA thread first waits on a barrier nothing completes
     const float *g;              // gated: [B, T, H] log decays
     int rep;                     // gated: value heads a key head
+    int dk, dv;                  // gated: 128 or less; the features up to 128 are zeros (TMA fills them in)
 };
 
 struct Bars {
@@ -233,6 +235,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
 
     const int tid = threadIdx.x, warp = tid >> 5;
     const uint64_t wait_ns = p.wait_ns;
+    const int dk = GATED ? p.dk : D, dv = GATED ? p.dv : D;
     long b, bos, eos;
     int h;
     int mode = 0;                    // 0: forward; 1: map from S = I, v = 0; 2: map from S = 0
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             bos = 0;
             eos = p.T;
         }
-        const size_t sbase = ((size_t)n * p.H + h) * D * D;
+        const size_t sbase = ((size_t)n * p.H + h) * dk * dv;
         if (p.S0) s0p = p.S0 + sbase;
         if (p.S_T) stp = p.S_T + sbase;
     }
@@ -300,9 +303,9 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
     const int nchunks = eos > bos ? (int)((eos - bos + C - 1) / C) : 0;
 
     if (nchunks == 0) {  // empty sequence: S_T = S0
-        if (stp && tid < D)
-            for (int i = 0; i < D; ++i)
-                stp[(size_t)i * D + tid] = mode == 1 ? (i == tid ? 1.f : 0.f) : s0p ? s0p[(size_t)i * D + tid] : 0.f;
+        if (stp && tid < dv)
+            for (int i = 0; i < dk; ++i)
+                stp[(size_t)i * dv + tid] = mode == 1 ? (i == tid ? 1.f : 0.f) : s0p ? s0p[(size_t)i * dv + tid] : 0.f;
         return;
     }
 
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             for (int g = 0; g < 4; g = opaque(g + 1)) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    r[i] = mode == 1 ? (g * 32 + i == j ? 1.f : 0.f) : s0p ? s0p[(size_t)(g * 32 + i) * D + j] : 0.f;
+                    r[i] = mode == 1 ? (g * 32 + i == j ? 1.f : 0.f) : s0p && (!GATED || (g * 32 < dk && j < dv)) ? s0p[(size_t)(g * 32 + i) * dv + j] : 0.f;
                 tmem_st32(lane_base + TM_S + g * 32, r);
             }
             tmem_st_wait();
@@ -622,13 +625,13 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             const bool full = p.cu_seqlens == nullptr || vc == C;
             auto store_rows = [&](int t_off, int n) {  // plain stores of staged rows (partial packed chunk)
 #pragma unroll 1
-                for (int t = 0; t < n; t = opaque(t + 1)) {
+                for (int t = 0; t < n && (!GATED || j < dv); t = opaque(t + 1)) {
                     const size_t rw = ((size_t)b * p.T + (size_t)(t0c + t_off + t)) * p.H + h;
                     if (OUT_BF16)
-                        static_cast<__nv_bfloat16 *>(p.o)[rw * D + j] =
+                        static_cast<__nv_bfloat16 *>(p.o)[rw * dv + j] =
                             reinterpret_cast<const __nv_bfloat16 *>(slice)[(t_off + t) * 32 + lane];
                     else
-                        static_cast<float *>(p.o)[rw * D + j] = reinterpret_cast<const float *>(slice)[t * 32 + lane];
+                        static_cast<float *>(p.o)[rw * dv + j] = reinterpret_cast<const float *>(slice)[t * 32 + lane];
                 }
             };
             if (OUT_BF16) {
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 if (full) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
+                    if (lane == 0 && (!GATED || warp * 32 < dv)) {
                         tma_store_4d(&p.map_o, slice, warp * 32, h, (int)t0c, (int)b);
                         bulk_commit();
                     }
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                     if (full) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (lane == 0 && (!GATED || warp * 32 < dv)) {
                             tma_store_4d(&p.map_o, slice, warp * 32, h, (int)(t0c + t_off), (int)b);
                             bulk_commit();
                         }
@@ -863,9 +866,10 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 float s32[32];
                 tmem_ld32(lane_base + TM_S + g * 32, s32);
                 tmem_ld_wait();
-                float *dst = stp + (size_t)(g * 32) * D + j;
+                if (GATED && (g * 32 >= dk || j >= dv)) continue;
+                float *dst = stp + (size_t)(g * 32) * dv + j;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) dst[(size_t)i * D] = s32[i];
+                for (int i = 0; i < 32; ++i) dst[(size_t)i * dv] = s32[i];
             }
         }
         if (lane == 0) bulk_wait0();  // TMA stores have completed before the CTA leaves
@@ -1109,14 +1113,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// 4-D map over a [B, T, H, 128] tensor: box of `box_x` features x 1 head x 64 tokens.
+// 4-D map over a [B, T, H, d] tensor: box of `box_x` features x 1 head x 64 tokens; what a box holds
+// beyond d features reads as zero.
 bool make_map(CUtensorMap *m, const void *ptr, int B, int T, int H, bool f32, int box_x, bool swizzle,
-              int box_t = C) {
+              int box_t = C, int d = D) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t es_b = f32 ? 4 : 2;
-    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
-    cuuint64_t strides[3] = {(cuuint64_t)D * es_b, (cuuint64_t)H * D * es_b, (cuuint64_t)T * H * D * es_b};
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    cuuint64_t strides[3] = {(cuuint64_t)d * es_b, (cuuint64_t)H * d * es_b, (cuuint64_t)T * H * d * es_b};
     cuuint32_t box[4] = {(cuuint32_t)box_x, 1, (cuuint32_t)box_t, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr),
@@ -1189,10 +1194,10 @@ cudaError_t launch_gated_chunk_tc(const GatedFwdArgs &a, const char **why) {
     memset(&p, 0, sizeof p);
     const bool o_bf16 = a.o_dtype == EFLA_BF16;
     if ((long long)a.B * a.T > 0) {
-        if (!make_map(&p.map_q, a.q, a.B, a.T, a.Hk, false, 64, true) ||
-            !make_map(&p.map_k, a.k, a.B, a.T, a.Hk, false, 64, true) ||
-            !make_map(&p.map_v, a.v, a.B, a.T, a.H, false, 64, true) ||
-            (a.o && !make_map(&p.map_o, a.o, a.B, a.T, a.H, !o_bf16, 32, false, o_bf16 ? 64 : 32))) {
+        if (!make_map(&p.map_q, a.q, a.B, a.T, a.Hk, false, 64, true, C, a.dk) ||
+            !make_map(&p.map_k, a.k, a.B, a.T, a.Hk, false, 64, true, C, a.dk) ||
+            !make_map(&p.map_v, a.v, a.B, a.T, a.H, false, 64, true, C, a.dv) ||
+            (a.o && !make_map(&p.map_o, a.o, a.B, a.T, a.H, !o_bf16, 32, false, o_bf16 ? 64 : 32, a.dv))) {
             *why = "cuTensorMapEncodeTiled failed";
             return cudaErrorInvalidValue;
         }
@@ -1210,6 +1215,8 @@ cudaError_t launch_gated_chunk_tc(const GatedFwdArgs &a, const char **why) {
     p.euler = a.euler;
     p.g = a.g;
     p.rep = a.H / a.Hk;
+    p.dk = a.dk;
+    p.dv = a.dv;
     if (a.ws) {
         const GatedWs w = gated_ws(a.B, a.T, a.Hk, a.H, a.dk, a.dv, a.in_dtype);
         p.states = reinterpret_cast<float *>(static_cast<char *>(a.ws) + w.states);

@@ -60,7 +60,7 @@ struct GatedDecodeArgs {
 
 // Workspace of the backward (bytes from its base, every region 256-byte aligned).  nc = ceil(T / 64).
 //   states and dse [B H][nc]: the state at the start of every chunk and the gradient of the state at
-//     its end, d_k x d_v x 4 bytes each;
+//     its end, d_k x d_v x 4 bytes each (tensor cores: 64 KB tiles whatever the head sizes);
 //   w [B H][nc]: T'' = (I + diag(alpha) L)^{-1} diag(alpha) of every chunk (the tensor-core path: the
 //     inverse without diag(alpha)), 64 x 64 x 4 bytes;
 //   p [B H][nc]: P likewise (CUDA-core path only);
@@ -71,11 +71,16 @@ struct GatedDecodeArgs {
 struct GatedWs {
     size_t states, dse, w, p, sdot, part, tok, bytes;
 };
-inline bool gated_tc(efla_dtype in_dtype, int dk, int dv) { return in_dtype == EFLA_BF16 && dk == 128 && dv == 128; }
+// Which kernels take a forward or backward: bf16 inputs the tensor cores, at every size (features up to
+// 128 are zeros that TMA fills in).  Even where that is most of the work they are ahead, forward and
+// forward with backward in us, tensor cores / CUDA cores:
+//   d_k = d_v = 32, 2 heads of 32 tokens  11 / 13, 33 / 45;   8 x 2048 tokens of 16 heads  160 / 428, 609 / 1526
+//   d_k = d_v = 64                        11 / 17, 34 / 73;                                161 / 1110, 612 / 3201
+inline bool gated_tc(efla_dtype in_dtype) { return in_dtype == EFLA_BF16; }
 inline GatedWs gated_ws(int B, int T, int Hk, int H, int dk, int dv, efla_dtype in_dtype) {
-    const size_t units = (size_t)B * H, nc = ((size_t)T + 63) / 64, mat = (size_t)dk * dv * 4;
-    const size_t tok = (size_t)B * T * H;
-    const bool tc = gated_tc(in_dtype, dk, dv);
+    const size_t units = (size_t)B * H, nc = ((size_t)T + 63) / 64, tok = (size_t)B * T * H;
+    const bool tc = gated_tc(in_dtype);
+    const size_t mat = tc ? 65536 : (size_t)dk * dv * 4;
     GatedWs w;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -94,10 +99,10 @@ inline GatedWs gated_ws(int B, int T, int Hk, int H, int dk, int dv, efla_dtype 
     return w;
 }
 
-// CUDA cores, every supported shape (gated_simt.cu).
+// CUDA cores, fp32 inputs (gated_simt.cu); the backward of T = 0 whatever the type.
 cudaError_t launch_gated_chunk_simt(const GatedFwdArgs &a);
 cudaError_t launch_gated_bwd_simt(const GatedBwdArgs &a);
-// Tensor cores: bf16, d_k = d_v = 128, gated_tc() (chunk_tc.cu).
+// Tensor cores: bf16 inputs (chunk_tc.cu).
 cudaError_t launch_gated_chunk_tc(const GatedFwdArgs &a, const char **why);
 cudaError_t launch_gated_bwd_tc(const GatedBwdArgs &a, const char **why);  // T > 0 (gated_bwd_tc.cu)
 cudaError_t launch_gated_decode_tokens_tc(const GatedDecodeArgs &a, const char **why);  // (decode_tc.cu)

@@ -71,7 +71,7 @@ efla_status need_workspace(const void *ws, size_t have, size_t need) {
 }
 
 cudaError_t run_fwd(const GatedFwdArgs &a, const char **why) {
-    if (gated_tc(a.in_dtype, a.dk, a.dv)) return launch_gated_chunk_tc(a, why);
+    if (gated_tc(a.in_dtype)) return launch_gated_chunk_tc(a, why);
     *why = "gated chunk kernel launch";
     return launch_gated_chunk_simt(a);
 }
@@ -168,7 +168,7 @@ efla_status efla_gated_bwd_chunked(const void *q, const void *k, const void *v, 
     GatedBwdArgs a{q, k, v, g, beta, S0, dO, dS_T, dq, dk, dv, dg, dbeta, dS0, B, T, H_k, H, d_k, d_v, in_dtype,
                    euler, cs, status, workspace};
     const char *why = "gated backward kernel launch";
-    const cudaError_t e = gated_tc(in_dtype, d_k, d_v) && T > 0 ? launch_gated_bwd_tc(a, &why) : launch_gated_bwd_simt(a);
+    const cudaError_t e = gated_tc(in_dtype) && T > 0 ? launch_gated_bwd_tc(a, &why) : launch_gated_bwd_simt(a);
     return launched(e, why);
 }
 
@@ -187,7 +187,7 @@ static efla_status decode(const void *q, const void *k, const void *v, const flo
                       reinterpret_cast<cudaStream_t>(stream), nullptr};
     if (step) return launched(launch_gated_decode_step(a), "gated decode kernel launch");
     const char *why = "gated decode-tokens kernel launch";
-    const cudaError_t e = gated_tc(in_dtype, d_k, d_v) ? launch_gated_decode_tokens_tc(a, &why) : launch_gated_decode_tokens(a);
+    const cudaError_t e = gated_tc(in_dtype) && d_k == 128 && d_v == 128 ? launch_gated_decode_tokens_tc(a, &why) : launch_gated_decode_tokens(a);
     return launched(e, why);
 }
 

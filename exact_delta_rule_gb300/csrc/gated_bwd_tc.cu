@@ -1,5 +1,5 @@
-// Backward of the gated delta rule on the sm_103a tensor cores (tcgen05 + TMEM + TMA): bf16, d_k = d_v =
-// 128, chunks of 64, rows of [B, T], after the training forward (chunk_tc.cu), which leaves in the
+// Backward of the gated delta rule on the sm_103a tensor cores (tcgen05 + TMEM + TMA): bf16, d_k, d_v up to
+// 128 (tiles of 128, the rest zeros that TMA fills in), chunks of 64, rows of [B, T], after the training forward (chunk_tc.cu), which leaves in the
 // workspace, as bf16 hi/lo operand tiles, every chunk's start state (S^T, rows = d_v) and
 // T = (I + diag(alpha) L)^{-1}.  The formulas are in gated_simt.cu; here they are taken through
 //   dY = T^T G,  dR = diag(alpha) dY,  U = T diag(alpha) R,
@@ -47,7 +47,6 @@ using namespace ptx;
 using namespace tc;
 
 constexpr int C = 64;
-constexpr int D = 128;
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 
 // x[0..15] as bf16 hi and lo of row `row`, columns col0 .. col0 + 15 (col0 + 15 < 64) of a swizzled
@@ -89,13 +88,13 @@ constexpr int BAR_PREP = 2, BAR_OUT = 3;
 constexpr int THREADS = 448;
 
 struct Params {
-    CUtensorMap map_q, map_k, map_do, map_dv;  // [B, T, heads, 128] bf16, box 64 x 1 x 64 x 1, 128B swizzle
+    CUtensorMap map_q, map_k, map_do, map_dv;  // [B, T, heads, d] bf16, box 64 x 1 x 64 x 1, 128B swizzle
     const float *gate, *beta, *dST;
     uint8_t *dse, *rod;  // tiles of every chunk: dS'^T; dY hi, dO, dY lo
     const uint8_t *tpp;
     float *dS0;
     int *status;
-    int T, H, rep;
+    int T, H, rep, dk, dv;
     int debug_stall;
     unsigned long long wait_ns;
 };
@@ -139,7 +138,7 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
     const uint64_t wait_ns = p.wait_ns;
     const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / p.rep;
     const int nchunks = (p.T + C - 1) / C;  // >= 1
-    const size_t ubase = (size_t)blockIdx.x * D * D;
+    const size_t ubase = (size_t)blockIdx.x * p.dk * p.dv;
     auto chunk_of = [&](int it) { return nchunks - 1 - it; };  // reverse order
 
     if (tid == 0) {
@@ -376,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
             fence_proxy_async_smem();
             named_bar(BAR_OUT, 128);
             if (j == 0) {
-                for (int cb = 0; cb < 2; ++cb) tma_store_4d(&p.map_dv, stg + cb * 8192, cb * 64, h, c * C, b);
+                for (int cb = 0; cb * 64 < p.dv; ++cb) tma_store_4d(&p.map_dv, stg + cb * 8192, cb * 64, h, c * C, b);
                 bulk_commit();
             }
         }
@@ -390,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
 #pragma unroll 1
             for (int g = 0; g < 4; g = opaque(g + 1)) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = p.dST ? p.dST[ubase + (size_t)(g * 32 + i) * D + j] : 0.f;
+                for (int i = 0; i < 32; ++i) r[i] = p.dST && g * 32 < p.dk && j < p.dv ? p.dST[ubase + (size_t)(g * 32 + i) * p.dv + j] : 0.f;
                 tmem_st32(lane_base + TM_S + g * 32, r);
             }
             tmem_st_wait();
@@ -465,7 +464,8 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
                     tmem_ld32(lane_base + TM_S + g * 32, sv);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) p.dS0[ubase + (size_t)(g * 32 + i) * D + j] = sv[i];
+                    for (int i = 0; i < 32; ++i)
+                        if (g * 32 < p.dk && j < p.dv) p.dS0[ubase + (size_t)(g * 32 + i) * p.dv + j] = sv[i];
                 }
             }
         }
@@ -650,11 +650,11 @@ struct Params {
     CUtensorMap map_q, map_k, map_v, map_dq, map_dk;
     const float *gate, *beta;
     const uint8_t *states, *dse, *rod, *tpp;
-    float *part;                   // [2][B, T, H, 128] in place of dq, dk where key heads are shared
+    float *part;                   // [2][B, T, H, dk] in place of dq, dk where key heads are shared
     float *dbeta, *dg;
     size_t plane;                  // elements of one part
     int *status;
-    int T, H, rep, items;
+    int T, H, rep, items, dk;
     int debug_stall;
     unsigned long long wait_ns;
 };
@@ -885,7 +885,7 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
             if (n >= 0) {
                 if (!wait(&bars->w_out, ph)) break;  // dq and dk staged (or written)
                 if (leader && !p.part) {
-                    for (int cb = 0; cb < 2; ++cb) {  // (rows past the sequence end are clipped)
+                    for (int cb = 0; cb * 64 < p.dk; ++cb) {  // (rows past the sequence end are clipped)
                         tma_store_4d(&p.map_dq, sm + OFF_UT + cb * 8192, cb * 64, ih, ic * C, ib);
                         tma_store_4d(&p.map_dk, sm + OFF_UT + 16384 + cb * 8192, cb * 64, ih, ic * C, ib);
                     }
@@ -1246,11 +1246,11 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
 #pragma unroll
                 for (int e = 0; e < 16; ++e) dk[e] = fmaf(f[e], x[e], dk[e]);
                 if (p.part) {
-                    float *o = p.part + (row0 + (size_t)col0 * p.H) * D + ln;
-                    const size_t step = (size_t)p.H * D;
+                    float *o = p.part + (row0 + (size_t)col0 * p.H) * p.dk + ln;
+                    const size_t step = (size_t)p.H * p.dk;
 #pragma unroll
                     for (int e = 0; e < 16; ++e, o += step)
-                        if (col0 + e < valid) {
+                        if (col0 + e < valid && ln < p.dk) {
                             o[0] = dq[e];
                             o[p.plane] = dk[e];
                         }
@@ -1295,7 +1295,7 @@ cudaError_t launch_gated_bwd_tc(const GatedBwdArgs &a, const char **why) {
     const long units = (long)a.B * a.H, nc = (a.T + C - 1) / C, items = units * nc;
     const GatedWs L = gated_ws(a.B, a.T, a.Hk, a.H, a.dk_dim, a.dv_dim, a.in_dtype);
     char *ws = static_cast<char *>(a.ws);
-    const size_t n = (size_t)a.B * a.T * a.H * D;
+    const size_t n = (size_t)a.B * a.T * a.H * a.dk_dim;
     const bool euler = a.euler != 0;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1316,10 +1316,11 @@ cudaError_t launch_gated_bwd_tc(const GatedBwdArgs &a, const char **why) {
     gr::Params p;
     memset(&s, 0, sizeof s);
     memset(&p, 0, sizeof p);
-    if (!bwd_row_map(&s.map_q, a.q, a.B, a.T, a.Hk) || !bwd_row_map(&s.map_k, a.k, a.B, a.T, a.Hk) ||
-        !bwd_row_map(&s.map_do, a.dO, a.B, a.T, a.H) || !bwd_row_map(&s.map_dv, a.dv, a.B, a.T, a.H) ||
-        !bwd_row_map(&p.map_v, a.v, a.B, a.T, a.H) || !bwd_row_map(&p.map_dq, a.dq, a.B, a.T, a.Hk) ||
-        !bwd_row_map(&p.map_dk, a.dk, a.B, a.T, a.Hk)) {
+    const int B = a.B, T = a.T, dk = a.dk_dim, dv = a.dv_dim;
+    if (!bwd_row_map(&s.map_q, a.q, B, T, a.Hk, dk) || !bwd_row_map(&s.map_k, a.k, B, T, a.Hk, dk) ||
+        !bwd_row_map(&s.map_do, a.dO, B, T, a.H, dv) || !bwd_row_map(&s.map_dv, a.dv, B, T, a.H, dv) ||
+        !bwd_row_map(&p.map_v, a.v, B, T, a.H, dv) || !bwd_row_map(&p.map_dq, a.dq, B, T, a.Hk, dk) ||
+        !bwd_row_map(&p.map_dk, a.dk, B, T, a.Hk, dk)) {
         *why = "cuTensorMapEncodeTiled failed";
         return cudaErrorInvalidValue;
     }
@@ -1334,6 +1335,8 @@ cudaError_t launch_gated_bwd_tc(const GatedBwdArgs &a, const char **why) {
     s.T = a.T;
     s.H = a.H;
     s.rep = a.H / a.Hk;
+    s.dk = dk;
+    s.dv = dv;
     s.wait_ns = wait_limit_ns();
     s.debug_stall = (debug_stall() & STALL_BWD_STATE) ? 1 : 0;
     *why = "tcgen05 gated state-gradient kernel launch";
@@ -1355,6 +1358,7 @@ cudaError_t launch_gated_bwd_tc(const GatedBwdArgs &a, const char **why) {
     p.T = a.T;
     p.H = a.H;
     p.rep = s.rep;
+    p.dk = dk;
     p.items = (int)items;
     p.wait_ns = s.wait_ns;
     p.debug_stall = (debug_stall() & STALL_BWD_GRAD) ? 1 : 0;

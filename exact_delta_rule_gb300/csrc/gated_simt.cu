@@ -1,6 +1,6 @@
 // Gated delta rule in chunks of 64 tokens on CUDA cores in fp32: forward, training forward and
-// backward for every supported shape that the tensor-core kernels do not cover (fp32 inputs, head
-// sizes 32 and 64, d_k != d_v).  The formulas of the forward are in gated.cuh.
+// backward of fp32 inputs (bf16 inputs take the tensor cores).  The formulas of the forward are in
+// gated.cuh.
 //
 // Backward, with dS' the gradient of a chunk's end state and dO of its outputs:
 //   G   = P^T dO + diag(c) K dS'          (the gradient of U)
@@ -39,41 +39,27 @@ __device__ __forceinline__ void st4(float *p, float4 v) { *reinterpret_cast<floa
 
 // ROWS x COLS of a row-major tensor (row stride `stride` elements) into shared memory [ROWS][ld] as
 // fp32, rows at or past `valid` as zeros; every load of a thread is issued before its first store.
-template <typename TIn, int ROWS, int COLS>
-__device__ __forceinline__ void load_block(float *dst, int ld, const TIn *src, size_t stride, int valid) {
-    constexpr int VE = 16 / sizeof(TIn), VPR = COLS / VE, NV = (ROWS * VPR + NT - 1) / NT;
-    uint4 r[NV];
+template <int ROWS, int COLS>
+__device__ __forceinline__ void load_block(float *dst, int ld, const float *src, size_t stride, int valid) {
+    constexpr int VPR = COLS / 4, NV = (ROWS * VPR + NT - 1) / NT;
+    float4 r[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const int v = threadIdx.x + n * NT, row = v / VPR, col = (v % VPR) * VE;
-        r[n] = row < ROWS && row < valid ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)row * stride + col))
-                                         : make_uint4(0, 0, 0, 0);
+        const int v = threadIdx.x + n * NT, row = v / VPR, col = (v % VPR) * 4;
+        r[n] = row < ROWS && row < valid ? __ldg(reinterpret_cast<const float4 *>(src + (size_t)row * stride + col))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const int v = threadIdx.x + n * NT, row = v / VPR, col = (v % VPR) * VE;
-        if (row >= ROWS) continue;
-        float *d = dst + row * ld + col;
-        if constexpr (sizeof(TIn) == 4) {
-            st4(d, make_float4(__uint_as_float(r[n].x), __uint_as_float(r[n].y), __uint_as_float(r[n].z),
-                               __uint_as_float(r[n].w)));
-        } else {
-            const uint32_t w[4] = {r[n].x, r[n].y, r[n].z, r[n].w};
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f[2 * e] = __uint_as_float(w[e] << 16);
-                f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-            }
-            st4(d, make_float4(f[0], f[1], f[2], f[3]));
-            st4(d + 4, make_float4(f[4], f[5], f[6], f[7]));
-        }
+        const int v = threadIdx.x + n * NT, row = v / VPR, col = (v % VPR) * 4;
+        if (row < ROWS) st4(dst + row * ld + col, r[n]);
     }
 }
-// The same for a fp32 matrix without a row limit.
+
+// The same for a whole matrix.
 template <int ROWS, int COLS>
 __device__ __forceinline__ void load_mat(float *dst, int ld, const float *src, size_t stride) {
-    load_block<float, ROWS, COLS>(dst, ld, src, stride, ROWS);
+    load_block<ROWS, COLS>(dst, ld, src, stride, ROWS);
 }
 
 // Per-token quantities of a chunk in shared memory.
@@ -176,7 +162,7 @@ constexpr size_t fwd_smem_floats() {
 
 // One CTA per (sequence, head, slab of 32 columns of d_v).  With a.ws the chunk-start states, T''
 // and P of every chunk go into the workspace (the matrices from slab 0).
-template <typename TIn, typename TOut, int DK>
+template <typename TOut, int DK>
 __global__ void __launch_bounds__(NT, 1) gated_fwd_kernel(GatedFwdArgs a, GatedWs L) {
     extern __shared__ __align__(16) float sm[];
     constexpr int LK = DK + 4;
@@ -200,7 +186,7 @@ __global__ void __launch_bounds__(NT, 1) gated_fwd_kernel(GatedFwdArgs a, GatedW
         bos = 0;
         eos = a.T;
     }
-    const TIn *q = static_cast<const TIn *>(a.q), *k = static_cast<const TIn *>(a.k), *v = static_cast<const TIn *>(a.v);
+    const float *q = static_cast<const float *>(a.q), *k = static_cast<const float *>(a.k), *v = static_cast<const float *>(a.v);
     TOut *o = static_cast<TOut *>(a.o);
     const size_t sbase = (size_t)unit * DK * a.dv + j0;
     const int nc = (int)((eos - bos + C - 1) / C);
@@ -223,9 +209,9 @@ __global__ void __launch_bounds__(NT, 1) gated_fwd_kernel(GatedFwdArgs a, GatedW
         const size_t tok0 = (size_t)b * a.T + (size_t)t0, row0 = tok0 * a.H + h, rowk = tok0 * a.Hk + hk;
         __syncthreads();  // the previous chunk is done with every buffer; S is complete
         if (ws) put_state(states + (size_t)c * DK * a.dv);
-        load_block<TIn, C, DK>(Ks, LK, k + rowk * DK, (size_t)a.Hk * DK, valid);
-        load_block<TIn, C, DK>(Qs, LK, q + rowk * DK, (size_t)a.Hk * DK, valid);
-        load_block<TIn, C, J>(Rs, LJ, v + row0 * a.dv + j0, (size_t)a.H * a.dv, valid);
+        load_block<C, DK>(Ks, LK, k + rowk * DK, (size_t)a.Hk * DK, valid);
+        load_block<C, DK>(Qs, LK, q + rowk * DK, (size_t)a.Hk * DK, valid);
+        load_block<C, J>(Rs, LJ, v + row0 * a.dv + j0, (size_t)a.H * a.dv, valid);
         load_gates(a, R, row0, valid);
         __syncthreads();
         chunk_matrices<DK>(Ks, Qs, R, nullptr, Pm, W, valid, a.euler, false);
@@ -333,7 +319,7 @@ __device__ __forceinline__ float block_sum(float x, float *red) {
 
 // One CTA per (b, h, slab of 32 columns) walks the chunks in reverse: dS' of every chunk and this
 // slab's share of <S, dS'> into the workspace, dS0 at the end.
-template <typename TIn, int DK>
+template <int DK>
 __global__ void __launch_bounds__(NT, 1) gated_bwd_state_kernel(GatedBwdArgs a, GatedWs L) {
     extern __shared__ __align__(16) float sm[];
     __shared__ float red[NT / 32];
@@ -345,7 +331,7 @@ __global__ void __launch_bounds__(NT, 1) gated_bwd_state_kernel(GatedBwdArgs a, 
     const int dv = a.dv_dim, slabs = dv / J, slab = blockIdx.x % slabs, unit = blockIdx.x / slabs, j0 = slab * J;
     const int b = unit / a.H, h = unit % a.H, hk = h / (a.H / a.Hk);
     const int nc = (a.T + C - 1) / C;
-    const TIn *q = static_cast<const TIn *>(a.q), *k = static_cast<const TIn *>(a.k), *dO = static_cast<const TIn *>(a.dO);
+    const float *q = static_cast<const float *>(a.q), *k = static_cast<const float *>(a.k), *dO = static_cast<const float *>(a.dO);
     char *ws = static_cast<char *>(a.ws);
     const float *states = reinterpret_cast<const float *>(ws + L.states) + (size_t)unit * nc * DK * dv + j0;
     float *dse = reinterpret_cast<float *>(ws + L.dse) + (size_t)unit * nc * DK * dv + j0;
@@ -369,9 +355,9 @@ __global__ void __launch_bounds__(NT, 1) gated_bwd_state_kernel(GatedBwdArgs a, 
         }
         dot = block_sum(dot, red);
         if (tid == 0) sdot[c * 4 + slab] = dot;
-        load_block<TIn, C, DK>(Ks, LK, k + rowk * DK, (size_t)a.Hk * DK, valid);
-        load_block<TIn, C, DK>(Qs, LK, q + rowk * DK, (size_t)a.Hk * DK, valid);
-        load_block<TIn, C, J>(dOs, LJ, dO + row0 * dv + j0, (size_t)a.H * dv, valid);
+        load_block<C, DK>(Ks, LK, k + rowk * DK, (size_t)a.Hk * DK, valid);
+        load_block<C, DK>(Qs, LK, q + rowk * DK, (size_t)a.Hk * DK, valid);
+        load_block<C, J>(dOs, LJ, dO + row0 * dv + j0, (size_t)a.H * dv, valid);
         load_mat<C, C>(W, LC, reinterpret_cast<const float *>(ws + L.w) + ((size_t)unit * nc + c) * C * C, C);
         load_mat<C, C>(Pm, LC, reinterpret_cast<const float *>(ws + L.p) + ((size_t)unit * nc + c) * C * C, C);
         load_gates(a, R, row0, valid);
@@ -452,7 +438,7 @@ constexpr size_t grad_smem_floats() {
 
 // One CTA per (b, h, chunk): every token's gradients from the chunk's S and dS'.  Where key heads
 // are shared (Hk < H) dq and dk of each value head go to part in fp32.
-template <typename TIn, int DK>
+template <int DK>
 __global__ void __launch_bounds__(NT, 1) gated_bwd_grad_kernel(GatedBwdArgs a, GatedWs L) {
     extern __shared__ __align__(16) float sm[];
     constexpr int LK = DK + 4;
@@ -467,14 +453,14 @@ __global__ void __launch_bounds__(NT, 1) gated_bwd_grad_kernel(GatedBwdArgs a, G
     const int nc = (a.T + C - 1) / C, unit = blockIdx.x / nc, c = blockIdx.x % nc;
     const int b = unit / a.H, h = unit % a.H, hk = h / (a.H / a.Hk);
     const int valid = min(C, a.T - c * C);
-    const TIn *q = static_cast<const TIn *>(a.q), *k = static_cast<const TIn *>(a.k), *v = static_cast<const TIn *>(a.v);
-    const TIn *dO = static_cast<const TIn *>(a.dO);
+    const float *q = static_cast<const float *>(a.q), *k = static_cast<const float *>(a.k), *v = static_cast<const float *>(a.v);
+    const float *dO = static_cast<const float *>(a.dO);
     char *ws = static_cast<char *>(a.ws);
     const float *Sc = reinterpret_cast<const float *>(ws + L.states) + ((size_t)unit * nc + c) * DK * dv;
     const float *dSe = reinterpret_cast<const float *>(ws + L.dse) + ((size_t)unit * nc + c) * DK * dv;
     const size_t tok0 = (size_t)b * a.T + (size_t)c * C, row0 = tok0 * a.H + h, rowk = tok0 * a.Hk + hk;
-    load_block<TIn, C, DK>(Ks, LK, k + rowk * DK, (size_t)a.Hk * DK, valid);
-    load_block<TIn, C, DK>(Qs, LK, q + rowk * DK, (size_t)a.Hk * DK, valid);
+    load_block<C, DK>(Ks, LK, k + rowk * DK, (size_t)a.Hk * DK, valid);
+    load_block<C, DK>(Qs, LK, q + rowk * DK, (size_t)a.Hk * DK, valid);
     load_gates(a, R, row0, valid);
     __syncthreads();
     chunk_matrices<DK>(Ks, Qs, R, Ab, Pm, nullptr, valid, a.euler, true);
@@ -497,8 +483,8 @@ __global__ void __launch_bounds__(NT, 1) gated_bwd_grad_kernel(GatedBwdArgs a, G
         __syncthreads();  // the previous slab's buffers are free
         load_mat<DK, J>(Ssl, LJ, Sc + j0, dv);
         load_mat<DK, J>(dSsl, LJ, dSe + j0, dv);
-        load_block<TIn, C, J>(Vsl, LJ, v + row0 * dv + j0, (size_t)a.H * dv, valid);
-        load_block<TIn, C, J>(dOsl, LJ, dO + row0 * dv + j0, (size_t)a.H * dv, valid);
+        load_block<C, J>(Vsl, LJ, v + row0 * dv + j0, (size_t)a.H * dv, valid);
+        load_block<C, J>(dOsl, LJ, dO + row0 * dv + j0, (size_t)a.H * dv, valid);
         __syncthreads();
         float x[8] = {}, gk[8] = {}, y[8] = {};  // row ts, columns jq ..: e^G K S, c K dS', e^G Q S
         {  // R = V - e^G K S and G = P^T dO + c K dS'
@@ -570,9 +556,9 @@ __global__ void __launch_bounds__(NT, 1) gated_bwd_grad_kernel(GatedBwdArgs a, G
                 w_part = fmaf(u[m], gk[m], w_part);
             }
             if (ts < valid) {  // dv = dR
-                TIn *dvp = static_cast<TIn *>(a.dv) + (row0 + (size_t)ts * a.H) * dv + j0 + jq;
+                float *dvp = static_cast<float *>(a.dv) + (row0 + (size_t)ts * a.H) * dv + j0 + jq;
 #pragma unroll
-                for (int m = 0; m < 8; ++m) dvp[m] = from_f32<TIn>(r[m]);
+                for (int m = 0; m < 8; ++m) dvp[m] = r[m];
             }
         }
         __syncthreads();
@@ -707,8 +693,8 @@ __global__ void __launch_bounds__(NT, 1) gated_bwd_grad_kernel(GatedBwdArgs a, G
                     pq[rowv * DK + i] = dQ[r][cc];
                     pk[rowv * DK + i] = dk;
                 } else {
-                    static_cast<TIn *>(a.dq)[rowo * DK + i] = from_f32<TIn>(dQ[r][cc]);
-                    static_cast<TIn *>(a.dk)[rowo * DK + i] = from_f32<TIn>(dk);
+                    static_cast<float *>(a.dq)[rowo * DK + i] = dQ[r][cc];
+                    static_cast<float *>(a.dk)[rowo * DK + i] = dk;
                 }
             }
         }
@@ -782,31 +768,31 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename TIn, typename TOut, int DK>
+template <typename TOut, int DK>
 cudaError_t fwd_launch(const GatedFwdArgs &a) {
     const size_t bytes = fwd_smem_floats<DK>() * 4;
     const GatedWs L = gated_ws(a.B, a.T, a.Hk, a.H, a.dk, a.dv, a.in_dtype);
-    cudaError_t e = allow_smem(gated_fwd_kernel<TIn, TOut, DK>, bytes);
+    cudaError_t e = allow_smem(gated_fwd_kernel<TOut, DK>, bytes);
     if (e != cudaSuccess) return e;
-    gated_fwd_kernel<TIn, TOut, DK><<<(unsigned)((long)a.N * a.H * (a.dv / J)), NT, bytes, a.stream>>>(a, L);
+    gated_fwd_kernel<TOut, DK><<<(unsigned)((long)a.N * a.H * (a.dv / J)), NT, bytes, a.stream>>>(a, L);
     return cudaGetLastError();
 }
-template <typename TIn, typename TOut>
+template <typename TOut>
 cudaError_t fwd_dk(const GatedFwdArgs &a) {
-    return a.dk == 32 ? fwd_launch<TIn, TOut, 32>(a) : a.dk == 64 ? fwd_launch<TIn, TOut, 64>(a) : fwd_launch<TIn, TOut, 128>(a);
+    return a.dk == 32 ? fwd_launch<TOut, 32>(a) : a.dk == 64 ? fwd_launch<TOut, 64>(a) : fwd_launch<TOut, 128>(a);
 }
 
-template <typename TIn, int DK>
+template <int DK>
 cudaError_t bwd_launch(const GatedBwdArgs &a) {
     const GatedWs L = gated_ws(a.B, a.T, a.Hk, a.H, a.dk_dim, a.dv_dim, a.in_dtype);
     const size_t b1 = state_smem_floats<DK>() * 4, b2 = grad_smem_floats<DK>() * 4;
     const long units = (long)a.B * a.H, nc = (a.T + C - 1) / C;
-    cudaError_t e = allow_smem(gated_bwd_state_kernel<TIn, DK>, b1);
-    if (e == cudaSuccess) e = allow_smem(gated_bwd_grad_kernel<TIn, DK>, b2);
+    cudaError_t e = allow_smem(gated_bwd_state_kernel<DK>, b1);
+    if (e == cudaSuccess) e = allow_smem(gated_bwd_grad_kernel<DK>, b2);
     if (e != cudaSuccess) return e;
-    gated_bwd_state_kernel<TIn, DK><<<(unsigned)(units * (a.dv_dim / J)), NT, b1, a.stream>>>(a, L);
+    gated_bwd_state_kernel<DK><<<(unsigned)(units * (a.dv_dim / J)), NT, b1, a.stream>>>(a, L);
     if ((e = cudaGetLastError()) != cudaSuccess || nc == 0) return e;
-    gated_bwd_grad_kernel<TIn, DK><<<(unsigned)(units * nc), NT, b2, a.stream>>>(a, L);
+    gated_bwd_grad_kernel<DK><<<(unsigned)(units * nc), NT, b2, a.stream>>>(a, L);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return a.Hk == a.H ? cudaSuccess
                        : launch_gated_reduce_heads(a, reinterpret_cast<const float *>(static_cast<char *>(a.ws) + L.part));
@@ -816,18 +802,15 @@ cudaError_t bwd_launch(const GatedBwdArgs &a) {
 
 cudaError_t launch_gated_chunk_simt(const GatedFwdArgs &a) {
     if (a.N == 0) return cudaSuccess;
-    const bool ib = a.in_dtype == EFLA_BF16, ob = a.o_dtype == EFLA_BF16;
-    if (ib) return ob ? fwd_dk<__nv_bfloat16, __nv_bfloat16>(a) : fwd_dk<__nv_bfloat16, float>(a);
-    return ob ? fwd_dk<float, __nv_bfloat16>(a) : fwd_dk<float, float>(a);
+    return a.o_dtype == EFLA_BF16 ? fwd_dk<__nv_bfloat16>(a) : fwd_dk<float>(a);
 }
 
 cudaError_t launch_gated_bwd_simt(const GatedBwdArgs &a) {
     if ((long)a.B * a.H == 0) return cudaSuccess;
-    const bool ib = a.in_dtype == EFLA_BF16;
     switch (a.dk_dim) {
-        case 32: return ib ? bwd_launch<__nv_bfloat16, 32>(a) : bwd_launch<float, 32>(a);
-        case 64: return ib ? bwd_launch<__nv_bfloat16, 64>(a) : bwd_launch<float, 64>(a);
-        default: return ib ? bwd_launch<__nv_bfloat16, 128>(a) : bwd_launch<float, 128>(a);
+        case 32: return bwd_launch<32>(a);
+        case 64: return bwd_launch<64>(a);
+        default: return bwd_launch<128>(a);
     }
 }
 

@@ -114,7 +114,7 @@ cudaError_t launch_bwd_grad_tc(const BwdArgs &a, const float *states, const floa
                                const void *do_split, const float *g, const void *dr_split, const char **why);
 // [B, T, H, 128] bf16 tensor map of the backward kernels: box 64 features x 1 head x 64 tokens
 // x 1, 128-byte swizzle (bwd_tc.cu).
-bool bwd_row_map(CUtensorMap *m, const void *ptr, int B, int T, int H);
+bool bwd_row_map(CUtensorMap *m, const void *ptr, int B, int T, int H, int d = 128);
 
 // Start states of the segments of split sequences from the segment maps (scan.cu).
 cudaError_t launch_scan_combine(const float *S0, const float *maps, float *s_in, int B, int G, int H,

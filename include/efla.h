@@ -366,8 +366,9 @@ efla_status efla_prep(const void *k, const void *v, const float *beta, float *la
  *         decay of 0: the state restarts).  Positive gates are evaluated by the same formulas as long
  *         as their sum over 64 tokens keeps e^sum finite.
  *   S0, S_T [N, H, d_k, d_v] fp32;  o [B, T, H, d_v] o_dtype;  cu_seqlens as for efla_fwd_chunked
- * Supported: d_k, d_v in {32, 64, 128}, bf16 or fp32.  bf16 inputs with d_k = d_v = 128 run on the
- * tensor cores, every other combination on CUDA cores in fp32.  State and sums are fp32 everywhere.
+ * Supported: d_k, d_v in {32, 64, 128}, bf16 or fp32.  The forward and backward of bf16 inputs run on
+ * the tensor cores, and so does decoding several tokens where d_k = d_v = 128; fp32 inputs and the rest
+ * run on CUDA cores in fp32.  State and sums are fp32 everywhere.
  */
 
 /* The forward over whole sequences, in chunks of 64 tokens.  S0 and S_T may be NULL (zeros / not

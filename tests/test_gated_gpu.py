@@ -25,7 +25,7 @@ BF16, F32 = torch.bfloat16, torch.float32
 def tol(dtype, dk, dv, grad=False):
     links = 2 if grad else 1
     t = links * 2 * (dk + 64) * 2.0 ** -24
-    if dtype == BF16 and dk == dv == 128:
+    if dtype == BF16:
         t += links * 8 * 2.0 ** -18
     return t
 
@@ -64,7 +64,7 @@ def check_fwd(x, update="euler", **kw):
     return o, S
 
 
-SHAPES = [(F32, 32, 32), (F32, 64, 128), (F32, 128, 128), (BF16, 64, 64), (BF16, 128, 64), (BF16, 128, 128)]
+SHAPES = [(F32, 32, 32), (F32, 64, 128), (F32, 128, 128), (BF16, 64, 64), (BF16, 128, 64), (BF16, 32, 128), (BF16, 128, 128)]
 
 
 @pytest.mark.parametrize("T", [0, 1, 2, 15, 63, 64, 65, 127, 128, 130, 321])
@@ -144,7 +144,7 @@ def test_forward_packed_bad_bounds_are_flagged(dtype, d):
         assert efla.device_status() == 0
 
 
-@pytest.mark.parametrize("dtype, dk, dv", [(F32, 64, 64), (F32, 32, 128), (BF16, 128, 128)])
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 64, 64), (F32, 32, 128), (BF16, 128, 128), (BF16, 32, 64), (BF16, 128, 32)])
 @pytest.mark.parametrize("what", ["none", "resets", "strong", "weak", "zero keys", "zero beta", "one beta", "same key"])
 def test_forward_extremes(dtype, dk, dv, what):
     x = make(B=1, T=190, dk=dk, dv=dv, dtype=dtype, seed=3)
@@ -223,7 +223,7 @@ def test_backward_heads_and_rules(dtype, dk, dv, Hk, H, update):
     check_bwd(x, update, dS=False, saved=False)
 
 
-@pytest.mark.parametrize("dtype, dk, dv", [(F32, 64, 64), (BF16, 128, 128)])
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 64, 64), (BF16, 128, 128), (BF16, 64, 128), (BF16, 32, 32)])
 @pytest.mark.parametrize("what", ["none", "strong", "weak", "zero keys", "zero beta", "one beta", "resets"])
 def test_backward_extremes(dtype, dk, dv, what):
     x = make(B=1, T=190, dk=dk, dv=dv, dtype=dtype, seed=3)
