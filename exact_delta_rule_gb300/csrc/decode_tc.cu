@@ -37,8 +37,9 @@
 //     HBM, then the bulk load of the S two units ahead into the same buffer.
 // Every wait is bounded; on expiry the CTA records EFLA_ERR_DEVICE_TIMEOUT and leaves.
 //
-// Gated instantiation (gated.cuh): A~ and P take Gamma_ts in the prep warp, X takes e^{G_t} and S the
-// block's decay where the state warpgroup waits for u, the state update takes c_t u_t (a second split
+// Gated instantiation (gated.cuh): A~ and P take Gamma_ts in the prep warp, X takes e^{G_t}, S in TMEM
+// the block's decay where it is split (209 us at 256
+// sequences of 32 heads, 16 tokens; a pass of its own while u is formed: 213), the state update takes c_t u_t (a second split
 // operand), and O = e^{G_t} O1 + u^T P^T is joined where it is read out.  Operands are rounded to
 // nearest in both parts.
 #include <cudaTypedefs.h>
@@ -69,8 +70,8 @@ constexpr uint32_t OFF_OT = OFF_PP + 4096;        // o tiles: 2 buffers x 8 KB (
 constexpr uint32_t OFF_G = OFF_OT + 2 * 8192;     // fp32 A~ [16][17], T~ [16][17]
 constexpr uint32_t G_LD = 17;
 constexpr uint32_t OFF_ROW = OFF_G + 2 * 16 * G_LD * 4;  // fp32 invn[16], gn[16]
-constexpr uint32_t OFF_DEC = OFF_ROW + 128;  // gated, fp32: G_t hi [16], lo [16], then per block parity e^{G_t} [16], c_t [16]
-constexpr uint32_t OFF_BAR = OFF_DEC + (2 + 4) * 64;
+constexpr uint32_t OFF_DEC = OFF_ROW + 128;  // gated, fp32: G_t hi [16], lo [16], then of four blocks e^{G_t} [16], c_t [16]
+constexpr uint32_t OFF_BAR = OFF_DEC + (2 + 8) * 64;
 constexpr uint32_t OFF_MISC = OFF_BAR + 256;  // tmem base, abort flag
 constexpr uint32_t SMEM_USED = OFF_MISC + 16;
 constexpr uint32_t SMEM_ALLOC = SMEM_USED + 1024;
@@ -116,6 +117,7 @@ struct Bars {
     uint64_t s_full[2], s_out[2];        // S staging buffer landed / holds the unit's new S (128 arrivals)
     uint64_t kqv_full[2], kqv_empty[2];  // K, Q, V stage landed / no longer read
     uint64_t g_done, g_free;             // Gram rows in TMEM / read by the prep warp
+    uint64_t dec_ready;                  // gated: decays of a block written
     uint64_t prep_ready, tp_free;        // T'', P of a block written / no longer read
     uint64_t sa_ready, x_done, r_ready, u_done, u_ready, s_done, o_done;
     uint64_t drain;
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
         mbar_init(&bars->g_done, 1);
         mbar_init(&bars->g_free, 1);
         mbar_init(&bars->prep_ready, 1);
+        mbar_init(&bars->dec_ready, 1);
         mbar_init(&bars->tp_free, 1);
         mbar_init(&bars->sa_ready, 128);
         mbar_init(&bars->x_done, 1);
@@ -216,8 +219,14 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
             float *stg = reinterpret_cast<float *>(sm + OFF_S + sb * S_BYTES);
             for (int blk = 0; blk < nblk && ok; ++blk, ++gb) {
                 const int t0 = blk * MB, mb = min(MB, p.m - t0);
+                const float *eg = dec + (gb & 3) * 32, *ec = eg + 16;  // gated: e^{G_t}, c_t of the block
+                float el = 1.f;                                        // ... and its last e^{G_t}, the state's factor
+                if constexpr (GATED) {
+                    ok = dt_wait_warp(&bars->dec_ready, gb & 1, abort_flag, wait_ns);
+                    if (ok) el = eg[MB - 1];
+                }
                 if (blk == 0) {  // S^T of the unit from its staging: fp32 into TM_S and split into TM_SA
-                    ok = dt_wait_warp(&bars->s_full[sb], (it >> 1) & 1, abort_flag, wait_ns);
+                    ok = ok && dt_wait_warp(&bars->s_full[sb], (it >> 1) & 1, abort_flag, wait_ns);
                     if (ok) {
 #pragma unroll 1
                         for (int g = 0; g < 4; ++g) {
@@ -225,15 +234,19 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                             uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int i = 0; i < 32; ++i) sv[i] = stg[(g * 32 + i) * D + j];
-                            tmem_st32(lane_base + TM_S + g * 32, sv);
                             tc::split_as<GATED, 16>(sv, hi, lo);
                             tmem_st16u(lane_base + TM_SA + g * 16, hi);
                             tmem_st16u(lane_base + TM_SA + 64 + g * 16, lo);
+                            if constexpr (GATED) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) sv[i] *= el;
+                            }
+                            tmem_st32(lane_base + TM_S + g * 32, sv);
                         }
                         tmem_st_wait();
                     }
                 } else {  // S^T after the previous block's update -> split
-                    ok = dt_wait_warp(&bars->s_done, (gb - 1) & 1, abort_flag, wait_ns);
+                    ok = ok && dt_wait_warp(&bars->s_done, (gb - 1) & 1, abort_flag, wait_ns);
                     if (ok) {
                         tc_fence_after();
 #pragma unroll 1
@@ -245,6 +258,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                             tc::split_as<GATED, 16>(sv, hi, lo);
                             tmem_st16u(lane_base + TM_SA + g * 16, hi);
                             tmem_st16u(lane_base + TM_SA + 64 + g * 16, lo);
+                            if constexpr (GATED) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) sv[i] *= el;
+                                tmem_st32(lane_base + TM_S + g * 32, sv);
+                            }
                         }
                         tmem_st_wait();
                     }
@@ -252,8 +270,6 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                 tc_fence_before();
                 mbar_arrive(&bars->sa_ready);
                 ok = ok && dt_wait_warp(&bars->x_done, gb & 1, abort_flag, wait_ns);
-                const float *eg = dec + (gb & 1) * 32, *ec = eg + 16;  // gated: e^{G_t}, c_t of the block
-                if constexpr (GATED) ok = ok && dt_wait_warp(&bars->prep_ready, gb & 1, abort_flag, wait_ns);
                 if (ok) {  // (-X)^T -> bf16 hi | lo (tokens past the block end are zero)
                     tc_fence_after();
                     float x[16];
@@ -268,19 +284,6 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(&bars->r_ready);
-                    if constexpr (GATED) {  // S times the block's decay while the tensor core forms u
-                        const float el = eg[MB - 1];
-#pragma unroll 1
-                        for (int g = 0; g < 4; ++g) {
-                            float sv[32];
-                            tmem_ld32(lane_base + TM_S + g * 32, sv);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) sv[i] *= el;
-                            tmem_st32(lane_base + TM_S + g * 32, sv);
-                        }
-                        tmem_st_wait();
-                    }
                 }
                 ok = ok && dt_wait_warp(&bars->u_done, gb & 1, abort_flag, wait_ns);
                 if (ok) {  // u^T -> bf16 hi | lo
@@ -373,9 +376,15 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                 const float bt = lane < mb ? p.beta[((size_t)b * p.m + t0 + lane) * p.H + h] : 0.f;
                 float gt = 0.f;
                 if constexpr (GATED) gt = lane < mb ? p.g[((size_t)b * p.m + t0 + lane) * p.H + h] : 0.f;
+                if constexpr (GATED) {
+                    // (four slots: this one's last readers, the outputs of block gb - 4, are done, since Gram rows
+                    // of block gb - 1 came behind the state warps' u of block gb - 2)
+                    block_decay16(gt, lane, dec_gh, dec_gl, dec + (gb & 3) * 32, dec + (gb & 3) * 32 + 16);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->dec_ready);
+                }
                 if (!(ok = dt_wait_warp(&bars->g_done, gb & 1, abort_flag, wait_ns))) break;
                 tc_fence_after();
-                if constexpr (GATED) block_decay16(gt, lane, dec_gh, dec_gl, dec + (gb & 1) * 32, dec + (gb & 1) * 32 + 16);
                 float row[16];  // lane t < 16: k_t . k_s; lane 16 + t: q_t . k_s
                 tmem_ld16(tmem + TM_G, row);
                 tmem_ld_wait();

@@ -104,6 +104,18 @@ def test_binding_refuses(over, what):
         efla.gated_decode_tokens(*args, torch.zeros(2, 4, 32, 32) if S0 is None else S0)
 
 
+def test_a_stream_of_another_device_is_refused():
+    from types import SimpleNamespace
+
+    from exact_delta_rule_gb300 import gated as binding
+    like = SimpleNamespace(get_device=lambda: 0, device="cuda:0")
+    assert binding._stream(SimpleNamespace(device_index=0, cuda_stream=11), like) == 11
+    with pytest.raises(efla.EflaError, match="the stream is on cuda:1"):
+        binding._stream(SimpleNamespace(device_index=1, cuda_stream=11), like)
+    with pytest.raises(efla.EflaError, match="CUDA tensors"):
+        binding._on_device(torch.zeros(1))
+
+
 def test_binding_refuses_more():
     args, S0 = cpu_args()
     with pytest.raises(efla.EflaError, match="unknown update"):

@@ -457,6 +457,87 @@ def test_streams():
     assert all(torch.equal(got[n], want[n]) for n in got), len(junk)
 
 
+def test_stream_outputs_wait_for_their_memory():
+    """An output on another stream does not land in memory that the current stream is still writing."""
+    x = make(T=300, dk=128, dv=128, dtype=BF16)
+    want_o, want_S = efla.gated_fwd_chunked(**x)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    late = [torch.empty_like(want_o), torch.empty_like(want_S)]
+    torch.cuda._sleep(100_000_000)  # the writes below happen long after the call on the other stream
+    for t in late:
+        t.fill_(7.0)
+    del late, t
+    o, S = efla.gated_fwd_chunked(**x, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want_o) and torch.equal(S, want_S)
+
+
+def test_two_graphs_and_an_eager_call_share_a_workspace():
+    """Replayed in turn on one stream, each graph's forward fills the workspace before its backward reads it."""
+    xs = [make(T=n, dk=64, dv=128, dtype=BF16, seed=n) for n in (130, 190)]
+    ws = torch.empty(max(efla.gated_bwd_workspace(2, n, 2, 4, 64, 128, BF16) for n in (130, 190)), dtype=torch.uint8,
+                     device="cuda")
+    dO = [torch.ones_like(x["v"]) for x in xs]
+    step = lambda i: efla.gated_bwd_chunked(*xs[i].values(), dO[i], workspace=ws)  # noqa: E731
+    want = [{n: t.clone() for n, t in step(i).items()} for i in (0, 1)]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for i in (0, 1):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            got.append(step(i))
+    for i in (0, 1, 1, 0):
+        graphs[i].replay()
+        eager = step(1 - i)
+        torch.cuda.synchronize()
+        for n in want[i]:
+            assert torch.equal(got[i][n], want[i][n]) and torch.equal(eager[n], want[1 - i][n]), n
+
+
+@pytest.mark.parametrize("stall", [1, 2, 4])
+@pytest.mark.parametrize("T", [64, 200])
+def test_expired_waits_are_reported(stall, T):
+    """A wait that runs out in the forward, the state pass or the gradient pass: the kernel records it and
+    leaves, and the next call is right."""
+    x = make(B=1, T=T, dk=128, dv=64, dtype=BF16)
+    dO = torch.ones_like(x["v"])
+    assert efla.device_status() == 0
+    efla.set_wait_limit_ns(50_000_000)
+    efla.set_debug_stall(stall)
+    try:
+        efla.gated_bwd_chunked(*x.values(), dO)
+        torch.cuda.synchronize()
+    finally:
+        efla.set_debug_stall(False)
+        efla.set_wait_limit_ns(0)
+    assert efla.device_status() == 4
+    assert efla.device_status() == 0
+    check_fwd(x)
+    check_bwd(x)
+
+
+@pytest.mark.parametrize("dk, dv", [(32, 128), (64, 32), (128, 64)])
+def test_small_heads_touch_only_their_memory(dk, dv):
+    """Head sizes that the tensor-core tiles exceed, every output between sentinels; partial chunks, packed too."""
+    T, H, N = 70, 4, 2
+    x = make(B=1, T=T, dk=dk, dv=dv, dtype=BF16, N=N)
+    cu = torch.tensor([0, 33, 66], dtype=torch.int32, device="cuda")  # (four tokens behind the last sequence)
+    big = torch.full((64 + T * H * dv + 64,), 7.0, device="cuda", dtype=BF16)
+    bigS = torch.full((64 + N * H * dk * dv + 64,), 7.0, device="cuda")
+    o, S = big[64:-64].view(1, T, H, dv), bigS[64:-64].view(N, H, dk, dv)
+    efla.gated_fwd_chunked(**x, cu_seqlens=cu, o=o, S_T=S)
+    ref = [gated.fwd(**{m: y[i:i + 1] if m == "S0" else y[:, 33 * i:33 * i + 33] for m, y in x.items()}) for i in (0, 1)]
+    t = tol(BF16, dk, dv)
+    close(o[:, :66], torch.cat([r[0] for r in ref], 1), t, "o")
+    close(S, torch.cat([r[1] for r in ref]), t, "S_T")
+    assert all(bool((e == 7).all()) for e in (big[:64], big[-64:], bigS[:64], bigS[-64:], o[:, 66:]))
+    y = make(B=2, T=T, Hk=4, H=4, dk=dk, dv=dv, dtype=BF16)
+    check_fwd(y)
+    check_bwd(y)
+
+
 @pytest.mark.parametrize("dtype, d", [(F32, 64), (BF16, 128)])
 def test_long_sequence(dtype, d):
     """4096 tokens, weak and strong decays side by side: errors do not pile up."""
