@@ -38,10 +38,9 @@
 // Every wait is bounded; on expiry the CTA records EFLA_ERR_DEVICE_TIMEOUT and leaves.
 //
 // Gated instantiation (gated.cuh): A~ and P take Gamma_ts in the prep warp, X takes e^{G_t}, S in TMEM
-// the block's decay where it is split (209 us at 256
-// sequences of 32 heads, 16 tokens; a pass of its own while u is formed: 213), the state update takes c_t u_t (a second split
-// operand), and O = e^{G_t} O1 + u^T P^T is joined where it is read out.  Operands are rounded to
-// nearest in both parts.
+// the block's decay where it is split (209 us at 256 sequences of 32 heads, 16 tokens; as a pass of its
+// own while u is formed: 213), the state update takes c_t u_t (a second split operand), and
+// O = e^{G_t} O1 + u^T P^T is joined where it is read out.  Operands are rounded to nearest in both parts.
 #include <cudaTypedefs.h>
 
 #include <mutex>
