@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             } else {
                 if (st_c) dump_state_rows(st_c, lane_base + TM_S, 0, j);
             }
-            if (c >= 2) release_staging(c - 2);  // its stores were issued during chunk c - 1
+            if (!GATED && c >= 2) release_staging(c - 2);  // its stores were issued during chunk c - 1
             const long tok0 = bos + (long)c * C;
             const int valid = (int)min((long)C, eos - tok0);
             ok = wait_bar_warp(&bars->x_done, c & 1, abort_flag, wait_ns);
@@ -765,22 +765,11 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             mbar_arrive(&bars->r_ready);
             if constexpr (GATED) {
                 decay_state_rows(lane_base + TM_S, 2, 4, eg[C - 1]);
-                if (write_o) {  // O1^T times e^{G_t}
-                    ok = wait_bar_warp(&bars->o1_done, c & 1, abort_flag, wait_ns);
+                if (c >= 1) {  // the outputs of the previous chunk leave while the tensor core forms u
+                    ok = wait_bar_warp(&bars->o_done[(c - 1) & 1], ((c - 1) >> 1) & 1, abort_flag, wait_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t ob = lane_base + TM_O + (uint32_t)(c & 1) * 64;
-#pragma unroll 1
-                    for (int hf = 0; hf < 2; hf = opaque(hf + 1)) {
-                        float x[32], f[32];
-                        tmem_ld32(ob + hf * 32, x);
-                        load32(eg + hf * 32, f);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int t = 0; t < 32; ++t) x[t] *= f[t];
-                        tmem_st32(ob + hf * 32, x);
-                    }
-                    tmem_st_wait();
+                    epilogue(c - 1);
                 }
             } else {
                 if (st_c) dump_state_rows(st_c, lane_base + TM_S, 2, j);
@@ -813,18 +802,30 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&bars->u_ready);
+                // while the tensor core updates the state: u_t split, O1^T times e^{G_t}
                 if (write_o) {
+                    ok = wait_bar_warp(&bars->o1_done, c & 1, abort_flag, wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t ob = lane_base + TM_O + (uint32_t)(c & 1) * 64;
 #pragma unroll 1
                     for (int hf = 0; hf < 2; hf = opaque(hf + 1)) {
-                        float u[32];
+                        float u[32], f[32];
                         tmem_ld32(lane_base + TM_X + hf * 32, u);
                         tmem_ld_wait();
                         split_half(lane_base + TM_X, hf, u);
+                        tmem_ld32(ob + hf * 32, u);
+                        load32(eg + hf * 32, f);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int t = 0; t < 32; ++t) u[t] *= f[t];
+                        tmem_st32(ob + hf * 32, u);
                     }
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(&bars->uo_ready);
                 }
+                if (c >= 1) release_staging(c - 1);
             } else {
             // u^T = U1 + U2 -> bf16 hi/lo operand in TMEM
 #pragma unroll 1
@@ -845,7 +846,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             mbar_arrive(&bars->u_ready);
             }
             // the outputs of the previous chunk leave while the tensor core updates the state
-            if (c >= 1) {
+            if (!GATED && c >= 1) {
                 ok = wait_bar_warp(&bars->o_done[(c - 1) & 1], ((c - 1) >> 1) & 1, abort_flag, wait_ns);
                 if (!ok) break;
                 tc_fence_after();
