@@ -6,8 +6,10 @@
 // of 256 threads holds the rows of S for COLS of the d_v columns in registers, read and written once
 // with 16-byte accesses; the column sums over the row groups go through shared memory.  The columns
 // are independent, so COLS trades CTAs for the repeated reading of k and q: with COLS = d_v a step of
-// 8192 heads streams at the copy rate, while few heads leave most SMs idle and the load latency of a
-// 64 KB state bare; then 32 columns a CTA (a row of it is still one 128-byte line).
+// 8192 heads streams at the copy rate (158 us, 1.08 GB), while fewer heads than SMs leave SMs idle and
+// the load latency of a 64 KB state bare; then 32 columns a CTA (a row of it is still one 128-byte line).
+// d = 128, bf16, 32 columns / d_v a CTA: 8 heads 2.3 / 3.2 us, 32 2.7 / 3.5, 128 5.1 / 5.3, 256 8.8 / 8.3,
+// 2048 48 / 45.
 #include "gated.cuh"
 
 namespace efla {
@@ -116,7 +118,7 @@ cudaError_t step_types(const GatedDecodeArgs &a) {
 
 template <int DK>
 cudaError_t step_cols(const GatedDecodeArgs &a) {
-    if (a.dv == 32 || (long)a.B * a.H < 304) return step_types<DK, 32>(a);  // fewer heads than two a SM
+    if (a.dv == 32 || (long)a.B * a.H < 152) return step_types<DK, 32>(a);  // fewer heads than SMs
     return a.dv == 64 ? step_types<DK, 64>(a) : step_types<DK, 128>(a);
 }
 

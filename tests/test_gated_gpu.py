@@ -535,6 +535,7 @@ def test_small_heads_touch_only_their_memory(dk, dv):
     assert all(bool((e == 7).all()) for e in (big[:64], big[-64:], bigS[:64], bigS[-64:], o[:, 66:]))
     y = make(B=2, T=T, Hk=4, H=4, dk=dk, dv=dv, dtype=BF16)
     check_fwd(y)
+    check_fwd(y, o_dtype=F32)
     check_bwd(y)
 
 
