@@ -116,7 +116,7 @@ struct Bars {
     uint64_t s_full[2], s_out[2];        // S staging buffer landed / holds the unit's new S (128 arrivals)
     uint64_t kqv_full[2], kqv_empty[2];  // K, Q, V stage landed / no longer read
     uint64_t g_done, g_free;             // Gram rows in TMEM / read by the prep warp
-    uint64_t dec_ready;                  // gated: decays of a block written
+    uint64_t dec_ready[2];               // gated: decays of a block written (by block parity: the prep may be a block ahead)
     uint64_t prep_ready, tp_free;        // T'', P of a block written / no longer read
     uint64_t sa_ready, x_done, r_ready, u_done, u_ready, s_done, o_done;
     uint64_t drain;
@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
         mbar_init(&bars->g_done, 1);
         mbar_init(&bars->g_free, 1);
         mbar_init(&bars->prep_ready, 1);
-        mbar_init(&bars->dec_ready, 1);
+        mbar_init(&bars->dec_ready[0], 1);
+        mbar_init(&bars->dec_ready[1], 1);
         mbar_init(&bars->tp_free, 1);
         mbar_init(&bars->sa_ready, 128);
         mbar_init(&bars->x_done, 1);
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                 const float *eg = dec + (gb & 3) * 32, *ec = eg + 16;  // gated: e^{G_t}, c_t of the block
                 float el = 1.f;                                        // ... and its last e^{G_t}, the state's factor
                 if constexpr (GATED) {
-                    ok = dt_wait_warp(&bars->dec_ready, gb & 1, abort_flag, wait_ns);
+                    ok = dt_wait_warp(&bars->dec_ready[gb & 1], (gb >> 1) & 1, abort_flag, wait_ns);
                     if (ok) el = eg[MB - 1];
                 }
                 if (blk == 0) {  // S^T of the unit from its staging: fp32 into TM_S and split into TM_SA
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_tc_kernel(const __grid_cons
                     // of block gb - 1 came behind the state warps' u of block gb - 2)
                     block_decay16(gt, lane, dec_gh, dec_gl, dec + (gb & 3) * 32, dec + (gb & 3) * 32 + 16);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->dec_ready);
+                    if (lane == 0) mbar_arrive(&bars->dec_ready[gb & 1]);
                 }
                 if (!(ok = dt_wait_warp(&bars->g_done, gb & 1, abort_flag, wait_ns))) break;
                 tc_fence_after();
