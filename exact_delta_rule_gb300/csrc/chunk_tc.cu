@@ -412,6 +412,13 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                         *reinterpret_cast<uint4 *>(KQ + cb * 16384 + (R >> 3) * 1024 + (R & 7) * 128 + ch * 16) =
                             make_uint4(0, 0, 0, 0);
                     }
+                    if constexpr (GATED) {  // and V's: 0 times what the next sequence holds there may be NaN
+                        for (int e = pi; e < 2 * rows * 8; e += 256) {
+                            const int ch = e & 7, R = valid + (e >> 3) % rows, cb = (e >> 3) / rows;
+                            *reinterpret_cast<uint4 *>(KQ + OFF_V + cb * 8192 + (R >> 3) * 1024 + (R & 7) * 128 + ch * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                    }
                     fence_proxy_async_smem();
                 }
                 if (named_bar_any(BAR_PREP, 256, !ok || *abort_flag)) {

@@ -127,6 +127,47 @@ def test_forward_packed(dtype, dk, dv):
     assert efla.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype, d", [(F32, 32), (BF16, 64), (BF16, 128)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_forward_packed_keeps_bad_values_in_their_sequence(dtype, d, bad):
+    lens = [70, 40, 64, 5]
+    x = make(B=1, T=sum(lens), N=4, dk=d, dv=d, dtype=dtype)
+    cu = torch.tensor([0, 70, 110, 174, 179], dtype=torch.int32, device="cuda")
+    want_o, want_S = efla.gated_fwd_chunked(**x, cu_seqlens=cu)
+    for n in ("q", "k", "v", "g", "beta"):
+        x[n][:, 70:110] = -bad if n == "g" else bad
+    x["S0"][1] = bad
+    o, S = efla.gated_fwd_chunked(**x, cu_seqlens=cu)
+    for a, b, i in ((0, 70, 0), (110, 174, 2), (174, 179, 3)):
+        assert torch.equal(o[:, a:b], want_o[:, a:b]) and torch.equal(S[i], want_S[i]), i
+    assert efla.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype, d", [(F32, 64), (BF16, 32), (BF16, 128)])
+def test_rows_keep_bad_values_to_themselves(dtype, d):
+    """A batch row of NaN leaves the other rows' outputs and gradients as they were, in every call."""
+    x = make(B=3, T=70, dk=d, dv=d, dtype=dtype)
+    dO, dS = torch.ones_like(x["v"]), torch.ones_like(x["S0"])
+    S1, S2 = x["S0"].clone(), x["S0"].clone()
+    tok = lambda x, n: [x[m][:, :n].contiguous() for m in ("q", "k", "v", "g", "beta")]  # noqa: E731
+    run = lambda x, dO, S1, S2: [*efla.gated_fwd_chunked(**x), *efla.gated_bwd_chunked(*x.values(), dO, dS).values(),  # noqa: E731
+                                 efla.gated_decode_tokens(*tok(x, 19), S1), S1,
+                                 efla.gated_decode_step(*[t[:, 0].contiguous() for t in tok(x, 1)], S2), S2]
+    want = run(x, dO, S1, S2)
+    S1, S2 = x["S0"].clone(), x["S0"].clone()
+    for t in (*x.values(), dO, S1, S2):
+        t[1] = math.nan
+    for got, ref in zip(run(x, dO, S1, S2), want):
+        assert torch.equal(got[[0, 2]], ref[[0, 2]])
+
+
+def test_positive_gates():
+    x = make(B=1, T=150, dk=64, dv=64, dtype=BF16)
+    x["g"].mul_(-0.01)
+    check_fwd(x)
+    check_bwd(x)
+
+
 @pytest.mark.parametrize("dtype, d", [(F32, 32), (BF16, 128)])
 def test_forward_packed_bad_bounds_are_flagged(dtype, d):
     """A sequence with bounds outside the tokens is not touched; the others are computed."""
