@@ -594,3 +594,36 @@ def test_many_heads():
     x = make(B=40, T=66, Hk=4, H=8, dk=128, dv=128, dtype=BF16)
     check_fwd(x)
     check_bwd(x)
+
+
+def test_offsets_past_32_bits():
+    """States, values and rows of more than 2^31 elements: the last of them against the same call on them alone."""
+    last = lambda *ts: [t[-1:].contiguous() for t in ts]  # noqa: E731
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    B, H, d = 3300, 40, 128  # 2^31 + 15 M elements of S
+    q, v, g, beta = r(B, H, d).bfloat16() / 12, r(B, H, d).bfloat16(), -r(B, H).abs(), torch.sigmoid(r(B, H))
+    S = torch.zeros(B, H, d, d, device="cuda")
+    S[-1] = r(H, d, d)
+    assert S.numel() > 2 ** 31
+    few = S[-33:].clone()  # (as many heads as take the same kernel variant)
+    x = [t[-33:].contiguous() for t in (q, q, v, g, beta)]
+    o, want = efla.gated_decode_step(q, q, v, g, beta, S), efla.gated_decode_step(*x, few)
+    assert torch.equal(o[-33:], want) and torch.equal(S[-33:], few)
+    o = efla.gated_decode_tokens(*(t[:, None].contiguous() for t in (q, q, v, g, beta)), S)
+    want = efla.gated_decode_tokens(*(t[:, None].contiguous() for t in x), few)
+    assert torch.equal(o[-33:], want) and torch.equal(S[-33:], few)
+    del S, o
+    rows = 2 ** 24 + 3
+    z, w = r(4096, d).bfloat16().repeat(rows // 4096 + 1, 1)[:rows], r(d)
+    assert z.numel() > 2 ** 31
+    got, want = efla.norm_gate_bwd(z, z, w, z), efla.norm_gate_bwd(*last(z, z), w, *last(z))
+    assert torch.equal(got["do"][-1:], want["do"]) and torch.equal(got["dz"][-1:], want["dz"])
+    assert torch.equal(efla.norm_gate(z, z, w)[-1:], efla.norm_gate(*last(z, z), w))
+    del got
+    heads = z[:rows // 8 * 8].view(-1, 8, d)
+    a = torch.zeros(heads.shape[0], 8, device="cuda", dtype=BF16)
+    A = torch.zeros(8, device="cuda")
+    p, want = efla.gated_prep(heads, heads, a, a, A, A), efla.gated_prep(*last(heads, heads, a, a), A, A)
+    assert all(torch.equal(p[n][-1:], want[n]) for n in p)
+    assert efla.device_status() == 0
