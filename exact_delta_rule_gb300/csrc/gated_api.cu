@@ -1,6 +1,7 @@
 // C-ABI entry points of the gated delta rule and of the norms around it: argument validation and
 // dispatch.  Declarations and the contract are in efla.h.
 #include <math.h>
+#include <string.h>
 
 #include <initializer_list>
 
@@ -21,11 +22,19 @@ struct Arg {
     const void *p;
     size_t bytes;
     Role role;
-    const void *may_be = nullptr;  // an output may be exactly this input
+    const char *may_be[2] = {nullptr, nullptr};  // an output may be exactly the inputs of these names
 };
 
+// Whether output o may lie where x does: x is an input that o's contract names, at the same address.
+bool may_share(const Arg &o, const Arg &x) {
+    if (x.p != o.p || x.bytes != o.bytes || (x.role != IN && x.role != IN_OPT)) return false;
+    for (const char *name : o.may_be)
+        if (name && strcmp(name, x.name) == 0) return true;
+    return false;
+}
+
 // Every non-optional argument with bytes > 0 present, every pointer 16-byte aligned, no output
-// overlapping any other argument.
+// overlapping any other argument than an input it may be.
 efla_status check_args(std::initializer_list<Arg> args) {
     for (const Arg &a : args) {
         if (!a.p && a.bytes > 0 && (a.role == IN || a.role == OUT))
@@ -37,7 +46,7 @@ efla_status check_args(std::initializer_list<Arg> args) {
         if ((o.role != OUT && o.role != OUT_OPT) || !o.p || o.bytes == 0) continue;
         const uintptr_t o0 = reinterpret_cast<uintptr_t>(o.p), o1 = o0 + o.bytes;
         for (const Arg &x : args) {
-            if (&x == &o || !x.p || x.bytes == 0 || (x.p == o.p && o.may_be == x.p)) continue;
+            if (&x == &o || !x.p || x.bytes == 0 || may_share(o, x)) continue;
             const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p), x1 = x0 + x.bytes;
             if (o0 < x1 && x0 < o1) return api_fail(EFLA_ERR_INVALID_ARG, "output %s overlaps %s", o.name, x.name);
         }
@@ -94,7 +103,7 @@ efla_status efla_gated_fwd_chunked(const void *q, const void *k, const void *v, 
     s = check_args({{"q", q, kb, IN}, {"k", k, kb, IN}, {"v", v, tok * H * d_v * es(in_dtype), IN}, {"g", g, tok * H * 4, IN},
                     {"beta", beta, tok * H * 4, IN}, {"S0", S0, st, IN_OPT},
                     {"cu_seqlens", cu_seqlens, cu_seqlens ? ((size_t)N + 1) * 4 : 0, IN_OPT},
-                    {"o", o, tok * H * d_v * es(o_dtype), OUT}, {"S_T", S_T, st, OUT_OPT, S0}});
+                    {"o", o, tok * H * d_v * es(o_dtype), OUT}, {"S_T", S_T, st, OUT_OPT, {"S0"}}});
     if (s != EFLA_OK) return s;
     if (N == 0) return api_ok();
     GatedFwdArgs a{q, k, v, g, beta, S0, cu_seqlens, o, S_T, B, T, H_k, H, d_k, d_v, N, in_dtype, o_dtype,
@@ -124,7 +133,7 @@ efla_status efla_gated_fwd_chunked_train(const void *q, const void *k, const voi
     const size_t tok = (size_t)B * T, kb = tok * H_k * d_k * es(in_dtype), vb = tok * H * d_v * es(in_dtype);
     const size_t st = (size_t)B * H * d_k * d_v * 4;
     s = check_args({{"q", q, kb, IN}, {"k", k, kb, IN}, {"v", v, vb, IN}, {"g", g, tok * H * 4, IN},
-                    {"beta", beta, tok * H * 4, IN}, {"S0", S0, st, IN_OPT}, {"o", o, vb, OUT}, {"S_T", S_T, st, OUT_OPT, S0},
+                    {"beta", beta, tok * H * 4, IN}, {"S0", S0, st, IN_OPT}, {"o", o, vb, OUT}, {"S_T", S_T, st, OUT_OPT, {"S0"}},
                     {"workspace", workspace, need, OUT_OPT}});
     if (s != EFLA_OK) return s;
     if (B == 0) return api_ok();
@@ -224,7 +233,7 @@ efla_status efla_gated_prep(const void *q, const void *k, const void *a, const v
     if (s != EFLA_OK) return s;
     const size_t n = (size_t)tokens, kb = n * H_k * d_k * es(dtype), ab = n * H * es(dtype), gb = n * H * 4;
     s = check_args({{"q", q, kb, IN}, {"k", k, kb, IN}, {"a", a, ab, IN}, {"b", b, ab, IN}, {"A_log", A_log, (size_t)H * 4, IN},
-                    {"dt_bias", dt_bias, (size_t)H * 4, IN}, {"q_out", q_out, kb, OUT, q}, {"k_out", k_out, kb, OUT, k},
+                    {"dt_bias", dt_bias, (size_t)H * 4, IN}, {"q_out", q_out, kb, OUT, {"q"}}, {"k_out", k_out, kb, OUT, {"k"}},
                     {"g", g, gb, OUT}, {"beta", beta, gb, OUT}});
     if (s != EFLA_OK) return s;
     MixerPrepArgs p{};
@@ -283,7 +292,7 @@ efla_status efla_norm_gate(const void *o, const void *z, const float *w, void *y
     efla_status s = check_norm(rows, d, dtype, eps);
     if (s != EFLA_OK) return s;
     const size_t n = (size_t)rows * d * es(dtype);
-    s = check_args({{"o", o, n, IN}, {"z", z, n, IN}, {"w", w, (size_t)d * 4, IN}, {"y", y, n, OUT, y == z ? z : o}});
+    s = check_args({{"o", o, n, IN}, {"z", z, n, IN}, {"w", w, (size_t)d * 4, IN}, {"y", y, n, OUT, {"o", "z"}}});
     if (s != EFLA_OK) return s;
     NormGateArgs p{};
     p.o = o, p.z = z, p.w = w, p.y = y, p.rows = rows, p.d = d, p.dtype = dtype, p.eps = eps;

@@ -234,3 +234,29 @@ def test_c_empty_calls_launch_nothing(lib):
     assert lib.efla_norm_gate(None, None, A[2], None, 0, 64, 0, 1e-6, None) == 0
     assert lib.efla_gated_prep(None, None, None, None, A[0], A[1], None, None, None, None, 0, 1, 2, 64, 0, 1.0, 1e-6,
                                None) == 0
+
+
+# ------------------------------------------------------------------------------ which memory an output may share
+def test_c_output_may_be_its_named_input_only(lib):
+    """An output may be the one input that its contract names, not whatever else lies at that address.  (Refused calls
+    only: an accepted one would launch.)"""
+    prep = dict(q=A[0], k=A[1], a=A[2], b=A[3], A=A[4], d=A[5], qo=A[6], ko=A[7], g=A[8], beta=A[9], n=4, Hk=1, H=2, dk=64,
+                t=0, scale=1.0, eps=1e-6, s=None)
+    for kw in (dict(k=A[0], qo=A[0]),                  # rows of q overwritten while they are read as k
+               dict(k=A[0], ko=A[0]),
+               dict(k=A[0], qo=A[0], ko=A[0]),         # two outputs in one place
+               dict(qo=A[6], ko=A[6]), dict(a=A[0], qo=A[0]), dict(A=A[0], qo=A[0])):
+        assert lib.efla_gated_prep(*(prep | kw).values()) == 1, kw
+        assert b"overlaps" in lib.efla_last_error()
+    norm = dict(o=A[0], z=A[1], w=A[2], y=A[3], rows=4, d=64, t=0, eps=1e-6, s=None)
+    for kw in (dict(w=A[0], y=A[0]), dict(w=A[1], y=A[1]), dict(z=A[0], w=A[0], y=A[0])):
+        assert lib.efla_norm_gate(*(norm | kw).values()) == 1, kw
+        assert b"overlaps" in lib.efla_last_error()
+    for kw in (dict(S0=A[2], S_T=A[2]),                # the state over v
+               dict(S0=A[4], S_T=A[4], beta=A[4]), dict(S0=A[6], S_T=A[6], cu=A[6])):
+        assert c_fwd(lib, **kw) == 1, kw
+        assert b"overlaps" in lib.efla_last_error()
+    train = dict(q=A[0], k=A[1], v=A[2], g=A[3], beta=A[4], S0=A[2], o=A[5], S_T=A[2], B=1, T=8, Hk=1, H=2, d=64, e=64,
+                 t=0, u=1, ws=A[10], size=1 << 40, s=None)
+    assert lib.efla_gated_fwd_chunked_train(*train.values()) == 1
+    assert b"overlaps" in lib.efla_last_error()
