@@ -62,9 +62,12 @@ efla_status check_sizes(int B, int T, int Hk, int H, int dk, int dv, efla_dtype 
         return api_fail(EFLA_ERR_UNSUPPORTED, "d_k=%d d_v=%d: supported head sizes are 32, 64, 128", dk, dv);
     if (!dtype_ok(in) || !dtype_ok(out)) return api_fail(EFLA_ERR_INVALID_ARG, "unknown dtype (in=%d, o=%d)", (int)in, (int)out);
     if (u != EFLA_UPDATE_EXACT && u != EFLA_UPDATE_EULER) return api_fail(EFLA_ERR_INVALID_ARG, "unknown update rule %d", (int)u);
-    // (launch grids count units x slabs of 32 columns, and units x chunks, in 31 bits)
-    if ((long long)B * T * H > (1LL << 31) - 1 || (long long)B * H * 4 > (1LL << 31) - 1)
-        return api_fail(EFLA_ERR_UNSUPPORTED, "B*T*H=%lld exceeds 2^31-1 token-heads", (long long)B * T * H);
+    // (launch grids count units x slabs of 32 columns, and units x chunks, in 31 bits; a product of three
+    // sizes may pass 64)
+    constexpr long long MOST = (1LL << 31) - 1;
+    const long long tok = (long long)B * T;
+    if (tok > MOST || tok * H > MOST || (long long)B * H > MOST / 4)
+        return api_fail(EFLA_ERR_UNSUPPORTED, "B=%d T=%d H=%d: more than 2^31-1 token-heads, or 2^29-1 heads of sequences", B, T, H);
     return EFLA_OK;
 }
 
@@ -95,7 +98,7 @@ efla_status efla_gated_fwd_chunked(const void *q, const void *k, const void *v, 
                                    efla_update update, efla_stream_t stream) {
     efla_status s = check_sizes(B, T, H_k, H, d_k, d_v, in_dtype, o_dtype, update);
     if (s != EFLA_OK) return s;
-    if (N < 0 || (long long)N * H * 4 > (1LL << 31) - 1) return api_fail(EFLA_ERR_INVALID_ARG, "bad number of sequences N=%d", N);
+    if (N < 0 || (long long)N * H > ((1LL << 31) - 1) / 4) return api_fail(EFLA_ERR_INVALID_ARG, "bad number of sequences N=%d", N);
     if (cu_seqlens ? B != 1 : N != B)
         return api_fail(EFLA_ERR_INVALID_ARG, cu_seqlens ? "cu_seqlens given with B=%d (must be 1), N=%d"
                                                          : "B=%d, N=%d: N must equal B when cu_seqlens is NULL", B, N);

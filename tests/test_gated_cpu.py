@@ -260,3 +260,11 @@ def test_c_output_may_be_its_named_input_only(lib):
                  t=0, u=1, ws=A[10], size=1 << 40, s=None)
     assert lib.efla_gated_fwd_chunked_train(*train.values()) == 1
     assert b"overlaps" in lib.efla_last_error()
+
+
+@pytest.mark.parametrize("B, T, H", [((1 << 31) - 1, 0, (1 << 31) - 1), ((1 << 31) - 1,) * 3, (1 << 21, 1 << 21, 1 << 22)])
+def test_c_sizes_whose_product_passes_64_bits(lib, B, T, H):
+    """Refused, not wrapped around to a size that looks small."""
+    nb = ctypes.c_size_t(0)
+    assert lib.efla_gated_bwd_workspace(B, T, 1, H, 64, 64, 0, ctypes.byref(nb)) == 2
+    assert b"token-heads" in lib.efla_last_error()
