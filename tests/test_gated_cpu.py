@@ -268,3 +268,26 @@ def test_c_sizes_whose_product_passes_64_bits(lib, B, T, H):
     nb = ctypes.c_size_t(0)
     assert lib.efla_gated_bwd_workspace(B, T, 1, H, 64, 64, 0, ctypes.byref(nb)) == 2
     assert b"token-heads" in lib.efla_last_error()
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """A size that ctypes would cut to its low 32 bits is refused, not taken for a small one (tensors without memory)."""
+    z = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="meta")  # noqa: E731
+    d, f = 2 ** 32 + 32, torch.float32
+    with pytest.raises(efla.EflaError, match="2147483647"):
+        efla.norm_gate(z(1, d), z(1, d), z(d, dtype=f))
+    with pytest.raises(efla.EflaError, match="2147483647"):
+        efla.norm_gate_bwd(z(1, d), z(1, d), z(d, dtype=f), z(1, d))
+    for dk, H in ((d, 4), (32, 2 ** 32 + 4)):
+        q, a, p = z(1, 1, dk), z(1, H), z(H, dtype=f)
+        with pytest.raises(efla.EflaError, match="2147483647"):
+            efla.gated_prep(q, q, a, a, p, p)
+    for dk, dv in ((d, 32), (32, d)):
+        q, v, g = z(1, 1, 1, dk), z(1, 1, 1, dv), z(1, 1, 1, dtype=f)
+        with pytest.raises(efla.EflaError, match="2147483647"):
+            efla.gated_fwd_chunked(q, q, v, g, g, return_state=False)
+    for i in range(6):
+        sizes = [1, 64, 1, 1, 32, 32]
+        sizes[i] += 2 ** 32
+        with pytest.raises(efla.EflaError, match="2147483647"):
+            efla.gated_bwd_workspace(*sizes, torch.bfloat16)
