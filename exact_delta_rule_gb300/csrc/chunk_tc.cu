@@ -102,7 +102,7 @@ constexpr uint32_t SMEM_USED = OFF_MISC_N + 16;
 constexpr uint32_t SMEM_ALLOC_N = SMEM_USED + 1024;       // + alignment slack for the 1024-byte base
 static_assert(OFF_TPP % 1024 == 0 && OFF_AT % 1024 == 0, "operand buffers must be 1024-byte aligned");
 static_assert(SMEM_ALLOC_N <= 232448, "exceeds the 227 KB per-CTA shared memory limit");
-// Gated: the hi and lo of G_t lie in the padding of At's rows (columns 64 and 65), e^{G_t} and c_t of
+// Gated: the two parts of G_t lie in the padding of At's rows (columns 64 and 65), e^{G_t} and c_t of
 // both chunk parities behind the barriers.  This leaves no room for alignment slack: the array itself
 // is declared 1024-byte aligned, and the kernel refuses to run on another base.
 constexpr uint32_t OFF_BAR_G = OFF_ROW + ROW_BYTES;
@@ -479,8 +479,8 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                         float up[2];
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const float2 gq = *reinterpret_cast<const float2 *>(At + (col0 + 16 * q) * AT_LD + 64);
-                            up[q] = pair_decay(gt.x, gt.y, gq.x, gq.y);
+                            const float2 gm = *reinterpret_cast<const float2 *>(At + (col0 + 16 * q + DECAY_MID) * AT_LD + 64);
+                            up[q] = from_quarter(gt.x, gt.y, gm.x, gm.y);
                         }
 #pragma unroll
                         for (int s = 0; s < 32; ++s) g[s] *= up[s >> 4] * At[(col0 + s) * AT_LD + 67];

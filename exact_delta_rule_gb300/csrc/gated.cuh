@@ -146,15 +146,33 @@ __device__ __forceinline__ Sum2 shfl2(Sum2 x, int lane) {
     return {__shfl_sync(0xffffffffu, x.h, lane), __shfl_sync(0xffffffffu, x.l, lane)};
 }
 
+// A sum of gates (log2) as its nearest whole number and the rest, to 2^-25: what is left of a difference
+// of two such pairs keeps that accuracy however far the sums are from 0.
+constexpr float WHOLE = 12582912.f;  // 1.5 2^23: a sum with it is rounded to a whole number, held in its low bits
+__device__ __forceinline__ float2 whole_rest(Sum2 G) {
+    const float n = (G.h + WHOLE) - WHOLE;
+    return make_float2(n, (G.h - n) + G.l);
+}
+// 2^(a - b) of two such pairs to the accuracy of ex2 (as one float an exponent of 64 or more is 2^-18 off):
+// the whole part goes into the exponent by itself.  0 below 2^-127, infinity from 2^128.
+__device__ __forceinline__ float from_quarter(float na, float ra, float nb, float rb) {
+    const uint32_t n = __float_as_uint(fminf(fmaxf(na - nb, -127.f), 128.f) + WHOLE);
+    return ex2(ra - rb) * __uint_as_float((n + 127u) << 23);
+}
+
 // The decays of a chunk's 64 tokens from its gates (0 past the chunk's end), by one warp: lane l holds
-// tokens 2 l and 2 l + 1.  Writes, token t at [t stride], the two floats of G_t (log2) to gh and gl, and
-// to dn e^{G_q - G_t} with q the first token of t's quarter of 16; to eg[t] e^{G_t} and to ec[t]
-// e^{G_C - G_t}.  Returns (in every lane) whether every dn is below 2^100: then Gamma_ts = e^{G_t - G_q}
-// dn_s for s in quarter q and t >= s costs a product an entry; otherwise pair_decay takes the
-// difference of the sums, an exponential an entry.
+// tokens 2 l and 2 l + 1.  Writes, token t at [t stride], G_t (log2) as whole_rest to gw and gr, and to dn
+// e^{G_m - G_t} with m = DECAY_MID the ninth token of t's quarter of 16; to eg[t] e^{G_t} and to ec[t]
+// e^{G_C - G_t}.  Returns (in every lane) whether every dn lies between 2^-100 and 2^60: then Gamma_ts =
+// e^{G_t - G_m} dn_s for s in quarter m and t >= s costs a product an entry (from_quarter gives the first
+// factor); otherwise pair_decay takes the difference of the sums, an exponential an entry.
+// Within these bounds neither factor overflows for t >= s, and the first one's underflow (2^-126) leaves
+// out only Gamma below 2^-66.  Measured from its middle a quarter may decay by up to 2^120.
 // The running sum is kept to about 2^-46: a plain 32-bit sum of 64 gates of size 2 is off by 2^-17 in
-// the exponent, more than every other rounding of the chunk.
-__device__ __forceinline__ bool chunk_decay(float g0, float g1, int lane, float *gh, float *gl, float *dn, int stride,
+// the exponent, more than every other rounding of the chunk.  For the same reason the exponents of the two
+// factors, which may both be far from 1 where their product is not, are taken in two parts.
+constexpr int DECAY_MID = 8;
+__device__ __forceinline__ bool chunk_decay(float g0, float g1, int lane, float *gw, float *gr, float *dn, int stride,
                                             float *eg, float *ec) {
     const Sum2 a = gate2(g0), b = gate2(g1);
     Sum2 G1 = add2(a, b);
@@ -166,20 +184,23 @@ __device__ __forceinline__ bool chunk_decay(float g0, float g1, int lane, float 
     Sum2 G0 = shfl_up2(G1, 1);  // G_{2 l - 1}
     if (lane == 0) G0 = {0.f, 0.f};
     G0 = add2(G0, a);
-    const Sum2 last = shfl2(G1, 31), q = shfl2(G0, lane & 24);
-    const float d0 = ex2(diff2(q, G0)), d1 = ex2(diff2(q, G1));
+    const float2 w0 = whole_rest(G0), w1 = whole_rest(G1);
+    const int mid = (lane & 24) + DECAY_MID / 2;
+    const float mn = __shfl_sync(0xffffffffu, w0.x, mid), mr = __shfl_sync(0xffffffffu, w0.y, mid);
+    const float d0 = from_quarter(mn, mr, w0.x, w0.y), d1 = from_quarter(mn, mr, w1.x, w1.y);
+    const Sum2 last = shfl2(G1, 31);
     const int t = 2 * lane;
-    gh[t * stride] = G0.h;
-    gh[(t + 1) * stride] = G1.h;
-    gl[t * stride] = G0.l;
-    gl[(t + 1) * stride] = G1.l;
+    gw[t * stride] = w0.x;
+    gw[(t + 1) * stride] = w1.x;
+    gr[t * stride] = w0.y;
+    gr[(t + 1) * stride] = w1.y;
     dn[t * stride] = d0;
     dn[(t + 1) * stride] = d1;
     eg[t] = ex2(G0.h + G0.l);
     eg[t + 1] = ex2(G1.h + G1.l);
     ec[t] = ex2(diff2(last, G0));
     ec[t + 1] = ex2(diff2(last, G1));
-    return __all_sync(0xffffffffu, d0 < 0x1p100f && d1 < 0x1p100f);
+    return __all_sync(0xffffffffu, fminf(d0, d1) > 0x1p-100f && fmaxf(d0, d1) < 0x1p60f);
 }
 
 // The same for a block of 16 tokens, one per lane (lanes 16-31 take part with g = 0 and write nothing).
@@ -202,7 +223,7 @@ __device__ __forceinline__ void block_decay16(float g, int lane, float *gh, floa
 // d alpha_t as (dY U^T)_tt / alpha_t; with U_t proportional to alpha_t that is exact for any alpha but 0,
 // and a step of 2^-90 changes no output.
 __device__ __forceinline__ float live_beta(float b) { return fabsf(b) < 0x1p-90f ? copysignf(0x1p-90f, b) : b; }
-// Gamma_ts from the two sums.
+// Gamma_ts from the two sums, each given in two parts (whole_rest, or the two floats of a Sum2).
 __device__ __forceinline__ float pair_decay(float ht, float lt, float hs, float ls) { return ex2((ht - hs) + (lt - ls)); }
 
 }  // namespace efla

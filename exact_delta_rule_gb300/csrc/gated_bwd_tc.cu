@@ -73,7 +73,7 @@ constexpr uint32_t OFF_DO = 32768;       // within a stage
 constexpr uint32_t OFF_TPP = NSTAGE * STAGE_BYTES;  // per chunk parity: T hi, lo, P hi, lo, [64][64] bf16 each
 constexpr uint32_t TPP_BYTES = 32768;
 constexpr uint32_t OFF_DRS = OFF_TPP + 2 * TPP_BYTES;  // dv on its way to HBM, [2 cb][64 rows][64]
-constexpr uint32_t OFF_DEC = OFF_DRS + 16384;      // {G hi, lo, dn, -} [64], then of four chunks e^G [64], c [64], alpha [64]
+constexpr uint32_t OFF_DEC = OFF_DRS + 16384;      // {G whole, rest, dn, -} [64], then of four chunks e^G [64], c [64], alpha [64]
 constexpr uint32_t DEC_LD = 192;
 constexpr uint32_t OFF_BAR = OFF_DEC + 1024 + 4 * DEC_LD * 4;
 constexpr uint32_t OFF_MISC = OFF_BAR + 256;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
                     float x[16];
                     tmem_ld16(lane_base + TM_G + 16 * q, x);
                     const float *gs = gsum + 64 * q;
-                    const float up = pair_decay(gt.x, gt.y, gs[0], gs[1]);
+                    const float up = from_quarter(gt.x, gt.y, gs[4 * DECAY_MID], gs[4 * DECAY_MID + 1]);
                     tmem_ld_wait();
                     if (fast) {
 #pragma unroll
@@ -627,7 +627,7 @@ constexpr uint32_t OFF_PART = OFF_ROD + 64 * DL_LD * 4;  // fp32 [2][16 warps][3
 static_assert(64 * DL_LD * 4 + (2 * 16 * 32 + 512 + 6 * 64) * 4 <= 32768 && OFF_PART % 16 == 0, "scratch leaves its region");
 
 struct RowData {
-    float4 g[C];              // G_t hi, lo and dn_t (chunk_decay), d alpha / d beta
+    float4 g[C];              // G_t (whole_rest) and dn_t (chunk_decay), d alpha / d beta
     float eg[C], ec[C];
     float al[C], dadl[C];
     float gate[C], beta[C];   // the next item's, copied in asynchronously
@@ -956,8 +956,8 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
         auto times_gamma = [&](float (&x)[16]) {
             const float4 gt = R.g[tr];
             if (*fast_flag) {
-                const float4 gq = R.g[col0];
-                const float up = pair_decay(gt.x, gt.y, gq.x, gq.y);
+                const float4 gm = R.g[col0 + DECAY_MID];
+                const float up = from_quarter(gt.x, gt.y, gm.x, gm.y);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[e] *= up * R.g[col0 + e].z;
             } else {

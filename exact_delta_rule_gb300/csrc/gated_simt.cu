@@ -65,7 +65,7 @@ __device__ __forceinline__ void load_mat(float *dst, int ld, const float *src, s
 
 // Per-token quantities of a chunk in shared memory.
 struct Rows {
-    float gh[C], gl[C], dn[C], eg[C], ec[C];  // chunk_decay
+    float gw[C], gr[C], dn[C], eg[C], ec[C];  // chunk_decay
     float al[C], invn[C], gn[C];         // alpha, 1/n, gamma/n
     float dadb[C], dadl[C], lam[C], bt[C];
 };
@@ -78,7 +78,7 @@ __device__ __forceinline__ void load_gates(const A &a, Rows &R, size_t row0, int
         const int t = 2 * tid;
         const float g0 = t < valid ? a.g[row0 + (size_t)t * a.H] : 0.f;
         const float g1 = t + 1 < valid ? a.g[row0 + (size_t)(t + 1) * a.H] : 0.f;
-        chunk_decay(g0, g1, tid, R.gh, R.gl, R.dn, 1, R.eg, R.ec);
+        chunk_decay(g0, g1, tid, R.gw, R.gr, R.dn, 1, R.eg, R.ec);
     } else if (tid >= 64 && tid < 64 + C) {
         const int t = tid - 64;
         R.bt[t] = t < valid ? a.beta[row0 + (size_t)t * a.H] : 0.f;
@@ -136,7 +136,7 @@ __device__ __forceinline__ void chunk_matrices(const float *Ks, const float *Qs,
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int t = r4 + 16 * r, s = c4 + 16 * c;
-            const float d = s <= t ? pair_decay(R.gh[t], R.gl[t], R.gh[s], R.gl[s]) : 0.f;
+            const float d = s <= t ? pair_decay(R.gw[t], R.gr[t], R.gw[s], R.gr[s]) : 0.f;
             const float l = s < t ? d * kk[r][c] : 0.f;
             if (Ab) Ab[t * LC + s] = l;
             Pm[t * LC + s] = s <= t ? d * qk[r][c] : 0.f;
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(NT, 1) gated_bwd_grad_kernel(GatedBwdArgs a, G
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
             const int t = r4 + 16 * r, s = c4 + 16 * cc;
-            const float d = s <= t ? pair_decay(R.gh[t], R.gl[t], R.gh[s], R.gl[s]) : 0.f;
+            const float d = s <= t ? pair_decay(R.gw[t], R.gr[t], R.gw[s], R.gr[s]) : 0.f;
             Ms[t * LC + s] = s < t ? fmaf(dP[r][cc], Pm[t * LC + s], -dLr[r][cc] * Ab[t * LC + s]) : 0.f;
             Pm[t * LC + s] = s <= t ? d * dP[r][cc] : 0.f;
             W[t * LC + s] = s < t ? -d * dLr[r][cc] : 0.f;

@@ -627,3 +627,74 @@ def test_offsets_past_32_bits():
     p, want = efla.gated_prep(heads, heads, a, a, A, A), efla.gated_prep(*last(heads, heads, a, a), A, A)
     assert all(torch.equal(p[n][-1:], want[n]) for n in p)
     assert efla.device_status() == 0
+
+
+# ------------------------------------------------------------------------------ decays inside a quarter of a chunk
+def quarters(H, seed):
+    """Gates of 64 tokens of H heads [1, 64, H]: by heads in turn, one strong gate in every 16 tokens among weak ones
+    (2^64 to 2^100 of decay; 2^40 to 2^66), and a steady decay of 2^5.2 to 2^6.6 a token."""
+    gen = torch.Generator().manual_seed(seed)
+    u = lambda lo, hi, *s: lo + (hi - lo) * torch.rand(s, generator=gen, dtype=torch.float64)  # noqa: E731
+    g = u(-0.3, 0.0, H, 4, 16)
+    at = torch.randint(0, 16, (H, 4, 1), generator=gen)
+    strong = torch.where(torch.arange(H)[:, None, None] % 3 == 0, u(-69.0, -45.0, H, 4, 1), u(-45.0, -28.0, H, 4, 1))
+    g.scatter_(2, at, strong)
+    g[2::3] = u(-4.6, -3.6, *g[2::3].shape)
+    return g.reshape(H, 64).t()[None].float().contiguous().cuda()
+
+
+def one_hot_tokens(H, d, seed):
+    """k_t = e_t, v_t = e_t, q_t = 1, beta = 1: u_t = e_t without rounding, so that o_t[s] = Gamma_ts."""
+    e = torch.eye(64, d, device="cuda", dtype=BF16)
+    k = e[None, :, None]
+    g = quarters(H, seed)
+    G = g[0].double().cumsum(0).t()  # [H, 64]
+    gamma = (G[:, :, None] - G[:, None, :]).tril().exp().tril()  # [H, t, s]
+    x = {"q": torch.ones_like(k), "k": k, "v": e[None, :, None].expand(1, 64, H, d).contiguous(), "g": g,
+         "beta": torch.ones_like(g), "S0": None}
+    return x, gamma
+
+
+def gamma_off(got, gamma, t):
+    """The worst of |got - gamma| over its tolerance: t, and 2^-23 for each power of two below one (two roundings of the
+    exponent); below 2^-60 anything up to 2^-60."""
+    got = got.double()
+    rel = t + 2.0 ** -23 * gamma.clamp(min=2.0 ** -60).log2().abs()
+    return float(((got - gamma).abs() / (rel * gamma + 2.0 ** -60)).max())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_forward_decays_within_a_quarter(d):
+    """Every Gamma_ts by itself.  Two exponentials of 2^-22, four fp32 roundings and P in two bf16 parts (each rounded by
+    half a step: 2^-17 of its value at most)."""
+    x, gamma = one_hot_tokens(96, d, 7)
+    o, _ = efla.gated_fwd_chunked(**x, o_dtype=F32)
+    assert gamma_off(o[0, :, :, :64].permute(1, 0, 2), gamma, 2.0 ** -17 + 2.0 ** -20) <= 1
+    assert bool((o[..., 64:] == 0).all()) and efla.device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_decays_within_a_quarter(d):
+    """One entry of dO a head, (t, s): dg is Gamma_ts between s and t (no operand of it is split: two exponentials and four
+    roundings), dbeta_s is Gamma_ts (through P, G and dY, each in two bf16 parts), and column s of dv is Gamma's row t (bf16)."""
+    H = 288
+    x, gamma = one_hot_tokens(H, d, 11)
+    gen = torch.Generator().manual_seed(3)
+    s = torch.randint(0, 54, (H,), generator=gen)
+    s[::4] = 16 * torch.randint(0, 3, (len(s[::4]),), generator=gen) + 15  # a quarter's last token
+    t = s + torch.randint(1, 10, (H,), generator=gen)
+    h = torch.arange(H)
+    want = gamma[h, t, s].cuda()
+    dO = torch.zeros_like(x["v"])
+    dO[0, t, h, s] = 1
+    ws = efla.gated_fwd_chunked_train(**x)[2]
+    got = efla.gated_bwd_chunked(*x.values(), dO, workspace=ws, saved=True)
+    r = torch.arange(64, device="cuda")[:, None]
+    s, t = s.cuda(), t.cuda()
+    ref = torch.where((r > s) & (r <= t), want, 0.0)  # [64, H]
+    assert gamma_off(got["dg"][0], ref, 2.0 ** -20) <= 1
+    assert gamma_off(got["dbeta"][0], torch.where(r == s, want, 0.0), 3 * 2.0 ** -17 + 2.0 ** -19) <= 1
+    dv = torch.zeros(64, H, d, device="cuda", dtype=torch.float64)
+    dv[:, h.cuda(), s] = gamma[h, t.cpu()].cuda().t()  # (every token up to t is read by q_t)
+    assert gamma_off(got["dv"][0], dv, 2.0 ** -8 + 3 * 2.0 ** -17 + 2.0 ** -19) <= 1
+    assert efla.device_status() == 0
