@@ -223,6 +223,12 @@ __device__ __forceinline__ void block_decay16(float g, int lane, float *gh, floa
 // d alpha_t as (dY U^T)_tt / alpha_t; with U_t proportional to alpha_t that is exact for any alpha but 0,
 // and a step of 2^-90 changes no output.
 __device__ __forceinline__ float live_beta(float b) { return fabsf(b) < 0x1p-90f ? copysignf(0x1p-90f, b) : b; }
+// alpha as the tensor-core backward takes it: the exact gate's is beta itself where beta lambda is so small
+// that the difference is lost (2^-25), as (1 - e^{-beta lambda}) / lambda is 0 once beta lambda is below the
+// smallest float.
+__device__ __forceinline__ float live_alpha(float b, float lam, int euler) {
+    return euler || fabsf(b * lam) < 0x1p-25f ? b : efla_alpha(b, lam, 0);
+}
 // Gamma_ts from the two sums, each given in two parts (whole_rest, or the two floats of a Sum2).
 __device__ __forceinline__ float pair_decay(float ht, float lt, float hs, float ls) { return ex2((ht - hs) + (lt - ls)); }
 

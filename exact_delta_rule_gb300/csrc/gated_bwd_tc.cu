@@ -4,7 +4,7 @@
 // T = (I + diag(alpha) L)^{-1}.  The formulas are in gated_simt.cu; here they are taken through
 //   dY = T^T G,  dR = diag(alpha) dY,  U = T diag(alpha) R,
 // which needs no second matrix and gives dalpha without forming Z = R - L U or keeping G:
-//   dalpha_t = dY_t . Z_t = (dY U^T)_tt / alpha_t         (live_beta keeps alpha off 0)
+//   dalpha_t = dY_t . Z_t = (dY U^T)_tt / alpha_t         (live_beta, live_alpha keep alpha off 0)
 //
 // 1. State pass (state_kernel): one CTA per (b, h) walks the chunks in reverse with dS^T fp32 in TMEM,
 //    lane j = column j of d_v, everything transposed as in the forward:
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
 #pragma unroll
                     for (int s = 0; s < 32; ++s) lam = s == lane ? x[s] : lam;
                 }
-                eg[128 + row] = efla_alpha(live_beta(bcur), lam, EULER);  // (dY is 0 past the end)
+                eg[128 + row] = live_alpha(live_beta(bcur), lam, EULER);  // (dY is 0 past the end)
             }
             if (named_bar_any(BAR_PREP, 128, !ok || *abort_flag)) {  // decays visible; also spreads an abort
                 *abort_flag = 1;
@@ -1063,7 +1063,7 @@ __global__ void __launch_bounds__(NTH, 1) grad_kernel(const __grid_constant__ Pa
                         gate_grad(bt, lam, 0, db, dl);
                         R.g[ln].w = db;
                         R.dadl[ln] = dl;
-                        R.al[ln] = efla_alpha(bt, lam, 0);
+                        R.al[ln] = live_alpha(bt, lam, 0);
                     }
                 }
                 if (!above) {

@@ -698,3 +698,16 @@ def test_backward_decays_within_a_quarter(d):
     dv[:, h.cuda(), s] = gamma[h, t.cpu()].cuda().t()  # (every token up to t is read by q_t)
     assert gamma_off(got["dv"][0], dv, 2.0 ** -8 + 3 * 2.0 ** -17 + 2.0 ** -19) <= 1
     assert efla.device_status() == 0
+
+
+# ------------------------------------------------------------------------------ exact gate, tokens that write next to nothing
+@pytest.mark.parametrize("dk, dv", [(128, 128), (64, 32)])
+@pytest.mark.parametrize("size, beta", [(1e-10, 0.0), (1e-14, 1e-20), (1e-10, 1.0)])
+def test_backward_exact_gate_of_vanishing_keys(dk, dv, size, beta):
+    """beta lambda below the smallest fp32 number: alpha is beta, and its gradients are finite."""
+    x = make(B=1, T=130, dk=dk, dv=dv, dtype=BF16, seed=3)
+    x["k"][:, ::3] *= size
+    x["beta"][:, ::2] = beta
+    check_fwd(x, "exact")
+    check_bwd(x, "exact")
+    check_bwd(x)
