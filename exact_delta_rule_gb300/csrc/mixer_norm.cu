@@ -4,7 +4,7 @@
 //   q^ = scale q r_q, k^ = k r_k,  r = rsqrt(||x||^2 + eps)
 //   g = -e^{A_log} softplus(a + dt_bias),  beta = sigmoid(b)
 //   dx = r (dy' - x^ (x^ . dy')) with x^ = r x, dy' = dy (times scale for q)
-//   da = -dg e^{A_log} sigmoid(a + dt_bias),  db = dbeta beta (1 - beta)
+//   da = -dg e^{A_log} sigmoid(a + dt_bias),  db = dbeta sigmoid(b) sigmoid(-b)
 //   dA_log = sum dg g,  ddt_bias = sum da              (over the tokens of a head)
 // After it (rows of d): with n = o r, r = rsqrt(mean(o^2) + eps), s = sigmoid(z)
 //   y = n w z s;  dn = dy w z s,  do = r (dn - n mean(dn n)),  dz = dy n w s (1 + z (1 - s)),
@@ -170,10 +170,11 @@ __global__ void __launch_bounds__(NT) prep_bwd_kernel(MixerPrepArgs p, unsigned 
             const long long e = tok * p.H + h;
             const float t = to_f32(static_cast<const T *>(p.a)[e]) + bias, b = to_f32(static_cast<const T *>(p.b)[e]);
             const float dg = p.dg_in[e], dbeta = p.dbeta_in[e];
-            const float g = -rate * (fmaxf(t, 0.f) + log1pf(expf(-fabsf(t)))), beta = 1.f / (1.f + expf(-b));
+            const float g = -rate * (fmaxf(t, 0.f) + log1pf(expf(-fabsf(t))));
+            const float eb = expf(-fabsf(b)), c = 1.f / (1.f + eb);  // (1 - sigmoid(b) would cancel for large b)
             const float da = -dg * rate / (1.f + expf(-t));
             static_cast<T *>(p.da_out)[e] = from_f32<T>(da);
-            static_cast<T *>(p.db_out)[e] = from_f32<T>(dbeta * beta * (1.f - beta));
+            static_cast<T *>(p.db_out)[e] = from_f32<T>(dbeta * (eb * c) * c);
             sA = fmaf(dg, g, sA);
             sD += da;
         }

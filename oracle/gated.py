@@ -94,7 +94,7 @@ def prep(q, k, a, b, A_log, dt_bias, scale=1.0, eps=1e-6):
 
 def prep_bwd(q, k, a, b, A_log, dt_bias, dq, dk, dg, dbeta, scale=1.0, eps=1e-6):
     out = prep(q, k, a, b, A_log, dt_bias, scale, eps)
-    q, k, a, dq, dk, dg, dbeta, A_log, dt_bias = _f64(q, k, a, dq, dk, dg, dbeta, A_log, dt_bias)
+    q, k, a, b, dq, dk, dg, dbeta, A_log, dt_bias = _f64(q, k, a, b, dq, dk, dg, dbeta, A_log, dt_bias)
 
     def grad(x, dy):
         n = torch.sqrt((x * x).sum(-1, keepdim=True) + eps)
@@ -102,7 +102,7 @@ def prep_bwd(q, k, a, b, A_log, dt_bias, dq, dk, dg, dbeta, scale=1.0, eps=1e-6)
 
     da = -dg * torch.exp(A_log) / (1 + torch.exp(-(a + dt_bias)))
     lead = tuple(range(a.dim() - 1))
-    return {"dq": scale * grad(q, dq), "dk": grad(k, dk), "da": da, "db": dbeta * out["beta"] * (1 - out["beta"]),
+    return {"dq": scale * grad(q, dq), "dk": grad(k, dk), "da": da, "db": dbeta * out["beta"] / (1 + torch.exp(b)),
             "dA_log": (dg * out["g"]).sum(lead), "ddt_bias": da.sum(lead)}
 
 

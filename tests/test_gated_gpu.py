@@ -711,3 +711,19 @@ def test_backward_exact_gate_of_vanishing_keys(dk, dv, size, beta):
     check_fwd(x, "exact")
     check_bwd(x, "exact")
     check_bwd(x)
+
+
+# ------------------------------------------------------------------------------ saturated gates
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_prep_gradient_of_saturated_gates(dtype):
+    """db = dbeta sigmoid(b) sigmoid(-b), relative to each value.  An exponential and a division within 2 steps of 2^-24, and
+    four roundings."""
+    b = torch.tensor([0.0, 0.5, 3.0, 9.0, 12.0, 15.0, 17.5, 30.0, 60.0, 80.0], device="cuda")
+    b = torch.cat([b, -b])[None].to(dtype)  # one token, 20 heads
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q, dbeta = torch.ones(1, 1, 32, device="cuda", dtype=dtype), torch.randn(1, 20, generator=gen, device="cuda")
+    A = torch.zeros(20, device="cuda")
+    db = efla.gated_prep_bwd(q, q, b, b, A, A, q, q, dbeta, dbeta)["db"].double()
+    ref = dbeta.double() * torch.sigmoid(b.double()) * torch.sigmoid(-b.double())
+    t = 2.0 ** -20 + (2.0 ** -8 if dtype == BF16 else 0.0)
+    assert bool(((db - ref).abs() <= t * ref.abs()).all()), (db / ref - 1).abs().max()
