@@ -50,10 +50,11 @@ def _bad(msg: str):
     raise EflaError(1, msg)
 
 
-def _c_ints(*sizes: int):
-    """Sizes that a C int holds (ctypes would pass the low 32 bits of any other)."""
-    if max(sizes) > 2147483647:
-        _bad(f"a size of {max(sizes)} exceeds 2147483647")
+_INT_MAX = 2147483647  # ctypes would pass the low 32 bits of a larger size
+
+
+def _too_large(*sizes: int):
+    _bad(f"a size of {max(sizes)} exceeds {_INT_MAX}")
 
 
 def _need(name: str, t: torch.Tensor, shape, dtype, like: torch.Tensor):
@@ -126,7 +127,8 @@ def _heads(q, k, v, g, beta, lead: int):
     qs = q.shape
     *at, Hk, dk = qs
     H, dv = v.shape[lead:]
-    _c_ints(*qs, H, dv)
+    if dk > _INT_MAX or dv > _INT_MAX or H > _INT_MAX:
+        _too_large(dk, dv, H)
     if Hk < 1 or H % Hk:
         _bad(f"v's {H} heads must be a multiple of q's and k's {Hk}")
     per_head = (*at, H)
@@ -192,7 +194,8 @@ def gated_bwd_workspace(B: int, T: int, Hk: int, H: int, dk: int, dv: int, dtype
     """Workspace bytes of ``gated_fwd_chunked_train`` and ``gated_bwd_chunked``."""
     if dtype not in _DT:
         _bad(f"unsupported dtype {dtype}")
-    _c_ints(B, T, Hk, H, dk, dv)
+    if max(B, T, Hk, H, dk, dv) > _INT_MAX:
+        _too_large(B, T, Hk, H, dk, dv)
     n = _sz(0)
     _check(_lib().efla_gated_bwd_workspace(B, T, Hk, H, dk, dv, _DT[dtype], ctypes.byref(n)))
     return n.value
@@ -294,7 +297,8 @@ def _prep_args(q, k, a, b, A_log, dt_bias):
     if q.dim() < 3 or a.dim() != q.dim() - 1:
         _bad(f"q must be [..., H_k, dk] and a [..., H], got {list(q.shape)} and {list(a.shape)}")
     lead, H = tuple(q.shape[:-2]), a.shape[-1]
-    _c_ints(*q.shape[-2:], H)
+    if H > _INT_MAX or q.shape[-1] > _INT_MAX:
+        _too_large(H, q.shape[-1])
     _need("q", q, q.shape, q.dtype, q)
     _need("k", k, q.shape, q.dtype, q)
     _need("a", a, (*lead, H), q.dtype, q)
@@ -354,7 +358,8 @@ def _norm_args(o, z, w):
         _bad("o must have at least one dimension")
     code = _first("o", o, o.dim())
     d = o.shape[-1]
-    _c_ints(d)
+    if d > _INT_MAX:
+        _too_large(d)
     _need("o", o, o.shape, o.dtype, o)
     _need("z", z, o.shape, o.dtype, o)
     _need("w", w, (d,), torch.float32, o)
