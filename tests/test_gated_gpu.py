@@ -727,3 +727,25 @@ def test_prep_gradient_of_saturated_gates(dtype):
     ref = dbeta.double() * torch.sigmoid(b.double()) * torch.sigmoid(-b.double())
     t = 2.0 ** -20 + (2.0 ** -8 if dtype == BF16 else 0.0)
     assert bool(((db - ref).abs() <= t * ref.abs()).all()), (db / ref - 1).abs().max()
+
+
+# ------------------------------------------------------------------------------ packed sequences around malformed bounds
+@pytest.mark.parametrize("dtype, d", [(F32, 32), (BF16, 64), (BF16, 128)])
+@pytest.mark.parametrize("bounds", [[0, 40, 200, 100], [-5, 10, 40, 100], [0, 70, 60, 60]])
+def test_forward_packed_around_bad_bounds(dtype, d, bounds):
+    """The sequences beside a malformed one are computed, and tokens of no sequence are left as they were."""
+    x = make(B=1, T=100, N=3, dk=d, dv=d, dtype=dtype)
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    S_T, o = torch.full((3, 4, d, d), 7.0, device="cuda"), torch.full((1, 100, 4, d), 7.0, device="cuda", dtype=dtype)
+    efla.gated_fwd_chunked(**x, cu_seqlens=cu, o=o, S_T=S_T)
+    assert efla.device_status() == 1
+    free = torch.ones(100, dtype=torch.bool)
+    for n, (a, b) in enumerate(zip(bounds, bounds[1:])):
+        if 0 <= a <= b <= 100:
+            free[a:b] = False
+            ro, rS = gated.fwd(**{m: y[n:n + 1] if m == "S0" else y[:, a:b] for m, y in x.items()})
+            close(o[:, a:b], ro, tol(dtype, d, d), f"o of sequence {n}")
+            close(S_T[n:n + 1], rS, tol(dtype, d, d), f"S_T of sequence {n}")
+        else:
+            assert bool((S_T[n] == 7).all())
+    assert bool((o[:, free] == 7).all())
