@@ -145,7 +145,7 @@ struct TcParams {
     int *status;
     int B, T, H, N;
     int euler;  // 1: delta-rule gate (gamma = beta * lambda)
-    // Sequences split into segments (seg_len > 0; rows of [B, T] only, no cu_seqlens):
+    // Sequences split into segments (seg_len > 0; rows of [B, T] only, no cu_seqlens; not gated):
     //   map launch (maps != nullptr): CTAs (pass, b, g < G-1, h); pass 0 runs segment g from
     //     S = I with v = 0, pass 1 from S = 0; neither writes o; S_T goes to maps[pass][b][g][h].
     //   output launch: CTAs (b, g, h) start from s_in[b][g][h]; only g = G-1 writes S_T[b][h].
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
     int mode = 0;                    // 0: forward; 1: map from S = I, v = 0; 2: map from S = 0
     const float *s0p = nullptr;      // this CTA's start state (nullptr: zero)
     float *stp = nullptr;            // where this CTA's final state goes (nullptr: nowhere)
-    if (p.seg_len > 0) {  // a segment of a split sequence
+    if (!GATED && p.seg_len > 0) {  // a segment of a split sequence
         int idx = blockIdx.x;
         const int Gu = p.maps ? p.G - 1 : p.G;
         if (p.maps) {

@@ -55,7 +55,6 @@ struct GatedDecodeArgs {
     efla_dtype in_dtype, o_dtype;
     int euler;
     cudaStream_t stream;
-    int *status;
 };
 
 // Workspace of the backward (bytes from its base, every region 256-byte aligned).  nc = ceil(T / 64).
@@ -165,7 +164,8 @@ __device__ __forceinline__ float from_quarter(float na, float ra, float nb, floa
 // e^{G_m - G_t} with m = DECAY_MID the ninth token of t's quarter of 16; to eg[t] e^{G_t} and to ec[t]
 // e^{G_C - G_t}.  Returns (in every lane) whether every dn lies between 2^-100 and 2^60: then Gamma_ts =
 // e^{G_t - G_m} dn_s for s in quarter m and t >= s costs a product an entry (from_quarter gives the first
-// factor); otherwise pair_decay takes the difference of the sums, an exponential an entry.
+// factor); otherwise, and without dn (nullptr), pair_decay takes the difference of the sums, an exponential an
+// entry.
 // Within these bounds neither factor overflows for t >= s, and the first one's underflow (2^-126) leaves
 // out only Gamma below 2^-66.  Measured from its middle a quarter may decay by up to 2^120.
 // The running sum is kept to about 2^-46: a plain 32-bit sum of 64 gates of size 2 is off by 2^-17 in
@@ -185,21 +185,22 @@ __device__ __forceinline__ bool chunk_decay(float g0, float g1, int lane, float 
     if (lane == 0) G0 = {0.f, 0.f};
     G0 = add2(G0, a);
     const float2 w0 = whole_rest(G0), w1 = whole_rest(G1);
-    const int mid = (lane & 24) + DECAY_MID / 2;
-    const float mn = __shfl_sync(0xffffffffu, w0.x, mid), mr = __shfl_sync(0xffffffffu, w0.y, mid);
-    const float d0 = from_quarter(mn, mr, w0.x, w0.y), d1 = from_quarter(mn, mr, w1.x, w1.y);
     const Sum2 last = shfl2(G1, 31);
     const int t = 2 * lane;
     gw[t * stride] = w0.x;
     gw[(t + 1) * stride] = w1.x;
     gr[t * stride] = w0.y;
     gr[(t + 1) * stride] = w1.y;
-    dn[t * stride] = d0;
-    dn[(t + 1) * stride] = d1;
     eg[t] = ex2(G0.h + G0.l);
     eg[t + 1] = ex2(G1.h + G1.l);
     ec[t] = ex2(diff2(last, G0));
     ec[t + 1] = ex2(diff2(last, G1));
+    if (!dn) return false;
+    const int mid = (lane & 24) + DECAY_MID / 2;
+    const float mn = __shfl_sync(0xffffffffu, w0.x, mid), mr = __shfl_sync(0xffffffffu, w0.y, mid);
+    const float d0 = from_quarter(mn, mr, w0.x, w0.y), d1 = from_quarter(mn, mr, w1.x, w1.y);
+    dn[t * stride] = d0;
+    dn[(t + 1) * stride] = d1;
     return __all_sync(0xffffffffu, fminf(d0, d1) > 0x1p-100f && fmaxf(d0, d1) < 0x1p60f);
 }
 

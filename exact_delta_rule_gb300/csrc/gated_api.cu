@@ -196,7 +196,7 @@ static efla_status decode(const void *q, const void *k, const void *v, const flo
     if (s != EFLA_OK) return s;
     if (tok == 0) return api_ok();
     GatedDecodeArgs a{q, k, v, g, beta, S, o, B, m, H_k, H, d_k, d_v, in_dtype, o_dtype, update == EFLA_UPDATE_EULER,
-                      reinterpret_cast<cudaStream_t>(stream), nullptr};
+                      reinterpret_cast<cudaStream_t>(stream)};
     if (step) return launched(launch_gated_decode_step(a), "gated decode kernel launch");
     const char *why = "gated decode-tokens kernel launch";
     const cudaError_t e = gated_tc(in_dtype) && d_k == 128 && d_v == 128 ? launch_gated_decode_tokens_tc(a, &why) : launch_gated_decode_tokens(a);

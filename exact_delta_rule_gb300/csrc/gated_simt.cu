@@ -65,7 +65,7 @@ __device__ __forceinline__ void load_mat(float *dst, int ld, const float *src, s
 
 // Per-token quantities of a chunk in shared memory.
 struct Rows {
-    float gw[C], gr[C], dn[C], eg[C], ec[C];  // chunk_decay
+    float gw[C], gr[C], eg[C], ec[C];  // chunk_decay
     float al[C], invn[C], gn[C];         // alpha, 1/n, gamma/n
     float dadb[C], dadl[C], lam[C], bt[C];
 };
@@ -78,7 +78,7 @@ __device__ __forceinline__ void load_gates(const A &a, Rows &R, size_t row0, int
         const int t = 2 * tid;
         const float g0 = t < valid ? a.g[row0 + (size_t)t * a.H] : 0.f;
         const float g1 = t + 1 < valid ? a.g[row0 + (size_t)(t + 1) * a.H] : 0.f;
-        chunk_decay(g0, g1, tid, R.gw, R.gr, R.dn, 1, R.eg, R.ec);
+        chunk_decay(g0, g1, tid, R.gw, R.gr, nullptr, 1, R.eg, R.ec);
     } else if (tid >= 64 && tid < 64 + C) {
         const int t = tid - 64;
         R.bt[t] = t < valid ? a.beta[row0 + (size_t)t * a.H] : 0.f;
