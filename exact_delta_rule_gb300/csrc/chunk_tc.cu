@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             const int valid = (int)min((long)C, eos - tok0);
             uint8_t *KQ = sm + OFF_STAGE + st * STAGE_BYTES;
 
-            const float beta_t = GATED ? live_beta(beta_next) : beta_next;
+            const float beta_t = GATED && writes_nothing(beta_next) ? 0.f : beta_next;
             beta_next = load_beta(c + 1);
             const float g0_c = g0_next, g1_c = g1_next;
             if constexpr (GATED) {
@@ -494,7 +494,8 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 }
                 if (row < C) {  // A~[t][col0 .. col0+31]
                     const int t = row;
-                    const float rs = row_gn[t];  // gamma_t / n_t
+                    float rs = row_gn[t];  // gamma_t / n_t
+                    if constexpr (GATED) rs = rs == 0.f ? BETA_MIN * At[t * AT_LD + 66] : rs;  // for T; T'' leaves the row out
                     float iv[32];  // all scales first: the stores below may alias them for the compiler
 #pragma unroll
                     for (int s4 = 0; s4 < 8; ++s4) {
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                 uint8_t *hi = sm + OFF_TPP + buf * TPP_BYTES, *lo = hi + 8192;
                 // the same tile for the backward (a zero key's diagonal is 0 here; the backward sets it)
                 uint8_t *ghi = p.tpp ? p.tpp + ((size_t)blockIdx.x * nchunks + c) * 16384 : nullptr;
-                const float rsc = row_invn[t];
+                const float rsc = row_invn[t], rsw = GATED && row_gn[t] == 0.f ? 0.f : rsc;
 #pragma unroll
                 for (int c8 = 0; c8 < 16; c8 += 8) {
                     float tt8[8], gn8[8];
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {  // (rsc T~) (gamma/n), two columns per packed multiply
-                        const float2 y = __fmul2_rn(__fmul2_rn(make_float2(rsc, rsc), make_float2(tt8[e], tt8[e + 1])),
+                        const float2 y = __fmul2_rn(__fmul2_rn(make_float2(rsw, rsw), make_float2(tt8[e], tt8[e + 1])),
                                                     make_float2(gn8[e], gn8[e + 1]));
                         x[e] = s0 + c8 + e <= t ? y.x : 0.f;
                         x[e + 1] = s0 + c8 + e + 1 <= t ? y.y : 0.f;

@@ -220,11 +220,13 @@ __device__ __forceinline__ void block_decay16(float g, int lane, float *gh, floa
         ec[lane] = ex2(diff2(last, G));
     }
 }
-// beta as the tensor-core path takes it: magnitudes below 2^-90 become 2^-90.  Its backward gets
-// d alpha_t as (dY U^T)_tt / alpha_t; with U_t proportional to alpha_t that is exact for any alpha but 0,
-// and a step of 2^-90 changes no output.
-__device__ __forceinline__ float live_beta(float b) { return fabsf(b) < 0x1p-90f ? copysignf(0x1p-90f, b) : b; }
-// alpha as the tensor-core backward takes it: the exact gate's is beta itself where beta lambda is so small
+// A beta of magnitude below 2^-90 writes nothing (the chunk kernels of bf16 inputs): u_t is 0, and so is dv_t.
+// Where alpha_t divides - dalpha_t is (dY U^T)_tt / alpha_t with U = T diag(alpha) R, whose row t is
+// proportional to alpha_t - it is 2^-90, in T too: exact for dalpha, and 2^-90 of a token's size off in dq and dk.
+constexpr float BETA_MIN = 0x1p-90f;
+__device__ __forceinline__ bool writes_nothing(float b) { return fabsf(b) < BETA_MIN; }
+__device__ __forceinline__ float live_beta(float b) { return writes_nothing(b) ? BETA_MIN : b; }
+// alpha where it divides: the exact gate's is beta itself where beta lambda is so small
 // that the difference is lost (2^-25), as (1 - e^{-beta lambda}) / lambda is 0 once beta lambda is below the
 // smallest float.
 __device__ __forceinline__ float live_alpha(float b, float lam, int euler) {

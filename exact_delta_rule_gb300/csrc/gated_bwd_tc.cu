@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(THREADS, 1) state_kernel(const __grid_constant
 #pragma unroll
                     for (int s = 0; s < 32; ++s) lam = s == lane ? x[s] : lam;
                 }
-                eg[128 + row] = live_alpha(live_beta(bcur), lam, EULER);  // (dY is 0 past the end)
+                eg[128 + row] = writes_nothing(bcur) ? 0.f : live_alpha(bcur, lam, EULER);
             }
             if (named_bar_any(BAR_PREP, 128, !ok || *abort_flag)) {  // decays visible; also spreads an abort
                 *abort_flag = 1;

@@ -366,6 +366,8 @@ efla_status efla_prep(const void *k, const void *v, const float *beta, float *la
  *         decay of 0: the state restarts).  Positive gates are evaluated by the same formulas as long
  *         as their sum over 64 tokens keeps e^sum finite.
  *   S0, S_T [N, H, d_k, d_v] fp32;  o [B, T, H, d_v] o_dtype;  cu_seqlens as for efla_fwd_chunked
+ * A token whose beta is 0 writes nothing (with bf16 inputs the forward and backward count a magnitude below
+ * 2^-90 as 0); its dbeta is the formula's.
  * An infinity or NaN stays in its sequence; there it may also reach outputs of the tokens before it in its
  * chunk of 64 (of 16 where several tokens are decoded).
  * Supported: d_k, d_v in {32, 64, 128}, bf16 or fp32.  The forward and backward of bf16 inputs run on

@@ -749,3 +749,29 @@ def test_forward_packed_around_bad_bounds(dtype, d, bounds):
         else:
             assert bool((S_T[n] == 7).all())
     assert bool((o[:, free] == 7).all())
+
+
+# ------------------------------------------------------------------------------ rows that write nothing
+@pytest.mark.parametrize("dtype, dk, dv", [(F32, 64, 64), (BF16, 128, 128), (BF16, 64, 32)])
+@pytest.mark.parametrize("update", ["euler", "exact"])
+def test_a_row_without_step_sizes_writes_nothing(dtype, dk, dv, update):
+    """A padded batch row (beta = 0 for every token): no state, no outputs and no dv, not small ones; with a state and no
+    decay, the state's bits.  The other row is as it is alone, and dbeta is the formula's."""
+    x = make(B=2, T=150, dk=dk, dv=dv, dtype=dtype, S0=False)
+    x["beta"][1] = 0
+    x["beta"][0, ::3] = 0
+    dO = torch.ones_like(x["v"])
+    alone = {n: None if t is None else t[:1].contiguous() for n, t in x.items()}
+    want_o, want_S = efla.gated_fwd_chunked(**alone, update=update)
+    for call in (efla.gated_fwd_chunked, efla.gated_fwd_chunked_train):
+        o, S = call(**x, update=update)[:2]
+        assert not o[1].any() and not S[1].any()
+        assert torch.equal(o[:1], want_o) and torch.equal(S[:1], want_S)
+    got, ref = efla.gated_bwd_chunked(*x.values(), dO, update=update), gated.bwd(*x.values(), dO, None, update)
+    assert not got["dv"][1].any() and not got["dv"][0, ::3].any()
+    for n, r in ref.items():
+        close(got[n][:1], r[:1], tol(dtype, dk, dv, True), n)
+    close(got["dbeta"][1:], ref["dbeta"][1:], tol(dtype, dk, dv, True), "dbeta of the row")
+    x["g"][1], x["S0"] = 0, torch.randn(2, 4, dk, dv, device="cuda")
+    for call in (efla.gated_fwd_chunked, efla.gated_fwd_chunked_train):
+        assert torch.equal(call(**x, update=update)[1][1], x["S0"][1])
