@@ -71,10 +71,13 @@ struct GatedWs {
     size_t states, dse, w, p, sdot, part, tok, bytes;
 };
 // Which kernels take a forward or backward: bf16 inputs the tensor cores, at every size (features up to
-// 128 are zeros that TMA fills in).  Even where that is most of the work they are ahead, forward and
-// forward with backward in us, tensor cores / CUDA cores:
-//   d_k = d_v = 32, 2 heads of 32 tokens  11 / 13, 33 / 45;   8 x 2048 tokens of 16 heads  160 / 428, 609 / 1526
-//   d_k = d_v = 64                        11 / 17, 34 / 73;                                161 / 1110, 612 / 3201
+// 128 are zeros that TMA fills in).  Even where that is most of the work they are ahead of the CUDA-core
+// kernels, which take fp32 inputs only.  Forward and forward with backward in us, bf16 on the tensor cores /
+// the same shape in fp32 on CUDA cores:
+//   d_k = d_v = 32, 2 heads of 32 tokens  12 / 13, 36 / 45;   8 x 2048 tokens of 16 heads  160 / 452, 629 / 1572
+//   d_k = d_v = 64                        12 / 17, 37 / 72;                                162 / 1111, 634 / 3429
+// What it costs is memory: the tiles are those of 128 features, so the workspace of 8 x 2048 tokens of 16 heads
+// is 768 MiB at d = 32, 64 and 128 alike, where the fp32 layout takes 160, 256 and 640.
 inline bool gated_tc(efla_dtype in_dtype) { return in_dtype == EFLA_BF16; }
 inline GatedWs gated_ws(int B, int T, int Hk, int H, int dk, int dv, efla_dtype in_dtype) {
     const size_t units = (size_t)B * H, nc = ((size_t)T + 63) / 64, tok = (size_t)B * T * H;

@@ -35,7 +35,7 @@
 // gradient pass, the update rule as a template argument, and the tile layout.
 //
 // dO and the inputs are exact bf16; every other operand is split into two bf16 parts rounded to nearest
-// (2^-18), fp32 accumulation.  Every wait is bounded; on expiry the CTA records EFLA_ERR_DEVICE_TIMEOUT
+// (2^-17 at most), fp32 accumulation.  Every wait is bounded; on expiry the CTA records EFLA_ERR_DEVICE_TIMEOUT
 // and leaves.
 #include <algorithm>
 

@@ -25,6 +25,8 @@ namespace {
 
 constexpr int NT = 256;
 
+// The output gate's, to 2 + 1.2 |x| ulp (__expf): 1e-6 of the value at |x| = 5.  The prep's gates, which the recurrence
+// multiplies up, take expf and a rounded division.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 template <typename T>
@@ -195,7 +197,8 @@ __global__ void __launch_bounds__(NT) prep_bwd_kernel(MixerPrepArgs p, unsigned 
 
 // out[i] = sum over parts of ws[part][i], i < n.  A warp reads 32 entries (a line) of every 32nd part and
 // the CTA's 32 warps are added in order (304 parts of 128: 4.5 us).
-// It is launched while the kernel before it still runs and waits here for that kernel's results.
+// Programmatic launch: its CTAs may be set up while the kernel before it ends, and wait here for that
+// kernel's results.  (That kernel gives no earlier signal, so the two do not overlap beyond this.)
 __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict__ ws, int parts, int n,
                                                          float *__restrict__ out0, float *__restrict__ out1, int split) {
     __shared__ float red[32][33];

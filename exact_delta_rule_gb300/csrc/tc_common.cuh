@@ -46,7 +46,7 @@ __device__ __forceinline__ int opaque(int i) {
 }
 
 // Splits pairs x[2c], x[2c+1] into packed bf16 hi and lo words with
-// x = hi + lo + e, |e| < 2^-14 |x|: hi is x truncated to bf16 (its upper 16
+// x = hi + lo + e, |e| < 2^-15 |x|: hi is x truncated to bf16 (its upper 16
 // bits), lo is the exact fp32 remainder x - hi truncated the same way.  Bit
 // operations only (one byte permute per packed pair).
 template <int NP>
@@ -62,8 +62,9 @@ __device__ __forceinline__ void split_pack(const float *x, uint32_t *hi, uint32_
     }
 }
 
-// The same with both parts rounded to nearest: |e| <= 2^-18 |x| and no bias, where the truncated split
-// is 2^-14 off in one direction (the state it feeds is an fp32 output of the gated kernels).
+// The same with both parts rounded to nearest: |e| <= 2^-17 |x| (2^-18.7 in the mean square) and no bias,
+// where the truncated split is up to 2^-15 off in one direction (the state it feeds is an fp32 output of
+// the gated kernels).
 template <int NP>
 __device__ __forceinline__ void split_pack_rn(const float *x, uint32_t *hi, uint32_t *lo) {
 #pragma unroll

@@ -5,7 +5,8 @@
 
 H value heads read H_k query/key heads (value head h reads key head ``h // (H // H_k)``);
 ``update="euler"`` (alpha = beta) is the gated delta rule, ``update="exact"`` the exact gate with the
-same decay.
+same decay.  The calls are plain functions: gradients come from the ``*_bwd*`` calls, and nothing is recorded
+for autograd.
 """
 from __future__ import annotations
 
@@ -288,7 +289,8 @@ def gated_decode_tokens(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: to
                         stream=None, update: str = "euler") -> torch.Tensor:
     """m tokens per sequence appended to the state, S [B,H,dk,dv] fp32 updated in place
     (``efla_gated_decode_tokens``).  q, k [B,m,H_k,dk], v [B,m,H,dv], g, beta [B,m,H] fp32.
-    Returns o [B,m,H,dv].  Equal to m ``gated_decode_step`` calls."""
+    Returns o [B,m,H,dv].  The formulas of m ``gated_decode_step`` calls, which are fp32 arithmetic throughout; bf16
+    inputs with dk = dv = 128 run on the tensor cores here (operands in two bf16 parts, about 3e-6)."""
     return _decode("efla_gated_decode_tokens", 2, q, k, v, g, beta, S, o, o_dtype, stream, update)
 
 

@@ -372,7 +372,11 @@ efla_status efla_prep(const void *k, const void *v, const float *beta, float *la
  * chunk of 64 (of 16 where several tokens are decoded).
  * Supported: d_k, d_v in {32, 64, 128}, bf16 or fp32.  The forward and backward of bf16 inputs run on
  * the tensor cores, and so does decoding several tokens where d_k = d_v = 128; fp32 inputs and the rest
- * run on CUDA cores in fp32.  State and sums are fp32 everywhere.
+ * run on CUDA cores in fp32.  State and sums are held in fp32 everywhere.  On the tensor cores a product
+ * reads every operand that is not a bf16 input (the state among them) as two bf16 parts, each rounded to
+ * nearest: 2^-17 of a value at most, so that fp32 outputs are 3e-6 to 7e-6 off in norm where fp32 arithmetic
+ * gives 2e-7.  A caller who wants fp32 arithmetic for bf16 data converts q, k, v (and dO) to fp32 and
+ * may still take o in bf16.
  */
 
 /* The forward over whole sequences, in chunks of 64 tokens.  S0 and S_T may be NULL (zeros / not
@@ -416,7 +420,8 @@ efla_status efla_gated_decode_step(const void *q, const void *k, const void *v, 
                                    efla_stream_t stream);
 
 /* m tokens per sequence, S updated in place, read and written once: q, k [B, m, H_k, d_k],
- * v [B, m, H, d_v], g, beta [B, m, H], o [B, m, H, d_v].  Equal to m steps. */
+ * v [B, m, H, d_v], g, beta [B, m, H], o [B, m, H, d_v].  The same formulas as m steps; a step is fp32
+ * arithmetic for every type and size, several tokens in bf16 with d_k = d_v = 128 run on the tensor cores. */
 efla_status efla_gated_decode_tokens(const void *q, const void *k, const void *v, const float *g,
                                      const float *beta, float *S, void *o, int B, int m, int H_k, int H,
                                      int d_k, int d_v, efla_dtype in_dtype, efla_dtype o_dtype,

@@ -775,3 +775,22 @@ def test_a_row_without_step_sizes_writes_nothing(dtype, dk, dv, update):
     x["g"][1], x["S0"] = 0, torch.randn(2, 4, dk, dv, device="cuda")
     for call in (efla.gated_fwd_chunked, efla.gated_fwd_chunked_train):
         assert torch.equal(call(**x, update=update)[1][1], x["S0"][1])
+
+
+def test_chunk_offsets_past_32_bits():
+    """Forward, training forward and backward over more than 2^31 elements of q, k, v and o: the last row against the
+    same call on it alone."""
+    B, T, H, d = 64, 16400, 16, 128
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=BF16)  # noqa: E731
+    q, v, dO = r(B, T, H, d) / 12, r(B, T, H, d), r(B, T, H, d)
+    assert q.numel() > 2 ** 31
+    g, beta = -r(B, T, H).float().abs(), torch.sigmoid(r(B, T, H).float())
+    x, one = (q, q, v, g, beta), [t[-1:].contiguous() for t in (q, q, v, g, beta)]
+    o, S, ws = efla.gated_fwd_chunked_train(*x)
+    o1, S1, ws1 = efla.gated_fwd_chunked_train(*one)
+    assert torch.equal(o[-1:], o1) and torch.equal(S[-1:], S1)
+    got = efla.gated_bwd_chunked(*x, None, dO, workspace=ws, saved=True)
+    want = efla.gated_bwd_chunked(*one, None, dO[-1:].contiguous(), workspace=ws1, saved=True)
+    assert all(torch.equal(got[n][-1:], want[n]) for n in want)
+    assert efla.device_status() == 0
