@@ -216,6 +216,22 @@ __device__ __noinline__ void dump_state_rows(uint8_t *tile, uint32_t ts, int g0,
     }
 }
 
+// Rows valid .. 63 of a stage's K, Q and V (they may hold the next sequence, and 0 times what is there may be NaN)
+// as zeros, by the 256 prep threads.  Out of line for the same reason.
+__device__ __noinline__ void zero_tail(uint8_t *stage, int valid, int pi) {
+    const int rows = C - valid;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int e = pi; e < 4 * rows * 8; e += 256) {
+        const int ch = e & 7, r = (e >> 3) % rows, part = (e >> 3) / rows;
+        const int R = valid + r + ((part >> 1) ? 64 : 0), cb = part & 1;
+        *reinterpret_cast<uint4 *>(stage + cb * 16384 + (R >> 3) * 1024 + (R & 7) * 128 + ch * 16) = zero;
+    }
+    for (int e = pi; e < 2 * rows * 8; e += 256) {
+        const int ch = e & 7, R = valid + (e >> 3) % rows, cb = (e >> 3) / rows;
+        *reinterpret_cast<uint4 *>(stage + OFF_V + cb * 8192 + (R >> 3) * 1024 + (R & 7) * 128 + ch * 16) = zero;
+    }
+}
+
 template <bool OUT_BF16, bool GATED>
 __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant__ TcParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -405,20 +421,7 @@ __global__ void __launch_bounds__(448, 1) chunk_tc_kernel(const __grid_constant_
             if (valid < C) {
                 ok = wait_bar(&bars->tma_full[st], (c / NSTAGE) & 1, abort_flag, wait_ns);
                 if (ok) {
-                    const int rows = C - valid;
-                    for (int e = pi; e < 4 * rows * 8; e += 256) {
-                        const int ch = e & 7, r = (e >> 3) % rows, part = (e >> 3) / rows;
-                        const int R = valid + r + ((part >> 1) ? 64 : 0), cb = part & 1;
-                        *reinterpret_cast<uint4 *>(KQ + cb * 16384 + (R >> 3) * 1024 + (R & 7) * 128 + ch * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    if constexpr (GATED) {  // and V's: 0 times what the next sequence holds there may be NaN
-                        for (int e = pi; e < 2 * rows * 8; e += 256) {
-                            const int ch = e & 7, R = valid + (e >> 3) % rows, cb = (e >> 3) / rows;
-                            *reinterpret_cast<uint4 *>(KQ + OFF_V + cb * 8192 + (R >> 3) * 1024 + (R & 7) * 128 + ch * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                    }
+                    zero_tail(KQ, valid, pi);
                     fence_proxy_async_smem();
                 }
                 if (named_bar_any(BAR_PREP, 256, !ok || *abort_flag)) {

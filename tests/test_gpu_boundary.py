@@ -80,3 +80,23 @@ def test_decode_step_exact_signature(lib):
         o_ref, S_ref = oracle.decode_step(inp["q"], inp["k"], inp["v"], inp["beta"], S_ref)
         check(o, o_ref, in_dtype="bf16", what=f"decode o step {step}", out_bf16=True)
         check(S, S_ref, in_dtype="bf16", what=f"decode S step {step}")
+
+
+@pytest.mark.parametrize("dtype, d", [(torch.float32, 64), (torch.bfloat16, 64), (torch.bfloat16, 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_packed_bad_values_stay_in_their_sequence(dtype, d, bad):
+    """An infinity or NaN in one sequence of a packed batch leaves the others' bits as they were."""
+    import exact_delta_rule_gb300 as efla
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    r = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731
+    cu = torch.tensor([0, 70, 110, 174, 179], dtype=torch.int32, device=DEV)
+    q, k, v = r(1, 179, 2, d).to(dtype), (r(1, 179, 2, d) * d ** -0.5).to(dtype), r(1, 179, 2, d).to(dtype)
+    beta, S0 = torch.rand(1, 179, 2, generator=gen, device=DEV), r(4, 2, d, d)
+    want_o, want_S = efla.fwd_chunked(q, k, v, beta, S0, cu)
+    for t in (q, k, v, beta):
+        t[:, 70:110] = bad
+    S0[1] = bad
+    o, S = efla.fwd_chunked(q, k, v, beta, S0, cu)
+    for a, b, n in ((0, 70, 0), (110, 174, 2), (174, 179, 3)):
+        assert torch.equal(o[:, a:b], want_o[:, a:b]) and torch.equal(S[n], want_S[n]), n
+    assert efla.device_status() == 0
