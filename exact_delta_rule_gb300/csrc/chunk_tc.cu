@@ -57,7 +57,7 @@
 //   S, in TMEM, is multiplied by e^{G_C} while the tensor core forms X and u; u is split twice, c_t u_t
 //   for S += K^T diag(c) u (first: the chain) and u_t for O += P u (while the state is updated, and there
 //   O1 = Q S is multiplied by e^{G_t}).  The previous chunk's outputs leave while u is formed.
-// 8 x 2048 tokens of 16 heads of 128: 160-168 us by GPU, 41 at the copy rate; 190 keeping the chunk states
+// 8 x 2048 tokens of 16 heads of 128: 160-168 us by GPU, 41 at the copy rate; 194 keeping the chunk states
 // for the backward.  Latency binds it: a chunk takes about 10 k cycles, the state warpgroup's phases nearly all of
 // them, and the prep beside it 9.4 k (4.1 k of it the inverse).  Outputs read out behind the state update
 // instead, 164; by a warpgroup of their own (576 threads, 96 registers, spills), 172.

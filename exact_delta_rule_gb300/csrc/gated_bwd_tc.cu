@@ -26,7 +26,7 @@
 //    out.  The next item's K, Q, S and its first two products are under way while this one ends.  Sums
 //    over features or rows are taken by shuffles and per-warp slots in a fixed order.
 //
-// 8 x 2048 tokens of 16 heads of 128 (4096 items): state pass 160 us (720 MB, 4.5 TB/s), gradient pass
+// 8 x 2048 tokens of 16 heads of 128 (4096 items): state pass 163 us (765 MB, 4.7 TB/s), gradient pass
 // 285 us (1.1 GB, 4 TB/s).  Both are bound by the latency of their CUDA-core phases, with the memory
 // traffic of the tiles between the passes not far behind: forming <S, dS'> in the state pass, which
 // reads 64 KB more a chunk there, gives 197 and 270.  What they cost most was not arithmetic: register spills (the few KB of L1 left beside the operand tiles turn each into an L2
