@@ -1,0 +1,368 @@
+// Short causal convolution over the tokens of every channel, before a token mixer (W = 2, 3 or 4 taps):
+//   s_t = bias + sum_{j < W} w_j x_{t-W+1+j},   y = s or silu(s) = s sigmoid(s)
+// the W - 1 inputs before a sequence's first token from its state (or 0), the last W - 1 of state and
+// sequence kept as the next state.  Reverse mode, ds = dy or dy silu'(s), silu'(s) = g (1 + s (1 - g)) with
+// g = sigmoid(s):
+//   dx_t = sum_j w_j ds_{t+W-1-j},  dw_j = sum_t ds_t x_{t-W+1+j},  dbias = sum_t ds_t
+// on rows extended by the state: place e = t + W - 1 >= 0, dfull_e = sum_j w_j ds_{e-j} (ds = 0 outside the
+// row), plus dstate_T's at the last W - 1 places; the first W - 1 are dstate0.
+//
+// Bound by HBM: x is read and y written once.  A thread keeps one 16-byte vector of channels (4 channels in
+// the backward, whose sums take registers) and walks down the tokens with the last W - 1 rows in registers, so
+// a row is read once by its tile and again only as the W - 1 rows before the next.  Arithmetic is fp32, each
+// output rounded once; the sums over tokens go in two stages of fixed order.
+#include <algorithm>
+#include <type_traits>
+
+#include "conv.cuh"
+#include "mixer_norm.cuh"
+#include "vec.cuh"
+
+namespace efla {
+namespace {
+
+constexpr int NT = CONV_NT;
+constexpr int FWD_ROWS = 16;  // tokens a thread
+
+// To 2 + 1.2 |x| ulp, as the output gate's.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// V channels of a row.
+template <typename T, int V>
+struct Pack;
+template <typename T>
+struct Pack<T, 8> {
+    uint4 r;
+};
+template <>
+struct Pack<float, 4> {
+    uint4 r;
+};
+template <>
+struct Pack<__nv_bfloat16, 4> {
+    uint2 r;
+};
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, 8> &p, float (&x)[8]) { Vec<__nv_bfloat16>::unpack(p.r, x); }
+__device__ __forceinline__ void unpack(const Pack<float, 4> &p, float (&x)[4]) { Vec<float>::unpack(p.r, x); }
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, 4> &p, float (&x)[4]) {
+    x[0] = __uint_as_float(p.r.x << 16);
+    x[1] = __uint_as_float(p.r.x & 0xffff0000u);
+    x[2] = __uint_as_float(p.r.y << 16);
+    x[3] = __uint_as_float(p.r.y & 0xffff0000u);
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Pack<__nv_bfloat16, 8> &p) { p.r = Vec<__nv_bfloat16>::pack(x); }
+__device__ __forceinline__ void pack(const float (&x)[4], Pack<float, 4> &p) { p.r = Vec<float>::pack(x); }
+__device__ __forceinline__ void pack(const float (&x)[4], Pack<__nv_bfloat16, 4> &p) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    p.r = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// Row `row` of p [rows, vecs], vector v.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load(const void *p, long long row, int vecs, int v) {
+    return static_cast<const Pack<T, V> *>(p)[row * vecs + v];
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(void *p, long long row, int vecs, int v, const float (&x)[V]) {
+    Pack<T, V> r;
+    pack(x, r);
+    static_cast<Pack<T, V> *>(p)[row * vecs + v] = r;
+}
+
+template <int W, int V>
+struct Taps {
+    float w[V][W], bias[V];
+    __device__ __forceinline__ void load(const ConvArgs &p, int c0) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[c][j] = p.w[(size_t)(c0 + c) * W + j];
+            bias[c] = p.bias ? p.bias[c0 + c] : 0.f;
+        }
+    }
+};
+
+// ------------------------------------------------------------------------------------ forward
+// CTAs [0, tiles * cblocks): a tile of the B T tokens x a block of the channels; the others copy the states.
+// first[i], seq[i]: where the sequence of the tile's token i begins, and which it is (-1: no sequence).
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(NT) conv_fwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, unsigned work_ctas) {
+    const int tid = threadIdx.x;
+    if (blockIdx.x >= work_ctas) {  // state_T: place j of a sequence's last W - 1 inputs
+        const long long e = (long long)(blockIdx.x - work_ctas) * NT + tid;
+        if (e >= (long long)p.N * (W - 1) * vecs) return;
+        const int v = (int)(e % vecs), j = (int)(e / vecs % (W - 1));
+        const int n = (int)(e / vecs / (W - 1));
+        long long lo, hi;
+        if (p.cu_seqlens) {
+            lo = p.cu_seqlens[n], hi = p.cu_seqlens[n + 1];
+            if (lo < 0 || hi < lo || hi > p.T) {
+                if (v == 0 && j == 0) atomicExch(p.status, (int)EFLA_ERR_INVALID_ARG);
+                return;
+            }
+        } else {
+            lo = (long long)n * p.T, hi = lo + p.T;
+        }
+        const long long at = hi - (W - 1) + j;
+        Pack<T, V> r{};
+        if (at >= lo)
+            r = load<T, V>(p.x, at, vecs, v);
+        else if (p.state0)
+            r = load<T, V>(p.state0, (long long)n * (W - 1) + (at - lo + W - 1), vecs, v);
+        static_cast<Pack<T, V> *>(p.state_T)[e] = r;
+        return;
+    }
+    extern __shared__ int shared[];
+    const int subs = NT / lanes, tile_rows = FWD_ROWS * subs;
+    int *first = shared, *seq = shared + tile_rows;
+    const long long tokens = (long long)p.B * p.T, t0 = (long long)(blockIdx.x / cblocks) * tile_rows;
+    if (p.cu_seqlens) {
+        for (int i = tid; i < tile_rows; i += NT) seq[i] = -1;
+        __syncthreads();
+        for (int n = tid; n < p.N; n += NT) {
+            const long long lo = p.cu_seqlens[n], hi = p.cu_seqlens[n + 1];
+            if (lo < 0 || hi < lo || hi > p.T) {
+                if (blockIdx.x == 0) atomicExch(p.status, (int)EFLA_ERR_INVALID_ARG);
+                continue;
+            }
+            const long long from = lo > t0 ? lo : t0, to = hi < t0 + tile_rows ? hi : t0 + tile_rows;
+            for (long long t = from; t < to; ++t) {
+                first[t - t0] = (int)lo;
+                seq[t - t0] = n;
+            }
+        }
+        __syncthreads();
+    }
+    const int v = (blockIdx.x % cblocks) * lanes + tid % lanes, sub = tid / lanes;
+    const long long begin = t0 + (long long)sub * FWD_ROWS, end = begin + FWD_ROWS < tokens ? begin + FWD_ROWS : tokens;
+    if (v >= vecs || begin >= end) return;
+    Taps<W, V> taps;
+    taps.load(p, v * V);
+    float win[W - 1][V];
+    long long start = -1;  // the first token of the sequence that win belongs to
+    bool fresh = true;
+    for (long long t = begin; t < end; ++t) {
+        long long lo;
+        int n;
+        if (p.cu_seqlens) {
+            n = seq[t - t0];
+            if (n < 0) {
+                fresh = true;
+                continue;
+            }
+            lo = first[t - t0];
+        } else {
+            n = (int)(t / p.T);
+            lo = (long long)n * p.T;
+        }
+        if (fresh || lo != start) {
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                const long long at = t - (W - 1) + i;
+                Pack<T, V> r{};
+                if (at >= lo)
+                    r = load<T, V>(p.x, at, vecs, v);
+                else if (p.state0)
+                    r = load<T, V>(p.state0, (long long)n * (W - 1) + (at - lo + W - 1), vecs, v);
+                unpack(r, win[i]);
+            }
+            start = lo;
+            fresh = false;
+        }
+        float x[V], s[V];
+        unpack(load<T, V>(p.x, t, vecs, v), x);
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            float a = taps.bias[c];
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
+            a = fmaf(taps.w[c][W - 1], x[c], a);
+            s[c] = p.silu ? a * sigmoid(a) : a;
+#pragma unroll
+            for (int i = 0; i + 1 < W - 1; ++i) win[i][c] = win[i + 1][c];
+            win[W - 2][c] = x[c];
+        }
+        store<T, V>(p.y, t, vecs, v, s);
+    }
+}
+
+// ------------------------------------------------------------------------------------ backward
+// A CTA: `lanes` vectors of 4 channels x NT / lanes runs of CONV_BWD_ROWS places of an extended row, and every
+// parts-th such tile after it; row_runs runs a row.
+template <typename T, int W>
+__global__ void __launch_bounds__(NT) conv_bwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, int parts, int row_runs) {
+    constexpr int V = 4, R = CONV_BWD_ROWS;
+    __shared__ float red[NT][V + 1];
+    const int tid = threadIdx.x, lane = tid % lanes, sub = tid / lanes, subs = NT / lanes;
+    const int cb = blockIdx.x % cblocks, tile = blockIdx.x / cblocks, v = cb * lanes + lane;
+    const long long runs = (long long)p.B * row_runs, ends = (long long)p.T + W - 1;
+    float dw[V][W] = {}, db[V] = {};
+    Taps<W, V> taps;
+    if (v < vecs) taps.load(p, v * V);
+    for (long long run = (long long)tile * subs + sub; v < vecs && run < runs; run += (long long)parts * subs) {
+        const int b = (int)(run / row_runs);
+        const long long e0 = run % row_runs * R;
+        const long long row = (long long)b * p.T;
+        // x at place e of the extended row
+        auto place = [&](long long e, float(&x)[V]) {
+            Pack<T, V> r{};
+            if (e >= W - 1) {
+                if (e < ends) r = load<T, V>(p.x, row + e - (W - 1), vecs, v);
+            } else if (e >= 0 && p.state0) {
+                r = load<T, V>(p.state0, (long long)b * (W - 1) + e, vecs, v);
+            }
+            unpack(r, x);
+        };
+        float win[W - 1][V], old[W - 1][V] = {};  // x at t .. t + W - 2 (extended), ds of the W - 1 tokens before t
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) place(e0 - (W - 1) + i, win[i]);
+        const long long e1 = e0 + R < ends ? e0 + R : ends;
+        for (long long t = e0 - (W - 1); t < e1; ++t) {  // token t's newest input is at place t + W - 1
+            float x[V], ds[V] = {};
+            place(t + W - 1, x);
+            if (t >= 0 && t < p.T) {
+                unpack(load<T, V>(p.dy, row + t, vecs, v), ds);
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    if (p.silu) {
+                        float a = taps.bias[c];
+#pragma unroll
+                        for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
+                        a = fmaf(taps.w[c][W - 1], x[c], a);
+                        const float g = sigmoid(a);
+                        ds[c] *= g * fmaf(a, 1.f - g, 1.f);
+                    }
+                    if (t >= e0) {
+#pragma unroll
+                        for (int i = 0; i < W - 1; ++i) dw[c][i] = fmaf(ds[c], win[i][c], dw[c][i]);
+                        dw[c][W - 1] = fmaf(ds[c], x[c], dw[c][W - 1]);
+                        db[c] += ds[c];
+                    }
+                }
+            }
+            if (t >= e0) {  // place e = t: sum_j w_j ds_{t-j}
+                float d[V] = {};
+                if (p.dstate_T && t >= p.T) unpack(load<T, V>(p.dstate_T, (long long)b * (W - 1) + t - p.T, vecs, v), d);
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    d[c] = fmaf(taps.w[c][0], ds[c], d[c]);
+#pragma unroll
+                    for (int j = 1; j < W; ++j) d[c] = fmaf(taps.w[c][j], old[W - 1 - j][c], d[c]);
+                }
+                if (t >= W - 1)
+                    store<T, V>(p.dx, row + t - (W - 1), vecs, v, d);
+                else if (p.dstate0)
+                    store<T, V>(p.dstate0, (long long)b * (W - 1) + t, vecs, v, d);
+            }
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+#pragma unroll
+                for (int i = 0; i + 1 < W - 1; ++i) {
+                    win[i][c] = win[i + 1][c];
+                    old[i][c] = old[i + 1][c];
+                }
+                win[W - 2][c] = x[c];
+                old[W - 2][c] = ds[c];
+            }
+        }
+    }
+    // the CTA's sums over its runs, in order: [D][W] then [D] of part `tile`
+    const int sums = p.dbias ? W + 1 : W;
+    float *part = p.ws + (size_t)tile * p.D * sums;
+#pragma unroll
+    for (int j = 0; j <= W; ++j) {
+        if (j == sums) break;
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < V; ++c) red[tid][c] = j < W ? dw[c][j < W ? j : 0] : db[c];
+        __syncthreads();
+        for (int i = tid; i < lanes * V; i += NT) {
+            const int l = i / V, c = i % V, ch = (cb * lanes + l) * V + c;
+            if (ch >= p.D) continue;
+            float s = 0.f;
+            for (int q = 0; q < subs; ++q) s += red[q * lanes + l][c];
+            part[j < W ? (size_t)ch * W + j : (size_t)p.D * W + ch] = s;
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------ one token
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(NT) conv_step_kernel(ConvArgs p, int vecs) {
+    const long long e = (long long)blockIdx.x * NT + threadIdx.x;
+    if (e >= (long long)p.B * vecs) return;
+    const int v = (int)(e % vecs);
+    const long long b = e / vecs;
+    Pack<T, V> raw[W];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) raw[i] = load<T, V>(p.state0, b * (W - 1) + i, vecs, v);
+    raw[W - 1] = load<T, V>(p.x, b, vecs, v);
+    Taps<W, V> taps;
+    taps.load(p, v * V);
+    float s[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) s[c] = taps.bias[c];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        float x[V];
+        unpack(raw[i], x);
+#pragma unroll
+        for (int c = 0; c < V; ++c) s[c] = fmaf(taps.w[c][i], x[c], s[c]);
+        if (i > 0) static_cast<Pack<T, V> *>(p.state_T)[(b * (W - 1) + i - 1) * vecs + v] = raw[i];
+    }
+    if (p.silu) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) s[c] *= sigmoid(s[c]);
+    }
+    store<T, V>(p.y, b, vecs, v, s);
+}
+
+template <typename T, int W>
+cudaError_t fwd(const ConvArgs &a) {
+    constexpr int V = Vec<T>::N;
+    const int vecs = a.D / V, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes;
+    const int tile_rows = FWD_ROWS * (NT / lanes);
+    const long long tokens = (long long)a.B * a.T, work = (tokens + tile_rows - 1) / tile_rows * cblocks;
+    const long long copies = a.state_T ? ((long long)a.N * (W - 1) * vecs + NT - 1) / NT : 0;
+    if (work + copies == 0) return cudaSuccess;
+    const size_t smem = a.cu_seqlens ? 2 * tile_rows * sizeof(int) : 0;
+    conv_fwd_kernel<T, V, W><<<(unsigned)(work + copies), NT, smem, a.stream>>>(a, vecs, lanes, cblocks, (unsigned)work);
+    return cudaGetLastError();
+}
+template <typename T, int W>
+cudaError_t bwd(const ConvArgs &a) {
+    const int vecs = a.D / 4, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes;
+    const int parts = conv_bwd_parts(a.B, a.T, a.D, a.W);
+    conv_bwd_kernel<T, W><<<(unsigned)parts * cblocks, NT, 0, a.stream>>>(a, vecs, lanes, cblocks, parts, conv_bwd_runs(a.T, a.W));
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_sum_parts(a.ws, parts, a.D * (a.dbias ? W + 1 : W), a.dw, a.dbias, a.D * W, a.stream);
+}
+template <typename T, int W>
+cudaError_t step(const ConvArgs &a) {
+    constexpr int V = Vec<T>::N;
+    const int vecs = a.D / V;
+    conv_step_kernel<T, V, W><<<(unsigned)(((long long)a.B * vecs + NT - 1) / NT), NT, 0, a.stream>>>(a, vecs);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t taps(const ConvArgs &a, int which) {
+    auto go = [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        return which == 0 ? fwd<T, W>(a) : which == 1 ? bwd<T, W>(a) : step<T, W>(a);
+    };
+    return a.W == 2 ? go(std::integral_constant<int, 2>{}) : a.W == 3 ? go(std::integral_constant<int, 3>{})
+                                                                      : go(std::integral_constant<int, 4>{});
+}
+cudaError_t types(const ConvArgs &a, int which) {
+    return a.dtype == EFLA_BF16 ? taps<__nv_bfloat16>(a, which) : taps<float>(a, which);
+}
+
+}  // namespace
+
+cudaError_t launch_conv(const ConvArgs &a) { return types(a, 0); }
+cudaError_t launch_conv_bwd(const ConvArgs &a) { return types(a, 1); }
+cudaError_t launch_conv_step(const ConvArgs &a) { return types(a, 2); }
+
+}  // namespace efla

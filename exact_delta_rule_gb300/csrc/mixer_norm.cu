@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "mixer_norm.cuh"
+#include "vec.cuh"
 
 namespace efla {
 namespace {
@@ -28,51 +29,6 @@ constexpr int NT = 256;
 // The output gate's, to 2 + 1.2 |x| ulp (__expf): 1e-6 of the value at |x| = 5.  The prep's gates, which the recurrence
 // multiplies up, take expf and a rounded division.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
-template <typename T>
-struct Vec;  // 16 bytes of T as fp32 values
-template <>
-struct Vec<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(const uint4 &r, float (&x)[4]) {
-        x[0] = __uint_as_float(r.x);
-        x[1] = __uint_as_float(r.y);
-        x[2] = __uint_as_float(r.z);
-        x[3] = __uint_as_float(r.w);
-    }
-    static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void unpack(const uint4 &r, float (&x)[8]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __uint_as_float(w[e] << 16);
-            x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
-    }
-    static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t *>(&p);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-
-// Sum over the LPR lanes that hold a row.
-template <int LPR>
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    return x;
-}
 
 template <typename T, int D>
 struct Rows {
@@ -217,7 +173,9 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict
     if (lane == 0 && i < n) (i < split ? out0[i] : out1[i - split]) = s;
 }
 
-cudaError_t sum_parts(const float *ws, int parts, int n, float *out0, float *out1, int split, cudaStream_t stream) {
+}  // namespace
+
+cudaError_t launch_sum_parts(const float *ws, int parts, int n, float *out0, float *out1, int split, cudaStream_t stream) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -225,6 +183,8 @@ cudaError_t sum_parts(const float *ws, int parts, int n, float *out0, float *out
     cfg.gridDim = dim3((n + 31) / 32), cfg.blockDim = dim3(1024), cfg.stream = stream, cfg.attrs = &attr, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, sum_parts_kernel, ws, parts, n, out0, out1, split);
 }
+
+namespace {
 
 // ------------------------------------------------------------------------------------ after: forward
 template <typename T, int D, int UNROLL>
@@ -357,7 +317,7 @@ cudaError_t prep_launch(const MixerPrepArgs &p, bool bwd) {
     prep_bwd_kernel<T, D, UF><<<row_ctas + parts * ((p.H + 31) / 32), NT, 0, p.stream>>>(p, row_ctas, parts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return sum_parts(p.ws, parts, 2 * p.H, p.dA_log, p.ddt_bias, p.H, p.stream);
+    return launch_sum_parts(p.ws, parts, 2 * p.H, p.dA_log, p.ddt_bias, p.H, p.stream);
 }
 template <typename T>
 cudaError_t prep_d(const MixerPrepArgs &p, bool bwd) {
@@ -376,7 +336,7 @@ cudaError_t norm_launch(const NormGateArgs &p, bool bwd) {
     norm_bwd_kernel<T, D, UF><<<parts, NT, 0, p.stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return sum_parts(p.ws, parts, D, p.dw, nullptr, D, p.stream);
+    return launch_sum_parts(p.ws, parts, D, p.dw, nullptr, D, p.stream);
 }
 template <typename T>
 cudaError_t norm_d(const NormGateArgs &p, bool bwd) {

@@ -1,0 +1,218 @@
+// Selective state space scan: argument blocks of its launchers and the arithmetic its kernels share.
+//
+//   delta_t = softplus(dt_t + dt_bias),   A = -e^{A_log}
+//   h_t = e^{A delta_t} h_{t-1} + delta_t x_t B_t,   y_t = (C_t . h_t + D x_t) silu(z_t)
+//
+// per channel d of D with a state h of N entries; B_t and C_t [G, N] are shared by the D / G channels of a group.
+//
+// Long rows are cut into segments where the channels alone do not fill the GPU: first each segment's end state
+// from h = 0 and its sum of delta (the carry kernel), then, segment after segment,
+// h_end = e^{A sum delta} h_start + local (the combine kernel), then all segments at once from their start states.
+// That costs the exponentials a second time, without the outputs: 0.6 of the work.
+#pragma once
+
+#include <algorithm>
+
+#include "internal.cuh"
+
+namespace efla {
+
+constexpr int SSM_NT = 128;   // threads a CTA
+constexpr int SSM_TOK = 16;   // tokens a stage; the training forward keeps the state at the start of each
+constexpr int SSM_PER = 16;   // state entries a thread (forward)
+
+struct SsmArgs {
+    const void *x, *dt, *z;              // [B, T, D]; z may be nullptr
+    const float *A_log, *Dskip, *dt_bias;  // [D, N], [D], [D]; the last two may be nullptr
+    const void *Bm, *Cm;                 // [B, T, G, N]
+    const float *S0;                     // [nseq, D, N] or nullptr
+    const int32_t *cu_seqlens;
+    void *y;
+    float *S_T;                          // may be nullptr
+    int B, T, D, N, G, nseq;
+    efla_dtype dtype;
+    cudaStream_t stream;
+    int *status;
+    int seg = 0;             // tokens a segment, a multiple of SSM_TOK; 0: rows are not cut
+    int slots = 0;           // segments: of all rows, or the most that cu_seqlens can make
+    float *state = nullptr;  // [slots, D, N]: a segment's local end state, then its start state
+    float *sum = nullptr;    // [slots, D]: its sum of delta
+    float *keep = nullptr;   // training: [B, ceil(T / SSM_TOK), D, N], the state at the start of each stage
+};
+
+struct SsmBwdArgs {
+    SsmArgs f;               // inputs, f.keep filled by the forward; f.state and f.sum: scratch of the segments
+    const void *dy;
+    const float *dS_T;       // may be nullptr
+    void *dx, *ddt, *dz, *dB, *dC;        // dz nullptr where z is
+    float *dA_log, *dD, *ddt_bias, *dS0;  // dD, ddt_bias, dS0 may be nullptr
+    float *part;             // [channel tiles, B T, 2 N]: a tile's share of dB and dC
+    float *sums;             // [slots][D N]: a segment's share of dA_log
+    float *sums2;            // [slots][2 D]: of dD and ddt_bias
+};
+
+// Channels a CTA.  Tiles do not cross a group.
+inline int ssm_channels(int N) { return SSM_NT * SSM_PER / N; }
+inline int ssm_tiles(int D, int N, int G) {
+    const int each = D / G, c = ssm_channels(N);
+    return G * ((each + c - 1) / c);
+}
+// Tokens a segment (0: rows stay whole) for `rows` rows of T tokens.
+int ssm_segment(long long rows, int T, int tiles);
+
+// Workspace of the training pair, in bytes from its base (16-byte aligned regions).
+struct SsmWs {
+    int seg, slots;
+    size_t keep, part, sums, sums2, state, sum, bytes;
+};
+inline SsmWs ssm_ws(int B, int T, int D, int N, int G) {
+    SsmWs w{};
+    const int tiles = ssm_tiles(D, N, G);
+    w.seg = ssm_segment(B, T, tiles);
+    w.slots = B * (w.seg ? (T + w.seg - 1) / w.seg : 1);
+    size_t at = 0;
+    auto take = [&](size_t floats) {
+        const size_t r = at;
+        at += (floats * 4 + 255) / 256 * 256;
+        return r;
+    };
+    const size_t tok = (size_t)B * T, dn = (size_t)D * N;
+    w.keep = take((size_t)B * ((T + SSM_TOK - 1) / SSM_TOK) * dn);
+    w.part = take(tok * tiles * 2 * N);
+    w.sums = take(w.slots * dn);
+    w.sums2 = take((size_t)w.slots * 2 * D);
+    w.state = take(w.seg ? w.slots * dn : 0);
+    w.sum = take(w.seg ? (size_t)w.slots * D : 0);
+    w.bytes = at;
+    return w;
+}
+
+cudaError_t launch_ssm_scan(const SsmArgs &a);
+cudaError_t launch_ssm_bwd(const SsmBwdArgs &a);
+cudaError_t launch_ssm_step(const SsmArgs &a);  // x, dt, z, y [B, D], Bm, Cm [B, G, N], S0 == S_T in place
+
+// 2^x (one MUFU instruction, relative error 1.5e-7 at most, 6e-8 rms, for x <= 0; underflows to 0).
+__device__ __forceinline__ float ssm_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float LOG2E = 1.44269504f;
+
+// log(1 + e^t) = max(t, 0) + log1p(u), u = e^{-|t|} in [0, 1]; log1p(u) = u P(u) with P of degree 9 fitted to
+// log1p(u) / u on [0, 1] for the smallest largest relative error (5e-9; 1.5e-7 with fp32 coefficients and
+// arithmetic).
+__device__ __forceinline__ float softplus(float t) {
+    const float u = ssm_ex2(-fabsf(t) * LOG2E);
+    float p = -0.0032439809292554855f;
+    p = fmaf(p, u, 0.019851263612508774f);
+    p = fmaf(p, u, -0.056959159672260284f);
+    p = fmaf(p, u, 0.10603617131710052f);
+    p = fmaf(p, u, -0.15305569767951965f);
+    p = fmaf(p, u, 0.19675931334495544f);
+    p = fmaf(p, u, -0.24954132735729218f);
+    p = fmaf(p, u, 0.3332996368408203f);
+    p = fmaf(p, u, -0.4999990165233612f);
+    p = fmaf(p, u, 1.f);
+    return fmaf(p, u, fmaxf(t, 0.f));
+}
+__device__ __forceinline__ float ssm_sigmoid(float x) { return __fdividef(1.f, 1.f + ssm_ex2(-x * LOG2E)); }
+// A in units of log2: e^{A delta} = 2^{rate delta}.
+__device__ __forceinline__ float ssm_rate(float a_log) { return -expf(a_log) * LOG2E; }
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Tokens [t0, t0 + SSM_TOK) of src, the first `have` of CHUNKS 16-byte pieces each, to dst; zeros for the others and
+// from token hi on.
+template <int CHUNKS>
+__device__ __forceinline__ void load_tile(uint8_t *dst, const uint8_t *src, size_t pitch, long long t0, long long hi, int have) {
+#pragma unroll
+    for (int k = 0; k < (SSM_TOK * CHUNKS + SSM_NT - 1) / SSM_NT; ++k) {
+        const int i = k * SSM_NT + threadIdx.x, t = i / CHUNKS, c = i % CHUNKS;
+        if (SSM_TOK * CHUNKS % SSM_NT && i >= SSM_TOK * CHUNKS) break;
+        const bool live = t0 + t < hi && c < have;
+        cp_async16(dst + 16 * i, live ? src + (size_t)(t0 + t) * pitch + 16 * c : src, live);
+    }
+}
+
+// Which tokens [lo, hi) of [B T] a segment covers, and whether it is its row's or sequence's first and last.
+struct SsmSpan {
+    int seq;
+    long long lo, hi;
+    bool first, last;
+};
+
+// Segment `slot` of rows of T tokens, `seg` tokens each.
+__device__ __forceinline__ SsmSpan ssm_row_span(const SsmArgs &p, int slot) {
+    const int per = p.seg ? (p.T + p.seg - 1) / p.seg : 1, row = slot / per, s = slot % per;
+    const long long row0 = (long long)row * p.T, lo = row0 + (long long)s * p.seg;
+    const long long hi = s + 1 < per ? lo + p.seg : row0 + p.T;
+    return {row, lo, hi, s == 0, s + 1 == per};
+}
+
+// Segments of sequence n of cu_seqlens: max(1, ceil(length / seg)), -1 if it is malformed.
+__device__ __forceinline__ int ssm_segments(const SsmArgs &p, int n, long long &lo, long long &hi) {
+    lo = p.cu_seqlens[n], hi = p.cu_seqlens[n + 1];
+    if (lo < 0 || hi < lo || hi > p.T) return -1;
+    return p.seg && hi > lo ? (int)((hi - lo + p.seg - 1) / p.seg) : 1;
+}
+
+// Segment `slot` of packed sequences, all segments of a sequence after those of the ones before it.  By all threads
+// of a CTA; false if there is none.  A malformed sequence has none and is reported by the CTA that `reports`.
+__device__ __forceinline__ bool ssm_packed_span(const SsmArgs &p, int slot, bool reports, SsmSpan &out) {
+    __shared__ long long box[4];
+    __shared__ int sums[SSM_NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long lo, hi;
+    if (!p.seg) {
+        if (ssm_segments(p, slot, lo, hi) < 0) {
+            if (tid == 0 && reports) atomicExch(p.status, (int)EFLA_ERR_INVALID_ARG);
+            return false;
+        }
+        out = {slot, lo, hi, true, true};
+        return true;
+    }
+    reports = reports && slot == 0;
+    if (tid == 0) box[0] = -1;
+    __syncthreads();
+    long long before = 0;
+    for (int base = 0; base < p.nseq && (before <= slot || reports); base += SSM_NT) {
+        const int n = base + tid;
+        int segs = n < p.nseq ? ssm_segments(p, n, lo, hi) : 0;
+        if (segs < 0) {
+            segs = 0;
+            if (reports) atomicExch(p.status, (int)EFLA_ERR_INVALID_ARG);
+        }
+        int run = segs;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, run, off);
+            if (lane >= off) run += y;
+        }
+        if (lane == 31) sums[warp] = run;
+        __syncthreads();
+        long long start = before + run - segs;
+        for (int w = 0; w < warp; ++w) start += sums[w];
+        if (slot >= start && slot < start + segs) {
+            const int s = (int)(slot - start);
+            box[0] = n;
+            box[1] = lo + (long long)s * p.seg;
+            box[2] = s + 1 < segs ? box[1] + p.seg : hi;
+            box[3] = (s == 0 ? 1 : 0) | (s + 1 == segs ? 2 : 0);
+        }
+        for (int w = 0; w < SSM_NT / 32; ++w) before += sums[w];
+        __syncthreads();
+    }
+    if (box[0] < 0) return false;
+    out = {(int)box[0], box[1], box[2], (box[3] & 1) != 0, (box[3] & 2) != 0};
+    return true;
+}
+
+}  // namespace efla

@@ -45,7 +45,7 @@
 extern "C" {
 #endif
 
-#define EFLA_ABI_VERSION 11
+#define EFLA_ABI_VERSION 12
 
 typedef enum {
     EFLA_OK = 0,
@@ -71,6 +71,12 @@ typedef enum {
     EFLA_UPDATE_EXACT = 0,
     EFLA_UPDATE_EULER = 1
 } efla_update;
+
+/* What follows the convolution and the group norm: nothing, or silu(s) = s / (1 + e^{-s}). */
+typedef enum {
+    EFLA_ACT_NONE = 0,
+    EFLA_ACT_SILU = 1
+} efla_activation;
 
 /* Same object as cudaStream_t; kept opaque so that this header needs no CUDA header. */
 typedef struct CUstream_st *efla_stream_t;
@@ -467,6 +473,85 @@ efla_status efla_norm_gate_bwd(const void *o, const void *z, const float *w, con
                                void *d_z, float *d_w, long long rows, int d, efla_dtype dtype, float eps,
                                void *workspace, size_t workspace_bytes, efla_stream_t stream);
 efla_status efla_norm_gate_bwd_workspace(int d, size_t *bytes);
+
+/*
+ * efla_causal_conv -- the short causal convolution before a token mixer, per channel, with its activation:
+ *
+ *   s_t = bias + sum_{j < W} w_j x_{t-W+1+j},   y_t = s_t or silu(s_t)
+ *
+ *   x, y     [B, T, D] dtype        w [D, W] fp32 (the newest token's weight last)   bias [D] fp32 or NULL
+ *   state0   [N, W-1, D] dtype: the W - 1 inputs before each sequence, oldest first, or NULL (zeros)
+ *   state_T  [N, W-1, D] dtype: the last W - 1 of state0's and the sequence's inputs, or NULL (not written)
+ *   cu_seqlens as for efla_fwd_chunked.  Tokens of no sequence are left alone.
+ * W in {2, 3, 4}, D a multiple of 8.  fp32 arithmetic, each output rounded once.  state_T may not be state0
+ * (a token at a time, efla_causal_conv_step keeps one state in place).
+ */
+efla_status efla_causal_conv(const void *x, const float *w, const float *bias, const void *state0,
+                             const int32_t *cu_seqlens, void *y, void *state_T, int B, int T, int D, int W,
+                             int N, efla_dtype dtype, efla_activation activation, efla_stream_t stream);
+
+/* Its gradients over rows of [B, T], from dy [B, T, D] and dstate_T [B, W-1, D] (or NULL: zero), in dtype:
+ * dx, dstate0 (or NULL) in dtype, dw [D, W] and dbias [D] (or NULL) fp32, summed over the tokens in a fixed
+ * order.  workspace: at least efla_causal_conv_bwd_workspace bytes, overlapping no argument. */
+efla_status efla_causal_conv_bwd(const void *x, const float *w, const float *bias, const void *state0,
+                                 const void *dy, const void *dstate_T, void *dx, float *dw, float *dbias,
+                                 void *dstate0, int B, int T, int D, int W, efla_dtype dtype,
+                                 efla_activation activation, void *workspace, size_t workspace_bytes,
+                                 efla_stream_t stream);
+efla_status efla_causal_conv_bwd_workspace(int B, int T, int D, int W, size_t *bytes);
+
+/* One token per sequence: x, y [B, D], state [B, W-1, D] shifted in place. */
+efla_status efla_causal_conv_step(const void *x, const float *w, const float *bias, void *state, void *y, int B,
+                                  int D, int W, efla_dtype dtype, efla_activation activation,
+                                  efla_stream_t stream);
+
+/*
+ * efla_ssm_scan -- the selective state space scan, per channel d with a state of d_state entries:
+ *
+ *   delta_t = softplus(dt_t + dt_bias),   h_t = exp(-e^{A_log} delta_t) h_{t-1} + delta_t x_t B_t
+ *   y_t     = (C_t . h_t + D_skip x_t) silu(z_t)
+ *
+ *   x, dt, z, y  [B, T, D] dtype (z may be NULL: no gate)
+ *   B, C     [B, T, G, d_state] dtype, shared by the D / G channels of a group: channel d reads group d G / D
+ *   A_log    [D, d_state] fp32 (finite);  D_skip, dt_bias [D] fp32, or NULL (zeros)
+ *   S0, S_T  [N, D, d_state] fp32, or NULL (zeros / not written); S0 == S_T is allowed
+ *   cu_seqlens as for efla_fwd_chunked.  Tokens of no sequence are left alone.
+ *   workspace  at least efla_ssm_scan_workspace bytes (0 where the channels fill the GPU and the rows stay whole),
+ *            overlapping no argument; calls that overlap in time need one each
+ * d_state in {16, 32, 64, 128}, D a multiple of 8 and D / G of 8 (bf16) or 4 (fp32).  fp32 arithmetic and state, each output rounded once.
+ * A token with dt = -inf has delta = 0: it leaves the state as it is (x finite), which is how a padded row ends.
+ */
+efla_status efla_ssm_scan(const void *x, const void *dt, const float *A_log, const void *B_t, const void *C_t,
+                          const float *D_skip, const float *dt_bias, const void *z, const float *S0,
+                          const int32_t *cu_seqlens, void *y, float *S_T, int B, int T, int D, int d_state, int G,
+                          int N, efla_dtype dtype, void *workspace, size_t workspace_bytes,
+                          efla_stream_t stream);
+/* packed: whether cu_seqlens will be given (N sequences, B = 1). */
+efla_status efla_ssm_scan_workspace(int B, int T, int D, int d_state, int G, int N, int packed, size_t *bytes);
+
+/* The training forward over rows of [B, T]: also keeps in `workspace` (efla_ssm_bwd_workspace bytes) the states that
+ * efla_ssm_scan_bwd(saved = 1) of the same inputs starts from, which serve one backward. */
+efla_status efla_ssm_scan_train(const void *x, const void *dt, const float *A_log, const void *B_t, const void *C_t,
+                                const float *D_skip, const float *dt_bias, const void *z, const float *S0, void *y,
+                                float *S_T, int B, int T, int D, int d_state, int G, efla_dtype dtype,
+                                void *workspace, size_t workspace_bytes, efla_stream_t stream);
+efla_status efla_ssm_bwd_workspace(int B, int T, int D, int d_state, int G, size_t *bytes);
+
+/* Its gradients, from dy [B, T, D] dtype and dS_T [B, D, d_state] fp32 (or NULL: zero): dx, ddt, dz (given exactly
+ * where z is) [B, T, D] and dB, dC [B, T, G, d_state] (sums over the channels of a group) in dtype; dA_log
+ * [D, d_state], dD and ddt_bias [D] (or NULL) fp32, sums over the tokens; dS0 [B, D, d_state] fp32 or NULL.
+ * saved = 0 runs the forward first.  Results do not depend on the order in which CTAs finish. */
+efla_status efla_ssm_scan_bwd(const void *x, const void *dt, const float *A_log, const void *B_t, const void *C_t,
+                              const float *D_skip, const float *dt_bias, const void *z, const float *S0,
+                              const void *dy, const float *dS_T, void *dx, void *ddt, float *dA_log, void *dB,
+                              void *dC, float *dD, float *ddt_bias, void *dz, float *dS0, int B, int T, int D,
+                              int d_state, int G, efla_dtype dtype, int saved, void *workspace,
+                              size_t workspace_bytes, efla_stream_t stream);
+
+/* One token per sequence, S [B, D, d_state] updated in place: x, dt, z, y [B, D], B_t, C_t [B, G, d_state]. */
+efla_status efla_ssm_step(const void *x, const void *dt, const float *A_log, const void *B_t, const void *C_t,
+                          const float *D_skip, const float *dt_bias, const void *z, float *S, void *y, int B, int D,
+                          int d_state, int G, efla_dtype dtype, efla_stream_t stream);
 
 /* Reads the calling thread's current device's status word on `stream`
  * (synchronising that stream), resets it to EFLA_OK and returns what it held:
