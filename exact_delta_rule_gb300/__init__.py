@@ -10,8 +10,9 @@ works but every call raises ``RuntimeError`` -- there is no fallback path.
     o      = decode_tokens(q, k, v, beta, S)      # m tokens per sequence, S in place
 
 The gated delta rule (a decay per token and head, shared key heads) and the norms around a gated
-mixer are the ``gated_*`` and ``norm_gate*`` calls of ``gated.py``; the selective state space scan and the short
-causal convolution before a mixer the ``ssm_*`` and ``causal_conv*`` calls of ``ssm.py``.
+mixer are the ``gated_*`` and ``norm_gate*`` calls of ``gated.py``; the selective state space scan, the short
+causal convolution before a mixer and the group norm the ``ssm_*``, ``causal_conv*`` and ``group_norm*`` calls of
+``ssm.py``.
 
 Semantics (per head): lambda = ||k||^2, alpha = (1 - e^{-beta*lambda})/lambda,
 S <- (I - alpha k k^T) S + alpha k v^T, o = S^T q with the updated S.
@@ -34,7 +35,7 @@ __all__ = ["EflaError", "lib_path", "load", "fwd_chunked", "fwd_chunked_scan", "
            "gated_fwd_chunked", "gated_fwd_chunked_train", "gated_bwd_chunked", "gated_bwd_workspace",
            "gated_decode_step", "gated_decode_tokens", "gated_prep", "gated_prep_bwd", "norm_gate", "norm_gate_bwd",
            "causal_conv", "causal_conv_bwd", "causal_conv_step", "ssm_scan", "ssm_scan_train", "ssm_scan_bwd", "ssm_step",
-           "ssm_scan_workspace", "ssm_bwd_workspace"]
+           "ssm_scan_workspace", "ssm_bwd_workspace", "group_norm", "group_norm_bwd", "group_norm_workspace"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_PKG, "libefla.so")
@@ -486,5 +487,6 @@ def set_debug_stall(on) -> None:
 
 from .gated import (gated_bwd_chunked, gated_bwd_workspace, gated_decode_step, gated_decode_tokens,  # noqa: E402
                     gated_fwd_chunked, gated_fwd_chunked_train, gated_prep, gated_prep_bwd, norm_gate, norm_gate_bwd)
-from .ssm import (causal_conv, causal_conv_bwd, causal_conv_step, ssm_bwd_workspace, ssm_scan, ssm_scan_bwd,  # noqa: E402
-                  ssm_scan_train, ssm_scan_workspace, ssm_step)
+from .ssm import (causal_conv, causal_conv_bwd, causal_conv_step, group_norm, group_norm_bwd,  # noqa: E402
+                  group_norm_workspace, ssm_bwd_workspace, ssm_scan, ssm_scan_bwd, ssm_scan_train, ssm_scan_workspace,
+                  ssm_step)

@@ -170,7 +170,10 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict
     __syncthreads();
     i = blockIdx.x * 32 + warp;
     s = row_sum<32>(red[lane][warp]);
-    if (lane == 0 && i < n) (i < split ? out0[i] : out1[i - split]) = s;
+    if (lane == 0 && i < n) {
+        if (i < split && out0) out0[i] = s;
+        if (i >= split && out1) out1[i - split] = s;
+    }
 }
 
 }  // namespace

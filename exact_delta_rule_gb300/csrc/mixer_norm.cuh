@@ -44,7 +44,7 @@ struct NormGateArgs {
 };
 constexpr int NORM_GATE_PARTS = 152 * 2;  // the CTAs that are resident at once (100 registers a thread)
 
-// out0[i] (i < split), out1[i - split] = the sums over `parts` rows of n floats, in one fixed order.
+// out0[i] (i < split), out1[i - split] = the sums over `parts` rows of n floats, in one fixed order (nullptr: not written).
 cudaError_t launch_sum_parts(const float *ws, int parts, int n, float *out0, float *out1, int split, cudaStream_t stream);
 cudaError_t launch_mixer_prep(const MixerPrepArgs &p, bool bwd);
 cudaError_t launch_norm_gate(const NormGateArgs &p, bool bwd);

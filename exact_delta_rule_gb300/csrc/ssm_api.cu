@@ -4,6 +4,7 @@
 
 #include "api_args.cuh"
 #include "conv.cuh"
+#include "group_norm.cuh"
 #include "ssm.cuh"
 
 using namespace efla;
@@ -54,6 +55,18 @@ efla_status check_ssm(int B, int T, int D, int N, int G, efla_dtype dtype) {
     if (D / G % vec) return api_fail(EFLA_ERR_UNSUPPORTED, "D=%d: a group's %d channels must be a multiple of %d", D, D / G, vec);
     if (((long long)B + 1) * ssm_tiles(D, N, G) > MOST / 4 || (long long)B * T > (1LL << 40) / ((long long)G * N))
         return api_fail(EFLA_ERR_UNSUPPORTED, "B=%d T=%d D=%d G=%d: too many rows of channels", B, T, D, G);
+    return EFLA_OK;
+}
+
+efla_status check_group_norm(int rows, int L, int C, int groups, efla_dtype dtype, efla_activation act, float eps) {
+    if (groups <= 0) return api_fail(EFLA_ERR_INVALID_ARG, "groups=%d must be positive", groups);
+    const efla_status s = check_rows("C", rows, L, C);
+    if (s != EFLA_OK) return s;
+    if (C % groups) return api_fail(EFLA_ERR_INVALID_ARG, "C=%d must be a multiple of groups=%d", C, groups);
+    if (!dtype_ok(dtype)) return api_fail(EFLA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (!activation_ok(act)) return api_fail(EFLA_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+    if (!(eps >= 0.f) || !isfinite(eps)) return api_fail(EFLA_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", eps);
+    if ((long long)rows * C > MOST * 4) return api_fail(EFLA_ERR_UNSUPPORTED, "rows=%d C=%d: too many rows of channels", rows, C);
     return EFLA_OK;
 }
 
@@ -269,6 +282,55 @@ efla_status efla_ssm_step(const void *x, const void *dt, const float *A_log, con
     a.y = y, a.B = B, a.T = 1, a.D = D, a.N = d_state, a.G = G, a.nseq = B, a.dtype = dtype;
     a.stream = reinterpret_cast<cudaStream_t>(stream);
     return launched(launch_ssm_step(a), "scan step launch");
+}
+
+efla_status efla_group_norm_workspace(int rows, int L, int C, int groups, efla_dtype dtype, int backward, size_t *bytes) {
+    if (!bytes) return api_fail(EFLA_ERR_INVALID_ARG, "bytes must be non-NULL");
+    const efla_status s = check_group_norm(rows, L, C, groups, dtype, EFLA_ACT_NONE, 0.f);
+    if (s != EFLA_OK) return s;
+    *bytes = (size_t)rows * L > 0 ? gn_ws(rows, L, C, groups, dtype, backward != 0) * sizeof(float) : 0;
+    return api_ok();
+}
+
+efla_status efla_group_norm(const void *x, const float *w, const float *b, void *y, float *stats, int rows, int L, int C,
+                            int groups, efla_dtype dtype, efla_activation activation, float eps, void *workspace,
+                            size_t workspace_bytes, efla_stream_t stream) {
+    efla_status s = check_group_norm(rows, L, C, groups, dtype, activation, eps);
+    if (s != EFLA_OK) return s;
+    size_t need = 0;
+    if ((s = efla_group_norm_workspace(rows, L, C, groups, dtype, 0, &need)) != EFLA_OK) return s;
+    if ((s = need_workspace(workspace, workspace_bytes, need)) != EFLA_OK) return s;
+    const size_t n = (size_t)rows * L * C * es(dtype), cb = (size_t)C * 4;
+    s = check_args({{"x", x, n, IN}, {"w", w, cb, IN_OPT}, {"b", b, cb, IN_OPT}, {"y", y, n, OUT, {"x"}},
+                    {"stats", stats, (size_t)rows * groups * 8, OUT_OPT}, {"workspace", workspace, need, OUT_OPT}});
+    if (s != EFLA_OK) return s;
+    if (n == 0) return api_ok();
+    GroupNormArgs a{};
+    a.x = x, a.w = w, a.b = b, a.y = y, a.stats = stats, a.ws = static_cast<float *>(workspace);
+    a.rows = rows, a.L = L, a.C = C, a.G = groups, a.dtype = dtype, a.silu = activation == EFLA_ACT_SILU, a.eps = eps;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    return launched(launch_group_norm(a), "group norm launch");
+}
+
+efla_status efla_group_norm_bwd(const void *x, const float *w, const float *b, const float *stats, const void *dy,
+                                void *dx, float *dw, float *db, int rows, int L, int C, int groups, efla_dtype dtype,
+                                efla_activation activation, void *workspace, size_t workspace_bytes, efla_stream_t stream) {
+    efla_status s = check_group_norm(rows, L, C, groups, dtype, activation, 0.f);
+    if (s != EFLA_OK) return s;
+    size_t need = 0;
+    if ((s = efla_group_norm_workspace(rows, L, C, groups, dtype, 1, &need)) != EFLA_OK) return s;
+    if ((s = need_workspace(workspace, workspace_bytes, need)) != EFLA_OK) return s;
+    const size_t n = (size_t)rows * L * C * es(dtype), cb = (size_t)C * 4;
+    s = check_args({{"x", x, n, IN}, {"w", w, cb, IN_OPT}, {"b", b, cb, IN_OPT}, {"stats", stats, n ? (size_t)rows * groups * 8 : 0, IN},
+                    {"dy", dy, n, IN}, {"dx", dx, n, OUT}, {"dw", dw, cb, OUT_OPT}, {"db", db, cb, OUT_OPT},
+                    {"workspace", workspace, need, OUT_OPT}});
+    if (s != EFLA_OK) return s;
+    GroupNormArgs a{};
+    a.x = x, a.w = w, a.b = b, a.stats = const_cast<float *>(stats), a.dy = dy, a.dx = dx, a.dw = dw, a.db = db;
+    a.ws = static_cast<float *>(workspace);
+    a.rows = rows, a.L = L, a.C = C, a.G = groups, a.dtype = dtype, a.silu = activation == EFLA_ACT_SILU;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    return launched(launch_group_norm_bwd(a), "group norm backward launch");
 }
 
 }  // extern "C"

@@ -5,6 +5,7 @@ marshalling only).
     y_t = silu(bias + sum_j w_j x_{t-W+1+j})                                       (causal_conv)
     delta_t = softplus(dt_t + dt_bias),  h_t = exp(-exp(A_log) delta_t) h_{t-1} + delta_t x_t B_t,
     y_t = (C_t . h_t + D x_t) silu(z_t)                                            (ssm_scan)
+    y = silu(w (x - mean) / sqrt(var + eps) + b) over the channels of a group      (group_norm)
 
 The calls are plain functions: gradients come from the ``*_bwd`` calls, and nothing is recorded for
 autograd.
@@ -20,7 +21,7 @@ from . import _check, load
 from .gated import (_DT, _INT_MAX, _bad, _empty, _empty_as, _first, _given, _need, _on_device, _ptr, _stream, _too_large,
                     _workspace)
 
-_vp, _ip, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_vp, _ip, _sz, _fl = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 _SIGNATURES = {
     "efla_causal_conv": [_vp] * 7 + [_ip] * 7 + [_vp],
     "efla_causal_conv_bwd": [_vp] * 10 + [_ip] * 6 + [_vp, _sz, _vp],
@@ -32,6 +33,9 @@ _SIGNATURES = {
     "efla_ssm_bwd_workspace": [_ip] * 5 + [ctypes.POINTER(_sz)],
     "efla_ssm_scan_bwd": [_vp] * 20 + [_ip] * 7 + [_vp, _sz, _vp],
     "efla_ssm_step": [_vp] * 10 + [_ip] * 5 + [_vp],
+    "efla_group_norm": [_vp] * 5 + [_ip] * 6 + [_fl, _vp, _sz, _vp],
+    "efla_group_norm_workspace": [_ip] * 6 + [ctypes.POINTER(_sz)],
+    "efla_group_norm_bwd": [_vp] * 8 + [_ip] * 6 + [_vp, _sz, _vp],
 }
 _ACTIVATIONS = {None: 0, "silu": 1}
 _bound = None
@@ -287,3 +291,74 @@ def ssm_step(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Te
     _check(_lib().efla_ssm_step(*_inputs(x, dt, A_log, B, C, D, dt_bias, z), S.data_ptr(), y.data_ptr(), rows, ch, N, G, code,
                                 _stream(stream, x)))
     return y
+
+
+def _group_norm_args(x, w, b, groups):
+    if x.dim() < 2:
+        _bad(f"x must be [rows, ..., C], got {list(x.shape)}")
+    code = _first("x", x, x.dim())
+    rows, C = x.shape[0], x.shape[-1]
+    L = 1
+    for n in x.shape[1:-1]:
+        L *= n
+    if max(rows, L, C, groups) > _INT_MAX:
+        _too_large(rows, L, C, groups)
+    if groups < 1 or C % groups:
+        _bad(f"x's {C} channels must be a multiple of groups={groups}")
+    _need("x", x, x.shape, x.dtype, x)
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            _need(name, t, (C,), torch.float32, x)
+    return code, rows, L, C
+
+
+def group_norm_workspace(rows: int, L: int, C: int, groups: int, dtype: torch.dtype, backward: bool = False) -> int:
+    """Workspace bytes of ``group_norm`` and, with ``backward``, of ``group_norm_bwd``."""
+    if dtype not in _DT:
+        _bad(f"unsupported dtype {dtype}")
+    if max(rows, L, C, groups) > _INT_MAX:
+        _too_large(rows, L, C, groups)
+    return _bytes("efla_group_norm_workspace", rows, L, C, groups, _DT[dtype], int(backward))
+
+
+def group_norm(x: torch.Tensor, w: Optional[torch.Tensor], b: Optional[torch.Tensor], groups: int, *, eps: float = 1e-5,
+               activation: Optional[str] = None, y: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor] = None,
+               return_stats: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """The group norm with its activation, channels last (``efla_group_norm``).
+
+    x [rows, ..., C] (bf16 or fp32), normalised over everything between and the C / groups channels of a group: a
+    token's heads for x [tokens, C], a feature map for x [batch, height, width, C].  w, b [C] fp32 or None.  ``y`` may
+    be x.  Returns y, or (y, stats) -- stats [rows, groups, 2] fp32 for ``group_norm_bwd`` -- where ``stats`` is given
+    or asked for."""
+    code, rows, L, C = _group_norm_args(x, w, b, groups)
+    act = _activation(activation)
+    _on_device(x)
+    Lb = _lib()
+    y = _given("y", y, x.shape, x.dtype, x, stream)
+    if stats is not None or return_stats:
+        stats = _given("stats", stats, (rows, groups, 2), torch.float32, x, stream)
+    need = _bytes("efla_group_norm_workspace", rows, L, C, groups, code, 0)
+    ws = _workspace(workspace, need, x, stream) if need else None
+    _check(Lb.efla_group_norm(x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(), _ptr(stats), rows, L, C, groups, code, act, eps,
+                              _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream, x)))
+    return y if stats is None else (y, stats)
+
+
+def group_norm_bwd(x: torch.Tensor, w: Optional[torch.Tensor], b: Optional[torch.Tensor], groups: int,
+                   stats: torch.Tensor, dy: torch.Tensor, *, activation: Optional[str] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of ``group_norm`` from dy in x's dtype and the forward's stats (``efla_group_norm_bwd``): a dict with dx
+    in x's dtype, dw and db [C] fp32 (None without w, b)."""
+    code, rows, L, C = _group_norm_args(x, w, b, groups)
+    act = _activation(activation)
+    _need("stats", stats, (rows, groups, 2), torch.float32, x)
+    _need("dy", dy, x.shape, x.dtype, x)
+    _on_device(x)
+    Lb = _lib()
+    ws = _workspace(workspace, _bytes("efla_group_norm_workspace", rows, L, C, groups, code, 1), x, stream)
+    out = {"dx": _empty_as(x, x.dtype, stream), "dw": None if w is None else _empty_as(w, torch.float32, stream),
+           "db": None if b is None else _empty_as(b, torch.float32, stream)}
+    _check(Lb.efla_group_norm_bwd(x.data_ptr(), _ptr(w), _ptr(b), stats.data_ptr(), dy.data_ptr(),
+                                  *(_ptr(t) for t in out.values()), rows, L, C, groups, code, act, ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _stream(stream, x)))
+    return out

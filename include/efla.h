@@ -553,6 +553,31 @@ efla_status efla_ssm_step(const void *x, const void *dt, const float *A_log, con
                           const float *D_skip, const float *dt_bias, const void *z, float *S, void *y, int B, int D,
                           int d_state, int G, efla_dtype dtype, efla_stream_t stream);
 
+/*
+ * efla_group_norm -- the group norm with its activation, channels last:
+ *
+ *   n = (x - mean) / sqrt(var + eps) over the L positions and C / groups neighbouring channels of a group,
+ *   y = w n + b or silu of it
+ *
+ *   x, y     [rows, L, C] dtype (L = 1: a token's heads);  w, b [C] fp32, or NULL (1, 0)
+ *   stats    [rows, groups, 2] fp32, each group's mean and 1 / sqrt(var + eps), or NULL (not written)
+ *   workspace  at least efla_group_norm_workspace bytes (0 for some sizes), overlapping no argument
+ * C a multiple of 8 and of groups.  y == x is allowed.  fp32 arithmetic, each output rounded once; the mean is taken
+ * from the values before the squares.
+ */
+efla_status efla_group_norm(const void *x, const float *w, const float *b, void *y, float *stats, int rows, int L,
+                            int C, int groups, efla_dtype dtype, efla_activation activation, float eps,
+                            void *workspace, size_t workspace_bytes, efla_stream_t stream);
+efla_status efla_group_norm_workspace(int rows, int L, int C, int groups, efla_dtype dtype, int backward,
+                                      size_t *bytes);
+
+/* Its gradients from dy [rows, L, C] and the forward's stats: dx in dtype, dw and db [C] (or NULL) fp32, summed over
+ * rows and positions in a fixed order.  workspace: that of backward = 1. */
+efla_status efla_group_norm_bwd(const void *x, const float *w, const float *b, const float *stats, const void *dy,
+                                void *dx, float *dw, float *db, int rows, int L, int C, int groups,
+                                efla_dtype dtype, efla_activation activation, void *workspace,
+                                size_t workspace_bytes, efla_stream_t stream);
+
 /* Reads the calling thread's current device's status word on `stream`
  * (synchronising that stream), resets it to EFLA_OK and returns what it held:
  * EFLA_ERR_DEVICE_TIMEOUT after a bounded in-kernel wait expired, or

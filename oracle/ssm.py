@@ -1,9 +1,11 @@
-"""The short causal convolution and the selective state space scan in 64 bits, straight from the definitions
+"""The short causal convolution, the selective state space scan and the group norm in 64 bits, straight from the definitions
 (torch, any device): token by token, the reverse modes written out by hand.
 
     s_t = bias + sum_j w_j x_{t-W+1+j},  y_t = s_t or silu(s_t)
     delta_t = softplus(dt_t + dt_bias),  h_t = e^{-e^{A_log} delta_t} h_{t-1} + delta_t x_t B_t,
     y_t = (C_t . h_t + D x_t) silu(z_t)
+
+    n = (x - mean) / sqrt(var + eps) over positions and channels of a group,  y = w n + b or silu of it
 
 x, dt, z [B, T, D], B, C [B, T, G, N], A_log [D, N]; channel d reads group d // (D // G).  With ``size=True`` every
 factor and every summand is taken without its sign: the sum of the magnitudes that an output is made of, which its
@@ -138,3 +140,41 @@ def scan_bwd(x, dt, A_log, B, C, D, dt_bias, z, S0, dy, dS_T=None, size=False):
     out |= {"dx": dx + D * g, "ddt": ddt, "dB": fold(dB), "dC": fold(dC), "dA_log": dA.sum(0) * A,
             "dD": (g * x).sum((0, 1)) if with_D else None, "ddt_bias": ddt.sum((0, 1)) if with_bias else None, "dS0": lam}
     return out
+
+
+def _normed(x, groups, eps):
+    xg = x.reshape(x.shape[0], -1, groups, x.shape[-1] // groups)
+    mean = xg.mean((1, 3), keepdim=True)
+    r = 1 / torch.sqrt(((xg - mean) ** 2).mean((1, 3), keepdim=True) + eps)
+    return (xg - mean) * r, mean, r
+
+
+def group_norm(x, w, b, groups, eps=1e-5, silu=False):
+    """(y, stats) for x [rows, ..., C]."""
+    x, w, b = _f64(x, w, b)
+    n, mean, r = _normed(x, groups, eps)
+    s = n.reshape(x.shape)
+    s = s if w is None else s * w
+    s = s if b is None else s + b
+    return _silu(s) if silu else s, torch.stack([mean[:, 0, :, 0], r[:, 0, :, 0]], -1)
+
+
+def group_norm_bwd(x, w, b, groups, dy, eps=1e-5, silu=False):
+    """Gradients, and the sum of the magnitudes that each is made of."""
+    x, w, b, dy = _f64(x, w, b, dy)
+    C = x.shape[-1]
+    n, _, r = _normed(x, groups, eps)
+    ww, bb = x.new_ones(C) if w is None else w, x.new_zeros(C) if b is None else b
+    flat = n.reshape(x.shape)
+    ds = dy * _dsilu(flat * ww + bb) if silu else dy
+    dn = (ds * ww).reshape(n.shape)
+    mean = lambda t: t.mean((1, 3), keepdim=True)  # noqa: E731
+    dx = (r * (dn - mean(dn) - n * mean(dn * n))).reshape(x.shape)
+    # (dn is rounded in the activation's slope too: 0.5 of the change of s at most)
+    mag = (dy.abs() * (1.1 + 0.5 * (flat * ww).abs() + 0.5 * bb.abs()) if silu else dy.abs())
+    dm = (mag * ww.abs()).reshape(n.shape)
+    size = (r * (dm * (1 + n.abs()) + mean(dm) + n.abs() * mean(dm * n.abs()))).reshape(x.shape)
+    lead = tuple(range(x.dim() - 1))
+    got = {"dx": dx, "dw": None if w is None else (ds * flat).sum(lead), "db": None if b is None else ds.sum(lead)}
+    sizes = {"dx": size, "dw": (mag * (1 + flat.abs())).sum(lead), "db": mag.sum(lead)}
+    return got, sizes

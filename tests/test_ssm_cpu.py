@@ -87,6 +87,21 @@ def test_oracle_scan_gradients_are_the_differences():
             assert abs(diff - float(got["d" + name].reshape(-1)[i])) <= 1e-6 * (1 + abs(diff)), (name, i)
 
 
+@pytest.mark.parametrize("shape, groups", [((3, 12), 4), ((2, 5, 6), 2), ((2, 2, 3, 4), 1)])
+@pytest.mark.parametrize("silu", [True, False])
+def test_oracle_group_norm(shape, groups, silu):
+    gen = torch.Generator().manual_seed(groups)
+    x, w, b = rand(gen, *shape, grad=True), rand(gen, shape[-1], grad=True), rand(gen, shape[-1], grad=True)
+    s = torch.nn.functional.group_norm(x.movedim(-1, 1), groups, w, b, 1e-5).movedim(1, -1)
+    y = torch.nn.functional.silu(s) if silu else s
+    torch.testing.assert_close(y.detach(), ssm.group_norm(x, w, b, groups, silu=silu)[0])
+    dy = torch.randn_like(y)
+    got, sizes = ssm.group_norm_bwd(x, w, b, groups, dy, silu=silu)
+    for a, name in zip(torch.autograd.grad(y, [x, w, b], dy), ("dx", "dw", "db")):
+        torch.testing.assert_close(a, got[name])
+        assert bool((sizes[name] >= a.abs() - 1e-12).all())
+
+
 # ------------------------------------------------------------------------------ refusals of the binding
 def conv_args(**over):
     a = {"x": torch.zeros(2, 5, 16), "w": torch.zeros(16, 4), "bias": torch.zeros(16), "state0": torch.zeros(2, 3, 16)} | over
@@ -175,6 +190,24 @@ def test_scan_refuses_more():
         efla.ssm_step(**one, S=torch.zeros(2, 16, 32))
     with pytest.raises(efla.EflaError, match="exceeds"):
         efla.ssm_scan_workspace(1, 1 << 32, 16, 16)
+
+
+def test_group_norm_refuses():
+    x, w = torch.zeros(3, 5, 16), torch.zeros(16)
+    for over, what in (({"x": torch.zeros(16)}, "x must be"), ({"x": x.half()}, "bfloat16 or float32"), ({"groups": 3}, "multiple of"),
+                       ({"groups": 0}, "multiple of"), ({"w": torch.zeros(8)}, "w must be"), ({"b": w.bfloat16()}, "b must be"),
+                       ({"x": torch.zeros(3, 16, 5).transpose(1, 2)}, "x must be contiguous"), ({}, "CUDA")):
+        a = {"x": x, "w": w, "b": w, "groups": 4} | over
+        with pytest.raises(efla.EflaError, match=what):
+            efla.group_norm(**a)
+        with pytest.raises(efla.EflaError):
+            efla.group_norm_bwd(**a, stats=torch.zeros(3, 4, 2), dy=x)
+    with pytest.raises(efla.EflaError, match="activation"):
+        efla.group_norm(x, w, w, 4, activation="relu")
+    with pytest.raises(efla.EflaError, match="stats must be"):
+        efla.group_norm_bwd(x, w, w, 4, torch.zeros(3, 4), x)
+    with pytest.raises(efla.EflaError, match="dy must be"):
+        efla.group_norm_bwd(x, w, w, 4, torch.zeros(3, 4, 2), x.bfloat16())
 
 
 # ------------------------------------------------------------------------------ refusals of the C ABI
@@ -281,6 +314,33 @@ def test_c_scan_training_and_step_refuse(lib):
         assert step(**kw) == 1, kw
     assert step(N=4) == 2
     assert step(rows=0, x=None, dt=None, B=None, C=None, S=None, y=None) == 0
+
+
+def test_c_group_norm_refuses(lib):
+    n = ctypes.c_size_t()
+    assert lib.efla_group_norm_workspace(2, 9, 64, 4, 0, 1, None) == 1
+    assert lib.efla_group_norm_workspace(2, 9, 60, 4, 0, 1, ctypes.byref(n)) == 2
+    assert lib.efla_group_norm_workspace(2, 1, 64, 4, 0, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.efla_group_norm_workspace(2, 9, 64, 4, 0, 1, ctypes.byref(n)) == 0
+
+    def fwd(**kw):
+        a = dict(x=A[0], w=A[1], b=A[2], y=A[3], stats=A[4], rows=2, L=9, C=64, groups=4, dt=0, act=1, eps=1e-5, ws=A[5], wb=n.value,
+                 s=None) | kw
+        return lib.efla_group_norm(*a.values())
+
+    for kw in (dict(rows=-1), dict(L=-1), dict(C=0), dict(groups=0), dict(groups=5), dict(dt=2), dict(act=-1), dict(eps=-1.0),
+               dict(eps=float("nan")), dict(x=None), dict(y=None), dict(w=A[1] + 4), dict(y=A[0] + 16), dict(stats=A[0]),
+               dict(ws=A[3])):
+        assert fwd(**kw) == 1, kw
+    assert fwd(rows=0, x=None, y=None) == 0
+
+    def bwd(**kw):
+        a = dict(x=A[0], w=A[1], b=A[2], stats=A[3], dy=A[4], dx=A[5], dw=A[6], db=A[7], rows=2, L=9, C=64, groups=4, dt=0, act=1,
+                 ws=A[8], wb=n.value, s=None) | kw
+        return lib.efla_group_norm_bwd(*a.values())
+
+    for kw in (dict(stats=None), dict(dy=None), dict(dx=None), dict(ws=None), dict(wb=n.value - 1), dict(dx=A[0]), dict(dw=A[1])):
+        assert bwd(**kw) == 1, kw
 
 
 def test_workspaces_of_whole_and_cut_rows():

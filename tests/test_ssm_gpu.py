@@ -363,6 +363,78 @@ def test_step_continues_the_prompt(dtype, N, B, D, G):
     close(S, ref_S, size_S, scan_share(3), "S")
 
 
+# ------------------------------------------------------------------------------------ group norm
+def norm_share(L):
+    return (L + 610) * U + 7e-7
+
+
+def check_group_norm(shape, groups, dtype, silu, affine=True, offset=0.0, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    C = shape[-1]
+    x = (randn(gen, *shape) * (0.5 + torch.rand(C, generator=gen, device="cuda")) + randn(gen, C) + offset).to(dtype)
+    w, b = (randn(gen, C), randn(gen, C)) if affine else (None, None)
+    dy, act = randn(gen, *shape).to(dtype), "silu" if silu else None
+    L = math.prod(shape[1:-1])
+    y, stats = efla.group_norm(x, w, b, groups, activation=act, return_stats=True)
+    assert torch.equal(y, efla.group_norm(x, w, b, groups, activation=act))
+    same = x.clone()
+    assert torch.equal(efla.group_norm(same, w, b, groups, activation=act, y=same), y)
+    if not x.numel():
+        assert efla.group_norm_bwd(x, w, b, groups, stats, dy, activation=act)["dw"].abs().sum() == 0
+        return
+    ref, ref_stats = ssm.group_norm(x, w, b, groups, silu=silu)
+    mean, r = ref_stats.unbind(-1)
+    width = (mean.abs() + 1 / r)  # the size of a group's values
+    share = norm_share(L)
+    close(stats[..., 0], mean, width, share, "mean")
+    close(stats[..., 1], r, r * width * r, 2 * share, "r")
+    spread = (width * r).reshape(shape[0], *[1] * (len(shape) - 2), groups).repeat_interleave(C // groups, -1)
+    n = ssm.group_norm(x, None, None, groups)[0].abs() + spread
+    size = n * (w.abs() if affine else 1) + (b.abs() if affine else 0)
+    close(y, ref, 1.1 * size, 4 * share, "y")
+    got = efla.group_norm_bwd(x, w, b, groups, stats, dy, activation=act)
+    ref, size = ssm.group_norm_bwd(x, w, b, groups, dy, silu=silu)
+    big = float(spread.max()) ** 2  # what an error of the mean or r, relative to the values' size, does to n
+    for name, v in ref.items():
+        if v is None:
+            assert got[name] is None
+            continue
+        close(got[name], v, size[name] * (1 + big), 4 * share + (0 if name == "dx" else x.numel() // C * U), name)
+    again = efla.group_norm_bwd(x, w, b, groups, stats, dy, activation=act)
+    for name, v in again.items():
+        assert v is None or torch.equal(v, got[name]), name
+
+
+@pytest.mark.parametrize("shape, groups", [
+    ((1, 8), 1), ((7, 2048), 16), ((1000, 256), 1), ((33, 64), 8), ((5, 24), 3), ((3, 40), 1), ((2, 96), 32), ((65, 640), 16),
+    ((9, 4096), 2), ((2, 8192), 1), ((700, 16), 16), ((0, 16), 2), ((3, 192), 4), ((513, 264), 11)])
+@pytest.mark.parametrize("dtype, silu", [(F32, True), (BF16, False)])
+def test_group_norm_of_tokens(dtype, silu, shape, groups):
+    check_group_norm(shape, groups, dtype, silu)
+
+
+@pytest.mark.parametrize("shape, groups", [
+    ((2, 2, 8), 8), ((1, 9, 320), 32), ((3, 5, 7, 40), 4), ((2, 1000, 64), 2), ((1, 64, 64, 320), 32), ((40, 3, 16), 1),
+    ((2, 0, 16), 2), ((1, 300, 1032), 3), ((200, 17, 8), 4)])
+@pytest.mark.parametrize("dtype, silu", [(F32, True), (BF16, True), (BF16, False)])
+def test_group_norm_of_maps(dtype, silu, shape, groups):
+    check_group_norm(shape, groups, dtype, silu)
+
+
+@pytest.mark.parametrize("shape, groups", [((20, 512), 4), ((2, 300, 64), 4)])
+def test_group_norm_extremes(shape, groups):
+    check_group_norm(shape, groups, F32, True, affine=False)
+    check_group_norm(shape, groups, F32, False, offset=300.0)  # a mean far from 0
+    y = efla.group_norm(torch.full(shape, 3.0, device="cuda"), None, torch.ones(shape[-1], device="cuda"), groups)
+    assert bool((y == 1).all())  # no variance: n = 0
+    x = torch.randn(shape, device="cuda")
+    y = efla.group_norm(x, None, None, groups)
+    x[1, ..., 0] = math.nan
+    y2 = efla.group_norm(x, None, None, groups)
+    each = shape[-1] // groups
+    assert bool(y2[1, ..., :each].isnan().all()) and torch.equal(y2[0], y[0]) and torch.equal(y2[1, ..., each:], y[1, ..., each:])
+
+
 # ------------------------------------------------------------------------------------ the manner of the calls
 def between_sentinels(t, pad=4096):
     """A copy of t in the middle of a larger allocation filled with a pattern, and a check of the rest."""
@@ -404,7 +476,11 @@ def test_streams_and_graphs():
         g = efla.ssm_scan_bwd(**a, dy=dy, workspace=ws, saved=True, stream=stream)
         gc = efla.causal_conv_bwd(**c, dy=dy, stream=stream)
         y2, S2 = efla.ssm_scan(**a, stream=stream)
-        return [y, out, S, y2, S2, *g.values(), *(v for v in gc.values() if v is not None)]
+        heads, st = efla.group_norm(out[0], a["D"], a["dt_bias"], 4, return_stats=True, stream=stream)
+        whole, st2 = efla.group_norm(out, None, None, 4, activation="silu", return_stats=True, stream=stream)
+        gn = efla.group_norm_bwd(out, None, None, 4, st2, dy, activation="silu", stream=stream)
+        gh = efla.group_norm_bwd(out[0], a["D"], a["dt_bias"], 4, st, dy[0], stream=stream)
+        return [y, out, S, y2, S2, heads, st, whole, st2, gn["dx"], *gh.values(), *g.values(), *(v for v in gc.values() if v is not None)]
 
     want = everything()
     torch.cuda.synchronize()
