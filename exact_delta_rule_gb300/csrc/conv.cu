@@ -22,7 +22,7 @@ namespace efla {
 namespace {
 
 constexpr int NT = CONV_NT;
-constexpr int FWD_ROWS = 16;  // tokens a thread
+constexpr int BATCH = 8;  // rows in flight a thread
 
 // To 2 + 1.2 |x| ulp, as the output gate's.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
@@ -72,21 +72,29 @@ __device__ __forceinline__ void store(void *p, long long row, int vecs, int v, c
 template <int W, int V>
 struct Taps {
     float w[V][W], bias[V];
-    __device__ __forceinline__ void load(const ConvArgs &p, int c0) {
+    __device__ __forceinline__ void load(const ConvArgs &p, int c0) {  // (V W floats from a multiple of 16 bytes)
+        float f[V * W];
+#pragma unroll
+        for (int i = 0; i < V * W / 4; ++i) {
+            const float4 r = reinterpret_cast<const float4 *>(p.w + (size_t)c0 * W)[i];
+            f[4 * i] = r.x, f[4 * i + 1] = r.y, f[4 * i + 2] = r.z, f[4 * i + 3] = r.w;
+        }
 #pragma unroll
         for (int c = 0; c < V; ++c) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[c][j] = p.w[(size_t)(c0 + c) * W + j];
+            for (int j = 0; j < W; ++j) w[c][j] = f[c * W + j];
             bias[c] = p.bias ? p.bias[c0 + c] : 0.f;
         }
     }
 };
 
 // ------------------------------------------------------------------------------------ forward
-// CTAs [0, tiles * cblocks): a tile of the B T tokens x a block of the channels; the others copy the states.
-// first[i], seq[i]: where the sequence of the tile's token i begins, and which it is (-1: no sequence).
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(NT) conv_fwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, unsigned work_ctas) {
+// CTAs [0, work_ctas): runs of `rows` tokens x a block of the channels; the others copy the states.  PACKED: the
+// runs are of all tokens, and first[i], seq[i] say where the sequence of the CTA's token i begins and which it is
+// (-1: none).  Otherwise they are of the rows, row_runs each.
+template <typename T, int V, int W, bool PACKED>
+__global__ void __launch_bounds__(NT, 2) conv_fwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, unsigned work_ctas, int rows,
+                                                      int row_runs) {
     const int tid = threadIdx.x;
     if (blockIdx.x >= work_ctas) {  // state_T: place j of a sequence's last W - 1 inputs
         const long long e = (long long)(blockIdx.x - work_ctas) * NT + tid;
@@ -94,7 +102,7 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(ConvArgs p, int vecs, int 
         const int v = (int)(e % vecs), j = (int)(e / vecs % (W - 1));
         const int n = (int)(e / vecs / (W - 1));
         long long lo, hi;
-        if (p.cu_seqlens) {
+        if (PACKED) {
             lo = p.cu_seqlens[n], hi = p.cu_seqlens[n + 1];
             if (lo < 0 || hi < lo || hi > p.T) {
                 if (v == 0 && j == 0) atomicExch(p.status, (int)EFLA_ERR_INVALID_ARG);
@@ -113,76 +121,96 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(ConvArgs p, int vecs, int 
         return;
     }
     extern __shared__ int shared[];
-    const int subs = NT / lanes, tile_rows = FWD_ROWS * subs;
-    int *first = shared, *seq = shared + tile_rows;
-    const long long tokens = (long long)p.B * p.T, t0 = (long long)(blockIdx.x / cblocks) * tile_rows;
-    if (p.cu_seqlens) {
+    const int subs = NT / lanes, tile = blockIdx.x / cblocks, sub = tid / lanes;
+    int *first = shared, *seq = shared + rows * subs;
+    long long t0 = 0, begin, end, lo = 0;
+    int n = 0;
+    if (PACKED) {
+        const int tile_rows = rows * subs;
+        t0 = (long long)tile * tile_rows;
         for (int i = tid; i < tile_rows; i += NT) seq[i] = -1;
         __syncthreads();
-        for (int n = tid; n < p.N; n += NT) {
-            const long long lo = p.cu_seqlens[n], hi = p.cu_seqlens[n + 1];
-            if (lo < 0 || hi < lo || hi > p.T) {
+        for (int i = tid; i < p.N; i += NT) {
+            const long long l = p.cu_seqlens[i], h = p.cu_seqlens[i + 1];
+            if (l < 0 || h < l || h > p.T) {
                 if (blockIdx.x == 0) atomicExch(p.status, (int)EFLA_ERR_INVALID_ARG);
                 continue;
             }
-            const long long from = lo > t0 ? lo : t0, to = hi < t0 + tile_rows ? hi : t0 + tile_rows;
+            const long long from = l > t0 ? l : t0, to = h < t0 + tile_rows ? h : t0 + tile_rows;
             for (long long t = from; t < to; ++t) {
-                first[t - t0] = (int)lo;
-                seq[t - t0] = n;
+                first[t - t0] = (int)l;
+                seq[t - t0] = i;
             }
         }
         __syncthreads();
+        begin = t0 + (long long)sub * rows;
+        end = begin + rows < p.T ? begin + rows : p.T;
+    } else {
+        const long long run = (long long)tile * subs + sub;
+        if (run >= (long long)p.B * row_runs) return;
+        n = (int)(run / row_runs);
+        lo = (long long)n * p.T;
+        begin = lo + run % row_runs * rows;
+        end = begin + rows < lo + p.T ? begin + rows : lo + p.T;
     }
-    const int v = (blockIdx.x % cblocks) * lanes + tid % lanes, sub = tid / lanes;
-    const long long begin = t0 + (long long)sub * FWD_ROWS, end = begin + FWD_ROWS < tokens ? begin + FWD_ROWS : tokens;
+    const int v = (blockIdx.x % cblocks) * lanes + tid % lanes;
     if (v >= vecs || begin >= end) return;
+    float win[W - 1][V];
+    // the W - 1 inputs before token t of the sequence n that begins at lo
+    auto before = [&](long long t) {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const long long at = t - (W - 1) + i;
+            Pack<T, V> r{};
+            if (at >= lo)
+                r = load<T, V>(p.x, at, vecs, v);
+            else if (p.state0)
+                r = load<T, V>(p.state0, (long long)n * (W - 1) + (at - lo + W - 1), vecs, v);
+            unpack(r, win[i]);
+        }
+    };
+    if (PACKED)
+        lo = -1;  // no sequence yet
+    else
+        before(begin);
     Taps<W, V> taps;
     taps.load(p, v * V);
-    float win[W - 1][V];
-    long long start = -1;  // the first token of the sequence that win belongs to
-    bool fresh = true;
-    for (long long t = begin; t < end; ++t) {
-        long long lo;
-        int n;
-        if (p.cu_seqlens) {
-            n = seq[t - t0];
-            if (n < 0) {
-                fresh = true;
-                continue;
+    for (long long t = begin; t < end; t += BATCH) {
+        Pack<T, V> raw[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            raw[k] = Pack<T, V>{};
+            if (t + k < end) raw[k] = load<T, V>(p.x, t + k, vecs, v);
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            if (t + k >= end) break;
+            if (PACKED) {
+                n = seq[t + k - t0];
+                if (n < 0) {
+                    lo = -1;
+                    continue;
+                }
+                if (lo != first[t + k - t0]) {
+                    lo = first[t + k - t0];
+                    before(t + k);
+                }
             }
-            lo = first[t - t0];
-        } else {
-            n = (int)(t / p.T);
-            lo = (long long)n * p.T;
-        }
-        if (fresh || lo != start) {
+            float x[V], s[V];
+            unpack(raw[k], x);
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) {
-                const long long at = t - (W - 1) + i;
-                Pack<T, V> r{};
-                if (at >= lo)
-                    r = load<T, V>(p.x, at, vecs, v);
-                else if (p.state0)
-                    r = load<T, V>(p.state0, (long long)n * (W - 1) + (at - lo + W - 1), vecs, v);
-                unpack(r, win[i]);
+            for (int c = 0; c < V; ++c) {
+                float a = taps.bias[c];
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
+                a = fmaf(taps.w[c][W - 1], x[c], a);
+                s[c] = p.silu ? a * sigmoid(a) : a;
+#pragma unroll
+                for (int i = 0; i + 1 < W - 1; ++i) win[i][c] = win[i + 1][c];
+                win[W - 2][c] = x[c];
             }
-            start = lo;
-            fresh = false;
+            store<T, V>(p.y, t + k, vecs, v, s);
         }
-        float x[V], s[V];
-        unpack(load<T, V>(p.x, t, vecs, v), x);
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-            float a = taps.bias[c];
-#pragma unroll
-            for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
-            a = fmaf(taps.w[c][W - 1], x[c], a);
-            s[c] = p.silu ? a * sigmoid(a) : a;
-#pragma unroll
-            for (int i = 0; i + 1 < W - 1; ++i) win[i][c] = win[i + 1][c];
-            win[W - 2][c] = x[c];
-        }
-        store<T, V>(p.y, t, vecs, v, s);
     }
 }
 
@@ -190,21 +218,22 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(ConvArgs p, int vecs, int 
 // A CTA: `lanes` vectors of 4 channels x NT / lanes runs of CONV_BWD_ROWS places of an extended row, and every
 // parts-th such tile after it; row_runs runs a row.
 template <typename T, int W>
-__global__ void __launch_bounds__(NT) conv_bwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, int parts, int row_runs) {
+__global__ void __launch_bounds__(NT, 2) conv_bwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, int parts, int row_runs) {
     constexpr int V = 4, R = CONV_BWD_ROWS;
     __shared__ float red[NT][V + 1];
     const int tid = threadIdx.x, lane = tid % lanes, sub = tid / lanes, subs = NT / lanes;
     const int cb = blockIdx.x % cblocks, tile = blockIdx.x / cblocks, v = cb * lanes + lane;
-    const long long runs = (long long)p.B * row_runs, ends = (long long)p.T + W - 1;
+    const long long runs = (long long)p.B * row_runs;
+    const int ends = p.T + W - 1;
     float dw[V][W] = {}, db[V] = {};
     Taps<W, V> taps;
     if (v < vecs) taps.load(p, v * V);
     for (long long run = (long long)tile * subs + sub; v < vecs && run < runs; run += (long long)parts * subs) {
         const int b = (int)(run / row_runs);
-        const long long e0 = run % row_runs * R;
+        const int e0 = (int)(run % row_runs) * R;
         const long long row = (long long)b * p.T;
         // x at place e of the extended row
-        auto place = [&](long long e, float(&x)[V]) {
+        auto place = [&](int e, float(&x)[V]) {
             Pack<T, V> r{};
             if (e >= W - 1) {
                 if (e < ends) r = load<T, V>(p.x, row + e - (W - 1), vecs, v);
@@ -216,12 +245,29 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(ConvArgs p, int vecs, int 
         float win[W - 1][V], old[W - 1][V] = {};  // x at t .. t + W - 2 (extended), ds of the W - 1 tokens before t
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) place(e0 - (W - 1) + i, win[i]);
-        const long long e1 = e0 + R < ends ? e0 + R : ends;
-        for (long long t = e0 - (W - 1); t < e1; ++t) {  // token t's newest input is at place t + W - 1
-            float x[V], ds[V] = {};
-            place(t + W - 1, x);
-            if (t >= 0 && t < p.T) {
-                unpack(load<T, V>(p.dy, row + t, vecs, v), ds);
+        const int e1 = min(e0 + R, ends);
+        for (int tb = e0 - (W - 1); tb < e1; tb += BATCH) {  // token t's newest input is at place t + W - 1
+            Pack<T, V> rx[BATCH], rd[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int t = tb + k;
+                rx[k] = rd[k] = Pack<T, V>{};
+                if (t < e1) {
+                    if (t >= 0 && t < p.T) {
+                        rx[k] = load<T, V>(p.x, row + t, vecs, v);
+                        rd[k] = load<T, V>(p.dy, row + t, vecs, v);
+                    } else if (t < 0 && t + W - 1 >= 0 && p.state0) {
+                        rx[k] = load<T, V>(p.state0, (long long)b * (W - 1) + t + W - 1, vecs, v);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int t = tb + k;
+                if (t >= e1) break;
+                float x[V], ds[V];
+                unpack(rx[k], x);
+                unpack(rd[k], ds);  // 0 outside the row
 #pragma unroll
                 for (int c = 0; c < V; ++c) {
                     if (p.silu) {
@@ -230,7 +276,7 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(ConvArgs p, int vecs, int 
                         for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
                         a = fmaf(taps.w[c][W - 1], x[c], a);
                         const float g = sigmoid(a);
-                        ds[c] *= g * fmaf(a, 1.f - g, 1.f);
+                        if (t >= 0 && t < p.T) ds[c] *= g * fmaf(a, 1.f - g, 1.f);
                     }
                     if (t >= e0) {
 #pragma unroll
@@ -239,30 +285,30 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(ConvArgs p, int vecs, int 
                         db[c] += ds[c];
                     }
                 }
-            }
-            if (t >= e0) {  // place e = t: sum_j w_j ds_{t-j}
-                float d[V] = {};
-                if (p.dstate_T && t >= p.T) unpack(load<T, V>(p.dstate_T, (long long)b * (W - 1) + t - p.T, vecs, v), d);
+                if (t >= e0) {  // place e = t: sum_j w_j ds_{t-j}
+                    float d[V] = {};
+                    if (p.dstate_T && t >= p.T) unpack(load<T, V>(p.dstate_T, (long long)b * (W - 1) + t - p.T, vecs, v), d);
+#pragma unroll
+                    for (int c = 0; c < V; ++c) {
+                        d[c] = fmaf(taps.w[c][0], ds[c], d[c]);
+#pragma unroll
+                        for (int j = 1; j < W; ++j) d[c] = fmaf(taps.w[c][j], old[W - 1 - j][c], d[c]);
+                    }
+                    if (t >= W - 1)
+                        store<T, V>(p.dx, row + t - (W - 1), vecs, v, d);
+                    else if (p.dstate0)
+                        store<T, V>(p.dstate0, (long long)b * (W - 1) + t, vecs, v, d);
+                }
 #pragma unroll
                 for (int c = 0; c < V; ++c) {
-                    d[c] = fmaf(taps.w[c][0], ds[c], d[c]);
 #pragma unroll
-                    for (int j = 1; j < W; ++j) d[c] = fmaf(taps.w[c][j], old[W - 1 - j][c], d[c]);
+                    for (int i = 0; i + 1 < W - 1; ++i) {
+                        win[i][c] = win[i + 1][c];
+                        old[i][c] = old[i + 1][c];
+                    }
+                    win[W - 2][c] = x[c];
+                    old[W - 2][c] = ds[c];
                 }
-                if (t >= W - 1)
-                    store<T, V>(p.dx, row + t - (W - 1), vecs, v, d);
-                else if (p.dstate0)
-                    store<T, V>(p.dstate0, (long long)b * (W - 1) + t, vecs, v, d);
-            }
-#pragma unroll
-            for (int c = 0; c < V; ++c) {
-#pragma unroll
-                for (int i = 0; i + 1 < W - 1; ++i) {
-                    win[i][c] = win[i + 1][c];
-                    old[i][c] = old[i + 1][c];
-                }
-                win[W - 2][c] = x[c];
-                old[W - 2][c] = ds[c];
             }
         }
     }
@@ -287,46 +333,66 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(ConvArgs p, int vecs, int 
 }
 
 // ------------------------------------------------------------------------------------ one token
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(NT) conv_step_kernel(ConvArgs p, int vecs) {
-    const long long e = (long long)blockIdx.x * NT + threadIdx.x;
-    if (e >= (long long)p.B * vecs) return;
+// A thread a vector of ROWS sequences, whose weights it reads once.
+constexpr int STEP_NT = 128;
+template <typename T, int V, int W, int ROWS>
+__global__ void __launch_bounds__(STEP_NT) conv_step_kernel(ConvArgs p, int vecs) {
+    const long long e = (long long)blockIdx.x * STEP_NT + threadIdx.x;
     const int v = (int)(e % vecs);
-    const long long b = e / vecs;
-    Pack<T, V> raw[W];
+    const long long b0 = e / vecs * ROWS;
+    if (b0 >= p.B) return;
+    Pack<T, V> raw[ROWS][W];
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) raw[i] = load<T, V>(p.state0, b * (W - 1) + i, vecs, v);
-    raw[W - 1] = load<T, V>(p.x, b, vecs, v);
+    for (int r = 0; r < ROWS; ++r) {
+        if (b0 + r >= p.B) break;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) raw[r][i] = load<T, V>(p.state0, (b0 + r) * (W - 1) + i, vecs, v);
+        raw[r][W - 1] = load<T, V>(p.x, b0 + r, vecs, v);
+    }
     Taps<W, V> taps;
     taps.load(p, v * V);
-    float s[V];
 #pragma unroll
-    for (int c = 0; c < V; ++c) s[c] = taps.bias[c];
+    for (int r = 0; r < ROWS; ++r) {
+        const long long b = b0 + r;
+        if (b >= p.B) break;
+        float s[V];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        float x[V];
-        unpack(raw[i], x);
+        for (int c = 0; c < V; ++c) s[c] = taps.bias[c];
 #pragma unroll
-        for (int c = 0; c < V; ++c) s[c] = fmaf(taps.w[c][i], x[c], s[c]);
-        if (i > 0) static_cast<Pack<T, V> *>(p.state_T)[(b * (W - 1) + i - 1) * vecs + v] = raw[i];
+        for (int i = 0; i < W; ++i) {
+            float x[V];
+            unpack(raw[r][i], x);
+#pragma unroll
+            for (int c = 0; c < V; ++c) s[c] = fmaf(taps.w[c][i], x[c], s[c]);
+            if (i > 0) static_cast<Pack<T, V> *>(p.state_T)[(b * (W - 1) + i - 1) * vecs + v] = raw[r][i];
+        }
+        if (p.silu) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) s[c] *= sigmoid(s[c]);
+        }
+        store<T, V>(p.y, b, vecs, v, s);
     }
-    if (p.silu) {
-#pragma unroll
-        for (int c = 0; c < V; ++c) s[c] *= sigmoid(s[c]);
-    }
-    store<T, V>(p.y, b, vecs, v, s);
 }
 
 template <typename T, int W>
 cudaError_t fwd(const ConvArgs &a) {
     constexpr int V = Vec<T>::N;
-    const int vecs = a.D / V, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes;
-    const int tile_rows = FWD_ROWS * (NT / lanes);
-    const long long tokens = (long long)a.B * a.T, work = (tokens + tile_rows - 1) / tile_rows * cblocks;
+    const int vecs = a.D / V, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes, subs = NT / lanes;
+    // Tokens a thread: 32 (3 rows of halo in 35) where that still leaves two CTAs a SM, down to 8.
+    const long long tokens = (long long)a.B * a.T;
+    int rows = 32;
+    while (rows > BATCH && tokens * vecs < 2LL * 152 * NT * rows) rows /= 2;
+    const int row_runs = (a.T + rows - 1) / rows;
+    const long long runs = a.cu_seqlens ? (tokens + rows - 1) / rows : (long long)a.B * row_runs;
+    const long long work = (runs + subs - 1) / subs * cblocks;
     const long long copies = a.state_T ? ((long long)a.N * (W - 1) * vecs + NT - 1) / NT : 0;
     if (work + copies == 0) return cudaSuccess;
-    const size_t smem = a.cu_seqlens ? 2 * tile_rows * sizeof(int) : 0;
-    conv_fwd_kernel<T, V, W><<<(unsigned)(work + copies), NT, smem, a.stream>>>(a, vecs, lanes, cblocks, (unsigned)work);
+    if (a.cu_seqlens)
+        conv_fwd_kernel<T, V, W, true><<<(unsigned)(work + copies), NT, 2 * rows * subs * sizeof(int), a.stream>>>(
+            a, vecs, lanes, cblocks, (unsigned)work, rows, row_runs);
+    else
+        conv_fwd_kernel<T, V, W, false><<<(unsigned)(work + copies), NT, 0, a.stream>>>(a, vecs, lanes, cblocks, (unsigned)work,
+                                                                                      rows, row_runs);
     return cudaGetLastError();
 }
 template <typename T, int W>
@@ -342,7 +408,11 @@ template <typename T, int W>
 cudaError_t step(const ConvArgs &a) {
     constexpr int V = Vec<T>::N;
     const int vecs = a.D / V;
-    conv_step_kernel<T, V, W><<<(unsigned)(((long long)a.B * vecs + NT - 1) / NT), NT, 0, a.stream>>>(a, vecs);
+    auto ctas = [&](int rows) { return (unsigned)(((long long)(a.B + rows - 1) / rows * vecs + STEP_NT - 1) / STEP_NT); };
+    if (ctas(4) >= 152)
+        conv_step_kernel<T, V, W, 4><<<ctas(4), STEP_NT, 0, a.stream>>>(a, vecs);
+    else
+        conv_step_kernel<T, V, W, 1><<<ctas(1), STEP_NT, 0, a.stream>>>(a, vecs);
     return cudaGetLastError();
 }
 

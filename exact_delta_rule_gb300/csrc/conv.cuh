@@ -30,7 +30,8 @@ inline int conv_lanes(int vecs) {
     while (n < vecs && n < 32) n *= 2;
     return n;
 }
-constexpr int CONV_NT = 256, CONV_BWD_ROWS = 32;  // threads a CTA; rows a thread of the backward
+// Threads a CTA; places a run of the backward (with the W - 1 before it: five batches of 8).
+constexpr int CONV_NT = 256, CONV_BWD_ROWS = 37;
 // Runs of CONV_BWD_ROWS places of a row extended by the W - 1 of its state, and the CTAs a block of channels that
 // share them: all that there are up to four a SM.
 inline int conv_bwd_runs(int T, int W) { return (int)(((long long)T + W - 1 + CONV_BWD_ROWS - 1) / CONV_BWD_ROWS); }

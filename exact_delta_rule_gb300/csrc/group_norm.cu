@@ -40,7 +40,7 @@ __device__ __forceinline__ void affine(const GroupNormArgs &p, int c0, float (&w
 // of groups, and every parts-th 8 rows after them.
 template <typename T, int TEAM, bool BWD>
 __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks, int parts) {
-    constexpr int V = Vec<T>::N, PER = 32 / TEAM, SUBS = NT / 32;
+    constexpr int V = Vec<T>::N, PER = 32 / TEAM, SUBS = NT / 32, UNROLL = 4;
     __shared__ float red[BWD ? SUBS : 1][BWD ? 32 * V : 1];
     const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5, l = lane % TEAM;
     const int block = blockIdx.x % blocks, part = blockIdx.x / blocks;
@@ -50,46 +50,66 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
     const float inv = 1.f / (float)(p.C / p.G);
     float w[V], b[V], dw[V] = {}, db[V] = {};
     affine(p, v * V, w, b);
-    for (long long row = (long long)part * SUBS + sub; row < p.rows; row += (long long)parts * SUBS) {  // (the same for a warp)
-        float x[V];
-        Vec<T>::unpack(live ? static_cast<const uint4 *>(p.x)[row * vecs + v] : make_uint4(0, 0, 0, 0), x);
-        if (!BWD) {
-            float m = 0.f, q = 0.f;
+    const long long step = (long long)parts * SUBS;
+    for (long long row0 = (long long)part * SUBS + sub; row0 < p.rows; row0 += step * UNROLL) {  // (the same for a warp)
+        uint4 rx[UNROLL], rd[UNROLL];
+        float2 st[UNROLL];
 #pragma unroll
-            for (int e = 0; e < V; ++e) m += x[e];
-            m = row_sum<TEAM>(m) * inv;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                x[e] = live ? x[e] - m : 0.f;
-                q = fmaf(x[e], x[e], q);
+        for (int i = 0; i < UNROLL; ++i) {
+            const long long row = row0 + i * step;
+            rx[i] = rd[i] = make_uint4(0, 0, 0, 0);
+            st[i] = make_float2(0.f, 0.f);
+            if (live && row < p.rows) {
+                rx[i] = static_cast<const uint4 *>(p.x)[row * vecs + v];
+                if (BWD) {
+                    rd[i] = static_cast<const uint4 *>(p.dy)[row * vecs + v];
+                    st[i] = reinterpret_cast<const float2 *>(p.stats)[row * p.G + g];
+                }
             }
-            const float r = rsqrtf(row_sum<TEAM>(q) * inv + p.eps);
+        }
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = act(fmaf(x[e] * r, w[e], b[e]), p.silu);
-            if (live) {
-                static_cast<uint4 *>(p.y)[row * vecs + v] = Vec<T>::pack(x);
-                if (p.stats && l == 0) reinterpret_cast<float2 *>(p.stats)[row * p.G + g] = make_float2(m, r);
+        for (int i = 0; i < UNROLL; ++i) {
+            const long long row = row0 + i * step;
+            if (row >= p.rows) break;
+            float x[V];
+            Vec<T>::unpack(rx[i], x);
+            if (!BWD) {
+                float m = 0.f, q = 0.f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) m += x[e];
+                m = row_sum<TEAM>(m) * inv;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    x[e] = live ? x[e] - m : 0.f;
+                    q = fmaf(x[e], x[e], q);
+                }
+                const float r = rsqrtf(row_sum<TEAM>(q) * inv + p.eps);
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[e] = act(fmaf(x[e] * r, w[e], b[e]), p.silu);
+                if (live) {
+                    static_cast<uint4 *>(p.y)[row * vecs + v] = Vec<T>::pack(x);
+                    if (p.stats && l == 0) reinterpret_cast<float2 *>(p.stats)[row * p.G + g] = make_float2(m, r);
+                }
+            } else {
+                float d[V], s1 = 0.f, s2 = 0.f;
+                Vec<T>::unpack(rd[i], d);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float n = (x[e] - st[i].x) * st[i].y;
+                    d[e] *= dact(fmaf(n, w[e], b[e]), p.silu);
+                    dw[e] = fmaf(d[e], n, dw[e]);
+                    db[e] += d[e];
+                    d[e] *= w[e];
+                    x[e] = n;
+                    s1 += d[e];
+                    s2 = fmaf(d[e], n, s2);
+                }
+                s1 = row_sum<TEAM>(s1) * inv;
+                s2 = row_sum<TEAM>(s2) * inv;
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[e] = st[i].y * (d[e] - s1 - x[e] * s2);
+                if (live) static_cast<uint4 *>(p.dx)[row * vecs + v] = Vec<T>::pack(x);
             }
-        } else {
-            float d[V], s1 = 0.f, s2 = 0.f;
-            Vec<T>::unpack(live ? static_cast<const uint4 *>(p.dy)[row * vecs + v] : make_uint4(0, 0, 0, 0), d);
-            const float2 st = live ? reinterpret_cast<const float2 *>(p.stats)[row * p.G + g] : make_float2(0.f, 0.f);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float n = (x[e] - st.x) * st.y;
-                d[e] *= dact(fmaf(n, w[e], b[e]), p.silu);
-                dw[e] = fmaf(d[e], n, dw[e]);
-                db[e] += d[e];
-                d[e] *= w[e];
-                x[e] = n;
-                s1 += d[e];
-                s2 = fmaf(d[e], n, s2);
-            }
-            s1 = row_sum<TEAM>(s1) * inv;
-            s2 = row_sum<TEAM>(s2) * inv;
-#pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = st.y * (d[e] - s1 - x[e] * s2);
-            if (live) static_cast<uint4 *>(p.dx)[row * vecs + v] = Vec<T>::pack(x);
         }
     }
     if (BWD) {  // the CTA's sums over its rows, in order: db then dw
@@ -278,7 +298,7 @@ __global__ void __launch_bounds__(NT) gn_apply_kernel(GroupNormArgs p, int lanes
 template <typename T, bool BWD>
 cudaError_t whole(const GroupNormArgs &a) {
     const int team = gn_team(a.C / a.G / Vec<T>::N), blocks = gn_blocks(a.C, a.G, a.dtype);
-    const int parts = BWD ? gn_row_parts(a.rows, a.C, a.G, a.dtype) : (a.rows + 7) / 8;
+    const int parts = BWD ? gn_row_parts(a.rows, a.C, a.G, a.dtype) : (a.rows + 31) / 32;
     auto go = [&](auto kernel) {
         kernel<<<(unsigned)parts * blocks, NT, 0, a.stream>>>(a, blocks, parts);
         return cudaGetLastError();

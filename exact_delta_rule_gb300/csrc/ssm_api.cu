@@ -20,8 +20,8 @@ efla_status check_rows(const char *what, int B, int T, int D) {
     if (B < 0 || T < 0 || D <= 0) return api_fail(EFLA_ERR_INVALID_ARG, "bad sizes B=%d T=%d %s=%d", B, T, what, D);
     if (D % 8) return api_fail(EFLA_ERR_UNSUPPORTED, "%s=%d must be a multiple of 8", what, D);
     const long long tok = (long long)B * T;
-    if (D > (1 << 20) || tok > MOST || tok > (1LL << 40) / D || (long long)B > (1LL << 33) / D)
-        return api_fail(EFLA_ERR_UNSUPPORTED, "B=%d T=%d %s=%d: more than 2^31-1 tokens, 2^20 channels or 2^40 elements", B, T, what, D);
+    if (D > (1 << 20) || tok > MOST - 4096 || tok > (1LL << 40) / D || (long long)B > (1LL << 33) / D)
+        return api_fail(EFLA_ERR_UNSUPPORTED, "B=%d T=%d %s=%d: more than 2^31-4097 tokens, 2^20 channels or 2^40 elements", B, T, what, D);
     return EFLA_OK;
 }
 
