@@ -17,9 +17,7 @@
 
 namespace efla {
 
-constexpr int SSM_NT = 128;   // threads a CTA
 constexpr int SSM_TOK = 16;   // tokens a stage; the training forward keeps the state at the start of each
-constexpr int SSM_PER = 16;   // state entries a thread (forward)
 
 struct SsmArgs {
     const void *x, *dt, *z;              // [B, T, D]; z may be nullptr
@@ -51,25 +49,32 @@ struct SsmBwdArgs {
     float *sums2;            // [slots][2 D]: of dD and ddt_bias
 };
 
-// Channels a CTA.  Tiles do not cross a group.
-inline int ssm_channels(int N) { return SSM_NT * SSM_PER / N; }
-inline int ssm_tiles(int D, int N, int G) {
-    const int each = D / G, c = ssm_channels(N);
-    return G * ((each + c - 1) / c);
-}
-// Tokens a segment (0: rows stay whole) for `rows` rows of T tokens.
-int ssm_segment(long long rows, int T, int tiles);
+// Threads a CTA and its channels, 16 entries of the state a thread.  Tiles do not cross a group, and a tile's row of a
+// token is 16 bytes or more.
+constexpr int ssm_fwd_threads(int N) { return N == 128 ? 64 : 32; }
+constexpr int ssm_fwd_channels(int N) { return ssm_fwd_threads(N) * 16 / N; }
+constexpr int SSM_BWD_NT = 128;
+constexpr int ssm_bwd_channels(int N) { return SSM_BWD_NT * 16 / N; }
+inline int ssm_tiles(int D, int G, int channels) { return G * ((D / G + channels - 1) / channels); }
+inline int ssm_fwd_tiles(int D, int N, int G) { return ssm_tiles(D, G, ssm_fwd_channels(N)); }
+inline int ssm_bwd_tiles(int D, int N, int G) { return ssm_tiles(D, G, ssm_bwd_channels(N)); }
+// Tokens a segment (0: rows stay whole) for `rows` rows of T tokens, D channels and N entries: of the forward (uneven:
+// T is the mean of sequences of unknown lengths), and of the backward.
+int ssm_segment(long long rows, int T, int D, int N, bool uneven);
+int ssm_bwd_segment(long long rows, int T, int D, int N, int tiles);
 
 // Workspace of the training pair, in bytes from its base (16-byte aligned regions).
 struct SsmWs {
-    int seg, slots;
+    int seg, slots, bwd_seg, bwd_slots;
     size_t keep, part, sums, sums2, state, sum, bytes;
 };
 inline SsmWs ssm_ws(int B, int T, int D, int N, int G) {
     SsmWs w{};
-    const int tiles = ssm_tiles(D, N, G);
-    w.seg = ssm_segment(B, T, tiles);
+    const int tiles = ssm_bwd_tiles(D, N, G);
+    w.seg = ssm_segment(B, T, D, N, false);
     w.slots = B * (w.seg ? (T + w.seg - 1) / w.seg : 1);
+    w.bwd_seg = ssm_bwd_segment(B, T, D, N, tiles);
+    w.bwd_slots = B * (w.bwd_seg ? (T + w.bwd_seg - 1) / w.bwd_seg : 1);
     size_t at = 0;
     auto take = [&](size_t floats) {
         const size_t r = at;
@@ -77,12 +82,13 @@ inline SsmWs ssm_ws(int B, int T, int D, int N, int G) {
         return r;
     };
     const size_t tok = (size_t)B * T, dn = (size_t)D * N;
+    const size_t cut = std::max(w.seg ? w.slots : 0, w.bwd_seg ? w.bwd_slots : 0);  // (the forward is done with its own)
     w.keep = take((size_t)B * ((T + SSM_TOK - 1) / SSM_TOK) * dn);
     w.part = take(tok * tiles * 2 * N);
-    w.sums = take(w.slots * dn);
-    w.sums2 = take((size_t)w.slots * 2 * D);
-    w.state = take(w.seg ? w.slots * dn : 0);
-    w.sum = take(w.seg ? (size_t)w.slots * D : 0);
+    w.sums = take(w.bwd_slots * dn);
+    w.sums2 = take((size_t)w.bwd_slots * 2 * D);
+    w.state = take(cut * dn);
+    w.sum = take(cut * D);
     w.bytes = at;
     return w;
 }
@@ -95,6 +101,12 @@ cudaError_t launch_ssm_step(const SsmArgs &a);  // x, dt, z, y [B, D], Bm, Cm [B
 __device__ __forceinline__ float ssm_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The same, kept where it is written among other such.
+__device__ __forceinline__ float ssm_ex2_here(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 constexpr float LOG2E = 1.44269504f;
@@ -116,7 +128,26 @@ __device__ __forceinline__ float softplus(float t) {
     p = fmaf(p, u, 1.f);
     return fmaf(p, u, fmaxf(t, 0.f));
 }
-__device__ __forceinline__ float ssm_sigmoid(float x) { return __fdividef(1.f, 1.f + ssm_ex2(-x * LOG2E)); }
+__device__ __forceinline__ float ssm_sigmoid(float x) {
+    float y;  // (1 / infinity is 0)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ssm_ex2(-x * LOG2E)));
+    return y;
+}
+// The same for two, packed.
+__device__ __forceinline__ float2 softplus2(float2 t) {
+    auto two = [](float c) { return make_float2(c, c); };
+    const float2 a = __fmul2_rn(make_float2(-fabsf(t.x), -fabsf(t.y)), two(LOG2E)), u = make_float2(ssm_ex2(a.x), ssm_ex2(a.y));
+    float2 p = __ffma2_rn(two(-0.0032439809292554855f), u, two(0.019851263612508774f));
+    p = __ffma2_rn(p, u, two(-0.056959159672260284f));
+    p = __ffma2_rn(p, u, two(0.10603617131710052f));
+    p = __ffma2_rn(p, u, two(-0.15305569767951965f));
+    p = __ffma2_rn(p, u, two(0.19675931334495544f));
+    p = __ffma2_rn(p, u, two(-0.24954132735729218f));
+    p = __ffma2_rn(p, u, two(0.3332996368408203f));
+    p = __ffma2_rn(p, u, two(-0.4999990165233612f));
+    p = __ffma2_rn(p, u, two(1.f));
+    return __ffma2_rn(p, u, make_float2(fmaxf(t.x, 0.f), fmaxf(t.y, 0.f)));
+}
 // A in units of log2: e^{A delta} = 2^{rate delta}.
 __device__ __forceinline__ float ssm_rate(float a_log) { return -expf(a_log) * LOG2E; }
 
@@ -130,15 +161,25 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Tokens [t0, t0 + SSM_TOK) of src, the first `have` of CHUNKS 16-byte pieces each, to dst; zeros for the others and
-// from token hi on.
-template <int CHUNKS>
+// from token hi on.  By NT threads.  (Whole tiles, nearly all, without a test and a 64-bit product a piece.)
+template <int CHUNKS, int NT>
 __device__ __forceinline__ void load_tile(uint8_t *dst, const uint8_t *src, size_t pitch, long long t0, long long hi, int have) {
+    constexpr int PASSES = (SSM_TOK * CHUNKS + NT - 1) / NT;
+    static_assert(NT % CHUNKS == 0, "a pass takes whole tokens");
+    const int t = threadIdx.x / CHUNKS, c = threadIdx.x % CHUNKS;
+    src += (size_t)t0 * pitch;
+    if (SSM_TOK * CHUNKS % NT == 0 && t0 + SSM_TOK <= hi && have == CHUNKS) {
+        const uint32_t off = t * (uint32_t)pitch + 16 * c;
 #pragma unroll
-    for (int k = 0; k < (SSM_TOK * CHUNKS + SSM_NT - 1) / SSM_NT; ++k) {
-        const int i = k * SSM_NT + threadIdx.x, t = i / CHUNKS, c = i % CHUNKS;
-        if (SSM_TOK * CHUNKS % SSM_NT && i >= SSM_TOK * CHUNKS) break;
-        const bool live = t0 + t < hi && c < have;
-        cp_async16(dst + 16 * i, live ? src + (size_t)(t0 + t) * pitch + 16 * c : src, live);
+        for (int k = 0; k < PASSES; ++k) cp_async16(dst + 16 * (k * NT + threadIdx.x), src + k * (NT / CHUNKS) * pitch + off, true);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+        const int tk = t + k * (NT / CHUNKS);
+        if (tk >= SSM_TOK) break;
+        const bool live = t0 + tk < hi && c < have;
+        cp_async16(dst + 16 * (k * NT + threadIdx.x), live ? src + (size_t)tk * pitch + 16 * c : src, live);
     }
 }
 
@@ -166,9 +207,10 @@ __device__ __forceinline__ int ssm_segments(const SsmArgs &p, int n, long long &
 
 // Segment `slot` of packed sequences, all segments of a sequence after those of the ones before it.  By all threads
 // of a CTA; false if there is none.  A malformed sequence has none and is reported by the CTA that `reports`.
+template <int NT>
 __device__ __forceinline__ bool ssm_packed_span(const SsmArgs &p, int slot, bool reports, SsmSpan &out) {
     __shared__ long long box[4];
-    __shared__ int sums[SSM_NT / 32];
+    __shared__ int sums[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long lo, hi;
     if (!p.seg) {
@@ -183,7 +225,7 @@ __device__ __forceinline__ bool ssm_packed_span(const SsmArgs &p, int slot, bool
     if (tid == 0) box[0] = -1;
     __syncthreads();
     long long before = 0;
-    for (int base = 0; base < p.nseq && (before <= slot || reports); base += SSM_NT) {
+    for (int base = 0; base < p.nseq && (before <= slot || reports); base += NT) {
         const int n = base + tid;
         int segs = n < p.nseq ? ssm_segments(p, n, lo, hi) : 0;
         if (segs < 0) {
@@ -207,7 +249,7 @@ __device__ __forceinline__ bool ssm_packed_span(const SsmArgs &p, int slot, bool
             box[2] = s + 1 < segs ? box[1] + p.seg : hi;
             box[3] = (s == 0 ? 1 : 0) | (s + 1 == segs ? 2 : 0);
         }
-        for (int w = 0; w < SSM_NT / 32; ++w) before += sums[w];
+        for (int w = 0; w < NT / 32; ++w) before += sums[w];
         __syncthreads();
     }
     if (box[0] < 0) return false;

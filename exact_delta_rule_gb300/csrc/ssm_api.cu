@@ -53,7 +53,7 @@ efla_status check_ssm(int B, int T, int D, int N, int G, efla_dtype dtype) {
     if (!dtype_ok(dtype)) return api_fail(EFLA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
     const int vec = 16 / (int)es(dtype);  // (a channel tile begins on 16 bytes)
     if (D / G % vec) return api_fail(EFLA_ERR_UNSUPPORTED, "D=%d: a group's %d channels must be a multiple of %d", D, D / G, vec);
-    if (((long long)B + 1) * ssm_tiles(D, N, G) > MOST / 4 || (long long)B * T > (1LL << 40) / ((long long)G * N))
+    if (((long long)B + 1) * ssm_fwd_tiles(D, N, G) > MOST / 4 || (long long)B * T > (1LL << 40) / ((long long)G * N))
         return api_fail(EFLA_ERR_UNSUPPORTED, "B=%d T=%d D=%d G=%d: too many rows of channels", B, T, D, G);
     return EFLA_OK;
 }
@@ -71,9 +71,8 @@ efla_status check_group_norm(int rows, int L, int C, int groups, efla_dtype dtyp
 }
 
 // Segments of a scan without training: their length (0: uncut) and number for N sequences of T / N tokens on average.
-void scan_segments(int T, int D, int d_state, int G, int N, bool packed, int &seg, int &slots) {
-    const int tiles = ssm_tiles(D, d_state, G);
-    seg = ssm_segment(N, packed && N > 0 ? (int)(((long long)T + N - 1) / N) : T, tiles);
+void scan_segments(int T, int D, int d_state, int N, bool packed, int &seg, int &slots) {
+    seg = ssm_segment(N, packed && N > 0 ? (int)(((long long)T + N - 1) / N) : T, D, d_state, packed && N > 1);
     slots = !seg ? N : packed ? T / seg + N : N * ((T + seg - 1) / seg);
 }
 size_t scan_bytes(int D, int d_state, int seg, int slots) { return seg ? (size_t)slots * D * (d_state + 1) * sizeof(float) : 0; }
@@ -155,7 +154,7 @@ efla_status efla_ssm_scan_workspace(int B, int T, int D, int d_state, int G, int
     if (N < 0 || (long long)N > (1LL << 33) / D || (packed ? B != 1 : N != B))
         return api_fail(EFLA_ERR_INVALID_ARG, "bad number of sequences N=%d", N);
     int seg, slots;
-    scan_segments(T, D, d_state, G, N, packed != 0, seg, slots);
+    scan_segments(T, D, d_state, N, packed != 0, seg, slots);
     *bytes = scan_bytes(D, d_state, seg, slots);
     return api_ok();
 }
@@ -167,9 +166,9 @@ efla_status efla_ssm_scan(const void *x, const void *dt, const float *A_log, con
     efla_status s = check_ssm(B, T, D, d_state, G, dtype);
     if (s != EFLA_OK) return s;
     if ((s = check_sequences(cu_seqlens, B, N, D)) != EFLA_OK) return s;
-    if ((long long)N * ssm_tiles(D, d_state, G) > MOST) return api_fail(EFLA_ERR_UNSUPPORTED, "N=%d D=%d: too many sequences of channels", N, D);
+    if ((long long)N * ssm_fwd_tiles(D, d_state, G) > MOST) return api_fail(EFLA_ERR_UNSUPPORTED, "N=%d D=%d: too many sequences of channels", N, D);
     int seg, slots;
-    scan_segments(T, D, d_state, G, N, cu_seqlens != nullptr, seg, slots);
+    scan_segments(T, D, d_state, N, cu_seqlens != nullptr, seg, slots);
     const size_t need = scan_bytes(D, d_state, seg, slots);
     if ((s = need_workspace(workspace, workspace_bytes, need)) != EFLA_OK) return s;
     const size_t tok = (size_t)B * T, xb = tok * D * es(dtype), bb = tok * G * d_state * es(dtype), st = (size_t)N * D * d_state * 4;
@@ -258,6 +257,7 @@ efla_status efla_ssm_scan_bwd(const void *x, const void *dt, const float *A_log,
         const cudaError_t e = launch_ssm_scan(a.f);
         if (e != cudaSuccess) return launched(e, "scan kernel launch");
     }
+    a.f.seg = w.bwd_seg, a.f.slots = w.bwd_slots;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.dy = dy, a.dS_T = dS_T, a.dx = dx, a.ddt = ddt, a.dz = dz, a.dB = dB, a.dC = dC;
     a.dA_log = dA_log, a.dD = dD, a.ddt_bias = ddt_bias, a.dS0 = dS0;

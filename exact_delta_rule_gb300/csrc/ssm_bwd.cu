@@ -20,7 +20,7 @@
 namespace efla {
 namespace {
 
-constexpr int NT = SSM_NT, TOK = SSM_TOK, WARPS = NT / 32;
+constexpr int NT = SSM_BWD_NT, TOK = SSM_TOK, WARPS = NT / 32;
 constexpr float LN2 = 0.693147181f;
 
 template <typename T, int LN>
@@ -82,6 +82,12 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
     float4 *kept = reinterpret_cast<float4 *>(smem + K::KEPT) + tid;
     float *red = reinterpret_cast<float *>(smem + K::RED);
 
+    // which of a token's sums reduce4 leaves in this lane: LEFT entries of dB and dC from bc_at, one channel's at ch_at
+    constexpr int LEFT = CG >= 4 ? 1 : 4 / CG;
+    const bool bc_writes = CG < 8 || (cg & 1) == 0, ch_writes = nq % (LN / 4) == 0;
+    const int bc_at = 4 * nq + (CG >= 4 ? reduced_index<CG < 4 ? 4 : CG, LN>(lane) : CG == 2 ? 2 * cg : 0);
+    const int ch_at = ch + reduced_index<LN, 1>(lane);
+
     // entry (pair q of channels, i): channels c0 + ch + 2 q, + 1, entry 4 nq + i
     float2 rate[2][4], l[2][4], dA[2][4];
     auto entry = [&](const float *base, int c, int i) { return base[(size_t)(c0 + ch + c) * N + 4 * nq + i]; };
@@ -94,8 +100,9 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
             l[q][i] = live && l0 ? make_float2(entry(l0, 2 * q, i), entry(l0, 2 * q + 1, i)) : make_float2(0.f, 0.f);
             dA[q][i] = make_float2(0.f, 0.f);
         }
-    // elementwise work: channel ec of the tile, tokens et, et + NT / CT, ..
-    const int ec = tid % CT, et = tid / CT, ed = c0 + ec;
+    // elementwise work, a warp on its own channels: channel ec of the tile, tokens et, et + 32 / CW, ..
+    constexpr int CW = CT / WARPS;
+    const int ec = warp * CW + lane % CW, et = lane / CW, ed = c0 + ec;
     const bool elive = ec < have;
     const float bias = elive && f.dt_bias ? f.dt_bias[ed] : 0.f, skip = elive && f.Dskip ? f.Dskip[ed] : 0.f;
     float sum_D = 0.f, sum_dt = 0.f;
@@ -109,18 +116,29 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
         if (s >= 0) {
             const long long t0 = span.lo + (long long)s * TOK;
             uint8_t *st = smem + (s & 1) * K::STAGE;
-            load_tile<K::ROW / 16>(st + K::X, xg, pitch, t0, span.hi, pieces);
-            load_tile<K::ROW / 16>(st + K::DT, dg, pitch, t0, span.hi, pieces);
-            if (zg) load_tile<K::ROW / 16>(st + K::Z, zg, pitch, t0, span.hi, pieces);
-            load_tile<K::ROW / 16>(st + K::DY, yg, pitch, t0, span.hi, pieces);
-            load_tile<K::BROW / 16>(st + K::B, bg, bpitch, t0, span.hi, K::BROW / 16);
-            load_tile<K::BROW / 16>(st + K::C, cgm, bpitch, t0, span.hi, K::BROW / 16);
+            load_tile<K::ROW / 16, NT>(st + K::X, xg, pitch, t0, span.hi, pieces);
+            load_tile<K::ROW / 16, NT>(st + K::DT, dg, pitch, t0, span.hi, pieces);
+            if (zg) load_tile<K::ROW / 16, NT>(st + K::Z, zg, pitch, t0, span.hi, pieces);
+            load_tile<K::ROW / 16, NT>(st + K::DY, yg, pitch, t0, span.hi, pieces);
+            load_tile<K::BROW / 16, NT>(st + K::B, bg, bpitch, t0, span.hi, K::BROW / 16);
+            load_tile<K::BROW / 16, NT>(st + K::C, cgm, bpitch, t0, span.hi, K::BROW / 16);
         }
         cp_async_commit();
     };
 
     const int chunks = (int)((span.hi - span.lo + TOK - 1) / TOK), nk = (f.T + TOK - 1) / TOK;
     const long long row0 = (long long)span.seq * f.T;
+    // dB and dC of the tile over the chunk that begins at t0, a token's 2 N values side by side
+    auto sum_warps = [&](long long t0) {
+        const int n = (int)min((long long)TOK, span.hi - t0) * 2 * N;
+        float *part = p.part + ((size_t)tile * f.B * f.T + t0) * 2 * N;
+        for (int i = tid; i < n; i += NT) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) v += red[w * TOK * 2 * N + i];
+            part[i] = v;
+        }
+    };
     load(chunks - 1);
     for (int s = chunks - 1; s >= 0; --s) {
         const uint8_t *st = smem + (s & 1) * K::STAGE;
@@ -136,9 +154,10 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
         cp_async_wait<0>();
         __syncthreads();  // the chunk's inputs are here, the one before is done with
         load(s - 1);
+        if (s + 1 < chunks) sum_warps(t0 + TOK);
         auto in = [&](int what, int t) { return to_f32(reinterpret_cast<const T *>(st + what)[t * CT + ec]); };
 #pragma unroll 4
-        for (int t = et; t < TOK; t += NT / CT) {  // past the row's end: a token that changes nothing
+        for (int t = et; t < TOK; t += 32 / CW) {  // past the row's end: a token that changes nothing
             const bool real = t < count;
             const float delta = real ? softplus(in(K::DT, t) + bias) : 0.f;
             float g = real ? in(K::DY, t) : 0.f;
@@ -196,6 +215,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
 #pragma unroll 1
         for (int k = 3; k >= 0; --k) {
             float2 a[4][2][4], hp[4][2][4];
+            float rB[4][LEFT], rC[4][LEFT], rU[4], rD[4], rY[4];  // a token's sums, as reduce4 leaves them
             if (k > 0) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -234,19 +254,20 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
                     dC[i] = acc.x + acc.y;
                 }
                 reduce4<CG, LN>(dC, lane);
-                float *to = red + (warp * TOK + t) * 2 * N + N + 4 * nq;
-                if (CG >= 4) {
-                    if (CG == 4 || (cg & 1) == 0) to[reduced_index<CG < 4 ? 4 : CG, LN>(lane)] = dC[0];
-                } else if (CG == 2) {
-                    to[2 * cg] = dC[0];
-                    to[2 * cg + 1] = dC[1];
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) to[i] = dC[i];
-                }
+                for (int i = 0; i < LEFT; ++i) rC[j][i] = dC[i];
                 float ys[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
                 reduce4<LN, 1>(ys, lane);
-                if (nq % (LN / 4) == 0) y_s[t * CT + ch + reduced_index<LN, 1>(lane)] = ys[0];
+                rY[j] = ys[0];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // (stored at the end: a store between would hold up the next token's loads)
+                const int t = 4 * k + j;
+                if (bc_writes) {
+#pragma unroll
+                    for (int i = 0; i < LEFT; ++i) red[(warp * TOK + t) * 2 * N + N + bc_at + i] = rC[j][i];
+                }
+                if (ch_writes) y_s[t * CT + ch_at] = rY[j];
             }
 #pragma unroll
             for (int j = 3; j >= 0; --j) {
@@ -275,39 +296,32 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
                     dB[i] = acc.x + acc.y;
                 }
                 reduce4<CG, LN>(dB, lane);
-                float *to = red + (warp * TOK + t) * 2 * N + 4 * nq;
-                if (CG >= 4) {
-                    if (CG == 4 || (cg & 1) == 0) to[reduced_index<CG < 4 ? 4 : CG, LN>(lane)] = dB[0];
-                } else if (CG == 2) {
-                    to[2 * cg] = dB[0];
-                    to[2 * cg + 1] = dB[1];
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) to[i] = dB[i];
-                }
+                for (int i = 0; i < LEFT; ++i) rB[j][i] = dB[i];
                 float v0[4] = {du[0].x, du[0].y, du[1].x, du[1].y}, v1[4] = {dd[0].x, dd[0].y, dd[1].x, dd[1].y};
                 reduce4<LN, 1>(v0, lane);
                 reduce4<LN, 1>(v1, lane);
-                __syncwarp();  // every lane has read this token's u and g
-                if (nq % (LN / 4) == 0) {
-                    const int e = t * CT + ch + reduced_index<LN, 1>(lane);
-                    u_s[e] = v0[0];
-                    g_s[e] = v1[0];
+                rU[j] = v0[0];
+                rD[j] = v1[0];
+            }
+            __syncwarp();  // every lane has read u and g of these tokens
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = 4 * k + j;
+                if (bc_writes) {
+#pragma unroll
+                    for (int i = 0; i < LEFT; ++i) red[(warp * TOK + t) * 2 * N + bc_at + i] = rB[j][i];
+                }
+                if (ch_writes) {
+                    u_s[t * CT + ch_at] = rU[j];
+                    g_s[t * CT + ch_at] = rD[j];
                 }
             }
         }
-        __syncthreads();
-        // dB and dC of the tile, a token's 2 N values side by side
-        float *part = p.part + ((size_t)tile * f.B * f.T + t0) * 2 * N;
-        for (int i = tid; i < count * 2 * N; i += NT) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) v += red[w * TOK * 2 * N + i];
-            part[i] = v;
-        }
+        __syncwarp();
         if (elive) {
 #pragma unroll 4
-            for (int t = et; t < count; t += NT / CT) {
+            for (int t = et; t < count; t += 32 / CW) {
                 const float x = in(K::X, t), dt = in(K::DT, t) + bias, delta = delta_s[t * CT + ec];
                 const float du = u_s[t * CT + ec], dd = fmaf(du, x, LN2 * g_s[t * CT + ec]);
                 float g = in(K::DY, t);
@@ -342,18 +356,15 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
             }
     }
     __syncthreads();
-    red[tid] = sum_D;
-    red[NT + tid] = sum_dt;
-    __syncthreads();
-    if (tid < have) {
-        float a = 0.f, b = 0.f;
+    if (chunks > 0) sum_warps(span.lo);
 #pragma unroll
-        for (int k = 0; k < NT / CT; ++k) {
-            a += red[k * CT + tid];
-            b += red[NT + k * CT + tid];
-        }
-        p.sums2[(size_t)slot * 2 * f.D + c0 + tid] = a;
-        p.sums2[(size_t)slot * 2 * f.D + f.D + c0 + tid] = b;
+    for (int m = CW; m < 32; m <<= 1) {
+        sum_D += __shfl_xor_sync(0xffffffffu, sum_D, m);
+        sum_dt += __shfl_xor_sync(0xffffffffu, sum_dt, m);
+    }
+    if (elive && et == 0) {
+        p.sums2[(size_t)slot * 2 * f.D + ed] = sum_D;
+        p.sums2[(size_t)slot * 2 * f.D + f.D + ed] = sum_dt;
     }
 }
 
@@ -361,14 +372,14 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
 // as in the forward: 16 entries of a channel.
 template <typename T, int NSUB>
 struct Carry {
-    static constexpr int N = NSUB * SSM_PER, CT = NT / NSUB, ROW = CT * sizeof(T), BROW = N * sizeof(T);
+    static constexpr int N = NSUB * 16, CT = NT / NSUB, ROW = CT * sizeof(T), BROW = N * sizeof(T);
     static constexpr int DT = 0, Z = TOK * ROW, DY = 2 * TOK * ROW, C = 3 * TOK * ROW, STAGE = C + TOK * BROW;
     static constexpr int SMEM = 2 * STAGE + TOK * N * 4;
 };
 template <typename T, int NSUB>
 __global__ void __launch_bounds__(NT) ssm_bwd_carry_kernel(SsmBwdArgs p, int tiles) {
     using K = Carry<T, NSUB>;
-    constexpr int N = K::N, CT = K::CT, PER = SSM_PER;
+    constexpr int N = K::N, CT = K::CT, PER = 16;
     extern __shared__ __align__(16) uint8_t smem[];
     const SsmArgs &f = p.f;
     float *cvt = reinterpret_cast<float *>(smem + 2 * K::STAGE);
@@ -396,10 +407,10 @@ __global__ void __launch_bounds__(NT) ssm_bwd_carry_kernel(SsmBwdArgs p, int til
         if (s >= 0) {
             const long long t0 = span.lo + (long long)s * TOK;
             uint8_t *st = smem + (s & 1) * K::STAGE;
-            load_tile<K::ROW / 16>(st + K::DT, dg, pitch, t0, span.hi, pieces);
-            if (zg) load_tile<K::ROW / 16>(st + K::Z, zg, pitch, t0, span.hi, pieces);
-            load_tile<K::ROW / 16>(st + K::DY, yg, pitch, t0, span.hi, pieces);
-            load_tile<K::BROW / 16>(st + K::C, cg, bpitch, t0, span.hi, K::BROW / 16);
+            load_tile<K::ROW / 16, NT>(st + K::DT, dg, pitch, t0, span.hi, pieces);
+            if (zg) load_tile<K::ROW / 16, NT>(st + K::Z, zg, pitch, t0, span.hi, pieces);
+            load_tile<K::ROW / 16, NT>(st + K::DY, yg, pitch, t0, span.hi, pieces);
+            load_tile<K::BROW / 16, NT>(st + K::C, cg, bpitch, t0, span.hi, K::BROW / 16);
         }
         cp_async_commit();
     };
@@ -454,11 +465,23 @@ __global__ void __launch_bounds__(NT) ssm_bwd_combine_kernel(SsmBwdArgs p) {
     float l = p.dS_T ? p.dS_T[row * size + e] : 0.f;
     float *state = f.state + (size_t)row * segs * size + e;
     const float *sum = f.sum + (size_t)row * segs * f.D + e / f.N;
-#pragma unroll 8
-    for (int s = segs - 1; s >= 0; --s) {
-        const float local = state[s * size];
-        state[s * size] = l;
-        l = fmaf(ssm_ex2(rate * sum[(size_t)s * f.D]), l, local);
+    constexpr int BATCH = 8;  // (all loaded before the first is written back)
+    for (int s0 = segs - 1; s0 >= 0; s0 -= BATCH) {
+        float local[BATCH], decay[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            local[i] = decay[i] = 0.f;
+            if (s0 - i >= 0) {
+                local[i] = state[(s0 - i) * size];
+                decay[i] = ssm_ex2(rate * sum[(size_t)(s0 - i) * f.D]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            if (s0 - i >= 0) {
+                state[(s0 - i) * size] = l;
+                l = fmaf(decay[i], l, local[i]);
+            }
     }
 }
 
@@ -490,7 +513,7 @@ cudaError_t backward(const SsmBwdArgs &a) {
     using KB = Back<T, 4 * NSUB>;
     using KC = Carry<T, NSUB>;
     const SsmArgs &f = a.f;
-    const int tiles = ssm_tiles(f.D, f.N, f.G), slots = f.slots;
+    const int tiles = ssm_bwd_tiles(f.D, f.N, f.G), slots = f.slots;
     const long long tokens = (long long)f.B * f.T;
     cudaError_t e = allow_smem(ssm_bwd_kernel<T, 4 * NSUB>, KB::SMEM);
     if (e != cudaSuccess) return e;
@@ -514,25 +537,12 @@ cudaError_t backward(const SsmBwdArgs &a) {
     return launch_sum_parts(a.sums, slots, f.D * f.N, a.dA_log, nullptr, f.D * f.N, f.stream);
 }
 
-// out[i] = the sum over the slots of sums2's dD (off = 0) or ddt_bias (off = D).
-__global__ void __launch_bounds__(256) ssm_channel_sums_kernel(const float *sums2, int slots, int D, float *dD, float *ddt_bias) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= 2 * D) return;
-    float *out = i < D ? dD : ddt_bias;
-    if (!out) return;
-    float v = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < slots; ++s) v += sums2[(size_t)s * 2 * D + i];
-    out[i < D ? i : i - D] = v;
-}
-
 template <typename T>
 cudaError_t states(const SsmBwdArgs &a) {
     const int N = a.f.N;
     const cudaError_t e = N == 16 ? backward<T, 1>(a) : N == 32 ? backward<T, 2>(a) : N == 64 ? backward<T, 4>(a) : backward<T, 8>(a);
     if (e != cudaSuccess || (!a.dD && !a.ddt_bias)) return e;
-    ssm_channel_sums_kernel<<<(2 * a.f.D + 255) / 256, 256, 0, a.f.stream>>>(a.sums2, a.f.slots, a.f.D, a.dD, a.ddt_bias);
-    return cudaGetLastError();
+    return launch_sum_parts(a.sums2, a.f.slots, 2 * a.f.D, a.dD, a.ddt_bias, a.f.D, a.f.stream);
 }
 
 }  // namespace

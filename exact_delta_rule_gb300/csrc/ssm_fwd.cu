@@ -1,68 +1,104 @@
 // Selective state space scan, forward (ssm.cuh has the formulas).
 //
-// The work is N exponentials and 3 N multiply-adds a token and channel, on inputs and outputs of a few bytes: bound
-// by the exponential unit (32 a clock and SM) and the fp32 pipe (128), not by HBM.  So a thread keeps 16 entries of
-// one channel's state in registers over all tokens of its segment (N / 16 lanes a channel, their shares of C . h
-// added by shuffles) and computes delta itself; only B and C, which all channels share, go through shared memory as
-// fp32.  Multiply-adds run packed in pairs, which leaves the issue slots to the exponentials.  Inputs come in
-// stages of 16 tokens by asynchronous copies two stages ahead; B and C of the next stage are converted while this
-// one is computed, so a stage costs one barrier.
+// The work is N exponentials and 3 N multiply-adds a token and channel, on inputs and outputs of a few bytes.  A warp's
+// token of 32 x 16 entries takes 20 clocks of the exponential unit, 22 of the fp32 pipe, 24 of issue and 22 of the
+// shared-memory and shuffle pipe: no one of them leads by much, and HBM is far from its bound.  A thread keeps 2
+// channels x 8 entries of the state in registers over all tokens of its segment, so that B and C, which all channels
+// share, are read from shared memory (as fp32, 4 clocks each 16 bytes a lane, broadcast or not) once for both channels;
+// multiply-adds run packed in pairs of entries.  Tokens go in groups of four, in straight code.  Their softplus
+// and gate are shared out among the N / 8 lanes of a pair of channels: the lane that computes a token's delta also gets
+// its sum of C . h and writes its output; a lane keeps its own channel first, so that two lanes swap what belongs to
+// the other without selecting.  A CTA is one warp (two for N = 128): 8 x 2048 tokens of 4096 channels are 1024 warps, 6.7
+// a SM.
+// Measured there (N = 16): 1 channel x 16 entries a thread 406 us, 1 x 8 449 us, 2 x 8 409 us.
+// Inputs come in stages of 16 tokens by asynchronous copies two stages ahead; B and C of the next stage are converted
+// while this one is computed, so a stage costs one barrier.
 #include "ssm.cuh"
 
 namespace efla {
 namespace {
 
-constexpr int NT = SSM_NT, TOK = SSM_TOK, PER = SSM_PER, STAGES = 3;
+constexpr int TOK = SSM_TOK, PER = 8, STAGES = 3;
 
 // CARRY: end state and sum of delta of a segment from h = 0, no outputs.
-template <typename T, int NSUB, bool CARRY>
+template <typename T, int N_, bool CARRY>
 struct Scan {
-    static constexpr int N = NSUB * PER, CT = NT / NSUB;
+    static constexpr int N = N_, NT = ssm_fwd_threads(N), CT = ssm_fwd_channels(N), SUB = N / PER;
+    static constexpr int TL = SUB / 2 < 4 ? SUB / 2 : 4, LOC = 4 / TL;  // lanes that share four tokens; tokens a lane
     static constexpr int ROW = CT * sizeof(T), BROW = N * sizeof(T);        // bytes a token
     static constexpr int X = 0, DT = TOK * ROW, Z = 2 * TOK * ROW, B = 3 * TOK * ROW, C = B + TOK * BROW;
     static constexpr int STAGE = C + TOK * BROW, CVT = 2 * TOK * N * 4;      // bytes a stage; of B and C as fp32
     static constexpr int SMEM = STAGES * STAGE + 2 * CVT;
 };
 
-// Where entry n of token t's B or C lies: the lanes of a channel read 16 bytes each side by side.
-template <int NSUB>
-__device__ __forceinline__ int cvt_at(int n) { return ((n % PER / 4) * NSUB + n / PER) * 4 + n % 4; }
+__device__ __forceinline__ void unpack8(const __nv_bfloat16 *src, float4 &a, float4 &b) {
+    const uint4 r = *reinterpret_cast<const uint4 *>(src);
+    a = make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+    b = make_float4(__uint_as_float(r.z << 16), __uint_as_float(r.z & 0xffff0000u), __uint_as_float(r.w << 16), __uint_as_float(r.w & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack8(const float *src, float4 &a, float4 &b) {
+    a = reinterpret_cast<const float4 *>(src)[0];
+    b = reinterpret_cast<const float4 *>(src)[1];
+}
 
-template <typename T, int NSUB, bool CARRY>
-__global__ void __launch_bounds__(NT) ssm_fwd_kernel(SsmArgs p, int tiles) {
-    using K = Scan<T, NSUB, CARRY>;
-    constexpr int N = K::N, CT = K::CT;
+// Sums of y[0..3] over the SUB / 2 lanes that differ in the bits above the lowest: token k's ends in the lanes of
+// (sub / 2) % TL = k % TL, at out[k / TL].
+template <int SUB, int LOC>
+__device__ __forceinline__ void owner_sums(const float (&y)[4], int sub, float (&out)[LOC]) {
+    if constexpr (SUB == 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k] = y[k];
+    } else if constexpr (SUB == 4) {
+        const bool up = sub & 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            out[i] = (up ? y[2 * i + 1] : y[2 * i]) + __shfl_xor_sync(0xffffffffu, up ? y[2 * i] : y[2 * i + 1], 2);
+    } else {
+        const bool b1 = sub & 4, b0 = sub & 2;
+        const float v0 = (b1 ? y[2] : y[0]) + __shfl_xor_sync(0xffffffffu, b1 ? y[0] : y[2], 4);
+        const float v1 = (b1 ? y[3] : y[1]) + __shfl_xor_sync(0xffffffffu, b1 ? y[1] : y[3], 4);
+        out[0] = (b0 ? v1 : v0) + __shfl_xor_sync(0xffffffffu, b0 ? v0 : v1, 2);
+        #pragma unroll
+        for (int off = 8; off < SUB; off <<= 1) out[0] += __shfl_xor_sync(0xffffffffu, out[0], off);
+    }
+}
+
+template <typename T, int N, bool CARRY>
+__global__ void __launch_bounds__(ssm_fwd_threads(N)) ssm_fwd_kernel(SsmArgs p, int tiles) {
+    using K = Scan<T, N, CARRY>;
+    constexpr int NT = K::NT, CT = K::CT, SUB = K::SUB, TL = K::TL, LOC = K::LOC;
     extern __shared__ __align__(16) uint8_t smem[];
     float *cvt = reinterpret_cast<float *>(smem + STAGES * K::STAGE);  // [2][B, C][TOK][N]
     const int tid = threadIdx.x, tile = blockIdx.x % tiles, slot = blockIdx.x / tiles;
     SsmSpan span;
     if (p.cu_seqlens) {
-        if (!ssm_packed_span(p, slot, tile == 0, span)) return;
+        if (!ssm_packed_span<NT>(p, slot, tile == 0, span)) return;
     } else {
         span = ssm_row_span(p, slot);
     }
     const int each = p.D / p.G, tpg = tiles / p.G, g = tile / tpg, c0 = g * each + tile % tpg * CT;
     const int have = min(CT, (g + 1) * each - c0);  // channels of the tile
-    const int c = tid / NSUB, sub = tid % NSUB, d = c0 + c;
-    const bool live = c < have;
+    // this lane's channel, and of the other (its partner lane's) the same entries
+    const int sub = tid % SUB, c = tid / SUB * 2 + (sub & 1), d = c0 + c, mine = sub / 2 % TL;
+    const bool live = c < have;  // (tiles have a multiple of 4 channels)
 
-    float2 rate[PER / 2], h[PER / 2];
+    float2 rate[2][PER / 2], h[2][PER / 2];
     float bias = 0.f, skip = 0.f, total = 0.f;
-    const size_t at = (size_t)(live ? d : 0) * N + sub * PER;
+    size_t at[2];
+    const float *h0 = CARRY ? nullptr : p.seg ? p.state + (size_t)slot * p.D * N : p.S0 ? p.S0 + (size_t)span.seq * p.D * N : nullptr;
 #pragma unroll
-    for (int i = 0; i < PER / 2; ++i) {
-        const float2 a = reinterpret_cast<const float2 *>(p.A_log + at)[i];
-        rate[i] = make_float2(ssm_rate(a.x), ssm_rate(a.y));
-        h[i] = make_float2(0.f, 0.f);
+    for (int q = 0; q < 2; ++q) {
+        at[q] = (size_t)(live ? c0 + (c ^ q) : 0) * N + sub * PER;
+#pragma unroll
+        for (int i = 0; i < PER / 2; ++i) {
+            const float2 a = reinterpret_cast<const float2 *>(p.A_log + at[q])[i];
+            rate[q][i] = make_float2(ssm_rate(a.x), ssm_rate(a.y));
+            h[q][i] = live && h0 ? reinterpret_cast<const float2 *>(h0 + at[q])[i] : make_float2(0.f, 0.f);
+        }
     }
     if (live) {
         if (p.dt_bias) bias = p.dt_bias[d];
         if (p.Dskip) skip = p.Dskip[d];
-        const float *h0 = CARRY ? nullptr : p.seg ? p.state + (size_t)slot * p.D * N : p.S0 ? p.S0 + (size_t)span.seq * p.D * N : nullptr;
-        if (h0) {
-#pragma unroll
-            for (int i = 0; i < PER / 2; ++i) h[i] = reinterpret_cast<const float2 *>(h0 + at)[i];
-        }
     }
 
     const uint8_t *xg = static_cast<const uint8_t *>(p.x) + (size_t)c0 * sizeof(T);
@@ -76,24 +112,31 @@ __global__ void __launch_bounds__(NT) ssm_fwd_kernel(SsmArgs p, int tiles) {
         const long long t0 = span.lo + (long long)s * TOK;
         if (t0 < span.hi) {
             uint8_t *st = smem + s % STAGES * K::STAGE;
-            load_tile<K::ROW / 16>(st + K::X, xg, pitch, t0, span.hi, pieces);
-            load_tile<K::ROW / 16>(st + K::DT, dg, pitch, t0, span.hi, pieces);
-            load_tile<K::BROW / 16>(st + K::B, bg, bpitch, t0, span.hi, K::BROW / 16);
+            load_tile<K::ROW / 16, NT>(st + K::X, xg, pitch, t0, span.hi, pieces);
+            load_tile<K::ROW / 16, NT>(st + K::DT, dg, pitch, t0, span.hi, pieces);
+            load_tile<K::BROW / 16, NT>(st + K::B, bg, bpitch, t0, span.hi, K::BROW / 16);
             if (!CARRY) {
-                if (zg) load_tile<K::ROW / 16>(st + K::Z, zg, pitch, t0, span.hi, pieces);
-                load_tile<K::BROW / 16>(st + K::C, cg, bpitch, t0, span.hi, K::BROW / 16);
+                if (zg) load_tile<K::ROW / 16, NT>(st + K::Z, zg, pitch, t0, span.hi, pieces);
+                load_tile<K::BROW / 16, NT>(st + K::C, cg, bpitch, t0, span.hi, K::BROW / 16);
             }
         }
         cp_async_commit();
     };
+    // Entry n of a token's B or C goes to ((n % 8 / 4) SUB + n / 8) 4 + n % 4: the lanes of a channel read 16 bytes side by side.
     auto convert = [&](int s) {
         const uint8_t *st = smem + s % STAGES * K::STAGE;
-        float *to = cvt + (s & 1) * 2 * TOK * N;
+        float4 *to = reinterpret_cast<float4 *>(cvt + (s & 1) * 2 * TOK * N);
+        constexpr int V = TOK * N / 8;  // eights of B; those of C follow
+        static_assert(V % NT == 0, "whole passes");
 #pragma unroll
-        for (int k = 0; k < TOK * N / NT; ++k) {
-            const int i = k * NT + tid, t = i / N, n = i % N;
-            to[t * N + cvt_at<NSUB>(n)] = to_f32(reinterpret_cast<const T *>(st + K::B)[i]);
-            if (!CARRY) to[TOK * N + t * N + cvt_at<NSUB>(n)] = to_f32(reinterpret_cast<const T *>(st + K::C)[i]);
+        for (int k = 0; k < (CARRY ? 1 : 2) * V / NT; ++k) {
+            const int i = k * NT + tid;
+            const int t = i % V / (N / 8), e = i % (N / 8);
+            float4 a, b;
+            unpack8(reinterpret_cast<const T *>(st + (i < V ? K::B : K::C)) + t * N + 8 * e, a, b);
+            float4 *at = to + (i / V * TOK + t) * (N / 4) + e;
+            at[0] = a;
+            at[SUB] = b;
         }
     };
 
@@ -114,60 +157,160 @@ __global__ void __launch_bounds__(NT) ssm_fwd_kernel(SsmArgs p, int tiles) {
         const int count = (int)min((long long)TOK, span.hi - t0);
         if (!CARRY && p.keep && live) {
             const int row = (int)(t0 / p.T), nk = (p.T + TOK - 1) / TOK;
-            float2 *k = reinterpret_cast<float2 *>(p.keep + ((size_t)row * nk + (size_t)(t0 - (long long)row * p.T) / TOK) * p.D * N + at);
+            float *k = p.keep + ((size_t)row * nk + (size_t)(t0 - (long long)row * p.T) / TOK) * p.D * N;
 #pragma unroll
-            for (int i = 0; i < PER / 2; ++i) k[i] = h[i];
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < PER / 4; ++i)
+                    reinterpret_cast<float4 *>(k + at[q])[i] = make_float4(h[q][2 * i].x, h[q][2 * i].y, h[q][2 * i + 1].x, h[q][2 * i + 1].y);
         }
-#pragma unroll 4
-        for (int t = 0; t < count; ++t) {
-            const float x = to_f32(reinterpret_cast<const T *>(st + K::X)[t * CT + c]);
-            const float delta = softplus(to_f32(reinterpret_cast<const T *>(st + K::DT)[t * CT + c]) + bias);
-            const float u = delta * x;
-            const float2 delta2 = make_float2(delta, delta), u2 = make_float2(u, u);
-            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // x, delta and u = delta x of this lane's channel and tokens of a group: those of number `mine`, + TL, ..
+        auto gates = [&](int tg, float(&x)[LOC], float(&delta)[LOC], float(&u)[LOC]) {
+            float v[LOC];
+#pragma unroll
+            for (int i = 0; i < LOC; ++i) {
+                const int t = tg + mine + i * TL;
+                x[i] = to_f32(reinterpret_cast<const T *>(st + K::X)[t * CT + c]);
+                v[i] = to_f32(reinterpret_cast<const T *>(st + K::DT)[t * CT + c]) + bias;
+            }
+            if constexpr (LOC > 1) {
+#pragma unroll
+                for (int i = 0; i < LOC; i += 2) {
+                    const float2 r = softplus2(make_float2(v[i], v[i + 1]));
+                    v[i] = r.x;
+                    v[i + 1] = r.y;
+                }
+            } else {
+                v[0] = softplus(v[0]);
+            }
+#pragma unroll
+            for (int i = 0; i < LOC; ++i) {
+                delta[i] = tg + mine + i * TL < count ? v[i] : 0.f;  // (past the end: a token that changes nothing)
+                u[i] = delta[i] * x[i];
+            }
+        };
+        // delta and u of token t of the group, of this lane's channel and of the other.
+        auto steps = [&](int t, const float(&delta)[LOC], const float(&u)[LOC], float2(&dk)[2], float2(&uk)[2]) {
+            const int k = t % 4;
+            float d0 = delta[k / TL], u0 = u[k / TL], d1, u1;
+            if (TL > 1) {  // from the lane of this token
+                const int from = (threadIdx.x & 31 & ~(SUB - 1)) | (k % TL * 2) | (sub & 1);
+                d1 = __shfl_sync(0xffffffffu, d0, from ^ 1);
+                u1 = __shfl_sync(0xffffffffu, u0, from ^ 1);
+                d0 = __shfl_sync(0xffffffffu, d0, from);
+                u0 = __shfl_sync(0xffffffffu, u0, from);
+            } else {
+                d1 = __shfl_xor_sync(0xffffffffu, d0, 1);
+                u1 = __shfl_xor_sync(0xffffffffu, u0, 1);
+            }
+            if (CARRY) total += d0;
+            dk[0] = make_float2(d0, d0), dk[1] = make_float2(d1, d1);
+            uk[0] = make_float2(u0, u0), uk[1] = make_float2(u1, u1);
+        };
+        auto fetch = [&](const float *from, float2(&v)[PER / 2]) {
 #pragma unroll
             for (int j = 0; j < PER / 4; ++j) {
-                const float4 b = *reinterpret_cast<const float4 *>(bc + t * N + j * NSUB * 4);
-                const float2 e0 = __fmul2_rn(delta2, rate[2 * j]), e1 = __fmul2_rn(delta2, rate[2 * j + 1]);
-                h[2 * j] = __ffma2_rn(make_float2(ssm_ex2(e0.x), ssm_ex2(e0.y)), h[2 * j], __fmul2_rn(u2, make_float2(b.x, b.y)));
-                h[2 * j + 1] = __ffma2_rn(make_float2(ssm_ex2(e1.x), ssm_ex2(e1.y)), h[2 * j + 1], __fmul2_rn(u2, make_float2(b.z, b.w)));
-                if (!CARRY) {
-                    const float4 cc = *reinterpret_cast<const float4 *>(bc + TOK * N + t * N + j * NSUB * 4);
-                    acc[0] = __ffma2_rn(h[2 * j], make_float2(cc.x, cc.y), acc[0]);
-                    acc[1] = __ffma2_rn(h[2 * j + 1], make_float2(cc.z, cc.w), acc[1]);
+                const float4 r = *reinterpret_cast<const float4 *>(from + j * SUB * 4);
+                v[2 * j] = make_float2(r.x, r.y);
+                v[2 * j + 1] = make_float2(r.z, r.w);
+            }
+        };
+        float x[LOC], delta[LOC], u[LOC];
+        float2 a[2][PER / 2], ub[2][PER / 2], cc[PER / 2];
+        gates(0, x, delta, u);
+        {
+            float2 dk[2], uk[2], b[PER / 2];
+            steps(0, delta, u, dk, uk);
+            fetch(bc, b);
+            if (!CARRY) fetch(bc + TOK * N, cc);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < PER / 2; ++i) {
+                    const float2 e = __fmul2_rn(dk[q], rate[q][i]);
+                    a[q][i] = make_float2(ssm_ex2(e.x), ssm_ex2(e.y));
+                    ub[q][i] = __fmul2_rn(uk[q], b[i]);
+                }
+        }
+#pragma unroll
+        for (int tg = 0; tg < TOK; tg += 4) {
+            if (tg >= count) break;
+            float xn[LOC], dn[LOC], un[LOC], y[4];
+            if (tg + 4 < TOK) gates(tg + 4, xn, dn, un);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = tg + k;
+                const bool more = t + 1 < TOK;
+                float2 dk[2], uk[2], b[PER / 2], cn[PER / 2], acc[2], e[2][PER / 2];
+                if (more) {
+                    if (k < 3)
+                        steps(t + 1, delta, u, dk, uk);
+                    else
+                        steps(t + 1, dn, un, dk, uk);
+                    fetch(bc + (t + 1) * N, b);
+                    if (!CARRY) fetch(bc + (TOK + t + 1) * N, cn);
+                    e[0][0] = __fmul2_rn(dk[0], rate[0][0]);
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < PER / 2; ++i) {
+                        // this token's state and output between the exponentials of the next
+                        constexpr int HALF = PER / 2;
+                        const int nq = (q * HALF + i + 1) / HALF, ni = (i + 1) % HALF;
+                        float2 an;
+                        if (more) an.x = ssm_ex2_here(e[q][i].x);
+                        h[q][i] = __ffma2_rn(a[q][i], h[q][i], ub[q][i]);
+                        if (more) {
+                            if (nq < 2) e[nq][ni] = __fmul2_rn(dk[nq], rate[nq][ni]);
+                            an.y = ssm_ex2_here(e[q][i].y);
+                            ub[q][i] = __fmul2_rn(uk[q], b[i]);
+                            a[q][i] = an;
+                        }
+                        if (!CARRY) acc[q] = i ? __ffma2_rn(h[q][i], cc[i], acc[q]) : __fmul2_rn(h[q][0], cc[0]);
+                    }
+                if (!CARRY) y[k] = acc[0].x + acc[0].y + __shfl_xor_sync(0xffffffffu, acc[1].x + acc[1].y, 1);
+#pragma unroll
+                for (int i = 0; i < PER / 2; ++i) cc[i] = cn[i];
+            }
+            if (!CARRY) {
+                float out[LOC];
+                owner_sums<SUB, LOC>(y, sub, out);
+#pragma unroll
+                for (int i = 0; i < LOC; ++i) {
+                    const int t = tg + mine + i * TL;
+                    out[i] = fmaf(skip, x[i], out[i]);
+                    if (p.z) {
+                        const float z = to_f32(reinterpret_cast<const T *>(st + K::Z)[t * CT + c]);
+                        out[i] *= z * ssm_sigmoid(z);
+                    }
+                    if (live && sub < 8 && t < count && p.y) static_cast<T *>(p.y)[(size_t)(t0 + t) * p.D + d] = from_f32<T>(out[i]);
                 }
             }
-            if (CARRY) {
-                total += delta;
-            } else {
-                float y = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
 #pragma unroll
-                for (int off = 1; off < NSUB; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-                y = fmaf(skip, x, y);
-                if (p.z) {
-                    const float z = to_f32(reinterpret_cast<const T *>(st + K::Z)[t * CT + c]);
-                    y *= z * ssm_sigmoid(z);
-                }
-                if (live && sub == 0 && p.y) static_cast<T *>(p.y)[(size_t)(t0 + t) * p.D + d] = from_f32<T>(y);
+            for (int i = 0; i < LOC; ++i) {
+                x[i] = xn[i];
+                delta[i] = dn[i];
+                u[i] = un[i];
             }
         }
     }
     if (!live) return;
-    if (CARRY) {
-        float2 *to = reinterpret_cast<float2 *>(p.state + (size_t)slot * p.D * N + at);
+    float *end = CARRY ? p.state + (size_t)slot * p.D * N : p.S_T && !p.seg ? p.S_T + (size_t)span.seq * p.D * N : nullptr;
+    if (end) {
 #pragma unroll
-        for (int i = 0; i < PER / 2; ++i) to[i] = h[i];
-        if (sub == 0) p.sum[(size_t)slot * p.D + d] = total;
-    } else if (p.S_T && !p.seg) {
-        float2 *to = reinterpret_cast<float2 *>(p.S_T + (size_t)span.seq * p.D * N + at);
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int i = 0; i < PER / 2; ++i) to[i] = h[i];
+            for (int i = 0; i < PER / 2; ++i) reinterpret_cast<float2 *>(end + at[q])[i] = h[q][i];
     }
+    if (CARRY && sub < 2) p.sum[(size_t)slot * p.D + d] = total;
 }
 
 // Start states of a row's or sequence's segments from their local end states, in place, and its last state.
 // A thread an entry of the state; blockIdx.y the row.
-__global__ void __launch_bounds__(NT) ssm_combine_kernel(SsmArgs p) {
+constexpr int COMBINE_NT = 128;
+__global__ void __launch_bounds__(COMBINE_NT) ssm_combine_kernel(SsmArgs p) {
+    constexpr int NT = COMBINE_NT;
     __shared__ int box[NT / 32];
     const int row = blockIdx.y, tid = threadIdx.x;
     int first, segs;
@@ -194,44 +337,56 @@ __global__ void __launch_bounds__(NT) ssm_combine_kernel(SsmArgs p) {
     float h = p.S0 ? p.S0[row * size + e] : 0.f;
     float *state = p.state + first * size + e;
     const float *sum = p.sum + (size_t)first * p.D + e / p.N;
-#pragma unroll 8
-    for (int s = 0; s < segs; ++s) {
-        const float local = state[s * size];
-        state[s * size] = h;
-        h = fmaf(ssm_ex2(rate * sum[(size_t)s * p.D]), h, local);
+    constexpr int BATCH = 8;  // (all loaded before the first is written back)
+    for (int s0 = 0; s0 < segs; s0 += BATCH) {
+        float local[BATCH], decay[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            local[i] = decay[i] = 0.f;
+            if (s0 + i < segs) {
+                local[i] = state[(s0 + i) * size];
+                decay[i] = ssm_ex2(rate * sum[(size_t)(s0 + i) * p.D]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            if (s0 + i < segs) {
+                state[(s0 + i) * size] = h;
+                h = fmaf(decay[i], h, local[i]);
+            }
     }
     if (p.S_T) p.S_T[row * size + e] = h;
 }
 
-template <typename T, int NSUB, bool CARRY>
+template <typename T, int N, bool CARRY>
 cudaError_t run(const SsmArgs &a, long long slots, int tiles) {
-    using K = Scan<T, NSUB, CARRY>;
+    using K = Scan<T, N, CARRY>;
     if (K::SMEM > 48 * 1024) {
         const cudaError_t e =
-            cudaFuncSetAttribute(ssm_fwd_kernel<T, NSUB, CARRY>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
+            cudaFuncSetAttribute(ssm_fwd_kernel<T, N, CARRY>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
         if (e != cudaSuccess) return e;
     }
-    ssm_fwd_kernel<T, NSUB, CARRY><<<(unsigned)(slots * tiles), NT, K::SMEM, a.stream>>>(a, tiles);
+    ssm_fwd_kernel<T, N, CARRY><<<(unsigned)(slots * tiles), K::NT, K::SMEM, a.stream>>>(a, tiles);
     return cudaGetLastError();
 }
 
-template <typename T, int NSUB>
+template <typename T, int N>
 cudaError_t forward(const SsmArgs &a) {
-    const int tiles = ssm_tiles(a.D, a.N, a.G);
+    const int tiles = ssm_fwd_tiles(a.D, a.N, a.G);
     const long long slots = a.seg ? a.slots : a.nseq;
     if (a.seg) {
-        cudaError_t e = run<T, NSUB, true>(a, slots, tiles);
+        cudaError_t e = run<T, N, true>(a, slots, tiles);
         if (e != cudaSuccess) return e;
-        const dim3 grid((unsigned)(((size_t)a.D * a.N + NT - 1) / NT), a.nseq);
-        ssm_combine_kernel<<<grid, NT, 0, a.stream>>>(a);
+        const dim3 grid((unsigned)(((size_t)a.D * a.N + COMBINE_NT - 1) / COMBINE_NT), a.nseq);
+        ssm_combine_kernel<<<grid, COMBINE_NT, 0, a.stream>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return run<T, NSUB, false>(a, slots, tiles);
+    return run<T, N, false>(a, slots, tiles);
 }
 
 template <typename T>
 cudaError_t states(const SsmArgs &a) {
-    return a.N == 16 ? forward<T, 1>(a) : a.N == 32 ? forward<T, 2>(a) : a.N == 64 ? forward<T, 4>(a) : forward<T, 8>(a);
+    return a.N == 16 ? forward<T, 16>(a) : a.N == 32 ? forward<T, 32>(a) : a.N == 64 ? forward<T, 64>(a) : forward<T, 128>(a);
 }
 
 // ------------------------------------------------------------------------------------ one token
@@ -297,13 +452,35 @@ cudaError_t step_states(const SsmArgs &a) {
 
 }  // namespace
 
-int ssm_segment(long long rows, int T, int tiles) {
-    // Enough CTAs for two a SM, but segments of 64 tokens at least.
-    const long long units = rows * tiles, want = 152 * 2;
-    if (units <= 0 || 2 * units > want || T < 128) return 0;
-    const long long parts = std::min<long long>(want / units, (T + 63) / 64);
-    const long long seg = (T + parts - 1) / parts;
-    return (int)((seg + SSM_TOK - 1) / SSM_TOK * SSM_TOK);
+namespace {
+// How many segments to cut a row of T tokens into: the number of the least estimated time.  A token costs one(w) clocks
+// on a unit of the GPU (of which there are `places`) that has w of the `work` pieces of a row's length, all rows
+// together; cutting costs `carry` of that again, and `step` a segment (its state through HBM: 8 bytes an entry).
+template <typename F>
+int cut(long long work, int T, int places, F one, double carry, double step, double uneven) {
+    int best = 1;
+    double least = 0.;
+    const int most = std::max(1, std::min(T / 64, 128));
+    for (int p = 1; p <= most; ++p) {
+        const long long w = (work * p + places - 1) / places;
+        const int tokens = ((T + p - 1) / p + SSM_TOK - 1) / SSM_TOK * SSM_TOK;
+        const double t = tokens * one(w) * (p > 1 ? 1. + carry : 1.) * (1. + uneven / p) + step * p;
+        if (p == 1 || t < least) best = p, least = t;
+    }
+    if (best == 1) return 0;
+    return ((T + best - 1) / best + SSM_TOK - 1) / SSM_TOK * SSM_TOK;
+}
+}  // namespace
+
+// A scheduler (608) with one warp takes 326 clocks a token, with more 183 each; the carry kernel 0.55 of the scan's
+// (8 x 2048 tokens of 2432, 4864 and 7296 channels, N = 16: 347, 407 and 567 us whole).
+int ssm_segment(long long rows, int T, int D, int N, bool uneven) {
+    return cut(rows * (((long long)D * N + 511) / 512), T, 608, [](long long w) { return w == 1 ? 326. : 183. * w; }, 0.55,
+               600. + 0.0023 * rows * D * N, uneven ? 1. : 0.);
+}
+// A SM (152) with two CTAs takes 1528 clocks for a token of both, with one 1086; the carry 0.2 of that.
+int ssm_bwd_segment(long long rows, int T, int D, int N, int tiles) {
+    return cut(rows * tiles, T, 152, [](long long w) { return w / 2 * 1528. + w % 2 * 1086.; }, 0.2, 600. + 0.0092 * rows * D * N, 0.);
 }
 
 cudaError_t launch_ssm_scan(const SsmArgs &a) { return a.dtype == EFLA_BF16 ? states<__nv_bfloat16>(a) : states<float>(a); }
