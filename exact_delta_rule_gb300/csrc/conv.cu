@@ -22,7 +22,8 @@ namespace efla {
 namespace {
 
 constexpr int NT = CONV_NT;
-constexpr int BATCH = 8;  // rows in flight a thread
+template <typename T>
+constexpr int BATCH = sizeof(T) == 2 ? 8 : 4;  // rows in flight a thread: 64 bytes of 4 channels
 
 // To 2 + 1.2 |x| ulp, as the output gate's.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
@@ -92,9 +93,10 @@ struct Taps {
 // CTAs [0, work_ctas): runs of `rows` tokens x a block of the channels; the others copy the states.  PACKED: the
 // runs are of all tokens, and first[i], seq[i] say where the sequence of the CTA's token i begins and which it is
 // (-1: none).  Otherwise they are of the rows, row_runs each.
-template <typename T, int V, int W, bool PACKED>
-__global__ void __launch_bounds__(NT, 2) conv_fwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, unsigned work_ctas, int rows,
+template <typename T, int V, int W, bool PACKED, bool SILU>
+__global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, unsigned work_ctas, int rows,
                                                       int row_runs) {
+    constexpr int BATCH = efla::BATCH<T>;
     const int tid = threadIdx.x;
     if (blockIdx.x >= work_ctas) {  // state_T: place j of a sequence's last W - 1 inputs
         const long long e = (long long)(blockIdx.x - work_ctas) * NT + tid;
@@ -175,41 +177,56 @@ __global__ void __launch_bounds__(NT, 2) conv_fwd_kernel(ConvArgs p, int vecs, i
         before(begin);
     Taps<W, V> taps;
     taps.load(p, v * V);
-    for (long long t = begin; t < end; t += BATCH) {
-        Pack<T, V> raw[BATCH];
+    auto token = [&](const Pack<T, V> &raw, Pack<T, V> *to) {
+        float x[V], s[V];
+        unpack(raw, x);
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            raw[k] = Pack<T, V>{};
-            if (t + k < end) raw[k] = load<T, V>(p.x, t + k, vecs, v);
+        for (int c = 0; c < V; ++c) {
+            float a = taps.bias[c];
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
+            a = fmaf(taps.w[c][W - 1], x[c], a);
+            s[c] = SILU ? a * sigmoid(a) : a;
+#pragma unroll
+            for (int i = 0; i + 1 < W - 1; ++i) win[i][c] = win[i + 1][c];
+            win[W - 2][c] = x[c];
+        }
+        Pack<T, V> r;
+        pack(s, r);
+        *to = r;
+    };
+    const Pack<T, V> *from = static_cast<const Pack<T, V> *>(p.x) + begin * vecs + v;
+    Pack<T, V> *to = static_cast<Pack<T, V> *>(p.y) + begin * vecs + v;
+    const int count = (int)(end - begin);
+    for (int t = 0; t < count; t += BATCH, from += (size_t)BATCH * vecs, to += (size_t)BATCH * vecs) {
+        Pack<T, V> raw[BATCH];
+        if (!PACKED && t + BATCH <= count) {  // straight code for whole batches
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) raw[k] = from[(size_t)k * vecs];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) token(raw[k], to + (size_t)k * vecs);
+            continue;
         }
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            if (t + k >= end) break;
+            raw[k] = Pack<T, V>{};
+            if (t + k < count) raw[k] = from[(size_t)k * vecs];
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            if (t + k >= count) break;
             if (PACKED) {
-                n = seq[t + k - t0];
+                n = seq[begin + t + k - t0];
                 if (n < 0) {
                     lo = -1;
                     continue;
                 }
-                if (lo != first[t + k - t0]) {
-                    lo = first[t + k - t0];
-                    before(t + k);
+                if (lo != first[begin + t + k - t0]) {
+                    lo = first[begin + t + k - t0];
+                    before(begin + t + k);
                 }
             }
-            float x[V], s[V];
-            unpack(raw[k], x);
-#pragma unroll
-            for (int c = 0; c < V; ++c) {
-                float a = taps.bias[c];
-#pragma unroll
-                for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
-                a = fmaf(taps.w[c][W - 1], x[c], a);
-                s[c] = p.silu ? a * sigmoid(a) : a;
-#pragma unroll
-                for (int i = 0; i + 1 < W - 1; ++i) win[i][c] = win[i + 1][c];
-                win[W - 2][c] = x[c];
-            }
-            store<T, V>(p.y, t + k, vecs, v, s);
+            token(raw[k], to + (size_t)k * vecs);
         }
     }
 }
@@ -217,9 +234,9 @@ __global__ void __launch_bounds__(NT, 2) conv_fwd_kernel(ConvArgs p, int vecs, i
 // ------------------------------------------------------------------------------------ backward
 // A CTA: `lanes` vectors of 4 channels x NT / lanes runs of CONV_BWD_ROWS places of an extended row, and every
 // parts-th such tile after it; row_runs runs a row.
-template <typename T, int W>
-__global__ void __launch_bounds__(NT, 2) conv_bwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, int parts, int row_runs) {
-    constexpr int V = 4, R = CONV_BWD_ROWS;
+template <typename T, int W, bool SILU>
+__global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, int parts, int row_runs) {
+    constexpr int V = 4, R = CONV_BWD_ROWS, BATCH = efla::BATCH<T>, NT = CONV_BWD_NT;
     __shared__ float red[NT][V + 1];
     const int tid = threadIdx.x, lane = tid % lanes, sub = tid / lanes, subs = NT / lanes;
     const int cb = blockIdx.x % cblocks, tile = blockIdx.x / cblocks, v = cb * lanes + lane;
@@ -246,8 +263,72 @@ __global__ void __launch_bounds__(NT, 2) conv_bwd_kernel(ConvArgs p, int vecs, i
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) place(e0 - (W - 1) + i, win[i]);
         const int e1 = min(e0 + R, ends);
+        // ds of token t, whose newest input is x, into the window; with `own` into dw and dbias too
+        auto token = [&](const float(&x)[V], float(&ds)[V], bool real, bool own) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                if (SILU) {
+                    float a = taps.bias[c];
+#pragma unroll
+                    for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
+                    a = fmaf(taps.w[c][W - 1], x[c], a);
+                    const float g = sigmoid(a);
+                    if (real) ds[c] *= g * fmaf(a, 1.f - g, 1.f);
+                }
+                if (own) {
+#pragma unroll
+                    for (int i = 0; i < W - 1; ++i) dw[c][i] = fmaf(ds[c], win[i][c], dw[c][i]);
+                    dw[c][W - 1] = fmaf(ds[c], x[c], dw[c][W - 1]);
+                    db[c] += ds[c];
+                }
+            }
+        };
+        // place e = t: d += sum_j w_j ds_{t-j}
+        auto place_sum = [&](const float(&ds)[V], float(&d)[V]) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                d[c] = fmaf(taps.w[c][0], ds[c], d[c]);
+#pragma unroll
+                for (int j = 1; j < W; ++j) d[c] = fmaf(taps.w[c][j], old[W - 1 - j][c], d[c]);
+            }
+        };
+        auto shift = [&](const float(&x)[V], const float(&ds)[V]) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+#pragma unroll
+                for (int i = 0; i + 1 < W - 1; ++i) {
+                    win[i][c] = win[i + 1][c];
+                    old[i][c] = old[i + 1][c];
+                }
+                win[W - 2][c] = x[c];
+                old[W - 2][c] = ds[c];
+            }
+        };
         for (int tb = e0 - (W - 1); tb < e1; tb += BATCH) {  // token t's newest input is at place t + W - 1
             Pack<T, V> rx[BATCH], rd[BATCH];
+            if (tb >= max(e0, W - 1) && tb + BATCH <= min(e1, p.T)) {  // straight code inside a run
+                const size_t at = (size_t)(row + tb) * vecs + v;
+                const Pack<T, V> *xs = static_cast<const Pack<T, V> *>(p.x) + at, *ys = static_cast<const Pack<T, V> *>(p.dy) + at;
+                Pack<T, V> *to = static_cast<Pack<T, V> *>(p.dx) + at - (size_t)(W - 1) * vecs;
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    rx[k] = xs[(size_t)k * vecs];
+                    rd[k] = ys[(size_t)k * vecs];
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    float x[V], ds[V], d[V] = {};
+                    unpack(rx[k], x);
+                    unpack(rd[k], ds);
+                    token(x, ds, true, true);
+                    place_sum(ds, d);
+                    shift(x, ds);
+                    Pack<T, V> r;
+                    pack(d, r);
+                    to[(size_t)k * vecs] = r;
+                }
+                continue;
+            }
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
                 const int t = tb + k;
@@ -268,47 +349,17 @@ __global__ void __launch_bounds__(NT, 2) conv_bwd_kernel(ConvArgs p, int vecs, i
                 float x[V], ds[V];
                 unpack(rx[k], x);
                 unpack(rd[k], ds);  // 0 outside the row
-#pragma unroll
-                for (int c = 0; c < V; ++c) {
-                    if (p.silu) {
-                        float a = taps.bias[c];
-#pragma unroll
-                        for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
-                        a = fmaf(taps.w[c][W - 1], x[c], a);
-                        const float g = sigmoid(a);
-                        if (t >= 0 && t < p.T) ds[c] *= g * fmaf(a, 1.f - g, 1.f);
-                    }
-                    if (t >= e0) {
-#pragma unroll
-                        for (int i = 0; i < W - 1; ++i) dw[c][i] = fmaf(ds[c], win[i][c], dw[c][i]);
-                        dw[c][W - 1] = fmaf(ds[c], x[c], dw[c][W - 1]);
-                        db[c] += ds[c];
-                    }
-                }
-                if (t >= e0) {  // place e = t: sum_j w_j ds_{t-j}
+                token(x, ds, t >= 0 && t < p.T, t >= e0);
+                if (t >= e0) {
                     float d[V] = {};
                     if (p.dstate_T && t >= p.T) unpack(load<T, V>(p.dstate_T, (long long)b * (W - 1) + t - p.T, vecs, v), d);
-#pragma unroll
-                    for (int c = 0; c < V; ++c) {
-                        d[c] = fmaf(taps.w[c][0], ds[c], d[c]);
-#pragma unroll
-                        for (int j = 1; j < W; ++j) d[c] = fmaf(taps.w[c][j], old[W - 1 - j][c], d[c]);
-                    }
+                    place_sum(ds, d);
                     if (t >= W - 1)
                         store<T, V>(p.dx, row + t - (W - 1), vecs, v, d);
                     else if (p.dstate0)
                         store<T, V>(p.dstate0, (long long)b * (W - 1) + t, vecs, v, d);
                 }
-#pragma unroll
-                for (int c = 0; c < V; ++c) {
-#pragma unroll
-                    for (int i = 0; i + 1 < W - 1; ++i) {
-                        win[i][c] = win[i + 1][c];
-                        old[i][c] = old[i + 1][c];
-                    }
-                    win[W - 2][c] = x[c];
-                    old[W - 2][c] = ds[c];
-                }
+                shift(x, ds);
             }
         }
     }
@@ -376,30 +427,34 @@ __global__ void __launch_bounds__(STEP_NT) conv_step_kernel(ConvArgs p, int vecs
 
 template <typename T, int W>
 cudaError_t fwd(const ConvArgs &a) {
-    constexpr int V = Vec<T>::N;
+    constexpr int V = 4;
     const int vecs = a.D / V, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes, subs = NT / lanes;
     // Tokens a thread: 32 (3 rows of halo in 35) where that still leaves two CTAs a SM, down to 8.
     const long long tokens = (long long)a.B * a.T;
     int rows = 32;
-    while (rows > BATCH && tokens * vecs < 2LL * 152 * NT * rows) rows /= 2;
+    while (rows > 8 && tokens * vecs < 2LL * 152 * NT * rows) rows /= 2;
     const int row_runs = (a.T + rows - 1) / rows;
     const long long runs = a.cu_seqlens ? (tokens + rows - 1) / rows : (long long)a.B * row_runs;
     const long long work = (runs + subs - 1) / subs * cblocks;
     const long long copies = a.state_T ? ((long long)a.N * (W - 1) * vecs + NT - 1) / NT : 0;
     if (work + copies == 0) return cudaSuccess;
+    auto go = [&](auto kernel, size_t smem) {
+        kernel<<<(unsigned)(work + copies), NT, smem, a.stream>>>(a, vecs, lanes, cblocks, (unsigned)work, rows, row_runs);
+    };
     if (a.cu_seqlens)
-        conv_fwd_kernel<T, V, W, true><<<(unsigned)(work + copies), NT, 2 * rows * subs * sizeof(int), a.stream>>>(
-            a, vecs, lanes, cblocks, (unsigned)work, rows, row_runs);
+        go(a.silu ? conv_fwd_kernel<T, V, W, true, true> : conv_fwd_kernel<T, V, W, true, false>, 2 * rows * subs * sizeof(int));
     else
-        conv_fwd_kernel<T, V, W, false><<<(unsigned)(work + copies), NT, 0, a.stream>>>(a, vecs, lanes, cblocks, (unsigned)work,
-                                                                                      rows, row_runs);
+        go(a.silu ? conv_fwd_kernel<T, V, W, false, true> : conv_fwd_kernel<T, V, W, false, false>, 0);
     return cudaGetLastError();
 }
 template <typename T, int W>
 cudaError_t bwd(const ConvArgs &a) {
     const int vecs = a.D / 4, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes;
     const int parts = conv_bwd_parts(a.B, a.T, a.D, a.W);
-    conv_bwd_kernel<T, W><<<(unsigned)parts * cblocks, NT, 0, a.stream>>>(a, vecs, lanes, cblocks, parts, conv_bwd_runs(a.T, a.W));
+    auto go = [&](auto kernel) {
+        kernel<<<(unsigned)parts * cblocks, CONV_BWD_NT, 0, a.stream>>>(a, vecs, lanes, cblocks, parts, conv_bwd_runs(a.T, a.W));
+    };
+    go(a.silu ? conv_bwd_kernel<T, W, true> : conv_bwd_kernel<T, W, false>);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_sum_parts(a.ws, parts, a.D * (a.dbias ? W + 1 : W), a.dw, a.dbias, a.D * W, a.stream);

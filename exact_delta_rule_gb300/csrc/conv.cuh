@@ -30,14 +30,14 @@ inline int conv_lanes(int vecs) {
     while (n < vecs && n < 32) n *= 2;
     return n;
 }
-// Threads a CTA; places a run of the backward (with the W - 1 before it: five batches of 8).
-constexpr int CONV_NT = 256, CONV_BWD_ROWS = 37;
+// Threads a CTA; of the backward, and the places of its runs.
+constexpr int CONV_NT = 256, CONV_BWD_NT = 128, CONV_BWD_ROWS = 37;
 // Runs of CONV_BWD_ROWS places of a row extended by the W - 1 of its state, and the CTAs a block of channels that
-// share them: all that there are up to four a SM.
+// share them: all that there are up to six a SM.
 inline int conv_bwd_runs(int T, int W) { return (int)(((long long)T + W - 1 + CONV_BWD_ROWS - 1) / CONV_BWD_ROWS); }
 inline int conv_bwd_parts(int B, int T, int D, int W) {
-    const int vecs = D / 4, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes, subs = CONV_NT / lanes;
-    const long long tiles = ((long long)B * conv_bwd_runs(T, W) + subs - 1) / subs, most = 152 * 4 / cblocks;
+    const int vecs = D / 4, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes, subs = CONV_BWD_NT / lanes;
+    const long long tiles = ((long long)B * conv_bwd_runs(T, W) + subs - 1) / subs, most = 152 * 6 / cblocks;
     return (int)std::max(1LL, std::min(tiles, most));
 }
 

@@ -18,8 +18,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import _check, load
-from .gated import (_DT, _INT_MAX, _bad, _empty, _empty_as, _first, _given, _need, _on_device, _ptr, _stream, _too_large,
-                    _workspace)
+from .gated import (_DT, _INT_MAX, _bad, _empty, _empty_as, _first, _given, _need, _ptr, _stream, _too_large, _workspace)
+from .gated import _on_device as _refuse_device
 
 _vp, _ip, _sz, _fl = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 _SIGNATURES = {
@@ -52,6 +52,20 @@ def _lib():
     return _bound
 
 
+def _all(like: torch.Tensor, *args):
+    """``_need`` of every (name, tensor or None, shape, dtype), 0.5 us each where nothing is amiss."""
+    device = like.get_device()
+    for name, t, shape, dtype in args:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous()):
+            _need(name, t, shape, dtype, like)
+
+
+def _on_device(t: torch.Tensor):
+    """The check of ``gated._on_device``, without what torch.cuda.current_device() does around it."""
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        _refuse_device(t)
+
+
 def _activation(activation) -> int:
     code = _ACTIVATIONS.get(activation, -1)
     if code < 0:
@@ -80,13 +94,11 @@ def _conv_args(x, w, bias, dims):
     code = _first("x", x, dims)
     if w.dim() != 2:
         _bad(f"w must be [D, W], got {list(w.shape)}")
-    D, W = x.shape[-1], w.shape[1]
-    if max(*x.shape, W) > _INT_MAX:
-        _too_large(*x.shape, W)
-    _need("x", x, x.shape, x.dtype, x)
-    _need("w", w, (D, W), torch.float32, x)
-    if bias is not None:
-        _need("bias", bias, (D,), torch.float32, x)
+    shape = x.shape
+    D, W = shape[-1], w.shape[1]
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX or D > _INT_MAX or W > _INT_MAX:
+        _too_large(*shape, W)
+    _all(x, ("x", x, shape, x.dtype), ("w", w, (D, W), torch.float32), ("bias", bias, (D,), torch.float32))
     return code, D, W
 
 
@@ -162,20 +174,14 @@ def _ssm_args(x, dt, A_log, B, C, D, dt_bias, z, lead: int):
     code = _first("x", x, lead + 1)
     if A_log.dim() != 2 or B.dim() != lead + 2:
         _bad(f"A_log must be [D, d_state] and B {lead + 2}-D, got {list(A_log.shape)} and {list(B.shape)}")
-    *at, ch = x.shape
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    *at, ch = shape
     N, G = A_log.shape[1], B.shape[lead]
-    if max(*x.shape, N, G) > _INT_MAX:
-        _too_large(*x.shape, N, G)
-    _need("x", x, x.shape, x.dtype, x)
-    _need("dt", dt, x.shape, x.dtype, x)
-    _need("A_log", A_log, (ch, N), torch.float32, x)
-    _need("B", B, (*at, G, N), x.dtype, x)
-    _need("C", C, (*at, G, N), x.dtype, x)
-    for name, t in (("D", D), ("dt_bias", dt_bias)):
-        if t is not None:
-            _need(name, t, (ch,), torch.float32, x)
-    if z is not None:
-        _need("z", z, x.shape, x.dtype, x)
+    if shape[0] > _INT_MAX or shape[lead - 1] > _INT_MAX or ch > _INT_MAX or N > _INT_MAX or G > _INT_MAX:
+        _too_large(*shape, N, G)
+    each, shared = (ch,), (*at, G, N)
+    _all(x, ("x", x, shape, dtype), ("dt", dt, shape, dtype), ("A_log", A_log, (ch, N), f32), ("B", B, shared, dtype),
+         ("C", C, shared, dtype), ("D", D, each, f32), ("dt_bias", dt_bias, each, f32), ("z", z, shape, dtype))
     return at, ch, N, G, code
 
 
