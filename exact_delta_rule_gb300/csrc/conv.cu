@@ -25,9 +25,6 @@ constexpr int NT = CONV_NT;
 template <typename T>
 constexpr int BATCH = sizeof(T) == 2 ? 8 : 4;  // rows in flight a thread: 64 bytes of 4 channels
 
-// To 2 + 1.2 |x| ulp, as the output gate's.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
 // V channels of a row.
 template <typename T, int V>
 struct Pack;
@@ -186,7 +183,7 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
             a = fmaf(taps.w[c][W - 1], x[c], a);
-            s[c] = SILU ? a * sigmoid(a) : a;
+            s[c] = SILU ? a * quick_sigmoid(a) : a;
 #pragma unroll
             for (int i = 0; i + 1 < W - 1; ++i) win[i][c] = win[i + 1][c];
             win[W - 2][c] = x[c];
@@ -272,7 +269,7 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
 #pragma unroll
                     for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
                     a = fmaf(taps.w[c][W - 1], x[c], a);
-                    const float g = sigmoid(a);
+                    const float g = quick_sigmoid(a);
                     if (real) ds[c] *= g * fmaf(a, 1.f - g, 1.f);
                 }
                 if (own) {
@@ -419,7 +416,7 @@ __global__ void __launch_bounds__(STEP_NT) conv_step_kernel(ConvArgs p, int vecs
         }
         if (p.silu) {
 #pragma unroll
-            for (int c = 0; c < V; ++c) s[c] *= sigmoid(s[c]);
+            for (int c = 0; c < V; ++c) s[c] *= quick_sigmoid(s[c]);
         }
         store<T, V>(p.y, b, vecs, v, s);
     }

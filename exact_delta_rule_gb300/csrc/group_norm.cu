@@ -17,12 +17,10 @@ namespace {
 
 constexpr int NT = GN_NT;
 
-// To 2 + 1.2 |x| ulp, as the output gate's.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-__device__ __forceinline__ float act(float s, int silu) { return silu ? s * sigmoid(s) : s; }
+__device__ __forceinline__ float act(float s, int silu) { return silu ? s * quick_sigmoid(s) : s; }
 __device__ __forceinline__ float dact(float s, int silu) {
     if (!silu) return 1.f;
-    const float g = sigmoid(s);
+    const float g = quick_sigmoid(s);
     return g * fmaf(s, 1.f - g, 1.f);
 }
 
@@ -134,15 +132,17 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
 
 // ------------------------------------------------------------------------------------ sums per channel
 // Forward: of x - K and (x - K)^2 with K the channel's first value of the row; backward: of ds and ds n.  A CTA
-// takes one chunk of a row's positions and a block of its channels: part[row chunks + chunk][2][C].
-template <typename T, bool BWD>
+// takes one chunk of a row's positions and a block of its channels: part[row chunks + chunk][2][C].  JOINT (backward):
+// one chunk of the positions of all rows.
+template <typename T, bool BWD, bool JOINT>
 __global__ void __launch_bounds__(NT) gn_sums_kernel(GroupNormArgs p, int lanes, int blocks, int chunks) {
     constexpr int V = Vec<T>::N;
     __shared__ float red[NT][V + 1];
     const int tid = threadIdx.x, lane = tid % lanes, sub = tid / lanes, subs = NT / lanes;
-    const int block = blockIdx.x % blocks, rc = blockIdx.x / blocks, row = rc / chunks, chunk = rc % chunks;
+    const int block = blockIdx.x % blocks, rc = blockIdx.x / blocks, row = JOINT ? 0 : rc / chunks, chunk = rc % chunks;
     const int vecs = p.C / V, v = block * lanes + lane, cg = p.C / p.G;
-    const int each = (p.L + chunks - 1) / chunks, from = chunk * each, to = min(p.L, from + each);
+    const long long all = JOINT ? (long long)p.rows * p.L : p.L, each = (all + chunks - 1) / chunks;
+    const long long from = chunk * each, to = min(all, from + each);
     float a[V] = {}, q[V] = {};
     if (v < vecs) {
         const uint4 *x = static_cast<const uint4 *>(p.x) + (size_t)row * p.L * vecs + v;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(NT) gn_sums_kernel(GroupNormArgs p, int lanes,
         if (BWD) {
             affine(p, v * V, w, b);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
+            for (int e = 0; e < V && !JOINT; ++e) {
                 const float2 st = reinterpret_cast<const float2 *>(p.stats)[(size_t)row * p.G + (v * V + e) / cg];
                 k[e] = st.x;
                 r[e] = st.y;
@@ -160,10 +160,19 @@ __global__ void __launch_bounds__(NT) gn_sums_kernel(GroupNormArgs p, int lanes,
         }
         const uint4 *dy = BWD ? static_cast<const uint4 *>(p.dy) + (size_t)row * p.L * vecs + v : nullptr;
 #pragma unroll 4
-        for (int t = from + sub; t < to; t += subs) {
+        for (long long t = from + sub; t < to; t += subs) {
             float f[V], d[V];
             Vec<T>::unpack(x[(size_t)t * vecs], f);
             if (BWD) Vec<T>::unpack(dy[(size_t)t * vecs], d);
+            if (JOINT) {
+                const float2 *stats = reinterpret_cast<const float2 *>(p.stats) + t / p.L * p.G;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float2 st = stats[(v * V + e) / cg];
+                    k[e] = st.x;
+                    r[e] = st.y;
+                }
+            }
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 if (BWD) {
@@ -295,6 +304,262 @@ __global__ void __launch_bounds__(NT) gn_apply_kernel(GroupNormArgs p, int lanes
     }
 }
 
+// ------------------------------------------------------------------------------------ a sample a warp
+// x (and dy) of a sample in shared memory.  The sums of a group by TEAM lanes (a power of two, at least C / G up to 32)
+// that walk through its channels one by one, as a group may begin and end inside a vector; then vector by vector.
+template <typename T, int TEAM, bool BWD>
+__global__ void __launch_bounds__(NT) gn_warp_kernel(GroupNormArgs p, int bytes) {
+    constexpr int V = Vec<T>::N, PER = 32 / TEAM;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % TEAM, cg = p.C / p.G;
+    const long long row = (long long)blockIdx.x * (blockDim.x / 32) + warp;
+    if (row >= p.rows) return;
+    const int n = p.L * p.C, vecs = n / V;
+    uint8_t *mine = smem + (size_t)warp * bytes;
+    T *x = reinterpret_cast<T *>(mine), *dy = x + (BWD ? n : 0);
+    float2 *group = reinterpret_cast<float2 *>(mine + (size_t)(BWD ? 2 : 1) * n * sizeof(T)), *means = group + p.G;
+    const uint4 *xs = static_cast<const uint4 *>(p.x) + row * vecs, *ys = BWD ? static_cast<const uint4 *>(p.dy) + row * vecs : nullptr;
+#pragma unroll 4
+    for (int i = lane; i < vecs; i += 32) {
+        reinterpret_cast<uint4 *>(x)[i] = xs[i];
+        if (BWD) reinterpret_cast<uint4 *>(dy)[i] = ys[i];
+    }
+    __syncwarp();
+    const float inv = 1.f / ((float)p.L * (float)cg);
+    float2 *stats = reinterpret_cast<float2 *>(p.stats) + row * p.G;
+    for (int g0 = 0; g0 < p.G; g0 += PER) {
+        const int g = g0 + lane / TEAM;
+        float first = 0.f, second = 0.f;
+        if (!BWD) {
+            if (g < p.G)
+                for (int t = 0; t < p.L; ++t)
+                    for (int c = l; c < cg; c += TEAM) first += to_f32(x[t * p.C + g * cg + c]);
+            first = row_sum<TEAM>(first) * inv;
+            if (g < p.G)
+                for (int t = 0; t < p.L; ++t)
+                    for (int c = l; c < cg; c += TEAM) {
+                        const float d = to_f32(x[t * p.C + g * cg + c]) - first;
+                        second = fmaf(d, d, second);
+                    }
+            second = rsqrtf(row_sum<TEAM>(second) * inv + p.eps);
+            if (g < p.G && l == 0) {
+                group[g] = make_float2(first, second);
+                if (p.stats) stats[g] = make_float2(first, second);
+            }
+        } else {
+            const float2 st = g < p.G ? stats[g] : make_float2(0.f, 0.f);
+            if (g < p.G)
+                for (int t = 0; t < p.L; ++t)
+                    for (int c = l; c < cg; c += TEAM) {
+                        const int ch = g * cg + c;
+                        const float w = p.w ? p.w[ch] : 1.f, m = (to_f32(x[t * p.C + ch]) - st.x) * st.y;
+                        const float dn = to_f32(dy[t * p.C + ch]) * dact(fmaf(m, w, p.b ? p.b[ch] : 0.f), p.silu) * w;
+                        first += dn;
+                        second = fmaf(dn, m, second);
+                    }
+            first = row_sum<TEAM>(first) * inv;
+            second = row_sum<TEAM>(second) * inv;
+            if (g < p.G && l == 0) {
+                group[g] = st;
+                means[g] = make_float2(first, second);
+            }
+        }
+    }
+    __syncwarp();
+    uint4 *out = static_cast<uint4 *>(BWD ? p.dx : p.y) + row * vecs;
+    const int per = p.C / V;
+    for (int i = lane; i < vecs; i += 32) {
+        const int c0 = i % per * V;
+        int g = c0 / cg, next = (g + 1) * cg;
+        float f[V], d[V], w[V], b[V];
+        Vec<T>::unpack(reinterpret_cast<const uint4 *>(x)[i], f);
+        if (BWD) Vec<T>::unpack(reinterpret_cast<const uint4 *>(dy)[i], d);
+        affine(p, c0, w, b);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (c0 + e == next) {
+                ++g;
+                next += cg;
+            }
+            const float2 st = group[g];
+            const float m = (f[e] - st.x) * st.y, s = fmaf(m, w[e], b[e]);
+            f[e] = BWD ? st.y * (d[e] * dact(s, p.silu) * w[e] - means[g].x - m * means[g].y) : act(s, p.silu);
+        }
+        out[i] = Vec<T>::pack(f);
+    }
+}
+
+// ------------------------------------------------------------------------------------ a sample a cluster
+// Forward: a tile of a sample's channels (whole groups) in the shared memory of a cluster, read once.  Each CTA
+// takes `each` positions: per channel the sums of x - K and (x - K)^2 (K its first value here), joined to a mean and
+// square deviation per group, which the CTAs read from one another and join in the order of their ranks.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ float2 cluster_read(const float2 *own, int rank) {
+    uint32_t at;
+    float2 v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(own))), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+template <typename T>
+__global__ void __launch_bounds__(NT) gn_slab_kernel(GroupNormArgs p, GnSlab s) {
+    constexpr int V = Vec<T>::N;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int tid = threadIdx.x, rank = blockIdx.x % s.cluster, unit = blockIdx.x / s.cluster, row = unit / s.tiles, tile = unit % s.tiles;
+    const int cg = p.C / p.G, tc = s.vecs * V, groups = tc / cg, c0 = tile * tc, vecs = p.C / V;
+    const int subs = NT / s.vecs, v = tid % s.vecs, sub = tid / s.vecs;
+    const int from = min(p.L, rank * s.each), len = min(p.L, from + s.each) - from;
+    uint4 *slab = reinterpret_cast<uint4 *>(smem);
+    float *red = reinterpret_cast<float *>(smem + (size_t)s.each * s.vecs * 16);  // [NT][V + 1], then sums [2][tc]
+    float *sums = red + NT * (V + 1);
+    float2 *part = reinterpret_cast<float2 *>(sums + 2 * tc), *all = part + groups;  // a group's mean and deviation; mean and r
+    const bool works = sub < subs;
+    const uint4 *x = static_cast<const uint4 *>(p.x) + ((size_t)row * p.L + from) * vecs + c0 / V + v;
+    if (works)
+        for (int t = sub; t < len; t += subs)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(slab + t * s.vecs + v))),
+                         "l"(x + (size_t)t * vecs)
+                         : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    float w[V], b[V];
+    affine(p, c0 + v * V, w, b);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float a[V] = {}, q[V] = {}, k[V];
+    if (len > 0) Vec<T>::unpack(slab[v], k);
+    if (works) {
+#pragma unroll 4
+        for (int t = sub; t < len; t += subs) {
+            float f[V];
+            Vec<T>::unpack(slab[t * s.vecs + v], f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                f[e] -= k[e];
+                a[e] += f[e];
+                q[e] = fmaf(f[e], f[e], q[e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < V; ++e) red[tid * (V + 1) + e] = which ? q[e] : a[e];
+        __syncthreads();
+        for (int i = tid; i < tc; i += NT) {
+            float z = 0.f;
+            for (int j = 0; j < subs; ++j) z += red[(j * s.vecs + i / V) * (V + 1) + i % V];
+            sums[which * tc + i] = z;
+        }
+    }
+    __syncthreads();
+    const T *first = reinterpret_cast<const T *>(slab);
+    for (int g = tid / 32; g < groups; g += NT / 32) {
+        const int lane = tid & 31;
+        const float per = len > 0 ? 1.f / (float)len : 0.f;
+        float m = 0.f, dev = 0.f;
+        if (len > 0) {
+            for (int c = g * cg + lane; c < (g + 1) * cg; c += 32) m += fmaf(sums[c], per, to_f32(first[c]));
+            m = row_sum<32>(m) / (float)cg;
+            for (int c = g * cg + lane; c < (g + 1) * cg; c += 32) {
+                const float cm = sums[c] * per, off = (to_f32(first[c]) - m) + cm;
+                dev += fmaxf(fmaf(-sums[c], cm, sums[tc + c]), 0.f) + (float)len * off * off;
+            }
+            dev = row_sum<32>(dev);
+        }
+        if (lane == 0) part[g] = make_float2(m, dev);
+    }
+    cluster_arrive();
+    cluster_wait();
+    for (int g = tid; g < groups; g += NT) {
+        float m = 0.f, dev = 0.f;
+        for (int r = 0; r < s.cluster; ++r) {
+            const int n = min(p.L, (r + 1) * s.each) - min(p.L, r * s.each);
+            m = fmaf((float)n, cluster_read(part + g, r).x, m);
+        }
+        m /= (float)p.L;
+        for (int r = 0; r < s.cluster; ++r) {
+            const int n = min(p.L, (r + 1) * s.each) - min(p.L, r * s.each);
+            const float2 o = cluster_read(part + g, r);
+            if (n > 0) dev += fmaf((float)n * (float)cg * (o.x - m), o.x - m, o.y);
+        }
+        const float r = rsqrtf(dev / ((float)p.L * (float)cg) + p.eps);
+        all[g] = make_float2(m, r);
+        if (p.stats && rank == 0) reinterpret_cast<float2 *>(p.stats)[(size_t)row * p.G + c0 / cg + g] = make_float2(m, r);
+    }
+    cluster_arrive();  // (no CTA leaves while another may read from it)
+    __syncthreads();
+    if (works) {
+        float m[V], r[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float2 st = all[(v * V + e) / cg];
+            m[e] = st.x;
+            r[e] = st.y;
+        }
+        uint4 *y = static_cast<uint4 *>(p.y) + ((size_t)row * p.L + from) * vecs + c0 / V + v;
+#pragma unroll 4
+        for (int t = sub; t < len; t += subs) {
+            float f[V];
+            Vec<T>::unpack(slab[t * s.vecs + v], f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[e] = act(fmaf((f[e] - m[e]) * r[e], w[e], b[e]), p.silu);
+            y[(size_t)t * vecs] = Vec<T>::pack(f);
+        }
+    }
+    cluster_wait();
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+}
+
+template <typename T>
+cudaError_t slab(const GroupNormArgs &a, const GnSlab &s) {
+    constexpr int V = Vec<T>::N;
+    const int tc = s.vecs * V;
+    const size_t smem = (size_t)s.each * s.vecs * 16 + (size_t)NT * (V + 1) * 4 + 2 * tc * 4 + (size_t)tc / (a.C / a.G) * 16;
+    const cudaError_t e = allow_smem(gn_slab_kernel<T>, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = s.cluster, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)a.rows * s.tiles * s.cluster), cfg.blockDim = dim3(NT), cfg.dynamicSmemBytes = smem;
+    cfg.stream = a.stream, cfg.attrs = &attr, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gn_slab_kernel<T>, a, s);
+}
+
+template <typename T, bool BWD>
+cudaError_t warps(const GroupNormArgs &a) {
+    const int cg = a.C / a.G, team = std::min(32, gn_team(cg));
+    const int bytes = (int)(((size_t)(BWD ? 2 : 1) * a.L * a.C * sizeof(T) + (size_t)a.G * (BWD ? 16 : 8) + 15) / 16 * 16);
+    const int count = std::max(1, std::min({8, (int)(64 * 1024 / bytes), (a.rows + 151) / 152}));
+    auto go = [&](auto kernel) {
+        const cudaError_t e = allow_smem(kernel, (size_t)count * bytes);
+        if (e != cudaSuccess) return e;
+        kernel<<<(unsigned)((a.rows + count - 1) / count), 32 * count, (size_t)count * bytes, a.stream>>>(a, bytes);
+        return cudaGetLastError();
+    };
+    cudaError_t e = team == 1    ? go(gn_warp_kernel<T, 1, BWD>)
+                    : team == 2  ? go(gn_warp_kernel<T, 2, BWD>)
+                    : team == 4  ? go(gn_warp_kernel<T, 4, BWD>)
+                    : team == 8  ? go(gn_warp_kernel<T, 8, BWD>)
+                    : team == 16 ? go(gn_warp_kernel<T, 16, BWD>)
+                                 : go(gn_warp_kernel<T, 32, BWD>);
+    if constexpr (BWD) {
+        if (e != cudaSuccess || (!a.dw && !a.db)) return e;
+        const int vecs = a.C / Vec<T>::N, lanes = gn_lanes(vecs), blocks = (vecs + lanes - 1) / lanes;
+        const int chunks = gn_column_chunks(a.rows, a.L, a.C, a.dtype);
+        gn_sums_kernel<T, true, true><<<(unsigned)chunks * blocks, NT, 0, a.stream>>>(a, lanes, blocks, chunks);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        return launch_sum_parts(a.ws, chunks, 2 * a.C, a.db, a.dw, a.C, a.stream);
+    }
+    return e;
+}
+
 template <typename T, bool BWD>
 cudaError_t whole(const GroupNormArgs &a) {
     const int team = gn_team(a.C / a.G / Vec<T>::N), blocks = gn_blocks(a.C, a.G, a.dtype);
@@ -319,7 +584,7 @@ cudaError_t general(GroupNormArgs a) {
     const int chunks = gn_chunks(a.rows, a.L, a.C, a.dtype), tiles = (a.L + NT / lanes * 4 - 1) / (NT / lanes * 4);
     float *joined = a.ws + (size_t)a.rows * chunks * 2 * a.C;
     if (!BWD && a.stats) joined = a.stats;
-    gn_sums_kernel<T, BWD><<<(unsigned)(a.rows * chunks) * blocks, NT, 0, a.stream>>>(a, lanes, blocks, chunks);
+    gn_sums_kernel<T, BWD, false><<<(unsigned)(a.rows * chunks) * blocks, NT, 0, a.stream>>>(a, lanes, blocks, chunks);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     gn_join_kernel<T, BWD><<<(unsigned)(((long long)a.rows * a.G + NT / 32 - 1) / (NT / 32)), NT, 0, a.stream>>>(a, chunks, joined);
@@ -333,6 +598,11 @@ cudaError_t general(GroupNormArgs a) {
 template <bool BWD>
 cudaError_t types(const GroupNormArgs &a) {
     if (gn_whole(a.L, a.C, a.G, a.dtype)) return a.dtype == EFLA_BF16 ? whole<__nv_bfloat16, BWD>(a) : whole<float, BWD>(a);
+    if (gn_warps(a.rows, a.L, a.C, a.dtype)) return a.dtype == EFLA_BF16 ? warps<__nv_bfloat16, BWD>(a) : warps<float, BWD>(a);
+    if (!BWD) {
+        const GnSlab s = gn_slab(a.rows, a.L, a.C, a.G, a.dtype);
+        if (s.vecs) return a.dtype == EFLA_BF16 ? slab<__nv_bfloat16>(a, s) : slab<float>(a, s);
+    }
     return a.dtype == EFLA_BF16 ? general<__nv_bfloat16, BWD>(a) : general<float, BWD>(a);
 }
 

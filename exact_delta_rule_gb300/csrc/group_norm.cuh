@@ -52,8 +52,43 @@ inline int gn_chunks(int rows, int L, int C, efla_dtype t) {
     const long long want = blocks > 0 ? (608 + blocks - 1) / blocks : 1, most = std::max(1, L / (4 * subs));
     return (int)std::max(1LL, std::min(want, most));
 }
+// The same where the rows are summed over too: chunks of all rows' positions.
+inline int gn_column_chunks(int rows, int L, int C, efla_dtype t) {
+    const int vecs = C / gn_vec(t), lanes = gn_lanes(vecs), subs = GN_NT / lanes, blocks = (vecs + lanes - 1) / lanes;
+    const long long most = std::max(1LL, (long long)rows * L / (4 * subs));
+    return (int)std::max(1LL, std::min<long long>(608 / blocks, most));
+}
+// Samples (rows) that lie in shared memory, one a warp: few elements, or many rows of up to 16 KB.  The warps a CTA.
+inline bool gn_warps(int rows, int L, int C, efla_dtype t) {
+    const long long n = (long long)L * C;
+    return n <= 1024 || (n * (t == EFLA_BF16 ? 2 : 4) <= 16384 && rows >= 608);
+}
+// Forward, other samples: a tile of whole groups and whole vectors of a sample in the shared memory of a cluster of
+// `cluster` CTAs, which share out its positions.  vecs = 0: it does not fit.
+struct GnSlab {
+    int vecs, tiles, cluster, each;  // vectors a row of the tile; tiles; CTAs; positions a CTA
+};
+inline GnSlab gn_slab(int rows, int L, int C, int G, efla_dtype t) {
+    const int V = gn_vec(t), cg = C / G;
+    int unit = cg;  // least common multiple with a vector
+    while (unit % V) unit += cg;
+    int vecs = unit / V;
+    const int units = C / unit;
+    if (vecs > GN_NT) return {0, 0, 0, 0};
+    for (int m = 1; m <= units && unit / V * m <= 16; ++m)  // up to 256 bytes of a row where groups are small
+        if (units % m == 0) vecs = unit / V * m;
+    const int tiles = C / V / vecs, subs = GN_NT / vecs;
+    const long long bytes = (long long)L * vecs * 16;
+    int k = 1;
+    while (k < 8 && (bytes / k > 64 * 1024 || ((long long)rows * tiles * k < 152 && L / k > 2 * subs))) k *= 2;
+    const int each = (L + k - 1) / k;
+    if ((long long)each * vecs * 16 > 160 * 1024) return {0, 0, 0, 0};
+    return {vecs, tiles, k, each};
+}
 inline size_t gn_ws(int rows, int L, int C, int G, efla_dtype t, bool bwd) {
     if (gn_whole(L, C, G, t)) return bwd ? (size_t)gn_row_parts(rows, C, G, t) * 2 * C : 0;
+    if (!bwd && (gn_warps(rows, L, C, t) || gn_slab(rows, L, C, G, t).vecs)) return 0;
+    if (gn_warps(rows, L, C, t)) return (size_t)gn_column_chunks(rows, L, C, t) * 2 * C;
     return (size_t)rows * gn_chunks(rows, L, C, t) * 2 * C + (size_t)rows * G * 2;
 }
 

@@ -42,6 +42,13 @@ struct Vec<__nv_bfloat16> {
     }
 };
 
+// 1 / (1 + e^{-x}) to 2 + 1.2 |x| ulp, as the output gate's; 0 for -infinity.
+__device__ __forceinline__ float quick_sigmoid(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + __expf(-x)));
+    return y;
+}
+
 // Sum over the LPR lanes that hold a row.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {

@@ -407,7 +407,8 @@ def check_group_norm(shape, groups, dtype, silu, affine=True, offset=0.0, seed=0
 
 @pytest.mark.parametrize("shape, groups", [
     ((1, 8), 1), ((7, 2048), 16), ((1000, 256), 1), ((33, 64), 8), ((5, 24), 3), ((3, 40), 1), ((2, 96), 32), ((65, 640), 16),
-    ((9, 4096), 2), ((2, 8192), 1), ((700, 16), 16), ((0, 16), 2), ((3, 192), 4), ((513, 264), 11)])
+    ((9, 4096), 2), ((2, 8192), 1), ((700, 16), 16), ((0, 16), 2), ((3, 192), 4), ((513, 264), 11),
+    ((700, 1000), 8), ((9, 5000), 40), ((3, 8192), 8192), ((650, 24), 24), ((2, 30000), 3)])
 @pytest.mark.parametrize("dtype, silu", [(F32, True), (BF16, False)])
 def test_group_norm_of_tokens(dtype, silu, shape, groups):
     check_group_norm(shape, groups, dtype, silu)
@@ -415,7 +416,8 @@ def test_group_norm_of_tokens(dtype, silu, shape, groups):
 
 @pytest.mark.parametrize("shape, groups", [
     ((2, 2, 8), 8), ((1, 9, 320), 32), ((3, 5, 7, 40), 4), ((2, 1000, 64), 2), ((1, 64, 64, 320), 32), ((40, 3, 16), 1),
-    ((2, 0, 16), 2), ((1, 300, 1032), 3), ((200, 17, 8), 4)])
+    ((2, 0, 16), 2), ((1, 300, 1032), 3), ((200, 17, 8), 4),
+    ((700, 5, 48), 16), ((2, 4099, 24), 24), ((1, 70001, 8), 1), ((3, 33, 2056), 1), ((1, 5000, 520), 5)])
 @pytest.mark.parametrize("dtype, silu", [(F32, True), (BF16, True), (BF16, False)])
 def test_group_norm_of_maps(dtype, silu, shape, groups):
     check_group_norm(shape, groups, dtype, silu)
