@@ -23,7 +23,7 @@ namespace {
 
 constexpr int NT = CONV_NT;
 template <typename T>
-constexpr int BATCH = sizeof(T) == 2 ? 8 : 4;  // rows in flight a thread: 64 bytes of 4 channels
+constexpr int BATCH = sizeof(T) == 2 ? 8 : 4;  // rows of a group of copies, of which a thread's run has four at most
 
 // V channels of a row.
 template <typename T, int V>
@@ -65,6 +65,28 @@ __device__ __forceinline__ void store(void *p, long long row, int vecs, int v, c
     Pack<T, V> r;
     pack(x, r);
     static_cast<Pack<T, V> *>(p)[row * vecs + v] = r;
+}
+
+// An asynchronous copy of a Pack into this thread's slot of shared memory; zeros where it is not live.
+template <typename P>
+__device__ __forceinline__ void fetch(P *dst, const P *src, bool live) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (sizeof(P) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(live ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(src), "r"(live ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most `left` (0 to 3) of the latest groups are under way.
+__device__ __forceinline__ void fetch_wait(int left) {
+    if (left >= 3)
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (left == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (left == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <int W, int V>
@@ -119,9 +141,10 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
         static_cast<Pack<T, V> *>(p.state_T)[e] = r;
         return;
     }
-    extern __shared__ int shared[];
+    extern __shared__ __align__(16) uint8_t shared[];
+    Pack<T, V> *slots = reinterpret_cast<Pack<T, V> *>(shared) + tid;  // row i of this thread's run at [i NT]
     const int subs = NT / lanes, tile = blockIdx.x / cblocks, sub = tid / lanes;
-    int *first = shared, *seq = shared + rows * subs;
+    int *first = reinterpret_cast<int *>(shared + (size_t)rows * NT * sizeof(Pack<T, V>)), *seq = first + rows * subs;
     long long t0 = 0, begin, end, lo = 0;
     int n = 0;
     if (PACKED) {
@@ -154,6 +177,15 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
     }
     const int v = (blockIdx.x % cblocks) * lanes + tid % lanes;
     if (v >= vecs || begin >= end) return;
+    const int count = (int)(end - begin);
+    {
+        const Pack<T, V> *from = static_cast<const Pack<T, V> *>(p.x) + begin * vecs + v;
+        for (int t = 0; t < count; t += BATCH) {
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) fetch(slots + (t + k) * NT, from + (size_t)(t + k < count ? t + k : 0) * vecs, t + k < count);
+            fetch_commit();
+        }
+    }
     float win[W - 1][V];
     // the W - 1 inputs before token t of the sequence n that begins at lo
     auto before = [&](long long t) {
@@ -192,24 +224,16 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
         pack(s, r);
         *to = r;
     };
-    const Pack<T, V> *from = static_cast<const Pack<T, V> *>(p.x) + begin * vecs + v;
     Pack<T, V> *to = static_cast<Pack<T, V> *>(p.y) + begin * vecs + v;
-    const int count = (int)(end - begin);
-    for (int t = 0; t < count; t += BATCH, from += (size_t)BATCH * vecs, to += (size_t)BATCH * vecs) {
-        Pack<T, V> raw[BATCH];
+    int left = (count + BATCH - 1) / BATCH;
+    for (int t = 0; t < count; t += BATCH, to += (size_t)BATCH * vecs) {
+        fetch_wait(--left);
         if (!PACKED && t + BATCH <= count) {  // straight code for whole batches
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) raw[k] = from[(size_t)k * vecs];
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) token(raw[k], to + (size_t)k * vecs);
+            for (int k = 0; k < BATCH; ++k) token(slots[(t + k) * NT], to + (size_t)k * vecs);
             continue;
         }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            raw[k] = Pack<T, V>{};
-            if (t + k < count) raw[k] = from[(size_t)k * vecs];
-        }
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < BATCH; ++k) {
             if (t + k >= count) break;
             if (PACKED) {
@@ -223,17 +247,19 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
                     before(begin + t + k);
                 }
             }
-            token(raw[k], to + (size_t)k * vecs);
+            token(slots[(t + k) * NT], to + (size_t)k * vecs);
         }
     }
 }
 
 // ------------------------------------------------------------------------------------ backward
-// A CTA: `lanes` vectors of 4 channels x NT / lanes runs of CONV_BWD_ROWS places of an extended row, and every
+// A CTA: `lanes` vectors of 4 channels x NT / lanes runs of R places of an extended row (with the W - 1 before them), and every
 // parts-th such tile after it; row_runs runs a row.
 template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, int parts, int row_runs) {
-    constexpr int V = 4, R = CONV_BWD_ROWS, BATCH = efla::BATCH<T>, NT = CONV_BWD_NT;
+    constexpr int V = 4, BATCH = efla::BATCH<T>, NT = CONV_BWD_NT, R = 4 * BATCH, PLACES = R + W - 1;
+    extern __shared__ __align__(16) uint8_t shared[];
+    Pack<T, V> *xs = reinterpret_cast<Pack<T, V> *>(shared) + threadIdx.x, *ys = xs + PLACES * NT;  // place i at [i NT]
     __shared__ float red[NT][V + 1];
     const int tid = threadIdx.x, lane = tid % lanes, sub = tid / lanes, subs = NT / lanes;
     const int cb = blockIdx.x % cblocks, tile = blockIdx.x / cblocks, v = cb * lanes + lane;
@@ -256,10 +282,27 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
             }
             unpack(r, x);
         };
+        // everything of the run, in four groups: token t at place t - (e0 - (W - 1))
+        const int tb0 = e0 - (W - 1), e1 = min(e0 + R, ends);
+        const Pack<T, V> *xrow = static_cast<const Pack<T, V> *>(p.x) + row * vecs + v, *yrow = static_cast<const Pack<T, V> *>(p.dy) + row * vecs + v;
+        const Pack<T, V> *srow = p.state0 ? static_cast<const Pack<T, V> *>(p.state0) + (long long)b * (W - 1) * vecs + v : nullptr;
+        const bool inside = tb0 >= 0 && e1 <= p.T && e1 == e0 + R;  // all of it tokens of the row
+#pragma unroll
+        for (int i = 0; i < PLACES; ++i) {
+            const int t = tb0 + i;
+            if (inside) {
+                fetch(xs + i * NT, xrow + (size_t)t * vecs, true);
+                fetch(ys + i * NT, yrow + (size_t)t * vecs, true);
+            } else {
+                const bool real = t >= 0 && t < p.T, state = t < 0 && t + W - 1 >= 0 && srow;
+                fetch(xs + i * NT, real ? xrow + (size_t)t * vecs : state ? srow + (size_t)(t + W - 1) * vecs : xrow, real || state);
+                fetch(ys + i * NT, real ? yrow + (size_t)t * vecs : yrow, real);
+            }
+            if (i >= W - 1 && (i - (W - 1)) % BATCH == BATCH - 1) fetch_commit();
+        }
         float win[W - 1][V], old[W - 1][V] = {};  // x at t .. t + W - 2 (extended), ds of the W - 1 tokens before t
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) place(e0 - (W - 1) + i, win[i]);
-        const int e1 = min(e0 + R, ends);
         // ds of token t, whose newest input is x, into the window; with `own` into dw and dbias too
         auto token = [&](const float(&x)[V], float(&ds)[V], bool real, bool own) {
 #pragma unroll
@@ -301,22 +344,26 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
                 old[W - 2][c] = ds[c];
             }
         };
-        for (int tb = e0 - (W - 1); tb < e1; tb += BATCH) {  // token t's newest input is at place t + W - 1
-            Pack<T, V> rx[BATCH], rd[BATCH];
-            if (tb >= max(e0, W - 1) && tb + BATCH <= min(e1, p.T)) {  // straight code inside a run
-                const size_t at = (size_t)(row + tb) * vecs + v;
-                const Pack<T, V> *xs = static_cast<const Pack<T, V> *>(p.x) + at, *ys = static_cast<const Pack<T, V> *>(p.dy) + at;
-                Pack<T, V> *to = static_cast<Pack<T, V> *>(p.dx) + at - (size_t)(W - 1) * vecs;
+        if (inside) {
+            fetch_wait(3);
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    rx[k] = xs[(size_t)k * vecs];
-                    rd[k] = ys[(size_t)k * vecs];
-                }
+            for (int i = 0; i < W - 1; ++i) {  // the tokens before the run: their ds
+                float x[V], ds[V];
+                unpack(xs[i * NT], x);
+                unpack(ys[i * NT], ds);
+                token(x, ds, true, false);
+                shift(x, ds);
+            }
+            Pack<T, V> *to = static_cast<Pack<T, V> *>(p.dx) + (size_t)(row + tb0) * vecs + v;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q, to += (size_t)BATCH * vecs) {
+                fetch_wait(3 - q);
+                const Pack<T, V> *xq = xs + (W - 1 + q * BATCH) * NT, *yq = ys + (W - 1 + q * BATCH) * NT;
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
                     float x[V], ds[V], d[V] = {};
-                    unpack(rx[k], x);
-                    unpack(rd[k], ds);
+                    unpack(xq[k * NT], x);
+                    unpack(yq[k * NT], ds);
                     token(x, ds, true, true);
                     place_sum(ds, d);
                     shift(x, ds);
@@ -324,40 +371,26 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
                     pack(d, r);
                     to[(size_t)k * vecs] = r;
                 }
-                continue;
             }
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int t = tb + k;
-                rx[k] = rd[k] = Pack<T, V>{};
-                if (t < e1) {
-                    if (t >= 0 && t < p.T) {
-                        rx[k] = load<T, V>(p.x, row + t, vecs, v);
-                        rd[k] = load<T, V>(p.dy, row + t, vecs, v);
-                    } else if (t < 0 && t + W - 1 >= 0 && p.state0) {
-                        rx[k] = load<T, V>(p.state0, (long long)b * (W - 1) + t + W - 1, vecs, v);
-                    }
-                }
+            continue;
+        }
+        fetch_wait(0);
+#pragma unroll 1
+        for (int t = tb0; t < e1; ++t) {  // token t's newest input is at place t + W - 1 of the extended row
+            float x[V], ds[V];
+            unpack(xs[(t - tb0) * NT], x);
+            unpack(ys[(t - tb0) * NT], ds);  // 0 outside the row
+            token(x, ds, t >= 0 && t < p.T, t >= e0);
+            if (t >= e0) {
+                float d[V] = {};
+                if (p.dstate_T && t >= p.T) unpack(load<T, V>(p.dstate_T, (long long)b * (W - 1) + t - p.T, vecs, v), d);
+                place_sum(ds, d);
+                if (t >= W - 1)
+                    store<T, V>(p.dx, row + t - (W - 1), vecs, v, d);
+                else if (p.dstate0)
+                    store<T, V>(p.dstate0, (long long)b * (W - 1) + t, vecs, v, d);
             }
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int t = tb + k;
-                if (t >= e1) break;
-                float x[V], ds[V];
-                unpack(rx[k], x);
-                unpack(rd[k], ds);  // 0 outside the row
-                token(x, ds, t >= 0 && t < p.T, t >= e0);
-                if (t >= e0) {
-                    float d[V] = {};
-                    if (p.dstate_T && t >= p.T) unpack(load<T, V>(p.dstate_T, (long long)b * (W - 1) + t - p.T, vecs, v), d);
-                    place_sum(ds, d);
-                    if (t >= W - 1)
-                        store<T, V>(p.dx, row + t - (W - 1), vecs, v, d);
-                    else if (p.dstate0)
-                        store<T, V>(p.dstate0, (long long)b * (W - 1) + t, vecs, v, d);
-                }
-                shift(x, ds);
-            }
+            shift(x, ds);
         }
     }
     // the CTA's sums over its runs, in order: [D][W] then [D] of part `tile`
@@ -422,37 +455,49 @@ __global__ void __launch_bounds__(STEP_NT) conv_step_kernel(ConvArgs p, int vecs
     }
 }
 
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+}
+
 template <typename T, int W>
 cudaError_t fwd(const ConvArgs &a) {
     constexpr int V = 4;
     const int vecs = a.D / V, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes, subs = NT / lanes;
-    // Tokens a thread: 32 (3 rows of halo in 35) where that still leaves two CTAs a SM, down to 8.
+    // Tokens a thread: four batches (3 rows of halo in 32 or 16) where that still leaves two CTAs a SM, down to 8.
     const long long tokens = (long long)a.B * a.T;
-    int rows = 32;
+    int rows = 4 * BATCH<T>;
     while (rows > 8 && tokens * vecs < 2LL * 152 * NT * rows) rows /= 2;
     const int row_runs = (a.T + rows - 1) / rows;
     const long long runs = a.cu_seqlens ? (tokens + rows - 1) / rows : (long long)a.B * row_runs;
     const long long work = (runs + subs - 1) / subs * cblocks;
     const long long copies = a.state_T ? ((long long)a.N * (W - 1) * vecs + NT - 1) / NT : 0;
     if (work + copies == 0) return cudaSuccess;
+    const size_t slots = (size_t)rows * NT * sizeof(Pack<T, V>);
     auto go = [&](auto kernel, size_t smem) {
+        const cudaError_t e = allow_smem(kernel, smem);
+        if (e != cudaSuccess) return e;
         kernel<<<(unsigned)(work + copies), NT, smem, a.stream>>>(a, vecs, lanes, cblocks, (unsigned)work, rows, row_runs);
+        return cudaGetLastError();
     };
     if (a.cu_seqlens)
-        go(a.silu ? conv_fwd_kernel<T, V, W, true, true> : conv_fwd_kernel<T, V, W, true, false>, 2 * rows * subs * sizeof(int));
-    else
-        go(a.silu ? conv_fwd_kernel<T, V, W, false, true> : conv_fwd_kernel<T, V, W, false, false>, 0);
-    return cudaGetLastError();
+        return go(a.silu ? conv_fwd_kernel<T, V, W, true, true> : conv_fwd_kernel<T, V, W, true, false>,
+                  slots + 2 * rows * subs * sizeof(int));
+    return go(a.silu ? conv_fwd_kernel<T, V, W, false, true> : conv_fwd_kernel<T, V, W, false, false>, slots);
 }
 template <typename T, int W>
 cudaError_t bwd(const ConvArgs &a) {
     const int vecs = a.D / 4, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes;
-    const int parts = conv_bwd_parts(a.B, a.T, a.D, a.W);
+    constexpr int RUN = 4 * BATCH<T>, PLACES = RUN + W - 1;  // RUN == conv_bwd_run(a.dtype)
+    const int parts = conv_bwd_parts(a.B, a.T, a.D, a.W, RUN);
+    const size_t smem = (size_t)2 * PLACES * CONV_BWD_NT * sizeof(Pack<T, 4>);
     auto go = [&](auto kernel) {
-        kernel<<<(unsigned)parts * cblocks, CONV_BWD_NT, 0, a.stream>>>(a, vecs, lanes, cblocks, parts, conv_bwd_runs(a.T, a.W));
+        const cudaError_t e = allow_smem(kernel, smem);
+        if (e != cudaSuccess) return e;
+        kernel<<<(unsigned)parts * cblocks, CONV_BWD_NT, smem, a.stream>>>(a, vecs, lanes, cblocks, parts, conv_bwd_runs(a.T, a.W, RUN));
+        return cudaGetLastError();
     };
-    go(a.silu ? conv_bwd_kernel<T, W, true> : conv_bwd_kernel<T, W, false>);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = go(a.silu ? conv_bwd_kernel<T, W, true> : conv_bwd_kernel<T, W, false>);
     if (e != cudaSuccess) return e;
     return launch_sum_parts(a.ws, parts, a.D * (a.dbias ? W + 1 : W), a.dw, a.dbias, a.D * W, a.stream);
 }

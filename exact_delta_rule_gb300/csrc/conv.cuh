@@ -30,15 +30,17 @@ inline int conv_lanes(int vecs) {
     while (n < vecs && n < 32) n *= 2;
     return n;
 }
-// Threads a CTA; of the backward, and the places of its runs.
-constexpr int CONV_NT = 256, CONV_BWD_NT = 128, CONV_BWD_ROWS = 37;
-// Runs of CONV_BWD_ROWS places of a row extended by the W - 1 of its state, and the CTAs a block of channels that
-// share them: all that there are up to six a SM.
-inline int conv_bwd_runs(int T, int W) { return (int)(((long long)T + W - 1 + CONV_BWD_ROWS - 1) / CONV_BWD_ROWS); }
-inline int conv_bwd_parts(int B, int T, int D, int W) {
+constexpr int CONV_NT = 256, CONV_BWD_NT = 128;  // threads a CTA; of the backward
+// Runs of `run` places of a row extended by the W - 1 of its state, and the CTAs a block of channels that share them:
+// one a tile of runs, or as many as are resident at once (three a SM).
+inline int conv_bwd_run(efla_dtype t) { return t == EFLA_BF16 ? 32 : 16; }
+inline int conv_bwd_runs(int T, int W, int run) { return (int)(((long long)T + W - 1 + run - 1) / run); }
+inline int conv_bwd_parts(int B, int T, int D, int W, int run) {
     const int vecs = D / 4, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes, subs = CONV_BWD_NT / lanes;
-    const long long tiles = ((long long)B * conv_bwd_runs(T, W) + subs - 1) / subs, most = 152 * 6 / cblocks;
-    return (int)std::max(1LL, std::min(tiles, most));
+    const long long tiles = ((long long)B * conv_bwd_runs(T, W, run) + subs - 1) / subs, most = std::max(1, 152 * 3 / cblocks);
+    if (tiles <= most) return (int)std::max(1LL, tiles);
+    const long long each = (tiles + most - 1) / most;  // (the same number for nearly all)
+    return (int)((tiles + each - 1) / each);
 }
 
 cudaError_t launch_conv(const ConvArgs &a);

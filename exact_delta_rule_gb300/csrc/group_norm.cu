@@ -27,9 +27,11 @@ __device__ __forceinline__ float dact(float s, int silu) {
 template <int V>
 __device__ __forceinline__ void affine(const GroupNormArgs &p, int c0, float (&w)[V], float (&b)[V]) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        w[e] = p.w ? p.w[c0 + e] : 1.f;
-        b[e] = p.b ? p.b[c0 + e] : 0.f;
+    for (int e = 0; e < V; e += 4) {
+        const float4 ww = p.w ? *reinterpret_cast<const float4 *>(p.w + c0 + e) : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float4 bb = p.b ? *reinterpret_cast<const float4 *>(p.b + c0 + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        w[e] = ww.x, w[e + 1] = ww.y, w[e + 2] = ww.z, w[e + 3] = ww.w;
+        b[e] = bb.x, b[e + 1] = bb.y, b[e + 2] = bb.z, b[e + 3] = bb.w;
     }
 }
 
@@ -563,7 +565,7 @@ cudaError_t warps(const GroupNormArgs &a) {
 template <typename T, bool BWD>
 cudaError_t whole(const GroupNormArgs &a) {
     const int team = gn_team(a.C / a.G / Vec<T>::N), blocks = gn_blocks(a.C, a.G, a.dtype);
-    const int parts = BWD ? gn_row_parts(a.rows, a.C, a.G, a.dtype) : (a.rows + 31) / 32;
+    const int parts = BWD ? gn_row_parts(a.rows, a.C, a.G, a.dtype) : (a.rows + 63) / 64;
     auto go = [&](auto kernel) {
         kernel<<<(unsigned)parts * blocks, NT, 0, a.stream>>>(a, blocks, parts);
         return cudaGetLastError();

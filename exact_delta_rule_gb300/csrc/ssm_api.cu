@@ -105,7 +105,8 @@ efla_status efla_causal_conv_bwd_workspace(int B, int T, int D, int W, size_t *b
     if (!bytes) return api_fail(EFLA_ERR_INVALID_ARG, "bytes must be non-NULL");
     const efla_status s = check_conv(B, T, D, W, EFLA_F32, EFLA_ACT_NONE);
     if (s != EFLA_OK) return s;
-    *bytes = (size_t)conv_bwd_parts(B, T, D, W) * D * (W + 1) * sizeof(float);
+    const int parts = std::max(conv_bwd_parts(B, T, D, W, conv_bwd_run(EFLA_BF16)), conv_bwd_parts(B, T, D, W, conv_bwd_run(EFLA_F32)));
+    *bytes = (size_t)parts * D * (W + 1) * sizeof(float);
     return api_ok();
 }
 

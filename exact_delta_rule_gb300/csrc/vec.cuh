@@ -44,8 +44,9 @@ struct Vec<__nv_bfloat16> {
 
 // 1 / (1 + e^{-x}) to 2 + 1.2 |x| ulp, as the output gate's; 0 for -infinity.
 __device__ __forceinline__ float quick_sigmoid(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + __expf(-x)));
+    float e, y;  // (flushing denormals is exact here and saves the scaling around both instructions)
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-x * 1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + e));
     return y;
 }
 
