@@ -330,7 +330,7 @@ def test_c_group_norm_refuses(lib):
 
     for kw in (dict(rows=-1), dict(L=-1), dict(C=0), dict(groups=0), dict(groups=5), dict(dt=2), dict(act=-1), dict(eps=-1.0),
                dict(eps=float("nan")), dict(x=None), dict(y=None), dict(w=A[1] + 4), dict(y=A[0] + 16), dict(stats=A[0]),
-               dict(ws=A[3])):
+               dict(L=30000, wb=1 << 28, ws=A[3]), dict(L=30000, wb=16), dict(L=30000, ws=None)):
         assert fwd(**kw) == 1, kw
     assert fwd(rows=0, x=None, y=None) == 0
 

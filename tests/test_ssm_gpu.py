@@ -417,7 +417,8 @@ def test_group_norm_of_tokens(dtype, silu, shape, groups):
 @pytest.mark.parametrize("shape, groups", [
     ((2, 2, 8), 8), ((1, 9, 320), 32), ((3, 5, 7, 40), 4), ((2, 1000, 64), 2), ((1, 64, 64, 320), 32), ((40, 3, 16), 1),
     ((2, 0, 16), 2), ((1, 300, 1032), 3), ((200, 17, 8), 4),
-    ((700, 5, 48), 16), ((2, 4099, 24), 24), ((1, 70001, 8), 1), ((3, 33, 2056), 1), ((1, 5000, 520), 5)])
+    ((700, 5, 48), 16), ((2, 4099, 24), 24), ((1, 70001, 8), 1), ((3, 33, 2056), 1), ((1, 5000, 520), 5),
+    ((2, 30000, 64), 2)])
 @pytest.mark.parametrize("dtype, silu", [(F32, True), (BF16, True), (BF16, False)])
 def test_group_norm_of_maps(dtype, silu, shape, groups):
     check_group_norm(shape, groups, dtype, silu)
