@@ -36,16 +36,27 @@ struct Back {
     static constexpr int SMEM = RED + WARPS * TOK * 2 * N * 4;
 };
 
-// Sums of v[0..3] over L lanes, `stride` apart; for L >= 4 the lane has that of v[its number's two upper bits] in v[0],
-// for L = 2 those of v[2 bit], v[2 bit + 1] in v[0], v[1], for L = 1 all four.
+// Two neighbouring channels.
+__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
+    const uint32_t r = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+}
+__device__ __forceinline__ void store2(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float2 v) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+
+// Sums of four values over L lanes, `stride` apart.  A lane has them in slots: slots 0, 1 are the values 2 b, 2 b + 1 with b
+// the uppermost bit of the lane's number among the L, slots 2, 3 the other two (L = 1: in order) - so that a lane
+// keeps slots 0, 1 and hands over 2, 3 without selecting.  For L >= 4 the lane ends with that value in v[0] that the two
+// upper bits of its number name, for L = 2 with two in v[0], v[1], for L = 1 with all four.
 template <int L, int STRIDE>
 __device__ __forceinline__ void reduce4(float (&v)[4], int lane) {
     if (L >= 2) {
         constexpr int M = L / 2 * STRIDE;
-        const bool up = lane & M;
-        const float s0 = up ? v[0] : v[2], s1 = up ? v[1] : v[3], k0 = up ? v[2] : v[0], k1 = up ? v[3] : v[1];
-        v[0] = k0 + __shfl_xor_sync(0xffffffffu, s0, M);
-        v[1] = k1 + __shfl_xor_sync(0xffffffffu, s1, M);
+        v[0] += __shfl_xor_sync(0xffffffffu, v[2], M);
+        v[1] += __shfl_xor_sync(0xffffffffu, v[3], M);
     }
     if (L >= 4) {
         constexpr int M = L / 4 * STRIDE;
@@ -88,9 +99,11 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
     const int bc_at = 4 * nq + (CG >= 4 ? reduced_index<CG < 4 ? 4 : CG, LN>(lane) : CG == 2 ? 2 * cg : 0);
     const int ch_at = ch + reduced_index<LN, 1>(lane);
 
-    // entry (pair q of channels, i): channels c0 + ch + 2 q, + 1, entry 4 nq + i
+    // the slots' order (reduce4): pair q of channels is ch + 2 (q ^ cflip), + 1; slot i of entries is 4 nq + (i ^ 2 nflip)
+    const int cflip = lane / (LN / 2) & 1, nflip = CG >= 2 ? lane / ((CG >= 2 ? CG / 2 : 1) * LN) & 1 : 0;
     float2 rate[2][4], l[2][4], dA[2][4];
-    auto entry = [&](const float *base, int c, int i) { return base[(size_t)(c0 + ch + c) * N + 4 * nq + i]; };
+    auto place = [&](int c, int i) { return (size_t)(c0 + ch + (c ^ 2 * cflip)) * N + 4 * nq + (i ^ 2 * nflip); };
+    auto entry = [&](const float *base, int c, int i) { return base[place(c, i)]; };
     const float *l0 = f.seg ? f.state + slot * dn : p.dS_T ? p.dS_T + span.seq * dn : nullptr;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
@@ -100,12 +113,13 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
             l[q][i] = live && l0 ? make_float2(entry(l0, 2 * q, i), entry(l0, 2 * q + 1, i)) : make_float2(0.f, 0.f);
             dA[q][i] = make_float2(0.f, 0.f);
         }
-    // elementwise work, a warp on its own channels: channel ec of the tile, tokens et, et + 32 / CW, ..
-    constexpr int CW = CT / WARPS;
-    const int ec = warp * CW + lane % CW, et = lane / CW, ed = c0 + ec;
+    // elementwise work, a warp on its own channels: channels ec, ec + 1 of the tile, tokens et, et + TSTEP, ..
+    constexpr int CW = CT / WARPS, TSTEP = 64 / CW;
+    const int ec = warp * CW + 2 * (lane % (CW / 2)), et = lane / (CW / 2), ed = c0 + ec;
     const bool elive = ec < have;
-    const float bias = elive && f.dt_bias ? f.dt_bias[ed] : 0.f, skip = elive && f.Dskip ? f.Dskip[ed] : 0.f;
-    float sum_D = 0.f, sum_dt = 0.f;
+    float2 bias = make_float2(0.f, 0.f), skip = bias, sum_D = bias, sum_dt = bias;
+    if (elive && f.dt_bias) bias = *reinterpret_cast<const float2 *>(f.dt_bias + ed);
+    if (elive && f.Dskip) skip = *reinterpret_cast<const float2 *>(f.Dskip + ed);
 
     const size_t esz = sizeof(T), pitch = f.D * esz, bpitch = (size_t)f.G * N * esz;
     auto at_tile = [&](const void *base) { return static_cast<const uint8_t *>(base) + (size_t)c0 * esz; };
@@ -155,19 +169,20 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
         __syncthreads();  // the chunk's inputs are here, the one before is done with
         load(s - 1);
         if (s + 1 < chunks) sum_warps(t0 + TOK);
-        auto in = [&](int what, int t) { return to_f32(reinterpret_cast<const T *>(st + what)[t * CT + ec]); };
+        auto in = [&](int what, int t) { return load2(reinterpret_cast<const T *>(st + what) + t * CT + ec); };
+        auto at = [&](float *base, int t) { return reinterpret_cast<float2 *>(base + t * CT + ec); };
 #pragma unroll 4
-        for (int t = et; t < TOK; t += 32 / CW) {  // past the row's end: a token that changes nothing
+        for (int t = et; t < TOK; t += TSTEP) {  // past the row's end: a token that changes nothing
             const bool real = t < count;
-            const float delta = real ? softplus(in(K::DT, t) + bias) : 0.f;
-            float g = real ? in(K::DY, t) : 0.f;
+            float2 delta = softplus2(__fadd2_rn(in(K::DT, t), bias)), g = in(K::DY, t);
             if (f.z) {
-                const float z = in(K::Z, t);
-                g *= z * ssm_sigmoid(z);
+                const float2 z = in(K::Z, t);
+                g = __fmul2_rn(g, __fmul2_rn(z, make_float2(ssm_sigmoid(z.x), ssm_sigmoid(z.y))));
             }
-            delta_s[t * CT + ec] = delta;
-            u_s[t * CT + ec] = real ? delta * in(K::X, t) : 0.f;
-            g_s[t * CT + ec] = g;
+            if (!real) delta = g = make_float2(0.f, 0.f);
+            *at(delta_s, t) = delta;
+            *at(u_s, t) = __fmul2_rn(delta, in(K::X, t));
+            *at(g_s, t) = g;
         }
 #pragma unroll
         for (int k = 0; k < TOK * N / NT; ++k) {
@@ -179,12 +194,11 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
         __syncthreads();
         // four values of channels ch .. ch + 3 as two pairs; four entries of B or C, each twice
         auto quad = [&](const float *base, int t, float2(&v)[2]) {
-            const float4 r = *reinterpret_cast<const float4 *>(base + t * CT + ch);
-            v[0] = make_float2(r.x, r.y);
-            v[1] = make_float2(r.z, r.w);
+            v[0] = *reinterpret_cast<const float2 *>(base + t * CT + ch + 2 * cflip);
+            v[1] = *reinterpret_cast<const float2 *>(base + t * CT + ch + 2 * (cflip ^ 1));
         };
         auto four = [&](const float4 *base, int t, float2(&v)[4]) {
-            const float4 r0 = base[t * (N / 2) + 2 * nq], r1 = base[t * (N / 2) + 2 * nq + 1];
+            const float4 r0 = base[t * (N / 2) + 2 * nq + nflip], r1 = base[t * (N / 2) + 2 * nq + (nflip ^ 1)];
             v[0] = make_float2(r0.x, r0.y);
             v[1] = make_float2(r0.z, r0.w);
             v[2] = make_float2(r1.x, r1.y);
@@ -321,21 +335,23 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
         __syncwarp();
         if (elive) {
 #pragma unroll 4
-            for (int t = et; t < count; t += 32 / CW) {
-                const float x = in(K::X, t), dt = in(K::DT, t) + bias, delta = delta_s[t * CT + ec];
-                const float du = u_s[t * CT + ec], dd = fmaf(du, x, LN2 * g_s[t * CT + ec]);
-                float g = in(K::DY, t);
-                const size_t at = (size_t)(t0 + t) * f.D + ed;
+            for (int t = et; t < count; t += TSTEP) {
+                const float2 x = in(K::X, t), dt = __fadd2_rn(in(K::DT, t), bias), du = *at(u_s, t), dd = *at(g_s, t);
+                float2 g = in(K::DY, t);
+                const size_t to = (size_t)(t0 + t) * f.D + ed;
                 if (f.z) {
-                    const float z = in(K::Z, t), sg = ssm_sigmoid(z), y = fmaf(skip, x, y_s[t * CT + ec]);
-                    static_cast<T *>(p.dz)[at] = from_f32<T>(g * y * sg * fmaf(z, 1.f - sg, 1.f));
-                    g *= z * sg;
+                    const float2 z = in(K::Z, t), y = __ffma2_rn(skip, x, *at(y_s, t)), sg = make_float2(ssm_sigmoid(z.x), ssm_sigmoid(z.y));
+                    const float2 slope = __fmul2_rn(sg, make_float2(fmaf(z.x, 1.f - sg.x, 1.f), fmaf(z.y, 1.f - sg.y, 1.f)));
+                    store2(static_cast<T *>(p.dz) + to, __fmul2_rn(__fmul2_rn(g, y), slope));
+                    g = __fmul2_rn(g, __fmul2_rn(z, sg));
                 }
-                const float ddt = dd * ssm_sigmoid(dt);
-                static_cast<T *>(p.dx)[at] = from_f32<T>(fmaf(du, delta, skip * g));
-                static_cast<T *>(p.ddt)[at] = from_f32<T>(ddt);
-                sum_D = fmaf(g, x, sum_D);
-                sum_dt += ddt;
+                // ddelta = ln2 (w . rate) + du x
+                const float2 ddelta = __ffma2_rn(du, x, make_float2(LN2 * dd.x, LN2 * dd.y));
+                const float2 ddt = __fmul2_rn(ddelta, make_float2(ssm_sigmoid(dt.x), ssm_sigmoid(dt.y)));
+                store2(static_cast<T *>(p.dx) + to, __ffma2_rn(du, *at(delta_s, t), __fmul2_rn(skip, g)));
+                store2(static_cast<T *>(p.ddt) + to, ddt);
+                sum_D = __ffma2_rn(g, x, sum_D);
+                sum_dt = __fadd2_rn(sum_dt, ddt);
             }
         }
     }
@@ -346,7 +362,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const size_t e = (size_t)(c0 + ch + 2 * q) * N + 4 * nq + i;
+                const size_t e = place(2 * q, i);
                 out[e] = LN2 * rate[q][i].x * dA[q][i].x;
                 out[e + N] = LN2 * rate[q][i].y * dA[q][i].y;
                 if (first) {
@@ -358,13 +374,15 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
     __syncthreads();
     if (chunks > 0) sum_warps(span.lo);
 #pragma unroll
-    for (int m = CW; m < 32; m <<= 1) {
-        sum_D += __shfl_xor_sync(0xffffffffu, sum_D, m);
-        sum_dt += __shfl_xor_sync(0xffffffffu, sum_dt, m);
+    for (int m = CW / 2; m < 32; m <<= 1) {
+        sum_D.x += __shfl_xor_sync(0xffffffffu, sum_D.x, m);
+        sum_D.y += __shfl_xor_sync(0xffffffffu, sum_D.y, m);
+        sum_dt.x += __shfl_xor_sync(0xffffffffu, sum_dt.x, m);
+        sum_dt.y += __shfl_xor_sync(0xffffffffu, sum_dt.y, m);
     }
     if (elive && et == 0) {
-        p.sums2[(size_t)slot * 2 * f.D + ed] = sum_D;
-        p.sums2[(size_t)slot * 2 * f.D + f.D + ed] = sum_dt;
+        *reinterpret_cast<float2 *>(p.sums2 + (size_t)slot * 2 * f.D + ed) = sum_D;
+        *reinterpret_cast<float2 *>(p.sums2 + (size_t)slot * 2 * f.D + f.D + ed) = sum_dt;
     }
 }
 
