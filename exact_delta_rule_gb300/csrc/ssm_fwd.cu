@@ -391,8 +391,14 @@ cudaError_t states(const SsmArgs &a) {
 
 // ------------------------------------------------------------------------------------ one token
 // HBM bound: the state is read and written once (8 N bytes a channel; everything else is a few).  A thread has four
-// entries of one channel's state and takes ROWS sequences, so that the rates are computed once for them.
+// entries of one channel's state and takes ROWS sequences, so that the rates are computed once for them; all that it
+// reads is under way before the first is used.
 constexpr int STEP_NT = 128;
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 r = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+}
 template <typename T, int N, int ROWS>
 __global__ void __launch_bounds__(STEP_NT) ssm_step_kernel(SsmArgs p) {
     constexpr int LN = N / 4, CT = STEP_NT / LN;
@@ -400,36 +406,37 @@ __global__ void __launch_bounds__(STEP_NT) ssm_step_kernel(SsmArgs p) {
     const int d = blockIdx.x % blocks * CT + tid / LN, b0 = blockIdx.x / blocks * ROWS;
     const bool live = d < p.D;
     const int dd = live ? d : p.D - 1, each = p.D / p.G, g = dd / each;
-    float4 h[ROWS];
+    float4 h[ROWS], B[ROWS], C[ROWS];
+    float x[ROWS], dt[ROWS], z[ROWS];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-        if (b0 + r < p.B) h[r] = *reinterpret_cast<const float4 *>(p.S0 + ((size_t)(b0 + r) * p.D + dd) * N + 4 * l);
+    for (int r = 0; r < ROWS; ++r) {
+        const int b = min(b0 + r, p.B - 1);  // (a row past the last: the last again, not written)
+        const size_t e = (size_t)b * p.D + dd, m = ((size_t)b * p.G + g) * N + 4 * l;
+        h[r] = *reinterpret_cast<const float4 *>(p.S0 + e * N + 4 * l);
+        B[r] = load4(static_cast<const T *>(p.Bm) + m);
+        C[r] = load4(static_cast<const T *>(p.Cm) + m);
+        x[r] = to_f32(static_cast<const T *>(p.x)[e]);
+        dt[r] = to_f32(static_cast<const T *>(p.dt)[e]);
+        z[r] = p.z ? to_f32(static_cast<const T *>(p.z)[e]) : 0.f;
+    }
     const float4 al = *reinterpret_cast<const float4 *>(p.A_log + (size_t)dd * N + 4 * l);
     const float rate[4] = {ssm_rate(al.x), ssm_rate(al.y), ssm_rate(al.z), ssm_rate(al.w)};
     const float bias = p.dt_bias ? p.dt_bias[dd] : 0.f, skip = p.Dskip ? p.Dskip[dd] : 0.f;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        const int b = b0 + r;
-        if (b >= p.B) break;
-        const size_t e = (size_t)b * p.D + dd, m = ((size_t)b * p.G + g) * N + 4 * l;
-        const float x = to_f32(static_cast<const T *>(p.x)[e]);
-        const float delta = softplus(to_f32(static_cast<const T *>(p.dt)[e]) + bias), u = delta * x;
-        const T *B = static_cast<const T *>(p.Bm) + m, *C = static_cast<const T *>(p.Cm) + m;
-        float hv[4] = {h[r].x, h[r].y, h[r].z, h[r].w}, y = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            hv[i] = fmaf(ssm_ex2(delta * rate[i]), hv[i], u * to_f32(B[i]));
-            y = fmaf(hv[i], to_f32(C[i]), y);
-        }
+        const float delta = softplus(dt[r] + bias), u = delta * x[r];
+        h[r].x = fmaf(ssm_ex2(delta * rate[0]), h[r].x, u * B[r].x);
+        h[r].y = fmaf(ssm_ex2(delta * rate[1]), h[r].y, u * B[r].y);
+        h[r].z = fmaf(ssm_ex2(delta * rate[2]), h[r].z, u * B[r].z);
+        h[r].w = fmaf(ssm_ex2(delta * rate[3]), h[r].w, u * B[r].w);
+        float y = fmaf(h[r].x, C[r].x, h[r].y * C[r].y) + fmaf(h[r].z, C[r].z, h[r].w * C[r].w);
 #pragma unroll
         for (int off = 1; off < LN; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-        y = fmaf(skip, x, y);
-        if (p.z) {
-            const float z = to_f32(static_cast<const T *>(p.z)[e]);
-            y *= z * ssm_sigmoid(z);
-        }
-        if (live) {
-            *reinterpret_cast<float4 *>(p.S_T + e * N + 4 * l) = make_float4(hv[0], hv[1], hv[2], hv[3]);
+        y = fmaf(skip, x[r], y);
+        if (p.z) y *= z[r] * ssm_sigmoid(z[r]);
+        if (live && b0 + r < p.B) {
+            const size_t e = (size_t)(b0 + r) * p.D + dd;
+            *reinterpret_cast<float4 *>(p.S_T + e * N + 4 * l) = h[r];
             if (l == 0) static_cast<T *>(p.y)[e] = from_f32<T>(y);
         }
     }
