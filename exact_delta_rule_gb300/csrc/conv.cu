@@ -257,52 +257,63 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
 // parts-th such tile after it; row_runs runs a row.
 template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, int parts, int row_runs) {
-    constexpr int V = 4, BATCH = efla::BATCH<T>, NT = CONV_BWD_NT, R = 4 * BATCH, PLACES = R + W - 1;
+    constexpr int V = 4, BATCH = efla::BATCH<T>, NT = CONV_BWD_NT, R = 4 * BATCH;
     extern __shared__ __align__(16) uint8_t shared[];
-    Pack<T, V> *xs = reinterpret_cast<Pack<T, V> *>(shared) + threadIdx.x, *ys = xs + PLACES * NT;  // place i at [i NT]
-    __shared__ float red[NT][V + 1];
+    constexpr int XS = R + 2 * (W - 1);  // slots of x: tokens from e0 - 2 (W - 1) on; of dy: from e0 - (W - 1) on
+    Pack<T, V> *xs = reinterpret_cast<Pack<T, V> *>(shared) + threadIdx.x, *ys = xs + XS * NT;  // slot i at [i NT]
     const int tid = threadIdx.x, lane = tid % lanes, sub = tid / lanes, subs = NT / lanes;
     const int cb = blockIdx.x % cblocks, tile = blockIdx.x / cblocks, v = cb * lanes + lane;
-    const long long runs = (long long)p.B * row_runs;
+    const long long runs = (long long)p.B * row_runs, step = (long long)parts * subs;
     const int ends = p.T + W - 1;
     float dw[V][W] = {}, db[V] = {};
     Taps<W, V> taps;
     if (v < vecs) taps.load(p, v * V);
-    for (long long run = (long long)tile * subs + sub; v < vecs && run < runs; run += (long long)parts * subs) {
-        const int b = (int)(run / row_runs);
-        const int e0 = (int)(run % row_runs) * R;
-        const long long row = (long long)b * p.T;
-        // x at place e of the extended row
-        auto place = [&](int e, float(&x)[V]) {
-            Pack<T, V> r{};
-            if (e >= W - 1) {
-                if (e < ends) r = load<T, V>(p.x, row + e - (W - 1), vecs, v);
-            } else if (e >= 0 && p.state0) {
-                r = load<T, V>(p.state0, (long long)b * (W - 1) + e, vecs, v);
-            }
-            unpack(r, x);
-        };
-        // everything of the run, in four groups: token t at place t - (e0 - (W - 1))
-        const int tb0 = e0 - (W - 1), e1 = min(e0 + R, ends);
-        const Pack<T, V> *xrow = static_cast<const Pack<T, V> *>(p.x) + row * vecs + v, *yrow = static_cast<const Pack<T, V> *>(p.dy) + row * vecs + v;
-        const Pack<T, V> *srow = p.state0 ? static_cast<const Pack<T, V> *>(p.state0) + (long long)b * (W - 1) * vecs + v : nullptr;
-        const bool inside = tb0 >= 0 && e1 <= p.T && e1 == e0 + R;  // all of it tokens of the row
+    // Group q of a run's copies: its batch q, and the first with what comes before it.  A group is fetched for the next
+    // run as soon as this one is done with its slots, so three are always under way behind the one that is needed.
+    auto fetch_group = [&](long long run, int q) {
+        if (v < vecs && run < runs) {
+            const int b = (int)(run / row_runs), e0 = (int)(run % row_runs) * R;
+            const long long at = (long long)b * p.T * vecs + v;
+            const Pack<T, V> *x = static_cast<const Pack<T, V> *>(p.x) + at, *y = static_cast<const Pack<T, V> *>(p.dy) + at;
+            if (e0 >= 2 * (W - 1) && e0 + R <= p.T) {
+                x += (long long)(e0 + q * BATCH) * vecs;
+                y += (long long)(e0 + q * BATCH) * vecs;
+                if (q == 0) {
 #pragma unroll
-        for (int i = 0; i < PLACES; ++i) {
-            const int t = tb0 + i;
-            if (inside) {
-                fetch(xs + i * NT, xrow + (size_t)t * vecs, true);
-                fetch(ys + i * NT, yrow + (size_t)t * vecs, true);
+                    for (int i = 0; i < 2 * (W - 1); ++i) fetch(xs + i * NT, x + (long long)(i - 2 * (W - 1)) * vecs, true);
+#pragma unroll
+                    for (int i = 0; i < W - 1; ++i) fetch(ys + i * NT, y + (long long)(i - (W - 1)) * vecs, true);
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    fetch(xs + (2 * (W - 1) + q * BATCH + k) * NT, x + (size_t)k * vecs, true);
+                    fetch(ys + (W - 1 + q * BATCH + k) * NT, y + (size_t)k * vecs, true);
+                }
             } else {
-                const bool real = t >= 0 && t < p.T, state = t < 0 && t + W - 1 >= 0 && srow;
-                fetch(xs + i * NT, real ? xrow + (size_t)t * vecs : state ? srow + (size_t)(t + W - 1) * vecs : xrow, real || state);
-                fetch(ys + i * NT, real ? yrow + (size_t)t * vecs : yrow, real);
+                const Pack<T, V> *state = p.state0 ? static_cast<const Pack<T, V> *>(p.state0) + (long long)b * (W - 1) * vecs + v : nullptr;
+                const int from = q == 0 ? 0 : 2 * (W - 1) + q * BATCH, to = 2 * (W - 1) + (q + 1) * BATCH;
+#pragma unroll 1
+                for (int i = from; i < to; ++i) {
+                    const int t = e0 - 2 * (W - 1) + i, j = i - (W - 1);
+                    const bool real = t >= 0 && t < p.T, old = t < 0 && t + W - 1 >= 0 && state;
+                    fetch(xs + i * NT, real ? x + (size_t)t * vecs : old ? state + (size_t)(t + W - 1) * vecs : x, real || old);
+                    if (j >= 0) fetch(ys + j * NT, real ? y + (size_t)t * vecs : y, real);
+                }
             }
-            if (i >= W - 1 && (i - (W - 1)) % BATCH == BATCH - 1) fetch_commit();
         }
-        float win[W - 1][V], old[W - 1][V] = {};  // x at t .. t + W - 2 (extended), ds of the W - 1 tokens before t
+        fetch_commit();
+    };
+    const long long run0 = (long long)tile * subs + sub;
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) place(e0 - (W - 1) + i, win[i]);
+    for (int q = 0; q < 4; ++q) fetch_group(run0, q);
+    for (long long run = run0; v < vecs && run < runs; run += step) {
+        const int b = (int)(run / row_runs);
+        const int e0 = (int)(run % row_runs) * R, tb0 = e0 - (W - 1), e1 = min(e0 + R, ends);
+        const long long row = (long long)b * p.T;
+        float win[W - 1][V], old[W - 1][V] = {};  // x at t - (W - 1) .. t - 1, ds of the W - 1 tokens before t
+        fetch_wait(3);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) unpack(xs[i * NT], win[i]);
         // ds of token t, whose newest input is x, into the window; with `own` into dw and dbias too
         auto token = [&](const float(&x)[V], float(&ds)[V], bool real, bool own) {
 #pragma unroll
@@ -344,12 +355,11 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
                 old[W - 2][c] = ds[c];
             }
         };
-        if (inside) {
-            fetch_wait(3);
+        if (e0 >= 2 * (W - 1) && e0 + R <= p.T) {  // all of it tokens of the row: straight code
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) {  // the tokens before the run: their ds
                 float x[V], ds[V];
-                unpack(xs[i * NT], x);
+                unpack(xs[(W - 1 + i) * NT], x);
                 unpack(ys[i * NT], ds);
                 token(x, ds, true, false);
                 shift(x, ds);
@@ -357,8 +367,8 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
             Pack<T, V> *to = static_cast<Pack<T, V> *>(p.dx) + (size_t)(row + tb0) * vecs + v;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q, to += (size_t)BATCH * vecs) {
-                fetch_wait(3 - q);
-                const Pack<T, V> *xq = xs + (W - 1 + q * BATCH) * NT, *yq = ys + (W - 1 + q * BATCH) * NT;
+                if (q > 0) fetch_wait(3);
+                const Pack<T, V> *xq = xs + (2 * (W - 1) + q * BATCH) * NT, *yq = ys + (W - 1 + q * BATCH) * NT;
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
                     float x[V], ds[V], d[V] = {};
@@ -371,6 +381,7 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
                     pack(d, r);
                     to[(size_t)k * vecs] = r;
                 }
+                fetch_group(run + step, q);
             }
             continue;
         }
@@ -378,7 +389,7 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
 #pragma unroll 1
         for (int t = tb0; t < e1; ++t) {  // token t's newest input is at place t + W - 1 of the extended row
             float x[V], ds[V];
-            unpack(xs[(t - tb0) * NT], x);
+            unpack(xs[(t - tb0 + W - 1) * NT], x);
             unpack(ys[(t - tb0) * NT], ds);  // 0 outside the row
             token(x, ds, t >= 0 && t < p.T, t >= e0);
             if (t >= e0) {
@@ -392,7 +403,11 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
             }
             shift(x, ds);
         }
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) fetch_group(run + step, q);
     }
+    fetch_wait(0);
+    float(*red)[V + 1] = reinterpret_cast<float(*)[V + 1]>(shared);  // (the slots are done with)
     // the CTA's sums over its runs, in order: [D][W] then [D] of part `tile`
     const int sums = p.dbias ? W + 1 : W;
     float *part = p.ws + (size_t)tile * p.D * sums;
@@ -488,9 +503,9 @@ cudaError_t fwd(const ConvArgs &a) {
 template <typename T, int W>
 cudaError_t bwd(const ConvArgs &a) {
     const int vecs = a.D / 4, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes;
-    constexpr int RUN = 4 * BATCH<T>, PLACES = RUN + W - 1;  // RUN == conv_bwd_run(a.dtype)
+    constexpr int RUN = 4 * BATCH<T>;  // conv_bwd_run(a.dtype)
     const int parts = conv_bwd_parts(a.B, a.T, a.D, a.W, RUN);
-    const size_t smem = (size_t)2 * PLACES * CONV_BWD_NT * sizeof(Pack<T, 4>);
+    const size_t smem = (size_t)(2 * RUN + 3 * (W - 1)) * CONV_BWD_NT * sizeof(Pack<T, 4>);
     auto go = [&](auto kernel) {
         const cudaError_t e = allow_smem(kernel, smem);
         if (e != cudaSuccess) return e;
