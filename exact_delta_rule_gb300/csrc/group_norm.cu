@@ -17,9 +17,11 @@ namespace {
 
 constexpr int NT = GN_NT;
 
-__device__ __forceinline__ float act(float s, int silu) { return silu ? s * quick_sigmoid(s) : s; }
-__device__ __forceinline__ float dact(float s, int silu) {
-    if (!silu) return 1.f;
+template <bool SILU>
+__device__ __forceinline__ float act(float s) { return SILU ? s * quick_sigmoid(s) : s; }
+template <bool SILU>
+__device__ __forceinline__ float dact(float s) {
+    if (!SILU) return 1.f;
     const float g = quick_sigmoid(s);
     return g * fmaf(s, 1.f - g, 1.f);
 }
@@ -38,7 +40,7 @@ __device__ __forceinline__ void affine(const GroupNormArgs &p, int c0, float (&w
 // ------------------------------------------------------------------------------------ whole rows (L = 1)
 // A warp holds 32 / TEAM groups of a row, a group in the first C / G / V lanes of its TEAM; a CTA 8 rows of one block
 // of groups, and every parts-th 8 rows after them.
-template <typename T, int TEAM, bool BWD>
+template <typename T, int TEAM, bool BWD, bool SILU>
 __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks, int parts) {
     constexpr int V = Vec<T>::N, PER = 32 / TEAM, SUBS = NT / 32, UNROLL = 4;
     __shared__ float red[BWD ? SUBS : 1][BWD ? 32 * V : 1];
@@ -70,7 +72,7 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
 #pragma unroll
         for (int i = 0; i < UNROLL; ++i) {
             const long long row = row0 + i * step;
-            if (row >= p.rows) break;
+            const bool writes = live && row < p.rows;  // (a row past the last is zeros: nothing in any sum)
             float x[V];
             Vec<T>::unpack(rx[i], x);
             if (!BWD) {
@@ -78,15 +80,16 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
 #pragma unroll
                 for (int e = 0; e < V; ++e) m += x[e];
                 m = row_sum<TEAM>(m) * inv;
+                const float off = live ? m : 0.f;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    x[e] = live ? x[e] - m : 0.f;
+                    x[e] -= off;
                     q = fmaf(x[e], x[e], q);
                 }
                 const float r = rsqrtf(row_sum<TEAM>(q) * inv + p.eps);
 #pragma unroll
-                for (int e = 0; e < V; ++e) x[e] = act(fmaf(x[e] * r, w[e], b[e]), p.silu);
-                if (live) {
+                for (int e = 0; e < V; ++e) x[e] = act<SILU>(fmaf(x[e] * r, w[e], b[e]));
+                if (writes) {
                     static_cast<uint4 *>(p.y)[row * vecs + v] = Vec<T>::pack(x);
                     if (p.stats && l == 0) reinterpret_cast<float2 *>(p.stats)[row * p.G + g] = make_float2(m, r);
                 }
@@ -96,7 +99,7 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float n = (x[e] - st[i].x) * st[i].y;
-                    d[e] *= dact(fmaf(n, w[e], b[e]), p.silu);
+                    d[e] *= dact<SILU>(fmaf(n, w[e], b[e]));
                     dw[e] = fmaf(d[e], n, dw[e]);
                     db[e] += d[e];
                     d[e] *= w[e];
@@ -108,7 +111,7 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
                 s2 = row_sum<TEAM>(s2) * inv;
 #pragma unroll
                 for (int e = 0; e < V; ++e) x[e] = st[i].y * (d[e] - s1 - x[e] * s2);
-                if (live) static_cast<uint4 *>(p.dx)[row * vecs + v] = Vec<T>::pack(x);
+                if (writes) static_cast<uint4 *>(p.dx)[row * vecs + v] = Vec<T>::pack(x);
             }
         }
     }
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
 // Forward: of x - K and (x - K)^2 with K the channel's first value of the row; backward: of ds and ds n.  A CTA
 // takes one chunk of a row's positions and a block of its channels: part[row chunks + chunk][2][C].  JOINT (backward):
 // one chunk of the positions of all rows.
-template <typename T, bool BWD, bool JOINT>
+template <typename T, bool BWD, bool JOINT, bool SILU>
 __global__ void __launch_bounds__(NT) gn_sums_kernel(GroupNormArgs p, int lanes, int blocks, int chunks) {
     constexpr int V = Vec<T>::N;
     __shared__ float red[NT][V + 1];
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(NT) gn_sums_kernel(GroupNormArgs p, int lanes,
             for (int e = 0; e < V; ++e) {
                 if (BWD) {
                     const float n = (f[e] - k[e]) * r[e];
-                    d[e] *= dact(fmaf(n, w[e], b[e]), p.silu);
+                    d[e] *= dact<SILU>(fmaf(n, w[e], b[e]));
                     a[e] += d[e];
                     q[e] = fmaf(d[e], n, q[e]);
                 } else {
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(NT) gn_join_kernel(GroupNormArgs p, int chunks
 }
 
 // y or dx from the groups' values (`means`: backward, what gn_join_kernel gave).  A thread a vector, UNROLL positions.
-template <typename T, bool BWD>
+template <typename T, bool BWD, bool SILU>
 __global__ void __launch_bounds__(NT) gn_apply_kernel(GroupNormArgs p, int lanes, int blocks, int tiles, const float *means) {
     constexpr int V = Vec<T>::N, UNROLL = 4;
     const int tid = threadIdx.x, lane = tid % lanes, sub = tid / lanes, subs = NT / lanes;
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(NT) gn_apply_kernel(GroupNormArgs p, int lanes
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float n = (f[e] - m[e]) * r[e], s = fmaf(n, w[e], b[e]);
-            f[e] = BWD ? r[e] * (d[e] * dact(s, p.silu) * w[e] - s1[e] - n * s2[e]) : act(s, p.silu);
+            f[e] = BWD ? r[e] * (d[e] * dact<SILU>(s) * w[e] - s1[e] - n * s2[e]) : act<SILU>(s);
         }
         if (t < p.L) out[(size_t)t * vecs] = Vec<T>::pack(f);
     }
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(NT) gn_apply_kernel(GroupNormArgs p, int lanes
 // ------------------------------------------------------------------------------------ a sample a warp
 // x (and dy) of a sample in shared memory.  The sums of a group by TEAM lanes (a power of two, at least C / G up to 32)
 // that walk through its channels one by one, as a group may begin and end inside a vector; then vector by vector.
-template <typename T, int TEAM, bool BWD>
+template <typename T, int TEAM, bool BWD, bool SILU>
 __global__ void __launch_bounds__(NT) gn_warp_kernel(GroupNormArgs p, int bytes) {
     constexpr int V = Vec<T>::N, PER = 32 / TEAM;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(NT) gn_warp_kernel(GroupNormArgs p, int bytes)
                     for (int c = l; c < cg; c += TEAM) {
                         const int ch = g * cg + c;
                         const float w = p.w ? p.w[ch] : 1.f, m = (to_f32(x[t * p.C + ch]) - st.x) * st.y;
-                        const float dn = to_f32(dy[t * p.C + ch]) * dact(fmaf(m, w, p.b ? p.b[ch] : 0.f), p.silu) * w;
+                        const float dn = to_f32(dy[t * p.C + ch]) * dact<SILU>(fmaf(m, w, p.b ? p.b[ch] : 0.f)) * w;
                         first += dn;
                         second = fmaf(dn, m, second);
                     }
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(NT) gn_warp_kernel(GroupNormArgs p, int bytes)
             }
             const float2 st = group[g];
             const float m = (f[e] - st.x) * st.y, s = fmaf(m, w[e], b[e]);
-            f[e] = BWD ? st.y * (d[e] * dact(s, p.silu) * w[e] - means[g].x - m * means[g].y) : act(s, p.silu);
+            f[e] = BWD ? st.y * (d[e] * dact<SILU>(s) * w[e] - means[g].x - m * means[g].y) : act<SILU>(s);
         }
         out[i] = Vec<T>::pack(f);
     }
@@ -404,7 +407,7 @@ __device__ __forceinline__ float2 cluster_read(const float2 *own, int rank) {
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
     return v;
 }
-template <typename T>
+template <typename T, bool SILU>
 __global__ void __launch_bounds__(NT) gn_slab_kernel(GroupNormArgs p, GnSlab s) {
     constexpr int V = Vec<T>::N;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(NT) gn_slab_kernel(GroupNormArgs p, GnSlab s) 
             float f[V];
             Vec<T>::unpack(slab[t * s.vecs + v], f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) f[e] = act(fmaf((f[e] - m[e]) * r[e], w[e], b[e]), p.silu);
+            for (int e = 0; e < V; ++e) f[e] = act<SILU>(fmaf((f[e] - m[e]) * r[e], w[e], b[e]));
             y[(size_t)t * vecs] = Vec<T>::pack(f);
         }
     }
@@ -518,12 +521,12 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
     return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
 }
 
-template <typename T>
+template <typename T, bool SILU>
 cudaError_t slab(const GroupNormArgs &a, const GnSlab &s) {
     constexpr int V = Vec<T>::N;
     const int tc = s.vecs * V;
     const size_t smem = (size_t)s.each * s.vecs * 16 + (size_t)NT * (V + 1) * 4 + 2 * tc * 4 + (size_t)tc / (a.C / a.G) * 16;
-    const cudaError_t e = allow_smem(gn_slab_kernel<T>, smem);
+    const cudaError_t e = allow_smem(gn_slab_kernel<T, SILU>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -531,10 +534,10 @@ cudaError_t slab(const GroupNormArgs &a, const GnSlab &s) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.rows * s.tiles * s.cluster), cfg.blockDim = dim3(NT), cfg.dynamicSmemBytes = smem;
     cfg.stream = a.stream, cfg.attrs = &attr, cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gn_slab_kernel<T>, a, s);
+    return cudaLaunchKernelEx(&cfg, gn_slab_kernel<T, SILU>, a, s);
 }
 
-template <typename T, bool BWD>
+template <typename T, bool BWD, bool SILU>
 cudaError_t warps(const GroupNormArgs &a) {
     const int cg = a.C / a.G, team = std::min(32, gn_team(cg));
     const int bytes = (int)(((size_t)(BWD ? 2 : 1) * a.L * a.C * sizeof(T) + (size_t)a.G * (BWD ? 16 : 8) + 15) / 16 * 16);
@@ -545,24 +548,24 @@ cudaError_t warps(const GroupNormArgs &a) {
         kernel<<<(unsigned)((a.rows + count - 1) / count), 32 * count, (size_t)count * bytes, a.stream>>>(a, bytes);
         return cudaGetLastError();
     };
-    cudaError_t e = team == 1    ? go(gn_warp_kernel<T, 1, BWD>)
-                    : team == 2  ? go(gn_warp_kernel<T, 2, BWD>)
-                    : team == 4  ? go(gn_warp_kernel<T, 4, BWD>)
-                    : team == 8  ? go(gn_warp_kernel<T, 8, BWD>)
-                    : team == 16 ? go(gn_warp_kernel<T, 16, BWD>)
-                                 : go(gn_warp_kernel<T, 32, BWD>);
+    cudaError_t e = team == 1    ? go(gn_warp_kernel<T, 1, BWD, SILU>)
+                    : team == 2  ? go(gn_warp_kernel<T, 2, BWD, SILU>)
+                    : team == 4  ? go(gn_warp_kernel<T, 4, BWD, SILU>)
+                    : team == 8  ? go(gn_warp_kernel<T, 8, BWD, SILU>)
+                    : team == 16 ? go(gn_warp_kernel<T, 16, BWD, SILU>)
+                                 : go(gn_warp_kernel<T, 32, BWD, SILU>);
     if constexpr (BWD) {
         if (e != cudaSuccess || (!a.dw && !a.db)) return e;
         const int vecs = a.C / Vec<T>::N, lanes = gn_lanes(vecs), blocks = (vecs + lanes - 1) / lanes;
         const int chunks = gn_column_chunks(a.rows, a.L, a.C, a.dtype);
-        gn_sums_kernel<T, true, true><<<(unsigned)chunks * blocks, NT, 0, a.stream>>>(a, lanes, blocks, chunks);
+        gn_sums_kernel<T, true, true, SILU><<<(unsigned)chunks * blocks, NT, 0, a.stream>>>(a, lanes, blocks, chunks);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         return launch_sum_parts(a.ws, chunks, 2 * a.C, a.db, a.dw, a.C, a.stream);
     }
     return e;
 }
 
-template <typename T, bool BWD>
+template <typename T, bool BWD, bool SILU>
 cudaError_t whole(const GroupNormArgs &a) {
     const int team = gn_team(a.C / a.G / Vec<T>::N), blocks = gn_blocks(a.C, a.G, a.dtype);
     const int parts = BWD ? gn_row_parts(a.rows, a.C, a.G, a.dtype) : (a.rows + 63) / 64;
@@ -570,42 +573,47 @@ cudaError_t whole(const GroupNormArgs &a) {
         kernel<<<(unsigned)parts * blocks, NT, 0, a.stream>>>(a, blocks, parts);
         return cudaGetLastError();
     };
-    cudaError_t e = team == 1    ? go(gn_rows_kernel<T, 1, BWD>)
-                    : team == 2  ? go(gn_rows_kernel<T, 2, BWD>)
-                    : team == 4  ? go(gn_rows_kernel<T, 4, BWD>)
-                    : team == 8  ? go(gn_rows_kernel<T, 8, BWD>)
-                    : team == 16 ? go(gn_rows_kernel<T, 16, BWD>)
-                                 : go(gn_rows_kernel<T, 32, BWD>);
+    cudaError_t e = team == 1    ? go(gn_rows_kernel<T, 1, BWD, SILU>)
+                    : team == 2  ? go(gn_rows_kernel<T, 2, BWD, SILU>)
+                    : team == 4  ? go(gn_rows_kernel<T, 4, BWD, SILU>)
+                    : team == 8  ? go(gn_rows_kernel<T, 8, BWD, SILU>)
+                    : team == 16 ? go(gn_rows_kernel<T, 16, BWD, SILU>)
+                                 : go(gn_rows_kernel<T, 32, BWD, SILU>);
     if (e != cudaSuccess || !BWD) return e;
     return launch_sum_parts(a.ws, parts, 2 * a.C, a.db, a.dw, a.C, a.stream);
 }
 
-template <typename T, bool BWD>
+template <typename T, bool BWD, bool SILU>
 cudaError_t general(GroupNormArgs a) {
     const int vecs = a.C / Vec<T>::N, lanes = gn_lanes(vecs), blocks = (vecs + lanes - 1) / lanes;
     const int chunks = gn_chunks(a.rows, a.L, a.C, a.dtype), tiles = (a.L + NT / lanes * 4 - 1) / (NT / lanes * 4);
     float *joined = a.ws + (size_t)a.rows * chunks * 2 * a.C;
     if (!BWD && a.stats) joined = a.stats;
-    gn_sums_kernel<T, BWD, false><<<(unsigned)(a.rows * chunks) * blocks, NT, 0, a.stream>>>(a, lanes, blocks, chunks);
+    gn_sums_kernel<T, BWD, false, SILU><<<(unsigned)(a.rows * chunks) * blocks, NT, 0, a.stream>>>(a, lanes, blocks, chunks);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     gn_join_kernel<T, BWD><<<(unsigned)(((long long)a.rows * a.G + NT / 32 - 1) / (NT / 32)), NT, 0, a.stream>>>(a, chunks, joined);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (!BWD) a.stats = joined;
-    gn_apply_kernel<T, BWD><<<(unsigned)(a.rows * tiles) * blocks, NT, 0, a.stream>>>(a, lanes, blocks, tiles, joined);
+    gn_apply_kernel<T, BWD, SILU><<<(unsigned)(a.rows * tiles) * blocks, NT, 0, a.stream>>>(a, lanes, blocks, tiles, joined);
     if ((e = cudaGetLastError()) != cudaSuccess || !BWD) return e;
     return launch_sum_parts(a.ws, a.rows * chunks, 2 * a.C, a.db, a.dw, a.C, a.stream);
 }
 
-template <bool BWD>
-cudaError_t types(const GroupNormArgs &a) {
-    if (gn_whole(a.L, a.C, a.G, a.dtype)) return a.dtype == EFLA_BF16 ? whole<__nv_bfloat16, BWD>(a) : whole<float, BWD>(a);
-    if (gn_warps(a.rows, a.L, a.C, a.dtype)) return a.dtype == EFLA_BF16 ? warps<__nv_bfloat16, BWD>(a) : warps<float, BWD>(a);
+template <typename T, bool BWD, bool SILU>
+cudaError_t path(const GroupNormArgs &a) {
+    if (gn_whole(a.L, a.C, a.G, a.dtype)) return whole<T, BWD, SILU>(a);
+    if (gn_warps(a.rows, a.L, a.C, a.dtype)) return warps<T, BWD, SILU>(a);
     if (!BWD) {
         const GnSlab s = gn_slab(a.rows, a.L, a.C, a.G, a.dtype);
-        if (s.vecs) return a.dtype == EFLA_BF16 ? slab<__nv_bfloat16>(a, s) : slab<float>(a, s);
+        if (s.vecs) return slab<T, SILU>(a, s);
     }
-    return a.dtype == EFLA_BF16 ? general<__nv_bfloat16, BWD>(a) : general<float, BWD>(a);
+    return general<T, BWD, SILU>(a);
+}
+template <bool BWD>
+cudaError_t types(const GroupNormArgs &a) {
+    if (a.silu) return a.dtype == EFLA_BF16 ? path<__nv_bfloat16, BWD, true>(a) : path<float, BWD, true>(a);
+    return a.dtype == EFLA_BF16 ? path<__nv_bfloat16, BWD, false>(a) : path<float, BWD, false>(a);
 }
 
 }  // namespace
