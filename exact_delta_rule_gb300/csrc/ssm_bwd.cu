@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
             for (int j = 0; j < 4; ++j)
                 kept[(k * 4 + j) * NT] = make_float4(h[j / 2][2 * (j & 1)].x, h[j / 2][2 * (j & 1)].y, h[j / 2][2 * (j & 1) + 1].x, h[j / 2][2 * (j & 1) + 1].y);
         }
-#pragma unroll 1
+#pragma unroll 2  // (1109 -> 1084 us of training 8 x 2048 x 2048; all four no longer fit the instruction cache: 1200)
         for (int k = 3; k >= 0; --k) {
             float2 a[4][2][4], hp[4][2][4];
             float rB[4][LEFT], rC[4][LEFT], rU[4], rD[4], rY[4];  // a token's sums, as reduce4 leaves them
