@@ -22,6 +22,7 @@ namespace efla {
 namespace {
 
 constexpr int NT = CONV_NT;
+constexpr int FOUND = 32;  // long sequences that a CTA of the packed forward fills in together
 template <typename T>
 constexpr int BATCH = sizeof(T) == 2 ? 8 : 4;  // rows of a group of copies, of which a thread's run has four at most
 
@@ -150,7 +151,9 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
     if (PACKED) {
         const int tile_rows = rows * subs;
         t0 = (long long)tile * tile_rows;
+        __shared__ int found, list[FOUND][4];  // long sequences of the tile: from, to, number, first token
         for (int i = tid; i < tile_rows; i += NT) seq[i] = -1;
+        if (tid == 0) found = 0;
         __syncthreads();
         for (int i = tid; i < p.N; i += NT) {
             const long long l = p.cu_seqlens[i], h = p.cu_seqlens[i + 1];
@@ -158,12 +161,23 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
                 if (blockIdx.x == 0) atomicExch(p.status, (int)EFLA_ERR_INVALID_ARG);
                 continue;
             }
-            const long long from = l > t0 ? l : t0, to = h < t0 + tile_rows ? h : t0 + tile_rows;
-            for (long long t = from; t < to; ++t) {
-                first[t - t0] = (int)l;
-                seq[t - t0] = i;
+            const int from = (int)(max(l, t0) - t0), to = (int)(min(h, t0 + tile_rows) - t0);
+            const int at = to - from > 16 ? atomicAdd(&found, 1) : FOUND;
+            if (at < FOUND) {
+                list[at][0] = from, list[at][1] = to, list[at][2] = i, list[at][3] = (int)l;
+                continue;
+            }
+            for (int t = from; t < to; ++t) {
+                first[t] = (int)l;
+                seq[t] = i;
             }
         }
+        __syncthreads();
+        for (int f = 0; f < min(found, FOUND); ++f)
+            for (int t = list[f][0] + tid; t < list[f][1]; t += NT) {
+                first[t] = list[f][3];
+                seq[t] = list[f][2];
+            }
         __syncthreads();
         begin = t0 + (long long)sub * rows;
         end = begin + rows < p.T ? begin + rows : p.T;

@@ -462,16 +462,18 @@ cudaError_t step_states(const SsmArgs &a) {
 namespace {
 // How many segments to cut a row of T tokens into: the number of the least estimated time.  A token costs one(w) clocks
 // on a unit of the GPU (of which there are `places`) that has w of the `work` pieces of a row's length, all rows
-// together; cutting costs `carry` of that again, and `step` a segment (its state through HBM: 8 bytes an entry).
+// together; cutting costs `carry` of that again, and `step` a segment (its state through HBM: 8 bytes an entry).  Rows of
+// uneven lengths take longer by `uneven` / w: the more pieces a unit has, the more they even out.
 template <typename F>
 int cut(long long work, int T, int places, F one, double carry, double step, double uneven) {
+    if (work <= 0) return 0;
     int best = 1;
     double least = 0.;
-    const int most = std::max(1, std::min(T / 64, 128));
-    for (int p = 1; p <= most; ++p) {
+    const int most = std::max(1, std::min(T / 64, 4096));
+    for (int p = 1; p <= most; p += 1 + p / 32) {
         const long long w = (work * p + places - 1) / places;
         const int tokens = ((T + p - 1) / p + SSM_TOK - 1) / SSM_TOK * SSM_TOK;
-        const double t = tokens * one(w) * (p > 1 ? 1. + carry : 1.) * (1. + uneven / p) + step * p;
+        const double t = tokens * one(w) * (p > 1 ? 1. + carry : 1.) * (1. + uneven / w) + step * p;
         if (p == 1 || t < least) best = p, least = t;
     }
     if (best == 1) return 0;
@@ -482,11 +484,13 @@ int cut(long long work, int T, int places, F one, double carry, double step, dou
 // A scheduler (608) with one warp takes 326 clocks a token, with more 183 each; the carry kernel 0.55 of the scan's
 // (8 x 2048 tokens of 2432, 4864 and 7296 channels, N = 16: 347, 407 and 567 us whole).
 int ssm_segment(long long rows, int T, int D, int N, bool uneven) {
+    if (rows > 65535) return 0;  // (the combine kernel's grid; rows enough without)
     return cut(rows * (((long long)D * N + 511) / 512), T, 608, [](long long w) { return w == 1 ? 326. : 183. * w; }, 0.55,
-               600. + 0.0023 * rows * D * N, uneven ? 1. : 0.);
+               600. + 0.0023 * rows * D * N, uneven ? 2. : 0.);
 }
 // A SM (152) with two CTAs takes 1528 clocks for a token of both, with one 1086; the carry 0.2 of that.
 int ssm_bwd_segment(long long rows, int T, int D, int N, int tiles) {
+    if (rows > 65535) return 0;
     return cut(rows * tiles, T, 152, [](long long w) { return w / 2 * 1528. + w % 2 * 1086.; }, 0.2, 600. + 0.0092 * rows * D * N, 0.);
 }
 

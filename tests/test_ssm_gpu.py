@@ -88,11 +88,12 @@ LENS = [5, 0, 16, 1, 2, 130, 0, 3, 63, 200, 4]
 @pytest.mark.parametrize("W", [2, 4])
 @pytest.mark.parametrize("state", [True, False])
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_convolution_packed(dtype, W, state):
-    a = conv_inputs(B=1, T=sum(LENS), D=72, W=W, dtype=dtype, state=state, N=len(LENS))
-    y, end = efla.causal_conv(**a, cu_seqlens=cu_of(LENS))
+@pytest.mark.parametrize("D, lens", [(72, LENS), (8, [40] * 100), (8, [1] * 300 + [500, 3]), (1000, [17] * 30)])
+def test_convolution_packed(dtype, W, state, D, lens):
+    a = conv_inputs(B=1, T=sum(lens), D=D, W=W, dtype=dtype, state=state, N=len(lens))
+    y, end = efla.causal_conv(**a, cu_seqlens=cu_of(lens))
     at = 0
-    for i, n in enumerate(LENS):
+    for i, n in enumerate(lens):
         one = {**a, "x": a["x"][:, at:at + n].contiguous(), "state0": a["state0"][i:i + 1].contiguous() if state else None}
         y1, end1 = efla.causal_conv(**one)
         assert torch.equal(y[:, at:at + n], y1) and torch.equal(end[i:i + 1], end1), i
