@@ -148,6 +148,14 @@ __device__ __forceinline__ float2 softplus2(float2 t) {
     p = __ffma2_rn(p, u, two(1.f));
     return __ffma2_rn(p, u, make_float2(fmaxf(t.x, 0.f), fmaxf(t.y, 0.f)));
 }
+// A token's exponent in units of log2, rate delta.  The exponential instruction's results are 0.6e-8 to 2.7e-8 too small
+// in the mean for exponents of 2^-13 to -1, which a state that many of them carry would add up; 2.1e-8 more in the
+// exponent leaves -1.3e-8 to 0.9e-8 (1e-6 in place of 2e-6 of a state that 100 tokens carry), and 0 remains 0 or 2^0 = 1.
+constexpr float EX2_MEAN = 2.1e-8f;
+__device__ __forceinline__ float ssm_exponent(float delta, float rate) { return fmaf(delta, rate, EX2_MEAN); }
+__device__ __forceinline__ float2 ssm_exponent(float2 delta, float2 rate) {
+    return __ffma2_rn(delta, rate, make_float2(EX2_MEAN, EX2_MEAN));
+}
 // A in units of log2: e^{A delta} = 2^{rate delta}.
 __device__ __forceinline__ float ssm_rate(float a_log) { return -expf(a_log) * LOG2E; }
 

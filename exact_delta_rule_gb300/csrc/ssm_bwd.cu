@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 e = __fmul2_rn(dl[q], rate[q][i]);
+                        const float2 e = ssm_exponent(dl[q], rate[q][i]);
                         h[q][i] = __ffma2_rn(make_float2(ssm_ex2(e.x), ssm_ex2(e.y)), h[q][i], __fmul2_rn(u[q], b[i]));
                     }
             }
@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
 #pragma unroll 2  // (1109 -> 1084 us of training 8 x 2048 x 2048; all four no longer fit the instruction cache: 1200)
         for (int k = 3; k >= 0; --k) {
             float2 a[4][2][4], hp[4][2][4];
+            float2 dAq[2][4];  // dA of these four tokens: a sum of four at a time into the long one halves its rounding
             float rB[4][LEFT], rC[4][LEFT], rU[4], rD[4], rY[4];  // a token's sums, as reduce4 leaves them
             if (k > 0) {
 #pragma unroll
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
                     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const float2 e = __fmul2_rn(dl[q], rate[q][i]);
+                        const float2 e = ssm_exponent(dl[q], rate[q][i]);
                         a[j][q][i] = make_float2(ssm_ex2(e.x), ssm_ex2(e.y));
                         hp[j][q][i] = h[q][i];
                         h[q][i] = __ffma2_rn(a[j][q][i], h[q][i], __fmul2_rn(u[q], b[i]));
@@ -304,7 +305,8 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
                         du[q] = __ffma2_rn(l[q][i], b[i], du[q]);
                         l[q][i] = __fmul2_rn(l[q][i], a[j][q][i]);
                         const float2 w = __fmul2_rn(l[q][i], hp[j][q][i]);
-                        dA[q][i] = __ffma2_rn(w, dl[q], dA[q][i]);
+                        dAq[q][i] = j == 3 ? __fmul2_rn(w, dl[q]) : __ffma2_rn(w, dl[q], dAq[q][i]);
+                        if (j == 0) dA[q][i] = __fadd2_rn(dA[q][i], dAq[q][i]);
                         dd[q] = __ffma2_rn(w, rate[q][i], dd[q]);
                     }
                     dB[i] = acc.x + acc.y;
@@ -334,6 +336,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
         }
         __syncwarp();
         if (elive) {
+            float2 chunk_D = make_float2(0.f, 0.f), chunk_dt = chunk_D;
 #pragma unroll 4
             for (int t = et; t < count; t += TSTEP) {
                 const float2 x = in(K::X, t), dt = __fadd2_rn(in(K::DT, t), bias), du = *at(u_s, t), dd = *at(g_s, t);
@@ -350,9 +353,11 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
                 const float2 ddt = __fmul2_rn(ddelta, make_float2(ssm_sigmoid(dt.x), ssm_sigmoid(dt.y)));
                 store2(static_cast<T *>(p.dx) + to, __ffma2_rn(du, *at(delta_s, t), __fmul2_rn(skip, g)));
                 store2(static_cast<T *>(p.ddt) + to, ddt);
-                sum_D = __ffma2_rn(g, x, sum_D);
-                sum_dt = __fadd2_rn(sum_dt, ddt);
+                chunk_D = __ffma2_rn(g, x, chunk_D);
+                chunk_dt = __fadd2_rn(chunk_dt, ddt);
             }
+            sum_D = __fadd2_rn(sum_D, chunk_D);
+            sum_dt = __fadd2_rn(sum_dt, chunk_dt);
         }
     }
     if (live) {
@@ -460,7 +465,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_carry_kernel(SsmBwdArgs p, int til
 #pragma unroll
             for (int j = 0; j < PER / 4; ++j) {
                 const float4 v = *reinterpret_cast<const float4 *>(cvt + t * N + (j * NSUB + sub) * 4);
-                const float2 e0 = __fmul2_rn(delta2, rate[2 * j]), e1 = __fmul2_rn(delta2, rate[2 * j + 1]);
+                const float2 e0 = ssm_exponent(delta2, rate[2 * j]), e1 = ssm_exponent(delta2, rate[2 * j + 1]);
                 l[2 * j] = __fmul2_rn(make_float2(ssm_ex2(e0.x), ssm_ex2(e0.y)), __ffma2_rn(g2, make_float2(v.x, v.y), l[2 * j]));
                 l[2 * j + 1] = __fmul2_rn(make_float2(ssm_ex2(e1.x), ssm_ex2(e1.y)), __ffma2_rn(g2, make_float2(v.z, v.w), l[2 * j + 1]));
             }

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(ssm_fwd_threads(N)) ssm_fwd_kernel(SsmArgs p, 
             for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int i = 0; i < PER / 2; ++i) {
-                    const float2 e = __fmul2_rn(dk[q], rate[q][i]);
+                    const float2 e = ssm_exponent(dk[q], rate[q][i]);
                     a[q][i] = make_float2(ssm_ex2(e.x), ssm_ex2(e.y));
                     ub[q][i] = __fmul2_rn(uk[q], b[i]);
                 }
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(ssm_fwd_threads(N)) ssm_fwd_kernel(SsmArgs p, 
                         steps(t + 1, dn, un, dk, uk);
                     fetch(bc + (t + 1) * N, b);
                     if (!CARRY) fetch(bc + (TOK + t + 1) * N, cn);
-                    e[0][0] = __fmul2_rn(dk[0], rate[0][0]);
+                    e[0][0] = ssm_exponent(dk[0], rate[0][0]);
                 }
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(ssm_fwd_threads(N)) ssm_fwd_kernel(SsmArgs p, 
                         if (more) an.x = ssm_ex2_here(e[q][i].x);
                         h[q][i] = __ffma2_rn(a[q][i], h[q][i], ub[q][i]);
                         if (more) {
-                            if (nq < 2) e[nq][ni] = __fmul2_rn(dk[nq], rate[nq][ni]);
+                            if (nq < 2) e[nq][ni] = ssm_exponent(dk[nq], rate[nq][ni]);
                             an.y = ssm_ex2_here(e[q][i].y);
                             ub[q][i] = __fmul2_rn(uk[q], b[i]);
                             a[q][i] = an;
@@ -425,10 +425,10 @@ __global__ void __launch_bounds__(STEP_NT) ssm_step_kernel(SsmArgs p) {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const float delta = softplus(dt[r] + bias), u = delta * x[r];
-        h[r].x = fmaf(ssm_ex2(delta * rate[0]), h[r].x, u * B[r].x);
-        h[r].y = fmaf(ssm_ex2(delta * rate[1]), h[r].y, u * B[r].y);
-        h[r].z = fmaf(ssm_ex2(delta * rate[2]), h[r].z, u * B[r].z);
-        h[r].w = fmaf(ssm_ex2(delta * rate[3]), h[r].w, u * B[r].w);
+        h[r].x = fmaf(ssm_ex2(ssm_exponent(delta, rate[0])), h[r].x, u * B[r].x);
+        h[r].y = fmaf(ssm_ex2(ssm_exponent(delta, rate[1])), h[r].y, u * B[r].y);
+        h[r].z = fmaf(ssm_ex2(ssm_exponent(delta, rate[2])), h[r].z, u * B[r].z);
+        h[r].w = fmaf(ssm_ex2(ssm_exponent(delta, rate[3])), h[r].w, u * B[r].w);
         float y = fmaf(h[r].x, C[r].x, h[r].y * C[r].y) + fmaf(h[r].z, C[r].z, h[r].w * C[r].w);
 #pragma unroll
         for (int off = 1; off < LN; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
