@@ -7,10 +7,14 @@
 // on rows extended by the state: place e = t + W - 1 >= 0, dfull_e = sum_j w_j ds_{e-j} (ds = 0 outside the
 // row), plus dstate_T's at the last W - 1 places; the first W - 1 are dstate0.
 //
-// Bound by HBM: x is read and y written once.  A thread keeps one 16-byte vector of channels (4 channels in
-// the backward, whose sums take registers) and walks down the tokens with the last W - 1 rows in registers, so
-// a row is read once by its tile and again only as the W - 1 rows before the next.  Arithmetic is fp32, each
-// output rounded once; the sums over tokens go in two stages of fixed order.
+// Bound by HBM: x is read and y written once.  A thread takes 4 channels and walks down a run of tokens with the last
+// W - 1 rows in registers, so a row is read once by its run and again only as the W - 1 rows before the next.  A run
+// comes into the thread's own slots of shared memory by asynchronous copies, four groups of them under way; the backward
+// refills a group for the next run as soon as it is done with it.  Code for runs inside their row is straight.
+// Arithmetic is fp32, each output rounded once; the sums over tokens go in two stages of fixed order.
+// 8 x 2048 tokens, W = 4, silu, bf16: forward of 6144 channels 78 us (403 MB, 5.2 TB/s), of 2048 27 (134 MB); backward of 2048 62
+// (201 MB, 3.2 TB/s).  An element of the forward is 17 instructions and one of the backward 33, 0.62 and
+// 0.54 of what issues: the copies no longer limit them.
 #include <algorithm>
 #include <type_traits>
 

@@ -9,11 +9,14 @@
 // from the kept state it recomputes h up to each quarter of the chunk (three are set aside in shared memory), then,
 // last quarter first, recomputes the quarter's four tokens with h and a of each in registers, and goes back over them.
 //
-// About 19 multiply-adds and 1.75 exponentials an entry of the state: bound by the fp32 pipe and by issue.  A thread
+// About 19 multiply-adds and 1.75 exponentials an entry of the state, 360 instructions a warp's token of 32 x 16
+// entries: bound like the forward by issue and the registers' read ports (114 packed multiply-adds), at the two warps a
+// scheduler that 255 registers leave.  8 x 2048 tokens of 2048 channels, N = 16, bf16: 640 us.  A thread
 // has 4 channels x 4 entries: a token's sums over the entries (of du, ddelta and y; over the N / 4 lanes of a
 // channel) and over the channels (of dB and dC; over the others) then take 14 shuffles for 16 entries, the fewest of
-// all splits of 16.  Sums over the four warps of a CTA go through shared memory and those over the CTAs through
-// the workspace, all in a fixed order.
+// all splits of 16; their first step needs no selecting (reduce4).  Elementwise work goes in pairs of channels, by each
+// warp on its own channels, so a chunk costs two barriers.  Sums over the four warps of a CTA go through shared memory and
+// those over the CTAs through the workspace, all in a fixed order.
 #include "mixer_norm.cuh"
 #include "ssm.cuh"
 

@@ -1,16 +1,21 @@
 // Selective state space scan, forward (ssm.cuh has the formulas).
 //
-// The work is N exponentials and 3 N multiply-adds a token and channel, on inputs and outputs of a few bytes.  A warp's
-// token of 32 x 16 entries takes 20 clocks of the exponential unit, 22 of the fp32 pipe, 24 of issue and 22 of the
-// shared-memory and shuffle pipe: no one of them leads by much, and HBM is far from its bound.  A thread keeps 2
-// channels x 8 entries of the state in registers over all tokens of its segment, so that B and C, which all channels
-// share, are read from shared memory (as fp32, 4 clocks each 16 bytes a lane, broadcast or not) once for both channels;
-// multiply-adds run packed in pairs of entries.  Tokens go in groups of four, in straight code.  Their softplus
+// The work is N exponentials and 3 N multiply-adds a token and channel, on inputs and outputs of a few bytes: HBM is far
+// from its bound (8 x 2048 tokens of 4096 channels, N = 16, bf16: 409 us for 540 MB).  A warp's token of 32 x 16 entries
+// is 118 instructions and takes 170 clocks of a scheduler however many warps it has (191 each with two, 326 with one).
+// What takes them is neither issue (0.65) nor the exponential unit (leaving the exponentials out changes nothing) but
+// the registers' read ports: a packed multiply-add of three different operands takes 2.4 to 3 clocks, one with a
+// constant 2, so 32 of them are 85 of the 170; gates and outputs are 50, copies and conversions 12.
+//
+// A thread keeps 2 channels x 8 entries of the state in registers over all tokens of its segment, so that B and C, which
+// all channels share, are read from shared memory (as fp32) once for both channels; multiply-adds run packed in pairs of
+// entries, and what the next token needs before it meets the state is computed between this one's
+// multiply-adds (8 % at 19456 channels).  Tokens go in groups of four, 16 in straight code.  Their softplus
 // and gate are shared out among the N / 8 lanes of a pair of channels: the lane that computes a token's delta also gets
 // its sum of C . h and writes its output; a lane keeps its own channel first, so that two lanes swap what belongs to
 // the other without selecting.  A CTA is one warp (two for N = 128): 8 x 2048 tokens of 4096 channels are 1024 warps, 6.7
-// a SM.
-// Measured there (N = 16): 1 channel x 16 entries a thread 406 us, 1 x 8 449 us, 2 x 8 409 us.
+// a SM.  Other splits of the state, at that size: 1 channel x 8 entries 449 us, 1 x 16 406 to 524, 2 x 4 427; eight tokens
+// in straight code 443, four 540 (copies between registers).
 // Inputs come in stages of 16 tokens by asynchronous copies two stages ahead; B and C of the next stage are converted
 // while this one is computed, so a stage costs one barrier.
 #include "ssm.cuh"
@@ -392,7 +397,8 @@ cudaError_t states(const SsmArgs &a) {
 // ------------------------------------------------------------------------------------ one token
 // HBM bound: the state is read and written once (8 N bytes a channel; everything else is a few).  A thread has four
 // entries of one channel's state and takes ROWS sequences, so that the rates are computed once for them; all that it
-// reads is under way before the first is used.
+// reads is under way before the first is used (256 sequences of 4096 channels, N = 16: 31 us, in L2 25; 42 with loads
+// a sequence at a time; 2 sequences 32, 8 32, 256 threads 38).
 constexpr int STEP_NT = 128;
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
