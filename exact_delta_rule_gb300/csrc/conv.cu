@@ -60,6 +60,23 @@ __device__ __forceinline__ void pack(const float (&x)[4], Pack<__nv_bfloat16, 4>
     p.r = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
+// Four channels as two pairs.
+__device__ __forceinline__ void unpack(const Pack<float, 4> &p, float2 (&x)[2]) {
+    x[0] = make_float2(__uint_as_float(p.r.x), __uint_as_float(p.r.y));
+    x[1] = make_float2(__uint_as_float(p.r.z), __uint_as_float(p.r.w));
+}
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, 4> &p, float2 (&x)[2]) {
+    x[0] = make_float2(__uint_as_float(p.r.x << 16), __uint_as_float(p.r.x & 0xffff0000u));
+    x[1] = make_float2(__uint_as_float(p.r.y << 16), __uint_as_float(p.r.y & 0xffff0000u));
+}
+__device__ __forceinline__ void pack(const float2 (&x)[2], Pack<float, 4> &p) {
+    p.r = make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+}
+__device__ __forceinline__ void pack(const float2 (&x)[2], Pack<__nv_bfloat16, 4> &p) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0].x, x[0].y), b = __floats2bfloat162_rn(x[1].x, x[1].y);
+    p.r = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
 // Row `row` of p [rows, vecs], vector v.
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> load(const void *p, long long row, int vecs, int v) {
@@ -113,14 +130,30 @@ struct Taps {
     }
 };
 
+// The same of four channels as two pairs.
+template <int W>
+struct Taps4 {
+    float2 w[2][W], bias[2];
+    __device__ __forceinline__ void load(const ConvArgs &p, int c0) {
+        Taps<W, 4> t;
+        t.load(p, c0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[h][j] = make_float2(t.w[2 * h][j], t.w[2 * h + 1][j]);
+            bias[h] = make_float2(t.bias[2 * h], t.bias[2 * h + 1]);
+        }
+    }
+};
+
 // ------------------------------------------------------------------------------------ forward
 // CTAs [0, work_ctas): runs of `rows` tokens x a block of the channels; the others copy the states.  PACKED: the
 // runs are of all tokens, and first[i], seq[i] say where the sequence of the CTA's token i begins and which it is
 // (-1: none).  Otherwise they are of the rows, row_runs each.
-template <typename T, int V, int W, bool PACKED, bool SILU>
+template <typename T, int W, bool PACKED, bool SILU>
 __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, unsigned work_ctas, int rows,
                                                       int row_runs) {
-    constexpr int BATCH = efla::BATCH<T>;
+    constexpr int V = 4, BATCH = efla::BATCH<T>;
     const int tid = threadIdx.x;
     if (blockIdx.x >= work_ctas) {  // state_T: place j of a sequence's last W - 1 inputs
         const long long e = (long long)(blockIdx.x - work_ctas) * NT + tid;
@@ -204,7 +237,7 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
             fetch_commit();
         }
     }
-    float win[W - 1][V];
+    float2 win[W - 1][2];
     // the W - 1 inputs before token t of the sequence n that begins at lo
     auto before = [&](long long t) {
 #pragma unroll
@@ -222,21 +255,21 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
         lo = -1;  // no sequence yet
     else
         before(begin);
-    Taps<W, V> taps;
+    Taps4<W> taps;
     taps.load(p, v * V);
     auto token = [&](const Pack<T, V> &raw, Pack<T, V> *to) {
-        float x[V], s[V];
+        float2 x[2], s[2];
         unpack(raw, x);
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-            float a = taps.bias[c];
+        for (int h = 0; h < 2; ++h) {
+            float2 a = taps.bias[h];
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
-            a = fmaf(taps.w[c][W - 1], x[c], a);
-            s[c] = SILU ? a * quick_sigmoid(a) : a;
+            for (int i = 0; i < W - 1; ++i) a = __ffma2_rn(taps.w[h][i], win[i][h], a);
+            a = __ffma2_rn(taps.w[h][W - 1], x[h], a);
+            s[h] = SILU ? __fmul2_rn(a, quick_sigmoid(a)) : a;
 #pragma unroll
-            for (int i = 0; i + 1 < W - 1; ++i) win[i][c] = win[i + 1][c];
-            win[W - 2][c] = x[c];
+            for (int i = 0; i + 1 < W - 1; ++i) win[i][h] = win[i + 1][h];
+            win[W - 2][h] = x[h];
         }
         Pack<T, V> r;
         pack(s, r);
@@ -283,8 +316,8 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
     const int cb = blockIdx.x % cblocks, tile = blockIdx.x / cblocks, v = cb * lanes + lane;
     const long long runs = (long long)p.B * row_runs, step = (long long)parts * subs;
     const int ends = p.T + W - 1;
-    float dw[V][W] = {}, db[V] = {};
-    Taps<W, V> taps;
+    float2 dw[2][W] = {}, db[2] = {};
+    Taps4<W> taps;
     if (v < vecs) taps.load(p, v * V);
     // Group q of a run's copies: its batch q, and the first with what comes before it.  A group is fetched for the next
     // run as soon as this one is done with its slots, so three are always under way behind the one that is needed.
@@ -328,55 +361,56 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
         const int b = (int)(run / row_runs);
         const int e0 = (int)(run % row_runs) * R, tb0 = e0 - (W - 1), e1 = min(e0 + R, ends);
         const long long row = (long long)b * p.T;
-        float win[W - 1][V], old[W - 1][V] = {};  // x at t - (W - 1) .. t - 1, ds of the W - 1 tokens before t
+        float2 win[W - 1][2], old[W - 1][2] = {};  // x at t - (W - 1) .. t - 1, ds of the W - 1 tokens before t
         fetch_wait(3);
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) unpack(xs[i * NT], win[i]);
         // ds of token t, whose newest input is x, into the window; with `own` into dw and dbias too
-        auto token = [&](const float(&x)[V], float(&ds)[V], bool real, bool own) {
+        auto token = [&](const float2(&x)[2], float2(&ds)[2], bool real, bool own) {
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
+            for (int h = 0; h < 2; ++h) {
                 if (SILU) {
-                    float a = taps.bias[c];
+                    float2 a = taps.bias[h];
 #pragma unroll
-                    for (int i = 0; i < W - 1; ++i) a = fmaf(taps.w[c][i], win[i][c], a);
-                    a = fmaf(taps.w[c][W - 1], x[c], a);
-                    const float g = quick_sigmoid(a);
-                    if (real) ds[c] *= g * fmaf(a, 1.f - g, 1.f);
+                    for (int i = 0; i < W - 1; ++i) a = __ffma2_rn(taps.w[h][i], win[i][h], a);
+                    a = __ffma2_rn(taps.w[h][W - 1], x[h], a);
+                    const float2 one = make_float2(1.f, 1.f), g = quick_sigmoid(a);
+                    const float2 slope = __fmul2_rn(g, __ffma2_rn(a, __ffma2_rn(g, make_float2(-1.f, -1.f), one), one));
+                    if (real) ds[h] = __fmul2_rn(ds[h], slope);
                 }
                 if (own) {
 #pragma unroll
-                    for (int i = 0; i < W - 1; ++i) dw[c][i] = fmaf(ds[c], win[i][c], dw[c][i]);
-                    dw[c][W - 1] = fmaf(ds[c], x[c], dw[c][W - 1]);
-                    db[c] += ds[c];
+                    for (int i = 0; i < W - 1; ++i) dw[h][i] = __ffma2_rn(ds[h], win[i][h], dw[h][i]);
+                    dw[h][W - 1] = __ffma2_rn(ds[h], x[h], dw[h][W - 1]);
+                    db[h] = __fadd2_rn(db[h], ds[h]);
                 }
             }
         };
         // place e = t: d += sum_j w_j ds_{t-j}
-        auto place_sum = [&](const float(&ds)[V], float(&d)[V]) {
+        auto place_sum = [&](const float2(&ds)[2], float2(&d)[2]) {
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
-                d[c] = fmaf(taps.w[c][0], ds[c], d[c]);
+            for (int h = 0; h < 2; ++h) {
+                d[h] = __ffma2_rn(taps.w[h][0], ds[h], d[h]);
 #pragma unroll
-                for (int j = 1; j < W; ++j) d[c] = fmaf(taps.w[c][j], old[W - 1 - j][c], d[c]);
+                for (int j = 1; j < W; ++j) d[h] = __ffma2_rn(taps.w[h][j], old[W - 1 - j][h], d[h]);
             }
         };
-        auto shift = [&](const float(&x)[V], const float(&ds)[V]) {
+        auto shift = [&](const float2(&x)[2], const float2(&ds)[2]) {
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int i = 0; i + 1 < W - 1; ++i) {
-                    win[i][c] = win[i + 1][c];
-                    old[i][c] = old[i + 1][c];
+                    win[i][h] = win[i + 1][h];
+                    old[i][h] = old[i + 1][h];
                 }
-                win[W - 2][c] = x[c];
-                old[W - 2][c] = ds[c];
+                win[W - 2][h] = x[h];
+                old[W - 2][h] = ds[h];
             }
         };
         if (e0 >= 2 * (W - 1) && e0 + R <= p.T) {  // all of it tokens of the row: straight code
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) {  // the tokens before the run: their ds
-                float x[V], ds[V];
+                float2 x[2], ds[2];
                 unpack(xs[(W - 1 + i) * NT], x);
                 unpack(ys[i * NT], ds);
                 token(x, ds, true, false);
@@ -389,7 +423,7 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
                 const Pack<T, V> *xq = xs + (2 * (W - 1) + q * BATCH) * NT, *yq = ys + (W - 1 + q * BATCH) * NT;
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
-                    float x[V], ds[V], d[V] = {};
+                    float2 x[2], ds[2], d[2] = {};
                     unpack(xq[k * NT], x);
                     unpack(yq[k * NT], ds);
                     token(x, ds, true, true);
@@ -404,20 +438,25 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
             continue;
         }
         fetch_wait(0);
+        auto put = [&](void *to, long long at, const float2(&d)[2]) {
+            Pack<T, V> r;
+            pack(d, r);
+            static_cast<Pack<T, V> *>(to)[at * vecs + v] = r;
+        };
 #pragma unroll 1
         for (int t = tb0; t < e1; ++t) {  // token t's newest input is at place t + W - 1 of the extended row
-            float x[V], ds[V];
+            float2 x[2], ds[2];
             unpack(xs[(t - tb0 + W - 1) * NT], x);
             unpack(ys[(t - tb0) * NT], ds);  // 0 outside the row
             token(x, ds, t >= 0 && t < p.T, t >= e0);
             if (t >= e0) {
-                float d[V] = {};
+                float2 d[2] = {};
                 if (p.dstate_T && t >= p.T) unpack(load<T, V>(p.dstate_T, (long long)b * (W - 1) + t - p.T, vecs, v), d);
                 place_sum(ds, d);
                 if (t >= W - 1)
-                    store<T, V>(p.dx, row + t - (W - 1), vecs, v, d);
+                    put(p.dx, row + t - (W - 1), d);
                 else if (p.dstate0)
-                    store<T, V>(p.dstate0, (long long)b * (W - 1) + t, vecs, v, d);
+                    put(p.dstate0, (long long)b * (W - 1) + t, d);
             }
             shift(x, ds);
         }
@@ -434,7 +473,11 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
         if (j == sums) break;
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < V; ++c) red[tid][c] = j < W ? dw[c][j < W ? j : 0] : db[c];
+        for (int h = 0; h < 2; ++h) {
+            const float2 r = j < W ? dw[h][j < W ? j : 0] : db[h];
+            red[tid][2 * h] = r.x;
+            red[tid][2 * h + 1] = r.y;
+        }
         __syncthreads();
         for (int i = tid; i < lanes * V; i += NT) {
             const int l = i / V, c = i % V, ch = (cb * lanes + l) * V + c;
@@ -514,9 +557,9 @@ cudaError_t fwd(const ConvArgs &a) {
         return cudaGetLastError();
     };
     if (a.cu_seqlens)
-        return go(a.silu ? conv_fwd_kernel<T, V, W, true, true> : conv_fwd_kernel<T, V, W, true, false>,
+        return go(a.silu ? conv_fwd_kernel<T, W, true, true> : conv_fwd_kernel<T, W, true, false>,
                   slots + 2 * rows * subs * sizeof(int));
-    return go(a.silu ? conv_fwd_kernel<T, V, W, false, true> : conv_fwd_kernel<T, V, W, false, false>, slots);
+    return go(a.silu ? conv_fwd_kernel<T, W, false, true> : conv_fwd_kernel<T, W, false, false>, slots);
 }
 template <typename T, int W>
 cudaError_t bwd(const ConvArgs &a) {

@@ -50,6 +50,18 @@ __device__ __forceinline__ float quick_sigmoid(float x) {
     return y;
 }
 
+// The same for two, packed.
+__device__ __forceinline__ float2 quick_sigmoid(float2 x) {
+    const float2 t = __fmul2_rn(x, make_float2(-1.44269504f, -1.44269504f));
+    float2 e, y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __fadd2_rn(e, make_float2(1.f, 1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(e.y));
+    return y;
+}
+
 // Sum over the LPR lanes that hold a row.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
