@@ -13,6 +13,7 @@ autograd.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -73,7 +74,9 @@ def _activation(activation) -> int:
     return code
 
 
+@functools.lru_cache(maxsize=4096)
 def _bytes(name: str, *sizes: int) -> int:
+    """A workspace query, which depends on nothing but its sizes: asked once for each."""
     n = _sz(0)
     _check(getattr(_lib(), name)(*sizes, ctypes.byref(n)))
     return n.value
