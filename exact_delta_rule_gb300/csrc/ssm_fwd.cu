@@ -397,8 +397,9 @@ cudaError_t states(const SsmArgs &a) {
 // ------------------------------------------------------------------------------------ one token
 // HBM bound: the state is read and written once (8 N bytes a channel; everything else is a few).  A thread has four
 // entries of one channel's state and takes ROWS sequences, so that the rates are computed once for them; all that it
-// reads is under way before the first is used (256 sequences of 4096 channels, N = 16: 31 us, in L2 25; 42 with loads
-// a sequence at a time; 2 sequences 32, 8 32, 256 threads 38).
+// reads is under way before the first is used.  Of a row's scalars (softplus, gate, the output) each of four threads
+// has one row's and hands them to the others: 256 sequences of 4096 channels, N = 16: 24 us (143 MB, 5.9 TB/s, what a
+// multiplication in place reaches), in L2 18; 30 and 22 with every thread computing all four rows' scalars.
 constexpr int STEP_NT = 128;
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
@@ -407,13 +408,14 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
 }
 template <typename T, int N, int ROWS>
 __global__ void __launch_bounds__(STEP_NT) ssm_step_kernel(SsmArgs p) {
+    static_assert(ROWS == 1 || ROWS == 4, "a row for each of four threads");
     constexpr int LN = N / 4, CT = STEP_NT / LN;
+    constexpr unsigned FULL = 0xffffffffu;
     const int tid = threadIdx.x, l = tid % LN, blocks = (p.D + CT - 1) / CT;
     const int d = blockIdx.x % blocks * CT + tid / LN, b0 = blockIdx.x / blocks * ROWS;
     const bool live = d < p.D;
     const int dd = live ? d : p.D - 1, each = p.D / p.G, g = dd / each;
     float4 h[ROWS], B[ROWS], C[ROWS];
-    float x[ROWS], dt[ROWS], z[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int b = min(b0 + r, p.B - 1);  // (a row past the last: the last again, not written)
@@ -421,31 +423,39 @@ __global__ void __launch_bounds__(STEP_NT) ssm_step_kernel(SsmArgs p) {
         h[r] = *reinterpret_cast<const float4 *>(p.S0 + e * N + 4 * l);
         B[r] = load4(static_cast<const T *>(p.Bm) + m);
         C[r] = load4(static_cast<const T *>(p.Cm) + m);
-        x[r] = to_f32(static_cast<const T *>(p.x)[e]);
-        dt[r] = to_f32(static_cast<const T *>(p.dt)[e]);
-        z[r] = p.z ? to_f32(static_cast<const T *>(p.z)[e]) : 0.f;
     }
+    const int mine = l % ROWS;  // the row whose scalars are this thread's
+    const size_t own = (size_t)min(b0 + mine, p.B - 1) * p.D + dd;
+    const float x = to_f32(static_cast<const T *>(p.x)[own]), dt = to_f32(static_cast<const T *>(p.dt)[own]);
+    const float z = p.z ? to_f32(static_cast<const T *>(p.z)[own]) : 0.f;
     const float4 al = *reinterpret_cast<const float4 *>(p.A_log + (size_t)dd * N + 4 * l);
     const float rate[4] = {ssm_rate(al.x), ssm_rate(al.y), ssm_rate(al.z), ssm_rate(al.w)};
     const float bias = p.dt_bias ? p.dt_bias[dd] : 0.f, skip = p.Dskip ? p.Dskip[dd] : 0.f;
+    const float step = softplus(dt + bias), in = step * x;
+    float y[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        const float delta = softplus(dt[r] + bias), u = delta * x[r];
+        const float delta = __shfl_sync(FULL, step, r, ROWS), u = __shfl_sync(FULL, in, r, ROWS);
         h[r].x = fmaf(ssm_ex2(ssm_exponent(delta, rate[0])), h[r].x, u * B[r].x);
         h[r].y = fmaf(ssm_ex2(ssm_exponent(delta, rate[1])), h[r].y, u * B[r].y);
         h[r].z = fmaf(ssm_ex2(ssm_exponent(delta, rate[2])), h[r].z, u * B[r].z);
         h[r].w = fmaf(ssm_ex2(ssm_exponent(delta, rate[3])), h[r].w, u * B[r].w);
-        float y = fmaf(h[r].x, C[r].x, h[r].y * C[r].y) + fmaf(h[r].z, C[r].z, h[r].w * C[r].w);
-#pragma unroll
-        for (int off = 1; off < LN; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-        y = fmaf(skip, x[r], y);
-        if (p.z) y *= z[r] * ssm_sigmoid(z[r]);
-        if (live && b0 + r < p.B) {
-            const size_t e = (size_t)(b0 + r) * p.D + dd;
-            *reinterpret_cast<float4 *>(p.S_T + e * N + 4 * l) = h[r];
-            if (l == 0) static_cast<T *>(p.y)[e] = from_f32<T>(y);
-        }
+        y[r] = fmaf(h[r].x, C[r].x, h[r].y * C[r].y) + fmaf(h[r].z, C[r].z, h[r].w * C[r].w);
+        if (live && b0 + r < p.B) *reinterpret_cast<float4 *>(p.S_T + ((size_t)(b0 + r) * p.D + dd) * N + 4 * l) = h[r];
     }
+    // Sums over the state: with four rows, half of them go to the neighbour at each of two exchanges, so that row l ends here.
+    float sum = y[0];
+    if constexpr (ROWS == 4) {
+        const bool odd = l & 1, high = l & 2;
+        const float a = (odd ? y[1] : y[0]) + __shfl_xor_sync(FULL, odd ? y[0] : y[1], 1);
+        const float c = (odd ? y[3] : y[2]) + __shfl_xor_sync(FULL, odd ? y[2] : y[3], 1);
+        sum = (high ? c : a) + __shfl_xor_sync(FULL, high ? a : c, 2);
+    }
+#pragma unroll
+    for (int off = ROWS; off < LN; off <<= 1) sum += __shfl_xor_sync(FULL, sum, off);
+    sum = fmaf(skip, x, sum);
+    if (p.z) sum *= z * ssm_sigmoid(z);
+    if (live && l < ROWS && b0 + l < p.B) static_cast<T *>(p.y)[own] = from_f32<T>(sum);
 }
 
 template <typename T, int N>
