@@ -8,13 +8,15 @@
 // row), plus dstate_T's at the last W - 1 places; the first W - 1 are dstate0.
 //
 // Bound by HBM: x is read and y written once.  A thread takes 4 channels and walks down a run of tokens with the last
-// W - 1 rows in registers, so a row is read once by its run and again only as the W - 1 rows before the next.  A run
-// comes into the thread's own slots of shared memory by asynchronous copies, four groups of them under way; the backward
-// refills a group for the next run as soon as it is done with it.  Code for runs inside their row is straight.
-// Arithmetic is fp32, each output rounded once; the sums over tokens go in two stages of fixed order.
-// 8 x 2048 tokens, W = 4, silu, bf16: forward of 6144 channels 78 us (403 MB, 5.2 TB/s), of 2048 27 (134 MB); backward of 2048 62
-// (201 MB, 3.2 TB/s).  An element of the forward is 17 instructions and one of the backward 33, 0.62 and
-// 0.54 of what issues: the copies no longer limit them.
+// W - 1 rows in registers, so a row is read once by its run and again only as the W - 1 rows before the next.  Rows
+// come into the thread's own slots of shared memory by asynchronous copies, a group of them at a time and the next groups under
+// way.  Code for groups inside their row is straight; channels go in pairs, in packed arithmetic.  Runs of the forward
+// are 32 tokens at most; those of the backward, which computes the gradients of the tokens before a run again, as
+// long as fills the GPU.  Arithmetic is fp32, each output rounded once; the sums over tokens go in two stages of fixed order.
+// 8 x 2048 tokens, W = 4, silu, bf16: forward of 6144 channels 70 us (403 MB, 5.8 TB/s), of 2048 26 (134 MB); backward with
+// its sums of 6144 115 us (604 MB, 5.2 TB/s), of 2048 45 (201 MB, 4.5 TB/s; 66 in runs of 32 places), in fp32 72 (403 MB, 5.6 TB/s).
+// The backward's threads need 140 registers: three CTAs of 128 a SM take 45 us, four with 128 registers 47, five 54, seven of
+// 64 threads 52; groups of 12 rows 48 to 53.
 #include <algorithm>
 #include <type_traits>
 
@@ -27,6 +29,8 @@ namespace {
 
 constexpr int NT = CONV_NT;
 constexpr int FOUND = 32;  // long sequences that a CTA of the packed forward fills in together
+template <typename T>
+constexpr int conv_bwd_depth = sizeof(T) == 2 ? 3 : 2;  // groups of the backward's ring: 48 KB a CTA
 template <typename T>
 constexpr int BATCH = sizeof(T) == 2 ? 8 : 4;  // rows of a group of copies, of which a thread's run has four at most
 
@@ -304,68 +308,50 @@ __global__ void __launch_bounds__(NT, 3) conv_fwd_kernel(ConvArgs p, int vecs, i
 }
 
 // ------------------------------------------------------------------------------------ backward
-// A CTA: `lanes` vectors of 4 channels x NT / lanes runs of R places of an extended row (with the W - 1 before them), and every
-// parts-th such tile after it; row_runs runs a row.
+// A CTA: `lanes` vectors of 4 channels x NT / lanes runs of R places of an extended row, and every parts-th such tile after
+// it; row_runs runs a row.  Place e needs ds_e and the W - 1 before, so those before a run are computed again; x and dy
+// come through a ring of groups of G rows in the thread's own slots, G a multiple of every window's length.
 template <typename T, int W, bool SILU>
-__global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, int parts, int row_runs) {
-    constexpr int V = 4, BATCH = efla::BATCH<T>, NT = CONV_BWD_NT, R = 4 * BATCH;
+__global__ void __launch_bounds__(CONV_BWD_NT, CONV_BWD_CTAS) conv_bwd_kernel(ConvArgs p, int vecs, int lanes, int cblocks, ConvRuns plan) {
+    constexpr int V = 4, G = CONV_BWD_GROUP, DEPTH = conv_bwd_depth<T>, NT = CONV_BWD_NT;
     extern __shared__ __align__(16) uint8_t shared[];
-    constexpr int XS = R + 2 * (W - 1);  // slots of x: tokens from e0 - 2 (W - 1) on; of dy: from e0 - (W - 1) on
-    Pack<T, V> *xs = reinterpret_cast<Pack<T, V> *>(shared) + threadIdx.x, *ys = xs + XS * NT;  // slot i at [i NT]
+    Pack<T, V> *xs = reinterpret_cast<Pack<T, V> *>(shared) + threadIdx.x, *ys = xs + DEPTH * G * NT;  // row i at [i NT]
     const int tid = threadIdx.x, lane = tid % lanes, sub = tid / lanes, subs = NT / lanes;
     const int cb = blockIdx.x % cblocks, tile = blockIdx.x / cblocks, v = cb * lanes + lane;
-    const long long runs = (long long)p.B * row_runs, step = (long long)parts * subs;
+    const long long runs = (long long)p.B * plan.row_runs, step = (long long)plan.parts * subs;
     const int ends = p.T + W - 1;
     float2 dw[2][W] = {}, db[2] = {};
     Taps4<W> taps;
     if (v < vecs) taps.load(p, v * V);
-    // Group q of a run's copies: its batch q, and the first with what comes before it.  A group is fetched for the next
-    // run as soon as this one is done with its slots, so three are always under way behind the one that is needed.
-    auto fetch_group = [&](long long run, int q) {
-        if (v < vecs && run < runs) {
-            const int b = (int)(run / row_runs), e0 = (int)(run % row_runs) * R;
-            const long long at = (long long)b * p.T * vecs + v;
-            const Pack<T, V> *x = static_cast<const Pack<T, V> *>(p.x) + at, *y = static_cast<const Pack<T, V> *>(p.dy) + at;
-            if (e0 >= 2 * (W - 1) && e0 + R <= p.T) {
-                x += (long long)(e0 + q * BATCH) * vecs;
-                y += (long long)(e0 + q * BATCH) * vecs;
-                if (q == 0) {
+    for (long long run = (long long)tile * subs + sub; v < vecs && run < runs; run += step) {
+        const int b = (int)(run / plan.row_runs), e0 = (int)(run % plan.row_runs) * plan.run, e1 = min(e0 + plan.run, ends);
+        const long long row = (long long)b * p.T;
+        const Pack<T, V> *x0 = static_cast<const Pack<T, V> *>(p.x) + row * vecs + v, *y0 = static_cast<const Pack<T, V> *>(p.dy) + row * vecs + v;
+        auto fetch_group = [&](int t0, int slot) {  // rows t0 .. of x and dy; past the row's end zeros
+            if (t0 < e1) {
+                const Pack<T, V> *x = x0 + (size_t)t0 * vecs, *y = y0 + (size_t)t0 * vecs;
+                Pack<T, V> *xt = xs + slot * G * NT, *yt = ys + slot * G * NT;
+                if (t0 + G <= p.T) {
 #pragma unroll
-                    for (int i = 0; i < 2 * (W - 1); ++i) fetch(xs + i * NT, x + (long long)(i - 2 * (W - 1)) * vecs, true);
-#pragma unroll
-                    for (int i = 0; i < W - 1; ++i) fetch(ys + i * NT, y + (long long)(i - (W - 1)) * vecs, true);
-                }
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    fetch(xs + (2 * (W - 1) + q * BATCH + k) * NT, x + (size_t)k * vecs, true);
-                    fetch(ys + (W - 1 + q * BATCH + k) * NT, y + (size_t)k * vecs, true);
-                }
-            } else {
-                const Pack<T, V> *state = p.state0 ? static_cast<const Pack<T, V> *>(p.state0) + (long long)b * (W - 1) * vecs + v : nullptr;
-                const int from = q == 0 ? 0 : 2 * (W - 1) + q * BATCH, to = 2 * (W - 1) + (q + 1) * BATCH;
+                    for (int k = 0; k < G; ++k) {
+                        fetch(xt + k * NT, x + (size_t)k * vecs, true);
+                        fetch(yt + k * NT, y + (size_t)k * vecs, true);
+                    }
+                } else {
 #pragma unroll 1
-                for (int i = from; i < to; ++i) {
-                    const int t = e0 - 2 * (W - 1) + i, j = i - (W - 1);
-                    const bool real = t >= 0 && t < p.T, old = t < 0 && t + W - 1 >= 0 && state;
-                    fetch(xs + i * NT, real ? x + (size_t)t * vecs : old ? state + (size_t)(t + W - 1) * vecs : x, real || old);
-                    if (j >= 0) fetch(ys + j * NT, real ? y + (size_t)t * vecs : y, real);
+                    for (int k = 0; k < G; ++k) {
+                        const bool real = t0 + k < p.T;
+                        fetch(xt + k * NT, real ? x + (size_t)k * vecs : x0, real);
+                        fetch(yt + k * NT, real ? y + (size_t)k * vecs : y0, real);
+                    }
                 }
             }
-        }
-        fetch_commit();
-    };
-    const long long run0 = (long long)tile * subs + sub;
+            fetch_commit();
+        };
 #pragma unroll
-    for (int q = 0; q < 4; ++q) fetch_group(run0, q);
-    for (long long run = run0; v < vecs && run < runs; run += step) {
-        const int b = (int)(run / row_runs);
-        const int e0 = (int)(run % row_runs) * R, tb0 = e0 - (W - 1), e1 = min(e0 + R, ends);
-        const long long row = (long long)b * p.T;
-        float2 win[W - 1][2], old[W - 1][2] = {};  // x at t - (W - 1) .. t - 1, ds of the W - 1 tokens before t
-        fetch_wait(3);
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i) unpack(xs[i * NT], win[i]);
-        // ds of token t, whose newest input is x, into the window; with `own` into dw and dbias too
+        for (int q = 0; q < DEPTH; ++q) fetch_group(e0 + q * G, q);
+        float2 win[W - 1][2], old[W - 1][2];  // x at t - (W - 1) .. t - 1, ds of the W - 1 tokens before t
+        // ds of token t, whose newest input is x (`real`: t is in the row); with `own` into dw and dbias too
         auto token = [&](const float2(&x)[2], float2(&ds)[2], bool real, bool own) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -407,22 +393,49 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
                 old[W - 2][h] = ds[h];
             }
         };
-        if (e0 >= 2 * (W - 1) && e0 + R <= p.T) {  // all of it tokens of the row: straight code
+        // The tokens before the run: their inputs (of the state before token 0) and ds
+        {
+            const Pack<T, V> *state = p.state0 ? static_cast<const Pack<T, V> *>(p.state0) + (long long)b * (W - 1) * vecs + v : nullptr;
+            Pack<T, V> xr[2 * (W - 1)], yr[W - 1];
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) {  // the tokens before the run: their ds
+            for (int i = 0; i < 2 * (W - 1); ++i) {
+                const int t = e0 - 2 * (W - 1) + i;
+                xr[i] = {};
+                if (t >= 0 && t < p.T)
+                    xr[i] = x0[(size_t)t * vecs];
+                else if (t < 0 && t + W - 1 >= 0 && state)
+                    xr[i] = state[(size_t)(t + W - 1) * vecs];
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                const int t = e0 - (W - 1) + i;
+                yr[i] = {};
+                if (t >= 0 && t < p.T) yr[i] = y0[(size_t)t * vecs];
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                unpack(xr[i], win[i]);
+                old[i][0] = old[i][1] = make_float2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                const int t = e0 - (W - 1) + i;
                 float2 x[2], ds[2];
-                unpack(xs[(W - 1 + i) * NT], x);
-                unpack(ys[i * NT], ds);
-                token(x, ds, true, false);
+                unpack(xr[W - 1 + i], x);
+                unpack(yr[i], ds);
+                token(x, ds, t >= 0 && t < p.T, false);
                 shift(x, ds);
             }
-            Pack<T, V> *to = static_cast<Pack<T, V> *>(p.dx) + (size_t)(row + tb0) * vecs + v;
+        }
+        Pack<T, V> *to = static_cast<Pack<T, V> *>(p.dx) + (row + e0 - (W - 1)) * vecs + v;  // (at place e0; used from place W - 1 on)
+        int slot = 0;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q, to += (size_t)BATCH * vecs) {
-                if (q > 0) fetch_wait(3);
-                const Pack<T, V> *xq = xs + (2 * (W - 1) + q * BATCH) * NT, *yq = ys + (W - 1 + q * BATCH) * NT;
+        for (int t0 = e0; t0 < e1; t0 += G, to += (size_t)G * vecs) {
+            fetch_wait(DEPTH - 1);
+            const Pack<T, V> *xq = xs + slot * G * NT, *yq = ys + slot * G * NT;
+            if (t0 >= W - 1 && t0 + G <= p.T) {  // all of it tokens of the row: straight code
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
+                for (int k = 0; k < G; ++k) {
                     float2 x[2], ds[2], d[2] = {};
                     unpack(xq[k * NT], x);
                     unpack(yq[k * NT], ds);
@@ -433,59 +446,46 @@ __global__ void __launch_bounds__(CONV_BWD_NT, 3) conv_bwd_kernel(ConvArgs p, in
                     pack(d, r);
                     to[(size_t)k * vecs] = r;
                 }
-                fetch_group(run + step, q);
+            } else {
+#pragma unroll 1
+                for (int t = t0; t < min(t0 + G, e1); ++t) {
+                    float2 x[2], ds[2], d[2] = {};
+                    unpack(xq[(t - t0) * NT], x);
+                    unpack(yq[(t - t0) * NT], ds);  // 0 past the row
+                    token(x, ds, t < p.T, true);
+                    if (p.dstate_T && t >= p.T) unpack(load<T, V>(p.dstate_T, (long long)b * (W - 1) + t - p.T, vecs, v), d);
+                    place_sum(ds, d);
+                    Pack<T, V> r;
+                    pack(d, r);
+                    if (t >= W - 1)
+                        to[(size_t)(t - t0) * vecs] = r;
+                    else if (p.dstate0)
+                        static_cast<Pack<T, V> *>(p.dstate0)[((long long)b * (W - 1) + t) * vecs + v] = r;
+                    shift(x, ds);
+                }
             }
-            continue;
+            fetch_group(t0 + DEPTH * G, slot);
+            slot = slot + 1 == DEPTH ? 0 : slot + 1;
         }
         fetch_wait(0);
-        auto put = [&](void *to, long long at, const float2(&d)[2]) {
-            Pack<T, V> r;
-            pack(d, r);
-            static_cast<Pack<T, V> *>(to)[at * vecs + v] = r;
-        };
-#pragma unroll 1
-        for (int t = tb0; t < e1; ++t) {  // token t's newest input is at place t + W - 1 of the extended row
-            float2 x[2], ds[2];
-            unpack(xs[(t - tb0 + W - 1) * NT], x);
-            unpack(ys[(t - tb0) * NT], ds);  // 0 outside the row
-            token(x, ds, t >= 0 && t < p.T, t >= e0);
-            if (t >= e0) {
-                float2 d[2] = {};
-                if (p.dstate_T && t >= p.T) unpack(load<T, V>(p.dstate_T, (long long)b * (W - 1) + t - p.T, vecs, v), d);
-                place_sum(ds, d);
-                if (t >= W - 1)
-                    put(p.dx, row + t - (W - 1), d);
-                else if (p.dstate0)
-                    put(p.dstate0, (long long)b * (W - 1) + t, d);
-            }
-            shift(x, ds);
-        }
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) fetch_group(run + step, q);
     }
-    fetch_wait(0);
-    float(*red)[V + 1] = reinterpret_cast<float(*)[V + 1]>(shared);  // (the slots are done with)
     // the CTA's sums over its runs, in order: [D][W] then [D] of part `tile`
+    float4 *red = reinterpret_cast<float4 *>(shared);  // (every thread is done with its slots)
     const int sums = p.dbias ? W + 1 : W;
     float *part = p.ws + (size_t)tile * p.D * sums;
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
-        if (j == sums) break;
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float2 r = j < W ? dw[h][j < W ? j : 0] : db[h];
-            red[tid][2 * h] = r.x;
-            red[tid][2 * h + 1] = r.y;
-        }
-        __syncthreads();
-        for (int i = tid; i < lanes * V; i += NT) {
-            const int l = i / V, c = i % V, ch = (cb * lanes + l) * V + c;
-            if (ch >= p.D) continue;
-            float s = 0.f;
-            for (int q = 0; q < subs; ++q) s += red[q * lanes + l][c];
-            part[j < W ? (size_t)ch * W + j : (size_t)p.D * W + ch] = s;
-        }
+        const float2 lo = j < W ? dw[0][j < W ? j : 0] : db[0], hi = j < W ? dw[1][j < W ? j : 0] : db[1];
+        red[j * NT + tid] = make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+    __syncthreads();
+    for (int i = tid; i < sums * lanes * V; i += NT) {
+        const int j = i / (lanes * V), l = i / V % lanes, c = i % V, ch = (cb * lanes + l) * V + c;
+        if (ch >= p.D) continue;
+        float s = 0.f;
+        for (int q = 0; q < subs; ++q) s += reinterpret_cast<const float *>(red + j * NT + q * lanes + l)[c];
+        part[j < W ? (size_t)ch * W + j : (size_t)p.D * W + ch] = s;
     }
 }
 
@@ -564,18 +564,18 @@ cudaError_t fwd(const ConvArgs &a) {
 template <typename T, int W>
 cudaError_t bwd(const ConvArgs &a) {
     const int vecs = a.D / 4, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes;
-    constexpr int RUN = 4 * BATCH<T>;  // conv_bwd_run(a.dtype)
-    const int parts = conv_bwd_parts(a.B, a.T, a.D, a.W, RUN);
-    const size_t smem = (size_t)(2 * RUN + 3 * (W - 1)) * CONV_BWD_NT * sizeof(Pack<T, 4>);
+    const ConvRuns plan = conv_bwd_runs(a.B, a.T, a.D, a.W);
+    constexpr size_t smem = (size_t)2 * conv_bwd_depth<T> * CONV_BWD_GROUP * CONV_BWD_NT * sizeof(Pack<T, 4>);
+    static_assert(smem >= (W + 1) * CONV_BWD_NT * sizeof(float4), "the sums");
     auto go = [&](auto kernel) {
         const cudaError_t e = allow_smem(kernel, smem);
         if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)parts * cblocks, CONV_BWD_NT, smem, a.stream>>>(a, vecs, lanes, cblocks, parts, conv_bwd_runs(a.T, a.W, RUN));
+        kernel<<<(unsigned)plan.parts * cblocks, CONV_BWD_NT, smem, a.stream>>>(a, vecs, lanes, cblocks, plan);
         return cudaGetLastError();
     };
     const cudaError_t e = go(a.silu ? conv_bwd_kernel<T, W, true> : conv_bwd_kernel<T, W, false>);
     if (e != cudaSuccess) return e;
-    return launch_sum_parts(a.ws, parts, a.D * (a.dbias ? W + 1 : W), a.dw, a.dbias, a.D * W, a.stream);
+    return launch_sum_parts(a.ws, plan.parts, a.D * (a.dbias ? W + 1 : W), a.dw, a.dbias, a.D * W, a.stream);
 }
 template <typename T, int W>
 cudaError_t step(const ConvArgs &a) {

@@ -30,17 +30,29 @@ inline int conv_lanes(int vecs) {
     while (n < vecs && n < 32) n *= 2;
     return n;
 }
-constexpr int CONV_NT = 256, CONV_BWD_NT = 128;  // threads a CTA; of the backward
-// Runs of `run` places of a row extended by the W - 1 of its state, and the CTAs a block of channels that share them:
-// one a tile of runs, or as many as are resident at once (three a SM).
-inline int conv_bwd_run(efla_dtype t) { return t == EFLA_BF16 ? 32 : 16; }
-inline int conv_bwd_runs(int T, int W, int run) { return (int)(((long long)T + W - 1 + run - 1) / run); }
-inline int conv_bwd_parts(int B, int T, int D, int W, int run) {
+constexpr int CONV_NT = 256;  // threads a CTA of the forward
+constexpr int CONV_BWD_NT = 128, CONV_BWD_CTAS = 3, CONV_BWD_GROUP = 6;  // of the backward; its CTAs a SM; rows a group of copies
+// The backward's runs: of `run` places (whole groups) of a row extended by the W - 1 of its state, row_runs a row, and
+// `parts` CTAs a block of channels that share them.  Runs are as long as fills the GPU once, twice, .. or four times over,
+// whichever takes the fewest places one after the other, 8 more a run for those before it and the start of its copies.
+struct ConvRuns {
+    int run, row_runs, parts;
+};
+inline ConvRuns conv_bwd_runs(int B, int T, int D, int W) {
     const int vecs = D / 4, lanes = conv_lanes(vecs), cblocks = (vecs + lanes - 1) / lanes, subs = CONV_BWD_NT / lanes;
-    const long long tiles = ((long long)B * conv_bwd_runs(T, W, run) + subs - 1) / subs, most = std::max(1, 152 * 3 / cblocks);
-    if (tiles <= most) return (int)std::max(1LL, tiles);
-    const long long each = (tiles + most - 1) / most;  // (the same number for nearly all)
-    return (int)((tiles + each - 1) / each);
+    const long long most = std::max(1, 152 * CONV_BWD_CTAS / cblocks), ends = (long long)T + W - 1;
+    ConvRuns best{};
+    long long least = 0;
+    for (int fill = 1; fill <= 4; ++fill) {
+        const long long want = std::max(1LL, std::min(fill * most * subs / std::max(1, B), ends / (4 * CONV_BWD_GROUP)));
+        const long long run = ((ends + want - 1) / want + CONV_BWD_GROUP - 1) / CONV_BWD_GROUP * CONV_BWD_GROUP;
+        const long long row_runs = (ends + run - 1) / run, tiles = std::max(1LL, (B * row_runs + subs - 1) / subs);
+        const long long each = (tiles + most - 1) / most, time = each * (run + 8);
+        if (fill > 1 && time >= least) continue;
+        least = time;
+        best.run = (int)run, best.row_runs = (int)row_runs, best.parts = (int)((tiles + each - 1) / each);
+    }
+    return best;
 }
 
 cudaError_t launch_conv(const ConvArgs &a);

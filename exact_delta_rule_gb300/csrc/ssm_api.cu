@@ -105,7 +105,7 @@ efla_status efla_causal_conv_bwd_workspace(int B, int T, int D, int W, size_t *b
     if (!bytes) return api_fail(EFLA_ERR_INVALID_ARG, "bytes must be non-NULL");
     const efla_status s = check_conv(B, T, D, W, EFLA_F32, EFLA_ACT_NONE);
     if (s != EFLA_OK) return s;
-    const int parts = std::max(conv_bwd_parts(B, T, D, W, conv_bwd_run(EFLA_BF16)), conv_bwd_parts(B, T, D, W, conv_bwd_run(EFLA_F32)));
+    const int parts = conv_bwd_runs(B, T, D, W).parts;
     *bytes = (size_t)parts * D * (W + 1) * sizeof(float);
     return api_ok();
 }
