@@ -15,7 +15,7 @@
 // long as fills the GPU.  Arithmetic is fp32, each output rounded once; the sums over tokens go in two stages of fixed order.
 // 8 x 2048 tokens, W = 4, silu, bf16: forward of 6144 channels 70 us (403 MB, 5.8 TB/s), of 2048 26 (134 MB); backward with
 // its sums of 6144 115 us (604 MB, 5.2 TB/s), of 2048 45 (201 MB, 4.5 TB/s; 66 in runs of 32 places), in fp32 72 (403 MB, 5.6 TB/s).
-// The backward's threads need 140 registers: three CTAs of 128 a SM take 45 us, four with 128 registers 47, five 54, seven of
+// The backward's threads need 148 registers: three CTAs of 128 a SM take 45 us, four with 128 registers 47, five 54, seven of
 // 64 threads 52; groups of 12 rows 48 to 53.
 #include <algorithm>
 #include <type_traits>
@@ -91,28 +91,6 @@ __device__ __forceinline__ void store(void *p, long long row, int vecs, int v, c
     Pack<T, V> r;
     pack(x, r);
     static_cast<Pack<T, V> *>(p)[row * vecs + v] = r;
-}
-
-// An asynchronous copy of a Pack into this thread's slot of shared memory; zeros where it is not live.
-template <typename P>
-__device__ __forceinline__ void fetch(P *dst, const P *src, bool live) {
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    if constexpr (sizeof(P) == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(live ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(src), "r"(live ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Until at most `left` (0 to 3) of the latest groups are under way.
-__device__ __forceinline__ void fetch_wait(int left) {
-    if (left >= 3)
-        asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (left == 2)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (left == 1)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <int W, int V>

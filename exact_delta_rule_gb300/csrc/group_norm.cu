@@ -5,7 +5,8 @@
 //
 // Bound by HBM: x (and dy) read, y (dx) written.  Which way a call goes:
 //   L = 1 and groups of whole vectors up to 32 of them: a group of a row lies in the registers of its lanes, whose sums
-//     are shuffles; one pass (16384 rows of 16 groups of 128, bf16: forward 26 us for 134 MB, backward 40 for 202);
+//     are shuffles; one pass, the next rows' copies under way (16384 rows of 16 groups of 128, bf16: forward 24 us for
+//     134 MB, backward with its sums 38 for 202; 65536 rows 86 and 128, 6.2 TB/s; 92 and 144 with four rows loaded together);
 //   samples of few elements, or many of up to 16 KB: one a warp, in shared memory;
 //   forward, other samples: tiles of whole groups in the shared memory of a cluster, whose CTAs share out the positions
 //     and read one another's sums; one pass (8 maps of 4096 positions x 320 channels in 32 groups: 14 us, 33 in three);
@@ -44,11 +45,16 @@ __device__ __forceinline__ void affine(const GroupNormArgs &p, int c0, float (&w
 
 // ------------------------------------------------------------------------------------ whole rows (L = 1)
 // A warp holds 32 / TEAM groups of a row, a group in the first C / G / V lanes of its TEAM; a CTA 8 rows of one block
-// of groups, and every parts-th 8 rows after them.
+// of groups, and every parts-th 8 rows after them; a warp's rows come through a ring of copies into its threads' own slots.
 template <typename T, int TEAM, bool BWD, bool SILU>
 __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks, int parts) {
-    constexpr int V = Vec<T>::N, PER = 32 / TEAM, SUBS = NT / 32, UNROLL = 4;
-    __shared__ float red[BWD ? SUBS : 1][BWD ? 32 * V : 1];
+    constexpr int V = Vec<T>::N, PER = 32 / TEAM, SUBS = NT / 32, DEPTH = 4;
+    constexpr int SLOTS = DEPTH * NT, SUMS = BWD ? SUBS * 32 * V : 0;  // (the sums take the place of the copies)
+    constexpr int BYTES = SLOTS * (BWD ? 40 : 16);
+    static_assert(SUMS * 4 <= BYTES, "the sums");
+    __shared__ __align__(16) uint8_t shared[BYTES];
+    uint4 *xs = reinterpret_cast<uint4 *>(shared) + threadIdx.x, *ds = xs + SLOTS;  // slot i at [i NT]
+    float2 *ss = reinterpret_cast<float2 *>(shared + SLOTS * 32) + threadIdx.x;
     const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5, l = lane % TEAM;
     const int block = blockIdx.x % blocks, part = blockIdx.x / blocks;
     const int g = block * PER + lane / TEAM, gv = p.C / p.G / V, vecs = p.C / V;
@@ -57,29 +63,31 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
     const float inv = 1.f / (float)(p.C / p.G);
     float w[V], b[V], dw[V] = {}, db[V] = {};
     affine(p, v * V, w, b);
-    const long long step = (long long)parts * SUBS;
-    for (long long row0 = (long long)part * SUBS + sub; row0 < p.rows; row0 += step * UNROLL) {  // (the same for a warp)
-        uint4 rx[UNROLL], rd[UNROLL];
-        float2 st[UNROLL];
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-            const long long row = row0 + i * step;
-            rx[i] = rd[i] = make_uint4(0, 0, 0, 0);
-            st[i] = make_float2(0.f, 0.f);
-            if (live && row < p.rows) {
-                rx[i] = static_cast<const uint4 *>(p.x)[row * vecs + v];
-                if (BWD) {
-                    rd[i] = static_cast<const uint4 *>(p.dy)[row * vecs + v];
-                    st[i] = reinterpret_cast<const float2 *>(p.stats)[row * p.G + g];
-                }
+    const long long step = (long long)parts * SUBS, first = (long long)part * SUBS + sub;
+    // A row's copies, zeros for what is not there: nothing in any sum
+    auto fetch_row = [&](long long row, int slot) {
+        if (row < p.rows) {
+            const long long at = row * vecs + v;
+            fetch(xs + slot * NT, static_cast<const uint4 *>(p.x) + at, live);
+            if (BWD) {
+                fetch(ds + slot * NT, static_cast<const uint4 *>(p.dy) + at, live);
+                fetch(ss + slot * NT, reinterpret_cast<const float2 *>(p.stats) + (live ? row * p.G + g : 0), live);
             }
         }
+        fetch_commit();
+    };
 #pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
+    for (int i = 0; i < DEPTH; ++i) fetch_row(first + i * step, i);
+    for (long long row0 = first; row0 < p.rows; row0 += step * DEPTH) {  // (the same for a warp)
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
             const long long row = row0 + i * step;
-            const bool writes = live && row < p.rows;  // (a row past the last is zeros: nothing in any sum)
+            if (row >= p.rows) break;
+            fetch_wait(DEPTH - 1);
+            const uint4 rx = xs[i * NT], rd = BWD ? ds[i * NT] : rx;
+            const float2 st = BWD ? ss[i * NT] : make_float2(0.f, 0.f);
             float x[V];
-            Vec<T>::unpack(rx[i], x);
+            Vec<T>::unpack(rx, x);
             if (!BWD) {
                 float m = 0.f, q = 0.f;
 #pragma unroll
@@ -94,16 +102,16 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
                 const float r = rsqrtf(row_sum<TEAM>(q) * inv + p.eps);
 #pragma unroll
                 for (int e = 0; e < V; ++e) x[e] = act<SILU>(fmaf(x[e] * r, w[e], b[e]));
-                if (writes) {
+                if (live) {
                     static_cast<uint4 *>(p.y)[row * vecs + v] = Vec<T>::pack(x);
                     if (p.stats && l == 0) reinterpret_cast<float2 *>(p.stats)[row * p.G + g] = make_float2(m, r);
                 }
             } else {
                 float d[V], s1 = 0.f, s2 = 0.f;
-                Vec<T>::unpack(rd[i], d);
+                Vec<T>::unpack(rd, d);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float n = (x[e] - st[i].x) * st[i].y;
+                    const float n = (x[e] - st.x) * st.y;
                     d[e] *= dact<SILU>(fmaf(n, w[e], b[e]));
                     dw[e] = fmaf(d[e], n, dw[e]);
                     db[e] += d[e];
@@ -115,25 +123,27 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
                 s1 = row_sum<TEAM>(s1) * inv;
                 s2 = row_sum<TEAM>(s2) * inv;
 #pragma unroll
-                for (int e = 0; e < V; ++e) x[e] = st[i].y * (d[e] - s1 - x[e] * s2);
-                if (writes) static_cast<uint4 *>(p.dx)[row * vecs + v] = Vec<T>::pack(x);
+                for (int e = 0; e < V; ++e) x[e] = st.y * (d[e] - s1 - x[e] * s2);
+                if (live) static_cast<uint4 *>(p.dx)[row * vecs + v] = Vec<T>::pack(x);
             }
+            fetch_row(row + step * DEPTH, i);
         }
     }
     if (BWD) {  // the CTA's sums over its rows, in order: db then dw
-        float *out = p.ws + (size_t)part * 2 * p.C;
+        fetch_wait(0);
+        float *red = reinterpret_cast<float *>(shared), *out = p.ws + (size_t)part * 2 * p.C;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < V; ++e) red[sub][lane * V + e] = which ? dw[e] : db[e];
+            for (int e = 0; e < V; ++e) red[(sub * 32 + lane) * V + e] = which ? dw[e] : db[e];
             __syncthreads();
             for (int i = threadIdx.x; i < 32 * V; i += NT) {
                 const int ln = i / V, gg = block * PER + ln / TEAM, ll = ln % TEAM;
                 if (gg >= p.G || ll >= gv) continue;
                 float s = 0.f;
 #pragma unroll
-                for (int k = 0; k < SUBS; ++k) s += red[k][i];
+                for (int k = 0; k < SUBS; ++k) s += red[k * 32 * V + i];
                 out[which * p.C + (gg * gv + ll) * V + i % V] = s;
             }
         }

@@ -40,7 +40,7 @@ inline int gn_blocks(int C, int G, efla_dtype t) {
     return (G + per - 1) / per;
 }
 inline int gn_row_parts(int rows, int C, int G, efla_dtype t) {
-    const int most = std::max(1, 304 / gn_blocks(C, G, t));
+    const int most = std::max(1, 456 / gn_blocks(C, G, t));
     return std::max(1, std::min(most, (rows + 7) / 8));
 }
 // Vectors of a row that a CTA's threads cover in the other kernels, and the chunks its positions come in: CTAs

@@ -70,4 +70,26 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
+// An asynchronous copy of 16 or 8 bytes into this thread's slot of shared memory; zeros where it is not live.
+template <typename P>
+__device__ __forceinline__ void fetch(P *dst, const P *src, bool live) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (sizeof(P) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(live ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(src), "r"(live ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most `left` (0 to 3) of the latest groups are under way.
+__device__ __forceinline__ void fetch_wait(int left) {
+    if (left >= 3)
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (left == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (left == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 }  // namespace efla

@@ -144,6 +144,13 @@ def test_convolution_backward_shapes(dtype, B, T, D):
     check_conv_bwd(conv_inputs(B=B, T=T, D=D, dtype=dtype), silu=True)
 
 
+@pytest.mark.parametrize("B, T, D", [(500, 20, 2048), (36, 250, 6144), (1, 9001, 512)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_convolution_backward_fills_the_gpu(dtype, B, T, D):
+    """Several tiles of runs a CTA, and runs longer than the ring of copies."""
+    check_conv_bwd(conv_inputs(B=B, T=T, D=D, dtype=dtype), silu=True)
+
+
 def check_conv_bwd(a, silu):
     gen = torch.Generator(device="cuda").manual_seed(5)
     B, T, D = a["x"].shape
