@@ -22,6 +22,7 @@ namespace efla {
 namespace {
 
 constexpr int NT = GN_NT;
+__host__ __device__ constexpr int gn_group_depth(int each) { return each > 2 ? 2 : 3; }  // samples of the ring
 
 template <bool SILU>
 __device__ __forceinline__ float act(float s) { return SILU ? s * quick_sigmoid(s) : s; }
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
     const int block = blockIdx.x % blocks, part = blockIdx.x / blocks;
     const int g = block * PER + lane / TEAM, gv = p.C / p.G / V, vecs = p.C / V;
     const bool live = g < p.G && l < gv;
-    const int v = live ? g * gv + l : 0;
+    const int v = live ? g * gv + l : min(g, p.G - 1) * gv;  // (of the same group: what its parameters do stays in it)
     const float inv = 1.f / (float)(p.C / p.G);
     float w[V], b[V], dw[V] = {}, db[V] = {};
     affine(p, v * V, w, b);
@@ -145,6 +146,146 @@ __global__ void __launch_bounds__(NT) gn_rows_kernel(GroupNormArgs p, int blocks
 #pragma unroll
                 for (int k = 0; k < SUBS; ++k) s += red[k * 32 * V + i];
                 out[which * p.C + (gg * gv + ll) * V + i % V] = s;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------ a group a team
+// A group of a sample lies in the registers of TEAM threads, EACH vectors of a thread, its sums are joined through shared
+// memory (two barriers forward, one backward).  A CTA has the same group of NTH / TEAM samples at a time, so that a thread's
+// channels stay the same, and its samples come through a ring of copies into its own slots.
+template <typename T, int TEAM, int EACH, bool BWD, bool SILU>
+__global__ void __launch_bounds__(TEAM > NT ? TEAM : NT) gn_group_kernel(GroupNormArgs p, int parts) {
+    constexpr int V = Vec<T>::N, NTH = TEAM > NT ? TEAM : NT, TEAMS = NTH / TEAM, DEPTH = gn_group_depth(EACH);
+    constexpr int SLOTS = DEPTH * EACH * NTH;
+    static_assert(!BWD || SLOTS * 32 >= NTH * EACH * V * 4, "the sums take the place of the copies");
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float2 joined[2][NTH / 32];
+    const int tid = threadIdx.x, team = tid / TEAM, l = tid % TEAM;
+    const int g = blockIdx.x % p.G, part = blockIdx.x / p.G, gv = p.C / p.G / V, vecs = p.C / V, total = p.L * gv;
+    uint4 *xs = reinterpret_cast<uint4 *>(smem) + tid, *ds = xs + SLOTS;  // vector k of slot i at [(i EACH + k) NTH]
+    float2 *ss = reinterpret_cast<float2 *>(smem + (size_t)SLOTS * 32) + tid;
+    const float inv = 1.f / ((float)p.L * (float)(p.C / p.G));
+    bool live[EACH];
+    long long at[EACH];
+    float w[EACH][V], b[EACH][V], dw[EACH][V] = {}, db[EACH][V] = {};
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int i = k * TEAM + l;
+        live[k] = i < total;
+        at[k] = live[k] ? (long long)(i / gv) * vecs + g * gv + i % gv : 0;
+        affine(p, (g * gv + i % gv) * V, w[k], b[k]);
+    }
+    const long long sample = (long long)p.L * vecs, step = (long long)parts * TEAMS, from = (long long)part * TEAMS;
+    // A sample's copies, zeros for what is not there: nothing in any sum
+    auto fetch_sample = [&](long long row, int slot) {
+        const bool real = row < p.rows;
+        const long long base = real ? row * sample : 0;
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+            fetch(xs + (slot * EACH + k) * NTH, static_cast<const uint4 *>(p.x) + base + at[k], real && live[k]);
+            if (BWD) fetch(ds + (slot * EACH + k) * NTH, static_cast<const uint4 *>(p.dy) + base + at[k], real && live[k]);
+        }
+        if (BWD) fetch(ss + slot * NTH, reinterpret_cast<const float2 *>(p.stats) + (real ? row * p.G + g : 0), real);
+        fetch_commit();
+    };
+    int turn = 0;  // (the buffer of the sums before last is free: every thread has been through a barrier since it read it)
+    auto join = [&](float2 v) {
+        v.x = row_sum<32>(v.x);
+        v.y = row_sum<32>(v.y);
+        if (tid % 32 == 0) joined[turn][tid / 32] = v;
+        __syncthreads();
+        v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < TEAM / 32; ++i) {
+            const float2 o = joined[turn][team * (TEAM / 32) + i];
+            v.x += o.x;
+            v.y += o.y;
+        }
+        turn ^= 1;
+        return v;
+    };
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) fetch_sample(from + team + i * step, i);
+    int slot = 0;
+    for (long long row0 = from; row0 < p.rows; row0 += step) {  // (the same for a CTA)
+        const long long row = row0 + team;
+        const bool real = row < p.rows;
+        fetch_wait(DEPTH - 1);
+        float x[EACH][V], d[EACH][V];
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+            Vec<T>::unpack(xs[(slot * EACH + k) * NTH], x[k]);
+            if (BWD) Vec<T>::unpack(ds[(slot * EACH + k) * NTH], d[k]);
+        }
+        if (!BWD) {
+            float m = 0.f, q = 0.f;
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) m += x[k][e];
+            m = join(make_float2(m, 0.f)).x * inv;
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    x[k][e] -= live[k] ? m : 0.f;
+                    q = fmaf(x[k][e], x[k][e], q);
+                }
+            const float r = rsqrtf(join(make_float2(q, 0.f)).x * inv + p.eps);
+#pragma unroll
+            for (int k = 0; k < EACH; ++k) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[k][e] = act<SILU>(fmaf(x[k][e] * r, w[k][e], b[k][e]));
+                if (real && live[k]) static_cast<uint4 *>(p.y)[row * sample + at[k]] = Vec<T>::pack(x[k]);
+            }
+            if (p.stats && real && l == 0) reinterpret_cast<float2 *>(p.stats)[row * p.G + g] = make_float2(m, r);
+        } else {
+            const float2 st = ss[slot * NTH];
+            float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float n = live[k] ? (x[k][e] - st.x) * st.y : 0.f;
+                    d[k][e] *= dact<SILU>(fmaf(n, w[k][e], b[k][e]));
+                    dw[k][e] = fmaf(d[k][e], n, dw[k][e]);
+                    db[k][e] += d[k][e];
+                    d[k][e] *= w[k][e];
+                    x[k][e] = n;
+                    s.x += d[k][e];
+                    s.y = fmaf(d[k][e], n, s.y);
+                }
+            s = join(s);
+            s.x *= inv;
+            s.y *= inv;
+#pragma unroll
+            for (int k = 0; k < EACH; ++k) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[k][e] = st.y * (d[k][e] - s.x - x[k][e] * s.y);
+                if (real && live[k]) static_cast<uint4 *>(p.dx)[row * sample + at[k]] = Vec<T>::pack(x[k]);
+            }
+        }
+        fetch_sample(row + DEPTH * step, slot);
+        slot = slot + 1 == DEPTH ? 0 : slot + 1;
+    }
+    if (BWD) {  // the CTA's sums over its samples and their positions, in order: db then dw
+        fetch_wait(0);
+        float *red = reinterpret_cast<float *>(smem), *out = p.ws + (size_t)part * 2 * p.C + g * gv * V;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) red[((team * EACH + k) * TEAM + l) * V + e] = which ? dw[k][e] : db[k][e];
+            __syncthreads();
+            for (int c = tid; c < gv * V; c += NTH) {
+                float s = 0.f;
+                for (int t = 0; t < TEAMS; ++t)
+                    for (int i = c / V; i < total; i += gv) s += red[(t * EACH * TEAM + i) * V + c % V];
+                out[(size_t)which * p.C + c] = s;
             }
         }
     }
@@ -533,7 +674,7 @@ __global__ void __launch_bounds__(NT) gn_slab_kernel(GroupNormArgs p, GnSlab s) 
 
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
-    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+    return bytes > 47 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
 }
 
 template <typename T, bool SILU>
@@ -599,6 +740,31 @@ cudaError_t whole(const GroupNormArgs &a) {
 }
 
 template <typename T, bool BWD, bool SILU>
+cudaError_t group(const GroupNormArgs &a) {
+    const GnTeam k = gn_group(a.L, a.C, a.G, a.dtype);
+    const int parts = gn_group_parts(a.rows, a.G, k), threads = std::max(k.threads, NT);
+    const size_t smem = (size_t)gn_group_depth(k.each) * threads * (k.each * (BWD ? 32 : 16) + (BWD ? 8 : 0));
+    auto go = [&](auto kernel) {
+        const cudaError_t e = allow_smem(kernel, smem);
+        if (e != cudaSuccess) return e;
+        kernel<<<(unsigned)parts * a.G, threads, smem, a.stream>>>(a, parts);
+        return cudaGetLastError();
+    };
+    cudaError_t e = cudaErrorInvalidValue;
+    if constexpr (sizeof(T) == 4) {
+        if (k.each == 4) e = go(gn_group_kernel<T, 512, 4, BWD, SILU>);
+    }
+    if (k.each < 4)
+        e = k.each == 2        ? go(gn_group_kernel<T, 512, 2, BWD, SILU>)
+            : k.threads == 512 ? go(gn_group_kernel<T, 512, 1, BWD, SILU>)
+            : k.threads == 256 ? go(gn_group_kernel<T, 256, 1, BWD, SILU>)
+            : k.threads == 128 ? go(gn_group_kernel<T, 128, 1, BWD, SILU>)
+                               : go(gn_group_kernel<T, 64, 1, BWD, SILU>);
+    if (e != cudaSuccess || !BWD) return e;
+    return launch_sum_parts(a.ws, parts, 2 * a.C, a.db, a.dw, a.C, a.stream);
+}
+
+template <typename T, bool BWD, bool SILU>
 cudaError_t general(GroupNormArgs a) {
     const int vecs = a.C / Vec<T>::N, lanes = gn_lanes(vecs), blocks = (vecs + lanes - 1) / lanes;
     const int chunks = gn_chunks(a.rows, a.L, a.C, a.dtype), tiles = (a.L + NT / lanes * 4 - 1) / (NT / lanes * 4);
@@ -617,11 +783,14 @@ cudaError_t general(GroupNormArgs a) {
 
 template <typename T, bool BWD, bool SILU>
 cudaError_t path(const GroupNormArgs &a) {
-    if (gn_whole(a.L, a.C, a.G, a.dtype)) return whole<T, BWD, SILU>(a);
-    if (gn_warps(a.rows, a.L, a.C, a.dtype)) return warps<T, BWD, SILU>(a);
-    if (!BWD) {
-        const GnSlab s = gn_slab(a.rows, a.L, a.C, a.G, a.dtype);
-        if (s.vecs) return slab<T, SILU>(a, s);
+    switch (gn_way(a.rows, a.L, a.C, a.G, a.dtype, BWD)) {
+        case GnWay::ROWS: return whole<T, BWD, SILU>(a);
+        case GnWay::WARP: return warps<T, BWD, SILU>(a);
+        case GnWay::GROUP: return group<T, BWD, SILU>(a);
+        case GnWay::SLAB:
+            if constexpr (!BWD) return slab<T, SILU>(a, gn_slab(a.rows, a.L, a.C, a.G, a.dtype));
+            break;
+        case GnWay::GENERAL: break;
     }
     return general<T, BWD, SILU>(a);
 }

@@ -85,11 +85,38 @@ inline GnSlab gn_slab(int rows, int L, int C, int G, efla_dtype t) {
     if ((long long)each * vecs * 16 > 160 * 1024) return {0, 0, 0, 0};
     return {vecs, tiles, k, each};
 }
+// A group of a sample, of whole vectors (two side by side at least where a sample has several positions), in the
+// registers of a team of threads, 8192 elements at most: the team's threads and the vectors of each.
+struct GnTeam {
+    int threads, each;
+};
+inline GnTeam gn_group(int L, int C, int G, efla_dtype t) {
+    const int V = gn_vec(t), cg = C / G;
+    const long long n = (long long)L * cg;
+    if (cg % V || (L > 1 && cg < 2 * V) || n > 8192 || n <= 32 * V) return {0, 0};
+    const int vecs = (int)(n / V);
+    return vecs <= 512 ? GnTeam{std::max(64, gn_team(vecs)), 1} : GnTeam{512, vecs <= 1024 ? 2 : 4};
+}
+// The CTAs of a group, which share its samples: three a SM of 256 threads, or one of 512, all groups together.
+inline int gn_group_parts(int rows, int G, const GnTeam &k) {
+    const int at_once = k.threads < GN_NT ? GN_NT / k.threads : 1, most = std::max(1, (k.threads > GN_NT ? 304 : 456) / G);
+    return std::max(1, std::min(most, (rows + at_once - 1) / at_once));
+}
+// Which way a call goes.
+enum class GnWay { ROWS, WARP, GROUP, SLAB, GENERAL };
+inline GnWay gn_way(int rows, int L, int C, int G, efla_dtype t, bool bwd) {
+    if (gn_whole(L, C, G, t)) return GnWay::ROWS;
+    if ((long long)L * C > 1024 && gn_group(L, C, G, t).threads) return GnWay::GROUP;
+    if (gn_warps(rows, L, C, t)) return GnWay::WARP;
+    return !bwd && gn_slab(rows, L, C, G, t).vecs ? GnWay::SLAB : GnWay::GENERAL;
+}
 inline size_t gn_ws(int rows, int L, int C, int G, efla_dtype t, bool bwd) {
-    if (gn_whole(L, C, G, t)) return bwd ? (size_t)gn_row_parts(rows, C, G, t) * 2 * C : 0;
-    if (!bwd && (gn_warps(rows, L, C, t) || gn_slab(rows, L, C, G, t).vecs)) return 0;
-    if (gn_warps(rows, L, C, t)) return (size_t)gn_column_chunks(rows, L, C, t) * 2 * C;
-    return (size_t)rows * gn_chunks(rows, L, C, t) * 2 * C + (size_t)rows * G * 2;
+    const GnWay way = gn_way(rows, L, C, G, t, bwd);
+    if (way == GnWay::GENERAL) return (size_t)rows * gn_chunks(rows, L, C, t) * 2 * C + (size_t)rows * G * 2;
+    if (!bwd) return 0;
+    return 2 * (size_t)C * (way == GnWay::ROWS    ? gn_row_parts(rows, C, G, t)
+                            : way == GnWay::GROUP ? gn_group_parts(rows, G, gn_group(L, C, G, t))
+                                                  : gn_column_chunks(rows, L, C, t));
 }
 
 cudaError_t launch_group_norm(const GroupNormArgs &a);

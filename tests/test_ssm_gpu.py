@@ -432,6 +432,28 @@ def test_group_norm_of_maps(dtype, silu, shape, groups):
     check_group_norm(shape, groups, dtype, silu)
 
 
+@pytest.mark.parametrize("shape, groups", [
+    ((5, 2048), 1), ((1, 1040), 2), ((901, 1032), 1), ((3, 4104), 3), ((2, 8192), 1), ((40, 16384), 2), ((3, 8200), 1),
+    ((700, 16, 256), 8), ((9, 100, 768), 12), ((5, 64, 512), 32), ((1, 5, 7, 240), 5), ((2, 511, 32), 2), ((610, 2, 4096), 1)])
+@pytest.mark.parametrize("dtype, silu", [(F32, True), (BF16, True), (BF16, False)])
+def test_group_norm_of_groups_a_team_holds(dtype, silu, shape, groups):
+    check_group_norm(shape, groups, dtype, silu)
+
+
+def test_group_norm_keeps_a_bad_parameter_in_its_group():
+    for shape, groups in [((33, 520), 13), ((33, 2080), 2), ((9, 20, 520), 5)]:
+        x, dy = torch.randn(shape, device="cuda"), torch.randn(shape, device="cuda")
+        w, b = torch.randn(shape[-1], device="cuda"), torch.randn(shape[-1], device="cuda")
+        y, stats = efla.group_norm(x, w, b, groups, activation="silu", return_stats=True)
+        good = efla.group_norm_bwd(x, w, b, groups, stats, dy, activation="silu")
+        b[0] = math.nan
+        y2 = efla.group_norm(x, w, b, groups, activation="silu")
+        bad = efla.group_norm_bwd(x, w, b, groups, stats, dy, activation="silu")
+        each = shape[-1] // groups
+        assert torch.equal(y2[..., 1:], y[..., 1:])
+        assert torch.equal(bad["dx"][..., each:], good["dx"][..., each:])
+
+
 @pytest.mark.parametrize("shape, groups", [((20, 512), 4), ((2, 300, 64), 4)])
 def test_group_norm_extremes(shape, groups):
     check_group_norm(shape, groups, F32, True, affine=False)
