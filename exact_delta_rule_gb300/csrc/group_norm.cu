@@ -7,6 +7,9 @@
 //   L = 1 and groups of whole vectors up to 32 of them: a group of a row lies in the registers of its lanes, whose sums
 //     are shuffles; one pass, the next rows' copies under way (16384 rows of 16 groups of 128, bf16: forward 24 us for
 //     134 MB, backward with its sums 38 for 202; 65536 rows 86 and 128, 6.2 TB/s; 92 and 144 with four rows loaded together);
+//   groups of whole vectors and up to 8192 elements of a sample: in the registers of 64 to 512 threads; one pass, bound by the
+//     barriers of its sums and by issue (16384 rows of 2048 in one group, bf16: forward 38 us, with gradients 92; 51 and
+//     189 as a warp's samples; 4096 samples of 16 x 256 in 8 groups 21 and 55; 94 and 238 a warp);
 //   samples of few elements, or many of up to 16 KB: one a warp, in shared memory;
 //   forward, other samples: tiles of whole groups in the shared memory of a cluster, whose CTAs share out the positions
 //     and read one another's sums; one pass (8 maps of 4096 positions x 320 channels in 32 groups: 14 us, 33 in three);
@@ -191,9 +194,9 @@ __global__ void __launch_bounds__(TEAM > NT ? TEAM : NT) gn_group_kernel(GroupNo
         fetch_commit();
     };
     int turn = 0;  // (the buffer of the sums before last is free: every thread has been through a barrier since it read it)
-    auto join = [&](float2 v) {
+    auto join = [&](float2 v) {  // (forward: of x alone)
         v.x = row_sum<32>(v.x);
-        v.y = row_sum<32>(v.y);
+        if (BWD) v.y = row_sum<32>(v.y);
         if (tid % 32 == 0) joined[turn][tid / 32] = v;
         __syncthreads();
         v = make_float2(0.f, 0.f);
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(TEAM > NT ? TEAM : NT) gn_group_kernel(GroupNo
         for (int i = 0; i < TEAM / 32; ++i) {
             const float2 o = joined[turn][team * (TEAM / 32) + i];
             v.x += o.x;
-            v.y += o.y;
+            if (BWD) v.y += o.y;
         }
         turn ^= 1;
         return v;
@@ -742,7 +745,7 @@ cudaError_t whole(const GroupNormArgs &a) {
 template <typename T, bool BWD, bool SILU>
 cudaError_t group(const GroupNormArgs &a) {
     const GnTeam k = gn_group(a.L, a.C, a.G, a.dtype);
-    const int parts = gn_group_parts(a.rows, a.G, k), threads = std::max(k.threads, NT);
+    const int parts = gn_group_parts(a.rows, a.G, k, BWD), threads = std::max(k.threads, NT);
     const size_t smem = (size_t)gn_group_depth(k.each) * threads * (k.each * (BWD ? 32 : 16) + (BWD ? 8 : 0));
     auto go = [&](auto kernel) {
         const cudaError_t e = allow_smem(kernel, smem);

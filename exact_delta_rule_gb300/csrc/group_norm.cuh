@@ -97,9 +97,10 @@ inline GnTeam gn_group(int L, int C, int G, efla_dtype t) {
     const int vecs = (int)(n / V);
     return vecs <= 512 ? GnTeam{std::max(64, gn_team(vecs)), 1} : GnTeam{512, vecs <= 1024 ? 2 : 4};
 }
-// The CTAs of a group, which share its samples: three a SM of 256 threads, or one of 512, all groups together.
-inline int gn_group_parts(int rows, int G, const GnTeam &k) {
-    const int at_once = k.threads < GN_NT ? GN_NT / k.threads : 1, most = std::max(1, (k.threads > GN_NT ? 304 : 456) / G);
+// The CTAs of a group, which share its samples: of 256 threads six a SM forward and three backward, of 512 half as
+// many, all groups together.
+inline int gn_group_parts(int rows, int G, const GnTeam &k, bool bwd) {
+    const int at_once = k.threads < GN_NT ? GN_NT / k.threads : 1, most = std::max(1, (k.threads > GN_NT ? (bwd ? 304 : 456) : bwd ? 456 : 912) / G);
     return std::max(1, std::min(most, (rows + at_once - 1) / at_once));
 }
 // Which way a call goes.
@@ -115,7 +116,7 @@ inline size_t gn_ws(int rows, int L, int C, int G, efla_dtype t, bool bwd) {
     if (way == GnWay::GENERAL) return (size_t)rows * gn_chunks(rows, L, C, t) * 2 * C + (size_t)rows * G * 2;
     if (!bwd) return 0;
     return 2 * (size_t)C * (way == GnWay::ROWS    ? gn_row_parts(rows, C, G, t)
-                            : way == GnWay::GROUP ? gn_group_parts(rows, G, gn_group(L, C, G, t))
+                            : way == GnWay::GROUP ? gn_group_parts(rows, G, gn_group(L, C, G, t), true)
                                                   : gn_column_chunks(rows, L, C, t));
 }
 
