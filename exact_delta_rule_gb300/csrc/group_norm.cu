@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(NT) gn_sums_kernel(GroupNormArgs p, int lanes,
     const long long all = JOINT ? (long long)p.rows * p.L : p.L, each = (all + chunks - 1) / chunks;
     const long long from = chunk * each, to = min(all, from + each);
     float a[V] = {}, q[V] = {};
-    if (v < vecs) {
+    if (v < vecs && sub < subs) {
         const uint4 *x = static_cast<const uint4 *>(p.x) + (size_t)row * p.L * vecs + v;
         float k[V], r[V], w[V], b[V];
         if (BWD) {
@@ -323,31 +323,46 @@ __global__ void __launch_bounds__(NT) gn_sums_kernel(GroupNormArgs p, int lanes,
             Vec<T>::unpack(x[0], k);
         }
         const uint4 *dy = BWD ? static_cast<const uint4 *>(p.dy) + (size_t)row * p.L * vecs + v : nullptr;
-#pragma unroll 4
-        for (long long t = from + sub; t < to; t += subs) {
-            float f[V], d[V];
-            Vec<T>::unpack(x[(size_t)t * vecs], f);
-            if (BWD) Vec<T>::unpack(dy[(size_t)t * vecs], d);
-            if (JOINT) {
-                const float2 *stats = reinterpret_cast<const float2 *>(p.stats) + t / p.L * p.G;
+        constexpr int AT_ONCE = 4;  // positions whose loads are under way together
+        for (long long t1 = from + sub; t1 < to; t1 += (long long)AT_ONCE * subs) {
+            uint4 rx[AT_ONCE], rd[AT_ONCE];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float2 st = stats[(v * V + e) / cg];
-                    k[e] = st.x;
-                    r[e] = st.y;
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const long long t = t1 + i * subs;
+                rx[i] = rd[i] = make_uint4(0, 0, 0, 0);
+                if (t < to) {
+                    rx[i] = x[(size_t)t * vecs];
+                    if (BWD) rd[i] = dy[(size_t)t * vecs];
                 }
             }
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (BWD) {
-                    const float n = (f[e] - k[e]) * r[e];
-                    d[e] *= dact<SILU>(fmaf(n, w[e], b[e]));
-                    a[e] += d[e];
-                    q[e] = fmaf(d[e], n, q[e]);
-                } else {
-                    const float s = f[e] - k[e];
-                    a[e] += s;
-                    q[e] = fmaf(s, s, q[e]);
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const long long t = t1 + i * subs;
+                if (t >= to) break;
+                float f[V], d[V];
+                Vec<T>::unpack(rx[i], f);
+                if (BWD) Vec<T>::unpack(rd[i], d);
+                if (JOINT) {
+                    const float2 *stats = reinterpret_cast<const float2 *>(p.stats) + t / p.L * p.G;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float2 st = stats[(v * V + e) / cg];
+                        k[e] = st.x;
+                        r[e] = st.y;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    if (BWD) {
+                        const float n = (f[e] - k[e]) * r[e];
+                        d[e] *= dact<SILU>(fmaf(n, w[e], b[e]));
+                        a[e] += d[e];
+                        q[e] = fmaf(d[e], n, q[e]);
+                    } else {
+                        const float s = f[e] - k[e];
+                        a[e] += s;
+                        q[e] = fmaf(s, s, q[e]);
+                    }
                 }
             }
         }
@@ -376,19 +391,30 @@ __global__ void __launch_bounds__(NT) gn_join_kernel(GroupNormArgs p, int chunks
     if (i >= (long long)p.rows * p.G) return;
     const int row = (int)(i / p.G), c0 = (int)(i % p.G) * cg;
     const float *part = p.ws + (size_t)row * chunks * 2 * p.C;
+    // a channel's sums: of its chunks by 32 / across lanes (of a group of few channels), then over these
+    int across = 1;
+    while (across < cg && across < 32) across *= 2;
+    const bool mine = lane < across;
     auto channel = [&](int c, float &a, float &q) {
         a = q = 0.f;
-        for (int k = 0; k < chunks; ++k) {
-            a += part[(size_t)k * 2 * p.C + c];
-            q += part[(size_t)k * 2 * p.C + p.C + c];
+        if (c < c0 + cg)
+            for (int k = lane / across; k < chunks; k += 32 / across) {
+                a += part[(size_t)k * 2 * p.C + c];
+                q += part[(size_t)k * 2 * p.C + p.C + c];
+            }
+        for (int off = across; off < 32; off <<= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, off);
+            q += __shfl_xor_sync(0xffffffffu, q, off);
         }
+        return mine && c < c0 + cg;
     };
     const float inv = 1.f / ((float)p.L * (float)cg);
     float first = 0.f, second = 0.f;
     if (BWD) {
-        for (int c = c0 + lane; c < c0 + cg; c += 32) {
+        for (int c1 = 0; c1 < cg; c1 += across) {
+            const int c = c0 + c1 + lane % across;
             float a, q;
-            channel(c, a, q);
+            if (!channel(c, a, q)) continue;
             const float w = p.w ? p.w[c] : 1.f;
             first = fmaf(w, a, first);
             second = fmaf(w, q, second);
@@ -399,16 +425,17 @@ __global__ void __launch_bounds__(NT) gn_join_kernel(GroupNormArgs p, int chunks
         const T *x = static_cast<const T *>(p.x) + (size_t)row * p.L * p.C;
         const float per = 1.f / (float)p.L;
         float sum = 0.f;
-        for (int c = c0 + lane; c < c0 + cg; c += 32) {
+        for (int c1 = 0; c1 < cg; c1 += across) {
+            const int c = c0 + c1 + lane % across;
             float a, q;
-            channel(c, a, q);
-            sum += fmaf(a, per, to_f32(x[c]));
+            if (channel(c, a, q)) sum += fmaf(a, per, to_f32(x[c]));
         }
         first = row_sum<32>(sum) / (float)cg;
         float dev = 0.f;
-        for (int c = c0 + lane; c < c0 + cg; c += 32) {
+        for (int c1 = 0; c1 < cg; c1 += across) {
+            const int c = c0 + c1 + lane % across;
             float a, q;
-            channel(c, a, q);
+            if (!channel(c, a, q)) continue;
             const float m = a * per, off = (to_f32(x[c]) - first) + m;
             dev += fmaxf(fmaf(-a, m, q), 0.f) + (float)p.L * off * off;
         }
@@ -424,7 +451,7 @@ __global__ void __launch_bounds__(NT) gn_apply_kernel(GroupNormArgs p, int lanes
     const int tid = threadIdx.x, lane = tid % lanes, sub = tid / lanes, subs = NT / lanes;
     const int block = blockIdx.x % blocks, rt = blockIdx.x / blocks, row = rt / tiles, tile = rt % tiles;
     const int vecs = p.C / V, v = block * lanes + lane, cg = p.C / p.G;
-    if (v >= vecs) return;
+    if (v >= vecs || sub >= subs) return;
     const uint4 *x = static_cast<const uint4 *>(p.x) + (size_t)row * p.L * vecs + v;
     const uint4 *dy = BWD ? static_cast<const uint4 *>(p.dy) + (size_t)row * p.L * vecs + v : nullptr;
     uint4 *out = static_cast<uint4 *>(BWD ? p.dx : p.y) + (size_t)row * p.L * vecs + v;

@@ -43,9 +43,12 @@ inline int gn_row_parts(int rows, int C, int G, efla_dtype t) {
     const int most = std::max(1, 456 / gn_blocks(C, G, t));
     return std::max(1, std::min(most, (rows + 7) / 8));
 }
-// Vectors of a row that a CTA's threads cover in the other kernels, and the chunks its positions come in: CTAs
-// enough for four a SM, four positions a thread at least.
-inline int gn_lanes(int vecs) { return std::min(32, gn_team(vecs)); }
+// Vectors of a row that a CTA's threads cover in the other kernels: up to 32, rows cut evenly (40: 20, not 32 and 8), and
+// the chunks its positions come in: CTAs enough for four a SM, four positions a thread at least.
+inline int gn_lanes(int vecs) {
+    const int blocks = std::max(1, (vecs + 31) / 32);
+    return std::max(1, (vecs + blocks - 1) / blocks);
+}
 inline int gn_chunks(int rows, int L, int C, efla_dtype t) {
     const int vecs = C / gn_vec(t), lanes = gn_lanes(vecs), subs = GN_NT / lanes;
     const long long blocks = (long long)rows * ((vecs + lanes - 1) / lanes);
