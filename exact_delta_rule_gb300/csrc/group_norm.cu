@@ -12,9 +12,10 @@
 //     189 as a warp's samples; 4096 samples of 16 x 256 in 8 groups 21 and 55; 94 and 238 a warp);
 //   samples of few elements, or many of up to 16 KB: one a warp, in shared memory;
 //   forward, other samples: tiles of whole groups in the shared memory of a cluster, whose CTAs share out the positions
-//     and read one another's sums; one pass (8 maps of 4096 positions x 320 channels in 32 groups: 14 us, 33 in three);
+//     and read one another's sums; one pass (8 maps of 4096 positions x 320 channels in 32 groups: 14 us; three kernels took 33);
 //   the rest in three kernels: sums per channel over chunks of the positions, joined to those of the groups, and
-//     applied, where x is found in L2 if it fits.
+//     applied, where x is found in L2 if it fits (backward of 64 maps of 4096 x 320, bf16: 97 us, 3 and 116; one position
+//     at a time and rows cut into 32 vectors and 8: 251, 3 and 167).
 // Channels are summed as x minus their first value and joined by their means and square deviations, so that a mean
 // far from 0 costs no accuracy; where a group is in registers or a warp's memory its mean is taken first.
 #include "group_norm.cuh"
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(NT) gn_join_kernel(GroupNormArgs p, int chunks
     auto channel = [&](int c, float &a, float &q) {
         a = q = 0.f;
         if (c < c0 + cg)
+#pragma unroll 8
             for (int k = lane / across; k < chunks; k += 32 / across) {
                 a += part[(size_t)k * 2 * p.C + c];
                 q += part[(size_t)k * 2 * p.C + p.C + c];
