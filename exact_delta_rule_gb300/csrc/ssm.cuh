@@ -156,8 +156,13 @@ __device__ __forceinline__ float ssm_exponent(float delta, float rate) { return 
 __device__ __forceinline__ float2 ssm_exponent(float2 delta, float2 rate) {
     return __ffma2_rn(delta, rate, make_float2(EX2_MEAN, EX2_MEAN));
 }
-// A in units of log2: e^{A delta} = 2^{rate delta}.
-__device__ __forceinline__ float ssm_rate(float a_log) { return -expf(a_log) * LOG2E; }
+// A in units of log2: e^{A delta} = 2^{rate delta}.  Held at the lowest finite number, which a_log = 88.4 reaches: a token
+// of delta = 0 has to keep the state, and 0 times an infinite rate would be NaN.
+__device__ __forceinline__ float ssm_rate(float a_log) {
+    constexpr float LOWEST = -3.402823466e38f;
+    const float rate = -expf(a_log) * LOG2E;
+    return rate < LOWEST ? LOWEST : rate;  // (a NaN stays one)
+}
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),

@@ -353,7 +353,9 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
                 }
                 // ddelta = ln2 (w . rate) + du x
                 const float2 ddelta = __ffma2_rn(du, x, make_float2(LN2 * dd.x, LN2 * dd.y));
-                const float2 ddt = __fmul2_rn(ddelta, make_float2(ssm_sigmoid(dt.x), ssm_sigmoid(dt.y)));
+                // (a slope of 0, of dt = -infinity: 0 whatever ddelta is, which a large A takes out of range)
+                const float2 rise = make_float2(ssm_sigmoid(dt.x), ssm_sigmoid(dt.y));
+                const float2 ddt = make_float2(rise.x == 0.f ? 0.f : ddelta.x * rise.x, rise.y == 0.f ? 0.f : ddelta.y * rise.y);
                 store2(static_cast<T *>(p.dx) + to, __ffma2_rn(du, *at(delta_s, t), __fmul2_rn(skip, g)));
                 store2(static_cast<T *>(p.ddt) + to, ddt);
                 chunk_D = __ffma2_rn(g, x, chunk_D);

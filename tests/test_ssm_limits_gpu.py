@@ -1,0 +1,74 @@
+"""Short convolution, selective scan and group norm at the ends of what their contract allows, on the GPU: decays that no
+float holds, runs and rows of the largest sizes, groups whose first value or mean is far from the others."""
+import math
+
+import pytest
+import torch
+
+import exact_delta_rule_gb300 as efla
+from oracle import ssm
+from test_ssm_gpu import BF16, F32, check_scan, check_scan_bwd, close, cu_of, scan_inputs, scan_share
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------ scan: decays out of range
+def steep(T, D=24, N=32, padded=5, seqs=None, **kw):
+    """A_log at and past the largest whose exponential an fp32 number holds, beside ordinary ones; the last tokens masked."""
+    a = scan_inputs(T=T, D=D, N=N, seqs=seqs, **kw)
+    for i, v in enumerate((88.2, 88.5, 89.0, 95.0, 700.0)):
+        a["A_log"][i::7, i::3] = v
+    if padded:
+        a["dt"][:, -padded:] = -math.inf
+    return a
+
+
+@pytest.mark.parametrize("T", [1, 2, 6, 7, 37, 130])
+@pytest.mark.parametrize("dtype, N", [(F32, 16), (BF16, 32), (F32, 128)])
+def test_scan_of_steep_decays(dtype, N, T):
+    """Tokens of delta = 0 (a row that ends inside a group of four, a masked one) keep the state, whatever the decay."""
+    check_scan(steep(T, N=N, dtype=dtype, padded=0))
+    y, S = check_scan(steep(T + 5, N=N, dtype=dtype))
+    assert bool(torch.isfinite(S).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_of_steep_decays_in_cut_rows(dtype):
+    a = steep(1500, B=1, N=16, dtype=dtype, padded=700)  # whole segments of masked tokens
+    assert efla.ssm_scan_workspace(1, 1500, 24, 16) > 0
+    check_scan(a)
+    lens = [3, 0, 700, 1, 90, 706]
+    a = steep(1500, B=1, N=16, dtype=dtype, padded=300, seqs=len(lens))
+    y, S = efla.ssm_scan(**a, cu_seqlens=cu_of(lens))
+    at = 0
+    for i, n in enumerate(lens):
+        one = {k: v[:, at:at + n].contiguous() if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items()}
+        one["S0"] = a["S0"][i:i + 1].contiguous()
+        ref, ref_S = ssm.scan(**one)
+        size, size_S = ssm.scan(**one, size=True)
+        close(y[:, at:at + n], ref, size, scan_share(n), f"y {i}")
+        close(S[i:i + 1], ref_S, size_S, scan_share(n), f"S {i}")
+        at += n
+
+
+@pytest.mark.parametrize("T, padded", [(6, 5), (37, 0), (37, 9), (900, 300)])
+@pytest.mark.parametrize("dtype, N", [(F32, 16), (BF16, 32), (F32, 128)])
+def test_scan_gradients_of_steep_decays(dtype, N, T, padded):
+    got, _, _ = check_scan_bwd(steep(T, N=N, dtype=dtype, padded=padded))
+    if padded:
+        assert bool((got["ddt"][:, -padded:] == 0).all())
+
+
+@pytest.mark.parametrize("B", [1, 600])
+@pytest.mark.parametrize("dtype, N", [(F32, 16), (BF16, 128)])
+def test_step_of_steep_decays(dtype, N, B):
+    a = steep(1, B=B, N=N, dtype=dtype, padded=0)
+    a["dt"][::2] = -math.inf
+    S = a["S0"].clone()
+    tok = {k: v[:, 0].contiguous() if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items() if k != "S0"}
+    y = efla.ssm_step(**tok, S=S)
+    ref, ref_S = ssm.scan(**a)
+    size, size_S = ssm.scan(**a, size=True)
+    close(y.unsqueeze(1), ref, size, scan_share(1), "y")
+    close(S, ref_S, size_S, scan_share(1), "S")
+    assert torch.equal(S[::2], a["S0"][::2])
