@@ -509,11 +509,6 @@ __global__ void __launch_bounds__(STEP_NT) conv_step_kernel(ConvArgs p, int vecs
     }
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
-}
-
 template <typename T, int W>
 cudaError_t fwd(const ConvArgs &a) {
     constexpr int V = 4;

@@ -704,11 +704,6 @@ __global__ void __launch_bounds__(NT) gn_slab_kernel(GroupNormArgs p, GnSlab s) 
     cluster_wait();
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    return bytes > 47 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
-}
-
 template <typename T, bool SILU>
 cudaError_t slab(const GroupNormArgs &a, const GnSlab &s) {
     constexpr int V = Vec<T>::N;

@@ -19,6 +19,7 @@
 // those over the CTAs through the workspace, all in a fixed order.
 #include "mixer_norm.cuh"
 #include "ssm.cuh"
+#include "vec.cuh"
 
 namespace efla {
 namespace {
@@ -529,11 +530,6 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(const float *part, T *dB, T
         dB[at + n] = from_f32<T>(v);
     else
         dC[at + n - N] = from_f32<T>(v);
-}
-
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes) {
-    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
 }
 
 template <typename T, int NSUB>

@@ -19,6 +19,7 @@
 // Inputs come in stages of 16 tokens by asynchronous copies two stages ahead; B and C of the next stage are converted
 // while this one is computed, so a stage costs one barrier.
 #include "ssm.cuh"
+#include "vec.cuh"
 
 namespace efla {
 namespace {
@@ -366,11 +367,8 @@ __global__ void __launch_bounds__(COMBINE_NT) ssm_combine_kernel(SsmArgs p) {
 template <typename T, int N, bool CARRY>
 cudaError_t run(const SsmArgs &a, long long slots, int tiles) {
     using K = Scan<T, N, CARRY>;
-    if (K::SMEM > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(ssm_fwd_kernel<T, N, CARRY>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(ssm_fwd_kernel<T, N, CARRY>, K::SMEM);
+    if (e != cudaSuccess) return e;
     ssm_fwd_kernel<T, N, CARRY><<<(unsigned)(slots * tiles), K::NT, K::SMEM, a.stream>>>(a, tiles);
     return cudaGetLastError();
 }

@@ -92,4 +92,11 @@ __device__ __forceinline__ void fetch_wait(int left) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// Lets a kernel have `bytes` of dynamic shared memory.  Without that the most is 48 KB together with what it declares
+// itself (under 1 KB in every kernel launched so).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    return bytes > 47 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+}
+
 }  // namespace efla

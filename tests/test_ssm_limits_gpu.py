@@ -72,3 +72,27 @@ def test_step_of_steep_decays(dtype, N, B):
     close(y.unsqueeze(1), ref, size, scan_share(1), "y")
     close(S, ref_S, size_S, scan_share(1), "S")
     assert torch.equal(S[::2], a["S0"][::2])
+
+
+# ------------------------------------------------------------------------------------ convolution: runs of 16 and 32 tokens
+@pytest.mark.parametrize("dtype, D, T, most", [
+    (BF16, 8, 700_001, 9000),     # 16 tokens a thread: 48 KB of dynamic shared memory to the byte (W and activation as in no other test)
+    (BF16, 8, 1_250_007, 20000),  # 32 tokens a thread
+    (BF16, 512, 25_003, 900), (BF16, 512, 10_007, 70), (F32, 512, 15_001, 400), (F32, 40, 130_001, 3000)])
+def test_packed_convolution_of_long_runs(dtype, D, T, most):
+    """Sequences that begin and end anywhere in the copy groups of a run, against each sequence by itself."""
+    gen = torch.Generator().manual_seed(D + T)
+    lens = []
+    while sum(lens) < T:
+        n = int(torch.randint(0, 2 * most, (1,), generator=gen))
+        lens += [min(n, T - sum(lens))] + [int(v) for v in torch.randint(0, 5, (3,), generator=gen)] * (sum(lens) + n + 12 < T)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(1, T, D, generator=g, device="cuda").to(dtype)
+    w, s0 = torch.randn(D, 3, generator=g, device="cuda"), torch.randn(len(lens), 2, D, generator=g, device="cuda").to(dtype)
+    y, end = efla.causal_conv(x, w, None, s0, cu_of(lens), activation=None)
+    at = 0
+    for i, n in enumerate(lens):
+        y1, end1 = efla.causal_conv(x[:, at:at + n].contiguous(), w, None, s0[i:i + 1].contiguous(), activation=None)
+        assert torch.equal(y[:, at:at + n], y1) and torch.equal(end[i:i + 1], end1), i
+        at += n
+    assert at == T and efla.device_status() == 0
