@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(CONV_BWD_NT, CONV_BWD_CTAS) conv_bwd_kernel(Co
     Taps4<W> taps;
     if (v < vecs) taps.load(p, v * V);
     for (long long run = (long long)tile * subs + sub; v < vecs && run < runs; run += step) {
-        const int b = (int)(run / plan.row_runs), e0 = (int)(run % plan.row_runs) * plan.run, e1 = min(e0 + plan.run, ends);
+        const int b = (int)(run / plan.row_runs), e0 = (int)(run % plan.row_runs) * plan.run;
+        const int e1 = e0 + min(plan.run, ends - e0);  // (a run is longer than what the longest row leaves below 2^31)
         const long long row = (long long)b * p.T;
         const Pack<T, V> *x0 = static_cast<const Pack<T, V> *>(p.x) + row * vecs + v, *y0 = static_cast<const Pack<T, V> *>(p.dy) + row * vecs + v;
         auto fetch_group = [&](int t0, int slot) {  // rows t0 .. of x and dy; past the row's end zeros

@@ -96,3 +96,34 @@ def test_packed_convolution_of_long_runs(dtype, D, T, most):
         assert torch.equal(y[:, at:at + n], y1) and torch.equal(end[i:i + 1], end1), i
         at += n
     assert at == T and efla.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------ the longest rows
+def need_memory(gb):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gb * 1e9:
+        pytest.skip(f"needs {gb} GB of free memory")
+
+
+LONGEST = 2 ** 31 - 1 - 4096  # tokens
+
+
+def test_convolution_backward_of_the_longest_row():
+    """The last run ends past 2^31 - 1 places: its gradients, and its share of the sums, against its tokens by themselves."""
+    need_memory(115)
+    D, W, n = 8, 4, 100_000  # (all but the last n tokens are 0 and add nothing)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    tail = {k: torch.randn(1, n, D, generator=gen, device="cuda").to(BF16) for k in ("x", "dy")}
+    long = {k: torch.zeros(1, LONGEST, D, dtype=BF16, device="cuda") for k in tail}
+    for k, v in tail.items():
+        long[k][:, -n:] = v
+    w, dend = torch.randn(D, W, generator=gen, device="cuda"), torch.randn(1, W - 1, D, generator=gen, device="cuda").to(BF16)
+    got = efla.causal_conv_bwd(long["x"], w, None, None, long["dy"], dend, activation=None)
+    want = efla.causal_conv_bwd(tail["x"], w, None, None, tail["dy"], dend, activation=None)
+    assert torch.equal(got["dx"][:, -n:], want["dx"]) and not bool(got["dstate0"].any())
+    assert not bool(got["dx"][:, -n - 1000:-n - W + 1].any())
+    ref = ssm.conv_bwd(tail["x"], w, None, None, tail["dy"], dend, silu=False)["dw"]
+    size = ssm.conv_bwd(tail["x"], w, None, None, tail["dy"], dend, silu=False, size=True)["dw"]
+    close(got["dw"], ref, size, n * 2.0 ** -24, "dw")  # a sum of n products
+    del got, long
+    torch.cuda.empty_cache()
