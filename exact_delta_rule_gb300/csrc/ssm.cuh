@@ -63,6 +63,9 @@ inline int ssm_bwd_tiles(int D, int N, int G) { return ssm_tiles(D, G, ssm_bwd_c
 int ssm_segment(long long rows, int T, int D, int N, bool uneven);
 int ssm_bwd_segment(long long rows, int T, int D, int N, int tiles);
 
+// Segments of `seg` tokens in a row of T, 1 where seg is 0.  (T + seg - 1 would pass 2^31 for the longest rows.)
+__host__ __device__ inline int ssm_pieces(int T, int seg) { return seg ? T / seg + (T % seg != 0) : 1; }
+
 // Workspace of the training pair, in bytes from its base (16-byte aligned regions).
 struct SsmWs {
     int seg, slots, bwd_seg, bwd_slots;
@@ -72,9 +75,9 @@ inline SsmWs ssm_ws(int B, int T, int D, int N, int G) {
     SsmWs w{};
     const int tiles = ssm_bwd_tiles(D, N, G);
     w.seg = ssm_segment(B, T, D, N, false);
-    w.slots = B * (w.seg ? (T + w.seg - 1) / w.seg : 1);
+    w.slots = B * ssm_pieces(T, w.seg);
     w.bwd_seg = ssm_bwd_segment(B, T, D, N, tiles);
-    w.bwd_slots = B * (w.bwd_seg ? (T + w.bwd_seg - 1) / w.bwd_seg : 1);
+    w.bwd_slots = B * ssm_pieces(T, w.bwd_seg);
     size_t at = 0;
     auto take = [&](size_t floats) {
         const size_t r = at;
@@ -205,7 +208,7 @@ struct SsmSpan {
 
 // Segment `slot` of rows of T tokens, `seg` tokens each.
 __device__ __forceinline__ SsmSpan ssm_row_span(const SsmArgs &p, int slot) {
-    const int per = p.seg ? (p.T + p.seg - 1) / p.seg : 1, row = slot / per, s = slot % per;
+    const int per = ssm_pieces(p.T, p.seg), row = slot / per, s = slot % per;
     const long long row0 = (long long)row * p.T, lo = row0 + (long long)s * p.seg;
     const long long hi = s + 1 < per ? lo + p.seg : row0 + p.T;
     return {row, lo, hi, s == 0, s + 1 == per};

@@ -73,7 +73,7 @@ efla_status check_group_norm(int rows, int L, int C, int groups, efla_dtype dtyp
 // Segments of a scan without training: their length (0: uncut) and number for N sequences of T / N tokens on average.
 void scan_segments(int T, int D, int d_state, int N, bool packed, int &seg, int &slots) {
     seg = ssm_segment(N, packed && N > 0 ? (int)(((long long)T + N - 1) / N) : T, D, d_state, packed && N > 1);
-    slots = !seg ? N : packed ? T / seg + N : N * ((T + seg - 1) / seg);
+    slots = !seg ? N : packed ? T / seg + N : N * ssm_pieces(T, seg);
 }
 size_t scan_bytes(int D, int d_state, int seg, int slots) { return seg ? (size_t)slots * D * (d_state + 1) * sizeof(float) : 0; }
 

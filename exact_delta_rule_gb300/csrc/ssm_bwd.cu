@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_carry_kernel(SsmBwdArgs p, int til
 // The gradient of the state at each segment's end, in place of what the segment alone hands on.
 __global__ void __launch_bounds__(NT) ssm_bwd_combine_kernel(SsmBwdArgs p) {
     const SsmArgs &f = p.f;
-    const int row = blockIdx.y, segs = (f.T + f.seg - 1) / f.seg;
+    const int row = blockIdx.y, segs = ssm_pieces(f.T, f.seg);
     const size_t e = (size_t)blockIdx.x * NT + threadIdx.x, size = (size_t)f.D * f.N;
     if (e >= size) return;
     const float rate = ssm_rate(f.A_log[e]);

@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(COMBINE_NT) ssm_combine_kernel(SsmArgs p) {
         for (int w = 0; w < NT / 32; ++w) first += box[w];
         if (first + segs > p.slots) return;  // sequences that overlap
     } else {
-        segs = (p.T + p.seg - 1) / p.seg;
+        segs = ssm_pieces(p.T, p.seg);
         first = row * segs;
     }
     const size_t e = (size_t)blockIdx.x * NT + tid, size = (size_t)p.D * p.N;

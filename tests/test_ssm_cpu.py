@@ -349,3 +349,17 @@ def test_workspaces_of_whole_and_cut_rows():
     one = efla.ssm_scan_workspace(1, 8192, 2048, 16)
     assert one > 0 and efla.ssm_scan_workspace(1, 8192, 2048, 16, N=1) >= one
     assert efla.ssm_bwd_workspace(0, 8, 64, 16) >= 0
+
+def test_workspaces_of_the_longest_rows():
+    """Rows up to the accepted length: the number of segments, and with it the workspace, goes on smoothly."""
+    longest = 2 ** 31 - 1 - 4096
+    for D, N in ((8, 16), (64, 128)):
+        for packed in (None, 1, 3):
+            if packed:
+                a, b = (efla.ssm_scan_workspace(1, T, D, N, N=packed) for T in (longest, longest - 20_000_000))
+            else:
+                a, b = (efla.ssm_scan_workspace(1, T, D, N) for T in (longest, longest - 20_000_000))
+            assert 0 < a < 1 << 32 and abs(a - b) <= 0.1 * b, (D, N, packed, a, b)
+        a, b = (efla.ssm_bwd_workspace(1, T, D, N) for T in (longest, longest - 20_000_000))
+        assert b < a < 1.02 * b, (D, N, a, b)
+    assert 0 < efla.ssm._bytes("efla_causal_conv_bwd_workspace", 1, longest, 8, 4) < 1 << 32
