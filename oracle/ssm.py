@@ -142,28 +142,31 @@ def scan_bwd(x, dt, A_log, B, C, D, dt_bias, z, S0, dy, dS_T=None, size=False):
     return out
 
 
-def _normed(x, groups, eps):
+def _normed(x, groups, eps, stats=None):
     xg = x.reshape(x.shape[0], -1, groups, x.shape[-1] // groups)
+    if stats is not None:
+        mean, r = (t[:, None, :, None] for t in stats.double().unbind(-1))
+        return (xg - mean) * r, mean, r
     mean = xg.mean((1, 3), keepdim=True)
     r = 1 / torch.sqrt(((xg - mean) ** 2).mean((1, 3), keepdim=True) + eps)
     return (xg - mean) * r, mean, r
 
 
-def group_norm(x, w, b, groups, eps=1e-5, silu=False):
-    """(y, stats) for x [rows, ..., C]."""
+def group_norm(x, w, b, groups, eps=1e-5, silu=False, stats=None):
+    """(y, stats) for x [rows, ..., C]; from given ``stats`` if there are."""
     x, w, b = _f64(x, w, b)
-    n, mean, r = _normed(x, groups, eps)
+    n, mean, r = _normed(x, groups, eps, stats)
     s = n.reshape(x.shape)
     s = s if w is None else s * w
     s = s if b is None else s + b
     return _silu(s) if silu else s, torch.stack([mean[:, 0, :, 0], r[:, 0, :, 0]], -1)
 
 
-def group_norm_bwd(x, w, b, groups, dy, eps=1e-5, silu=False):
-    """Gradients, and the sum of the magnitudes that each is made of."""
+def group_norm_bwd(x, w, b, groups, dy, eps=1e-5, silu=False, stats=None):
+    """Gradients, and the sum of the magnitudes that each is made of; with ``stats`` taken for x's own."""
     x, w, b, dy = _f64(x, w, b, dy)
     C = x.shape[-1]
-    n, _, r = _normed(x, groups, eps)
+    n, _, r = _normed(x, groups, eps, stats)
     ww, bb = x.new_ones(C) if w is None else w, x.new_zeros(C) if b is None else b
     flat = n.reshape(x.shape)
     ds = dy * _dsilu(flat * ww + bb) if silu else dy

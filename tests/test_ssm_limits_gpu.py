@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import exact_delta_rule_gb300 as efla
+from norm_bounds import check_gradients, check_stats, check_y, far_values
 from oracle import ssm
 from test_ssm_gpu import BF16, F32, check_scan, check_scan_bwd, close, cu_of, scan_inputs, scan_share
 
@@ -127,3 +128,33 @@ def test_convolution_backward_of_the_longest_row():
     close(got["dw"], ref, size, n * 2.0 ** -24, "dw")  # a sum of n products
     del got, long
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------------------------ group norm: values far from the others or from 0
+# depth: a thread's additions one after the other, those that join the threads, chunks and channels
+@pytest.mark.parametrize("shape, groups, depth, whole", [
+    ((20, 512), 4, 14, 16),                # a group in a warp's registers
+    ((9, 4096), 2, 30, 32),                # in a team's
+    ((40, 16384), 2, 38, 40),
+    ((5, 64, 512), 32, 30, 32),
+    ((2, 500, 8), 4, 32 * 274, 20),        # a cluster's shared memory: channels, CTAs and quotients of the mean
+    ((1, 64, 64, 320), 32, 32 * 62, 20),
+    ((1, 5000, 520), 5, 32 * 71, 24),      # (fp32: three kernels)
+    ((1, 70001, 8), 1, 32 * 307, 20),
+    ((2, 30000, 64), 2, 347, 4),           # three kernels
+    ((1, 20000, 40), 40, 80, 4),
+    ((4, 72000), 3, 779, 4)])
+@pytest.mark.parametrize("kind", ["mean", "first"])
+@pytest.mark.parametrize("dtype, silu", [(F32, True), (F32, False), (BF16, True)])
+def test_group_norm_of_far_values(dtype, silu, kind, shape, groups, depth, whole):
+    check_far_values(dtype, silu, kind, shape, groups, depth, whole)
+
+
+def check_far_values(dtype, silu, kind, shape, groups, depth, whole):
+    x, w, b, dy = far_values(shape, groups, dtype, kind, "cuda")
+    act = "silu" if silu else None
+    y, stats = efla.group_norm(x, w, b, groups, activation=act, return_stats=True)
+    check_stats(x, groups, stats, depth, whole)
+    check_y(x, w, b, groups, silu, stats, y)
+    got = efla.group_norm_bwd(x, w, b, groups, stats, dy, activation=act)
+    check_gradients(x, w, b, groups, silu, stats, dy, got, depth)
