@@ -150,6 +150,17 @@ def test_group_norm_of_far_values(dtype, silu, kind, shape, groups, depth, whole
     check_far_values(dtype, silu, kind, shape, groups, depth, whole)
 
 
+@pytest.mark.parametrize("shape, groups, depth, whole", [
+    ((610, 500, 8), 8, 506, 4), ((3, 100, 8), 8, 106, 4), ((610, 33, 24), 3, 39, 4),   # a lane has many values
+    ((700, 16, 256), 32, 22, 24), ((610, 32, 16), 4, 38, 40),                          # up to 32
+    ((610, 500, 8), 1, 506, 40)])                                                      # (fp32: a team's)
+@pytest.mark.parametrize("kind", ["mean", "first", "narrow"])
+@pytest.mark.parametrize("dtype, silu", [(F32, True), (BF16, False)])
+def test_group_norm_of_far_values_in_small_samples(dtype, silu, kind, shape, groups, depth, whole):
+    """Samples that a warp takes from its memory: the mean is as good as a few roundings whatever a long sum loses."""
+    check_far_values(dtype, silu, kind, shape, groups, depth, whole)
+
+
 def check_far_values(dtype, silu, kind, shape, groups, depth, whole):
     x, w, b, dy = far_values(shape, groups, dtype, kind, "cuda")
     act = "silu" if silu else None
