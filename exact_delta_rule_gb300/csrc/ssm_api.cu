@@ -305,7 +305,9 @@ efla_status efla_group_norm(const void *x, const float *w, const float *b, void 
     s = check_args({{"x", x, n, IN}, {"w", w, cb, IN_OPT}, {"b", b, cb, IN_OPT}, {"y", y, n, OUT, {"x"}},
                     {"stats", stats, (size_t)rows * groups * 8, OUT_OPT}, {"workspace", workspace, need, OUT_OPT}});
     if (s != EFLA_OK) return s;
-    if (n == 0) return api_ok();
+    if (n == 0)  // no values have no mean: NaN
+        return launched(stats && rows > 0 ? cudaMemsetAsync(stats, 0xff, (size_t)rows * groups * 8, reinterpret_cast<cudaStream_t>(stream)) : cudaSuccess,
+                        "group norm of no positions");
     GroupNormArgs a{};
     a.x = x, a.w = w, a.b = b, a.y = y, a.stats = stats, a.ws = static_cast<float *>(workspace);
     a.rows = rows, a.L = L, a.C = C, a.G = groups, a.dtype = dtype, a.silu = activation == EFLA_ACT_SILU, a.eps = eps;

@@ -560,7 +560,7 @@ efla_status efla_ssm_step(const void *x, const void *dt, const float *A_log, con
  *   y = w n + b or silu of it
  *
  *   x, y     [rows, L, C] dtype (L = 1: a token's heads);  w, b [C] fp32, or NULL (1, 0)
- *   stats    [rows, groups, 2] fp32, each group's mean and 1 / sqrt(var + eps), or NULL (not written)
+ *   stats    [rows, groups, 2] fp32, each group's mean and 1 / sqrt(var + eps) (NaN where L = 0), or NULL (not written)
  *   workspace  at least efla_group_norm_workspace bytes (0 for some sizes), overlapping no argument
  * C a multiple of 8 and of groups.  y == x is allowed.  fp32 arithmetic, each output rounded once.  A mean far from 0
  * costs what holding it in fp32 does: it is off by a few of its own roundings (2^-24 of the values' size, 40 times at

@@ -13,6 +13,8 @@ rounding errors are proportional to.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 
@@ -143,7 +145,7 @@ def scan_bwd(x, dt, A_log, B, C, D, dt_bias, z, S0, dy, dS_T=None, size=False):
 
 
 def _normed(x, groups, eps, stats=None):
-    xg = x.reshape(x.shape[0], -1, groups, x.shape[-1] // groups)
+    xg = x.reshape(x.shape[0], math.prod(x.shape[1:-1]), groups, x.shape[-1] // groups)
     if stats is not None:
         mean, r = (t[:, None, :, None] for t in stats.double().unbind(-1))
         return (xg - mean) * r, mean, r

@@ -169,3 +169,17 @@ def check_far_values(dtype, silu, kind, shape, groups, depth, whole):
     check_y(x, w, b, groups, silu, stats, y)
     got = efla.group_norm_bwd(x, w, b, groups, stats, dy, activation=act)
     check_gradients(x, w, b, groups, silu, stats, dy, got, depth)
+
+
+@pytest.mark.parametrize("shape, groups", [((3, 0, 16), 2), ((700, 4, 0, 24), 24), ((0, 7, 16), 4)])
+def test_group_norm_of_no_positions(shape, groups):
+    """Statistics of nothing are NaN, as the mean of no values is, and no memory's last content."""
+    stats = torch.full((shape[0], groups, 2), 7.0, device="cuda")
+    x = torch.zeros(shape, device="cuda")
+    y, got = efla.group_norm(x, None, None, groups, stats=stats)
+    assert y.shape == x.shape and bool(got.isnan().all()) and got.data_ptr() == stats.data_ptr()
+    ref = ssm.group_norm(x, None, None, groups)[1]
+    assert ref.shape == got.shape and bool(ref.isnan().all())
+    w = torch.ones(shape[-1], device="cuda")
+    g = efla.group_norm_bwd(x, w, w, groups, stats, x)
+    assert not bool(g["dw"].any()) and not bool(g["db"].any())
