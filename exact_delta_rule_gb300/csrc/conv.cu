@@ -520,7 +520,7 @@ cudaError_t fwd(const ConvArgs &a) {
     while (rows > 8 && tokens * vecs < 2LL * 152 * NT * rows) rows /= 2;
     const int row_runs = (a.T + rows - 1) / rows;
     const long long runs = a.cu_seqlens ? (tokens + rows - 1) / rows : (long long)a.B * row_runs;
-    const long long work = (runs + subs - 1) / subs * cblocks;
+    const long long work = std::max((runs + subs - 1) / subs * cblocks, a.cu_seqlens ? 1LL : 0LL);  // (the first CTA looks at all bounds)
     const long long copies = a.state_T ? ((long long)a.N * (W - 1) * vecs + NT - 1) / NT : 0;
     if (work + copies == 0) return cudaSuccess;
     const size_t slots = (size_t)rows * NT * sizeof(Pack<T, V>);

@@ -183,3 +183,19 @@ def test_group_norm_of_no_positions(shape, groups):
     w = torch.ones(shape[-1], device="cuda")
     g = efla.group_norm_bwd(x, w, w, groups, stats, x)
     assert not bool(g["dw"].any()) and not bool(g["db"].any())
+
+
+@pytest.mark.parametrize("call", ["conv", "scan"])
+@pytest.mark.parametrize("state", [True, False])
+def test_bounds_of_an_empty_batch(call, state):
+    """Bounds are looked at where there are no tokens too, whether or not states are asked for."""
+    for bounds, bad in (([0, 0, 0], False), ([0, 5, 0], True), ([-1, 0, 0], True)):
+        cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+        if call == "conv":
+            y, end = efla.causal_conv(torch.zeros(1, 0, 16, device="cuda"), torch.zeros(16, 4, device="cuda"), None, None, cu,
+                                      return_state=state)
+        else:
+            a = scan_inputs(B=1, T=0, D=16, seqs=2)
+            y, end = efla.ssm_scan(**a, cu_seqlens=cu, return_state=state)
+        assert y.shape == (1, 0, 16) and (end is None) == (not state)
+        assert efla.device_status() == int(bad), bounds
