@@ -222,7 +222,8 @@ __device__ __forceinline__ int ssm_segments(const SsmArgs &p, int n, long long &
 }
 
 // Segment `slot` of packed sequences, all segments of a sequence after those of the ones before it.  By all threads
-// of a CTA; false if there is none.  A malformed sequence has none and is reported by the CTA that `reports`.
+// of a CTA; false if there is none.  A malformed sequence has none and is reported by the CTA that `reports`; one whose segments
+// are not all among p.slots (behind sequences that overlap) is left out, here and where segments are joined.
 template <int NT>
 __device__ __forceinline__ bool ssm_packed_span(const SsmArgs &p, int slot, bool reports, SsmSpan &out) {
     __shared__ long long box[4];
@@ -258,7 +259,7 @@ __device__ __forceinline__ bool ssm_packed_span(const SsmArgs &p, int slot, bool
         __syncthreads();
         long long start = before + run - segs;
         for (int w = 0; w < warp; ++w) start += sums[w];
-        if (slot >= start && slot < start + segs) {
+        if (slot >= start && slot < start + segs && start + segs <= p.slots) {
             const int s = (int)(slot - start);
             box[0] = n;
             box[1] = lo + (long long)s * p.seg;

@@ -515,7 +515,8 @@ efla_status efla_causal_conv_step(const void *x, const float *w, const float *bi
  *   B, C     [B, T, G, d_state] dtype, shared by the D / G channels of a group: channel d reads group d G / D
  *   A_log    [D, d_state] fp32 (finite; from 88.3 on e^{A_log} counts as 2.3e38);  D_skip, dt_bias [D] fp32, or NULL (zeros)
  *   S0, S_T  [N, D, d_state] fp32, or NULL (zeros / not written); S0 == S_T is allowed
- *   cu_seqlens as for efla_fwd_chunked.  Tokens of no sequence are left alone.
+ *   cu_seqlens as for efla_fwd_chunked.  Tokens of no sequence are left alone, and where a malformed list's other
+ *            sequences overlap, those behind them may be.
  *   workspace  at least efla_ssm_scan_workspace bytes (0 where the channels fill the GPU and the rows stay whole),
  *            overlapping no argument; calls that overlap in time need one each
  * d_state in {16, 32, 64, 128}, D a multiple of 8 and D / G of 8 (bf16) or 4 (fp32).  fp32 arithmetic and state, each output rounded once.

@@ -8,7 +8,7 @@ import torch
 import exact_delta_rule_gb300 as efla
 from norm_bounds import check_gradients, check_stats, check_y, far_values
 from oracle import ssm
-from test_ssm_gpu import BF16, F32, check_scan, check_scan_bwd, close, cu_of, scan_inputs, scan_share
+from test_ssm_gpu import BF16, F32, between_sentinels, check_scan, check_scan_bwd, close, cu_of, scan_inputs, scan_share
 
 pytestmark = pytest.mark.gpu
 
@@ -199,3 +199,44 @@ def test_bounds_of_an_empty_batch(call, state):
             y, end = efla.ssm_scan(**a, cu_seqlens=cu, return_state=state)
         assert y.shape == (1, 0, 16) and (end is None) == (not state)
         assert efla.device_status() == int(bad), bounds
+
+
+@pytest.mark.parametrize("bounds, exact", [
+    ([0, 40, 5000, 4200, 5000], [0]), ([-3, 2500, 2600, 5001, 5000], [1]), ([10, 10, 3000, 3001, 4990], [0, 1, 2, 3]),
+    ([0, 3000, 2000, 3000, 5000], []),     # more segments than 5000 tokens have: the last sequence is left out
+    ([5000, 0, 5000, 0, 5000], [])])
+def test_cut_sequences_around_bad_bounds(bounds, exact):
+    """Malformed bounds are reported, their states left alone; a sequence is computed or left alone as a whole, unless
+    another one has its tokens too; nothing else is written."""
+    T, D, n = 5000, 16, len(bounds) - 1
+    a = scan_inputs(B=1, T=T, D=D, seqs=n)
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    need = efla.ssm_scan_workspace(1, T, D, 16, N=n)
+    assert need > 0
+    y, ok_y = between_sentinels(torch.full((1, T, D), 7.0, device="cuda"))
+    end, ok_end = between_sentinels(torch.full((n, D, 16), 7.0, device="cuda"))
+    ws, ok_ws = between_sentinels(torch.zeros(need, dtype=torch.uint8, device="cuda"))
+    efla.ssm_scan(**a, cu_seqlens=cu, y=y, S_T=end, workspace=ws)
+    good = [i for i in range(n) if 0 <= bounds[i] <= bounds[i + 1] <= T]
+    assert efla.device_status() == int(len(good) < n)
+    assert ok_y() and ok_end() and ok_ws()
+    covered = torch.zeros(T, dtype=torch.int32, device="cuda")
+    for i in range(n):
+        if i in good:
+            covered[bounds[i]:bounds[i + 1]] += 1
+        else:
+            assert bool((end[i] == 7).all())
+    assert bool((y[0, covered == 0] == 7).all())
+    for i in good:
+        lo, hi = bounds[i:i + 2]
+        if bool((covered[lo:hi] > 1).any()):
+            continue
+        if i not in exact and bool((end[i] == 7).all()):
+            assert bool((y[0, lo:hi] == 7).all()), i
+            continue
+        one = {k: v[:, lo:hi].contiguous() if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items()}
+        one["S0"] = a["S0"][i:i + 1].contiguous()
+        ref, ref_S = ssm.scan(**one)
+        size, size_S = ssm.scan(**one, size=True)
+        close(y[:, lo:hi], ref, size, scan_share(hi - lo), f"y {i}")
+        close(end[i:i + 1], ref_S, size_S, scan_share(hi - lo), f"S {i}")
