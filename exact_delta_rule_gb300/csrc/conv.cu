@@ -10,7 +10,7 @@
 // Bound by HBM: x is read and y written once.  A thread takes 4 channels and walks down a run of tokens with the last
 // W - 1 rows in registers, so a row is read once by its run and again only as the W - 1 rows before the next.  Rows
 // come into the thread's own slots of shared memory by asynchronous copies, a group of them at a time and the next groups under
-// way.  Code for groups inside their row is straight; channels go in pairs, in packed arithmetic.  Runs of the forward
+// way.  Code for groups inside their row is straight (packed sequences go token by token); channels go in pairs, in packed arithmetic.  Runs of the forward
 // are 32 tokens at most; those of the backward, which computes the gradients of the tokens before a run again, as
 // long as fills the GPU.  Arithmetic is fp32, each output rounded once; the sums over tokens go in two stages of fixed order.
 // 8 x 2048 tokens, W = 4, silu, bf16: forward of 6144 channels 70 us (403 MB, 5.8 TB/s), of 2048 26 (134 MB); backward with

@@ -16,7 +16,7 @@ struct ConvArgs {
     const void *dy, *dstate_T;  // backward
     void *dx, *dstate0;
     float *dw, *dbias;
-    float *ws;                // backward: conv_bwd_parts(..) x D (W + 1) floats
+    float *ws;                // backward: ConvRuns::parts x D (W + 1) floats
     int B, T, D, W, N;
     efla_dtype dtype;
     int silu;
@@ -24,7 +24,7 @@ struct ConvArgs {
     int *status;
 };
 
-// Vectors a row of a CTA's threads covers (forward: 16 bytes, backward: 4 channels), a power of two up to 32.
+// Vectors of 4 channels that a row of a CTA's threads covers, a power of two up to 32.
 inline int conv_lanes(int vecs) {
     int n = 1;
     while (n < vecs && n < 32) n *= 2;

@@ -15,7 +15,7 @@ struct GroupNormArgs {
     const void *dy;          // backward
     void *dx;
     float *dw, *db;          // [C] or nullptr
-    float *ws;               // group_norm_ws(..) floats
+    float *ws;               // gn_ws(..) floats
     int rows, L, C, G;
     efla_dtype dtype;
     int silu;
@@ -34,7 +34,7 @@ inline int gn_team(int vecs) {
     return n;
 }
 inline bool gn_whole(int L, int C, int G, efla_dtype t) { return L == 1 && C / G % gn_vec(t) == 0 && C / G <= 32 * gn_vec(t); }
-// Rows a CTA of the whole-row backward shares out among `parts` CTAs a block of channels: two CTAs a SM.
+// Rows a CTA of the whole-row backward shares out among `parts` CTAs a block of channels: three CTAs a SM.
 inline int gn_blocks(int C, int G, efla_dtype t) {
     const int per = 32 / gn_team(C / G / gn_vec(t));
     return (G + per - 1) / per;

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(NT) ssm_bwd_kernel(SsmBwdArgs p, int tiles) {
     const int each = f.D / f.G, tpg = tiles / f.G, group = tile / tpg, c0 = group * each + tile % tpg * CT;
     const int have = min(CT, (group + 1) * each - c0);
     const int ch = warp * CG * 4 + cg * 4;  // this thread's first channel of the tile
-    const bool live = ch < have;            // (tiles have a multiple of 8 channels)
+    const bool live = ch < have;            // (tiles have a multiple of 4 channels)
     const size_t dn = (size_t)f.D * N;
 
     float *delta_s = reinterpret_cast<float *>(smem + K::F), *u_s = delta_s + TOK * CT, *g_s = u_s + TOK * CT, *y_s = g_s + TOK * CT;

@@ -217,7 +217,8 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Te
     x, dt, z [B,T,D] and B, C [B,T,G,d_state] (bf16 or fp32; the D / G channels of a group share B and C), A_log
     [D,d_state], D and dt_bias [D] fp32; S0 [N,D,d_state] fp32; cu_seqlens [N+1] int32 (then the batch is 1).
     Returns (y [B,T,D] in x's dtype, S_T [N,D,d_state] fp32 or None when ``return_state`` is False).  ``workspace`` (of
-    ``ssm_scan_workspace(...)`` bytes) is allocated here when not given.
+    ``ssm_scan_workspace(...)`` bytes) is allocated here when not given.  How packed sequences are cut goes by their mean
+    length: one that is far longer than many short ones is faster in a call of its own.
     """
     (rows, T), ch, N, G, code = _ssm_args(x, dt, A_log, B, C, D, dt_bias, z, 2)
     seqs = _sequences(cu_seqlens, rows, x)
