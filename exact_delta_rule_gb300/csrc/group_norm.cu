@@ -8,11 +8,11 @@
 //     are shuffles; one pass, the next rows' copies under way (16384 rows of 16 groups of 128, bf16: forward 24 us for
 //     134 MB, backward with its sums 38 for 202; 65536 rows 86 and 128, 6.2 TB/s; 92 and 144 with four rows loaded together);
 //   groups of whole vectors and up to 8192 elements of a sample: in the registers of 64 to 512 threads; one pass, bound by the
-//     barriers of its sums and by issue (16384 rows of 2048 in one group, bf16: forward 38 us, with gradients 92; 51 and
+//     exchange of its sums (shuffles, shared memory, barriers) and by issue (16384 rows of 2048 in one group, bf16: forward 38 us, with gradients 92; 51 and
 //     189 as a warp's samples; 4096 samples of 16 x 256 in 8 groups 21 and 55; 94 and 238 a warp);
 //   samples of few elements, or many of up to 16 KB: one a warp, in shared memory;
 //   forward, other samples: tiles of whole groups in the shared memory of a cluster, whose CTAs share out the positions
-//     and read one another's sums; one pass (8 maps of 4096 positions x 320 channels in 32 groups: 14 us; three kernels took 33);
+//     and read one another's sums; one pass (8 maps of 4096 positions x 320 channels in 32 groups: 17 us, three kernels 24; 64 maps 103, 124);
 //   the rest in three kernels: sums per channel over chunks of the positions, joined to those of the groups, and
 //     applied, where x is found in L2 if it fits (backward of 64 maps of 4096 x 320, bf16: 97 us, 3 and 116; one position
 //     at a time and rows cut into 32 vectors and 8: 251, 3 and 167).
