@@ -565,7 +565,7 @@ efla_status efla_ssm_step(const void *x, const void *dt, const float *A_log, con
  *   workspace  at least efla_group_norm_workspace bytes (0 for some sizes), overlapping no argument
  * C a multiple of 8 and of groups.  y == x is allowed.  fp32 arithmetic, each output rounded once.  A mean far from 0
  * costs what holding it in fp32 does: it is off by a few of its own roundings (2^-24 of the values' size, 40 times at
- * most), and n by that over sqrt(var); the variance is taken from the mean.
+ * most, 90 for maps in groups of 1000 channels and more), and n by that over sqrt(var); the variance is taken from the mean.
  */
 efla_status efla_group_norm(const void *x, const float *w, const float *b, void *y, float *stats, int rows, int L,
                             int C, int groups, efla_dtype dtype, efla_activation activation, float eps,

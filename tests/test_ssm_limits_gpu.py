@@ -141,8 +141,10 @@ def test_convolution_backward_of_the_longest_row():
     ((1, 64, 64, 320), 32, 32 * 62, 20),
     ((1, 5000, 520), 5, 32 * 71, 24),      # (fp32: three kernels)
     ((1, 70001, 8), 1, 32 * 307, 20),
+    ((3, 33, 2040), 1, 32 * 86, 90),       # (fp32: three kernels)
     ((2, 30000, 64), 2, 347, 4),           # three kernels
     ((1, 20000, 40), 40, 80, 4),
+    ((10, 6000, 512), 512, 84, 4),         # three kernels, a warp for each of many groups
     ((4, 72000), 3, 779, 4)])
 @pytest.mark.parametrize("kind", ["mean", "first"])
 @pytest.mark.parametrize("dtype, silu", [(F32, True), (F32, False), (BF16, True)])
@@ -151,7 +153,7 @@ def test_group_norm_of_far_values(dtype, silu, kind, shape, groups, depth, whole
 
 
 @pytest.mark.parametrize("shape, groups, depth, whole", [
-    ((610, 500, 8), 8, 506, 4), ((3, 100, 8), 8, 106, 4), ((610, 33, 24), 3, 39, 4),   # a lane has many values
+    ((610, 500, 8), 8, 506, 4), ((3, 100, 8), 8, 106, 4), ((610, 33, 24), 3, 39, 4), ((610, 20, 152), 4, 46, 4),  # a lane has many values
     ((700, 16, 256), 32, 22, 24), ((610, 32, 16), 4, 38, 40),                          # up to 32
     ((610, 500, 8), 1, 506, 40)])                                                      # (fp32: a team's)
 @pytest.mark.parametrize("kind", ["mean", "first", "narrow"])
