@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(NT, BWD ? 0 : 4) gn_sums_kernel(GroupNormArgs 
 
 // Forward: a group's mean and r, by TEAM threads, from its pieces, each the mean and deviations of one channel of one chunk.  (A
 // warp a group took 38 us for 2 maps of 65536 x 128 in 8 groups, 304 chunks: 16 warps walk through 4864 pieces each; a CTA a
-// group 8.)
+// group 9.)
 template <int TEAM>
 __global__ void __launch_bounds__(NT) gn_moments_kernel(GroupNormArgs p, int chunks, float *out) {
     __shared__ float box[3][NT / 32];
